@@ -145,6 +145,9 @@ typedef struct {
 #define TDG_WHERE_MOE_EXPERT 4 /* an expert id outside [0, E)                 */
 #define TDG_WHERE_RING 5       /* ring AllReduce waiting on a tile of a step   */
 #define TDG_WHERE_RS_SIGNAL 6  /* GEMM-RS arrival counter update did not settle */
+#define TDG_WHERE_PAGE 7       /* a page id outside the pools, or a length outside the page table */
+#define TDG_WHERE_POS 8        /* a rotary position outside the table          */
+#define TDG_WHERE_CU 9         /* row offsets of packed sequences out of order or range */
 
 /*
  * Copy the status block to *out (may be NULL) after synchronising `stream`,
@@ -447,6 +450,181 @@ typedef struct {
 TDG_API size_t tdg_flash_decode_part_bytes(int world, int64_t B, int64_t Hq, int64_t D, int64_t S,
                                            int64_t chunk);
 TDG_API int tdg_flash_decode(tdg_symm *h, const tdg_flash_decode_args *args, void *stream);
+
+/* ---- paged key-value cache ------------------------------------------------- */
+/*
+ * The cache that tdg_rope_append writes and tdg_paged_decode reads: one pool
+ * of pages for keys and one for values in every rank's region, each
+ * pages x Hkv x page_size x D elements (a page holds page_size tokens of every
+ * key head, one head after another).  Page id p, 0 <= p < world * pages, is
+ * page p % pages of rank p / pages.  A sequence's row of the page table lists
+ * the ids of its pages in order (int32): token j of the sequence is slot
+ * j % page_size of page table[j / page_size].  A table row has table_entries
+ * entries and rows are table_stride entries apart; entries past the sequence's
+ * last page are not read.
+ * TDG_KV_E4M3 stores 8 bits (sign, 4 exponent, 3 mantissa bits; largest 448):
+ * the value that stands for x of head h is x / scale[h], clamped to +-448 and
+ * rounded to nearest even.
+ * Requirements: D 64 or 128; page_size 16, 32, 64, 128 or 256; Hkv >= 1;
+ * world * pages < 2^31; k_off and v_off multiples of 1024; the pools
+ * (tdg_paged_pool_bytes each) inside the region (TDG_ERR_NOMEM otherwise) and
+ * not overlapping; k_scale and v_scale given exactly for TDG_KV_E4M3
+ * (positive finite values).
+ */
+#define TDG_KV_BF16 0
+#define TDG_KV_E4M3 1
+
+typedef struct {
+    int64_t pages;        /* pages in each rank's pools                        */
+    int page_size;        /* tokens of a page                                  */
+    int kv_type;          /* TDG_KV_BF16 or TDG_KV_E4M3                        */
+    int64_t Hkv, D;
+    size_t k_off, v_off;  /* offsets of the pools in every region              */
+    const float *k_scale; /* device, Hkv float32: TDG_KV_E4M3 only             */
+    const float *v_scale;
+} tdg_paged_cache;
+
+/* Bytes of one pool (keys or values) in one region; 0 for sizes not supported. */
+TDG_API size_t tdg_paged_pool_bytes(int64_t pages, int page_size, int64_t Hkv, int64_t D, int kv_type);
+
+/* ---- rotary positions and the cache write ----------------------------------- */
+/*
+ * For every row t of T new tokens: queries and keys are turned by their
+ * positions, written to q_out and k_out, and keys and values are written into
+ * the cache.  q: T rows of Hq heads, k and v: T rows of Hkv heads, head h at
+ * h * D of its row, rows *_stride elements apart (so the three may be columns
+ * of one projection's output); q_out and k_out likewise.
+ *   Rotation: pairs i = 0 .. rot_dim/2 - 1 of a head are elements
+ * (i, i + rot_dim/2), or (2i, 2i + 1) with interleaved = 1; elements from
+ * rot_dim on are kept.  With (c, s) = (cos_sin[p][i], cos_sin[p][rot_dim/2 + i])
+ * the pair (x, y) becomes (c x - s y, c y + s x) in float32.  p is the row's
+ * position on the axis that pair i belongs to: the first sections[0] pairs go
+ * by pos[t], the next sections[1] by pos[pos_stride + t], the next sections[2]
+ * by pos[2 * pos_stride + t] (axes 1, 2 or 3; with axes = 1 the sections are
+ * not read).  A position outside [0, max_pos) is reported as TDG_ERR_DEVICE
+ * (TDG_WHERE_POS, index t) and nothing of that row is written.
+ *   Cache write: rows [cu[b], cu[b+1]) are the last rows of sequence b, whose
+ * length with them is lens[b]; with cu NULL row b is the last token of
+ * sequence b (T == B).  Rows from cu[B] on belong to no sequence and are not
+ * stored.  Keys are rounded once, from float32.  A length that does not fit
+ * the table row, that is below the sequence's new rows, or a page id outside
+ * the pools is reported (TDG_WHERE_PAGE, index t) and the row is not stored.
+ * Two rows must not share a slot of the cache.
+ *   What is not wanted is left out: q and q_out NULL (no queries, Hq = 0),
+ * k_out NULL, table NULL (no cache write; v, cu, lens and the pools are then
+ * not read), rot_dim = 0 (no rotation).  q_out may be q, and k_out may be k
+ * (same stride); other overlaps are not allowed.
+ * Requirements: world the heap's; 0 <= T < 2^31; B >= 0; Hq, Hkv <= 65536;
+ * rot_dim a multiple of 16, at most D; sections non-negative with the sum
+ * rot_dim/2; strides multiples of 8 elements and at least the row's extent;
+ * device pointers 16-byte aligned (pos, cu, table, lens, scales 4-byte); the
+ * table as for tdg_paged_decode.  T == 0 is a no-op.  The cache's D and Hkv describe k also when table is NULL.
+ */
+typedef struct {
+    int world;
+    tdg_paged_cache cache;
+    int64_t T, B, Hq;
+    const void *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;
+    void *q_out, *k_out;
+    int64_t q_out_stride, k_out_stride;
+    const float *cos_sin; /* max_pos x rot_dim float32: cosines, then sines    */
+    int64_t max_pos;
+    int rot_dim;
+    int interleaved;
+    int axes;
+    int sections[3];
+    const int32_t *pos;   /* axes rows of positions, pos_stride apart          */
+    int64_t pos_stride;
+    const int32_t *cu;    /* B + 1 row offsets, or NULL                        */
+    const int32_t *table;
+    int64_t table_entries, table_stride;
+    const int32_t *lens;
+} tdg_rope_append_args;
+
+TDG_API int tdg_rope_append(tdg_symm *h, const tdg_rope_append_args *args, void *stream);
+
+/* ---- attention over whole prompts -------------------------------------------- */
+/*
+ * B sequences packed one after another: rows [cu_q[b], cu_q[b+1]) of q and
+ * rows [cu_k[b], cu_k[b+1]) of k and v belong to sequence b (Lq and Lk rows).
+ * Query row i of a sequence, head h, sees key rows j <= i + Lk - Lq (causal =
+ * 1: the last query sees the last key) or all Lk (causal = 0):
+ *   out[i][h] = sum_j softmax_j(scale * q[i][h] . k[j][g]) v[j][g],
+ * g = h / (Hq/Hkv).  A row that sees no key gives 0.  lse (NULL or Tq x Hq
+ * float32) receives log sum_j exp(scale * q . k), -inf for a row that sees no
+ * key.  Keys and values of masked rows of other sequences never reach a
+ * result, whatever they hold; within a sequence a masked row takes part with
+ * the weight 0, so its key may hold anything, its value must be finite.
+ * Scores, softmax statistics and sums are float32; the weights are rounded to
+ * bf16 for the product with v.
+ * q, out: Tq rows of Hq heads of D; k, v: Tk rows of Hkv heads; head h at h*D
+ * of a row, rows *_stride elements apart.  Rows of q that no sequence covers
+ * are left alone.  Offsets out of order, negative or past Tq / Tk are reported
+ * as TDG_ERR_DEVICE (TDG_WHERE_CU, index b) and the sequence is skipped.
+ * Requirements: D 64 or 128; Hq % Hkv == 0, Hq/Hkv <= 128; 0 <= Tq, Tk < 2^31;
+ * 0 <= B <= 65535; strides multiples of 8 elements and at least the row's
+ * extent; pointers 16-byte aligned (cu_q, cu_k, lse 4-byte); scale finite and
+ * >= 0 (0 = 1/sqrt(D)); causal 0 or 1; out overlapping no input.  Tq == 0 or
+ * B == 0 is a no-op; Tk == 0 gives rows that see nothing.
+ */
+typedef struct {
+    int64_t Tq, Tk, B, Hq, Hkv, D;
+    const void *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;
+    void *out;
+    int64_t out_stride;
+    float *lse;
+    const int32_t *cu_q, *cu_k; /* device, B + 1 each                          */
+    int causal;
+    float scale;
+} tdg_prompt_attention_args;
+
+TDG_API int tdg_prompt_attention(tdg_symm *h, const tdg_prompt_attention_args *args, void *stream);
+
+/* ---- attention of one new token over the paged cache ------------------------- */
+/*
+ * For every sequence b and head h, over the lens[b] tokens of its cache (the
+ * new token's own key and value among them, see tdg_rope_append):
+ *   out[b][h] = sum_j softmax_j(scale * q[b][h] . k_j) v_j,  g = h / (Hq/Hkv).
+ * A sequence of length 0 gives 0, and -inf in lse (NULL or B x Hq float32, the
+ * natural logarithm of the sum of exponentials).  The work is divided evenly
+ * over the GPU whatever the lengths: it is cut into 64-token tiles, and every
+ * CTA takes an equal run of them, so long sequences are split and short ones
+ * grouped.  Partial results (row maximum, row sum, unnormalised output,
+ * float32) go to region(root) + part_off (tdg_paged_decode_part_bytes), and a
+ * second, stream-ordered launch joins the split ones in a fixed order.
+ * What the pages hold behind a sequence's length never reaches a result.
+ * A negative length, one that does not fit the table row, or a page id
+ * outside the pools is reported as TDG_ERR_DEVICE (TDG_WHERE_PAGE, index b);
+ * that sequence's output is then undefined.
+ * q, out: B rows of Hq heads of D, head h at h*D, rows *_stride elements apart.
+ * Requirements: those of the cache; Hq % Hkv == 0, Hq/Hkv <= 128; 0 <= B <=
+ * 65535; 0 <= table_entries <= table_stride, table_entries * page_size < 2^31; 0 <= root <
+ * world; strides multiples of 8 elements and at least the row's extent; q,
+ * out and part_off 16-byte aligned; scale finite and >= 0 (0 = 1/sqrt(D));
+ * the partials overlapping neither pool, out not overlapping q.  B == 0 is a
+ * no-op.
+ */
+typedef struct {
+    int world, root;
+    tdg_paged_cache cache;
+    int64_t B, Hq;
+    const void *q;
+    int64_t q_stride;
+    void *out;
+    int64_t out_stride;
+    float *lse;
+    const int32_t *table;
+    int64_t table_entries, table_stride;
+    const int32_t *lens;
+    size_t part_off;
+    float scale;
+} tdg_paged_decode_args;
+
+/* Bytes of the partial results for the given heads (any B and lengths). */
+TDG_API size_t tdg_paged_decode_part_bytes(int64_t Hq, int64_t Hkv, int64_t D);
+TDG_API int tdg_paged_decode(tdg_symm *h, const tdg_paged_decode_args *args, void *stream);
 
 /* ---- MoE dispatch / combine ------------------------------------------------ */
 /*

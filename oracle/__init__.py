@@ -76,6 +76,13 @@ def _L():
             lib.orc_allreduce.argtypes = [i32, i64, vp, vp]
             lib.orc_attention_decode.argtypes = [i64, i64, i64, i64, i64, vp, vp, vp,
                                                  ctypes.c_double, vp]
+            lib.orc_e4m3_to_f64.restype = ctypes.c_double
+            lib.orc_e4m3_to_f64.argtypes = [ctypes.c_uint8]
+            lib.orc_f64_to_e4m3.restype = ctypes.c_uint8
+            lib.orc_f64_to_e4m3.argtypes = [ctypes.c_double]
+            lib.orc_rope.argtypes = [i64, i64, i64, i32, i32, i32, vp, vp, vp, vp, vp, vp]
+            lib.orc_attention.argtypes = [i64, i64, i64, i64, i64, i32, vp, vp, vp, ctypes.c_double,
+                                          vp, vp, vp, vp]
             _lib = lib
     return _lib
 
@@ -273,3 +280,66 @@ def attention_decode(q, k, v, scale=None):
     out = np.empty((B, Hq, D), np.float64)
     _L().orc_attention_decode(B, Hq, Hkv, D, S, _p(q), _p(k), _p(v), float(scale), _p(out))
     return out
+
+
+# ------------------------------------------------------ the paged cache ----
+def e4m3_to_f64(b: np.ndarray) -> np.ndarray:
+    """8-bit codes (uint8) to the values they stand for."""
+    table = np.array([_L().orc_e4m3_to_f64(i) for i in range(256)])
+    return table[np.ascontiguousarray(b, np.uint8)]
+
+
+def f64_to_e4m3(x) -> np.ndarray:
+    """Nearest 8-bit codes, ties to even, clamped to +-448."""
+    x = np.ascontiguousarray(x, np.float64)
+    return np.array([_L().orc_f64_to_e4m3(float(v)) for v in x.reshape(-1)], np.uint8).reshape(x.shape)
+
+
+def rope(x, cos_sin, pos, sections=None, interleaved=False):
+    """x: (T, H, D) bf16 bits; cos_sin: (positions, rot) float32; pos: (axes, T)
+    int32.  Returns float64 (values, error scale), both (T, H, D)."""
+    x = _u16(x)
+    cos_sin = np.ascontiguousarray(cos_sin, np.float32)
+    pos = np.ascontiguousarray(np.atleast_2d(pos), np.int32)
+    T, H, D = x.shape
+    assert pos.shape[1] == T and pos.min(initial=0) >= 0 and pos.max(initial=0) < len(cos_sin)
+    sec = np.ascontiguousarray(sections if sections is not None else [cos_sin.shape[1] // 2], np.int32)
+    assert sec.size == pos.shape[0] and int(sec.sum()) == cos_sin.shape[1] // 2
+    out, mag = np.empty(x.shape, np.float64), np.empty(x.shape, np.float64)
+    _L().orc_rope(T, H, D, cos_sin.shape[1], int(interleaved), pos.shape[0], _p(sec), _p(x), _p(cos_sin),
+                  _p(pos), _p(out), _p(mag))
+    return out, mag
+
+
+def cache_rows(table, lens, page_size, cu=None):
+    """(page id, slot) of every row that an append stores: rows [cu[b], cu[b+1])
+    are the last rows of sequence b (cu None: one row each)."""
+    out = []
+    for b, n in enumerate(int(v) for v in lens):
+        new = 1 if cu is None else int(cu[b + 1]) - int(cu[b])
+        for j in range(n - new, n):
+            out.append((int(table[b][j // page_size]), j % page_size))
+    return out
+
+
+def gather_pages(pool, table_row, n):
+    """The first n tokens of a sequence, (n, Hkv, D), from a pool (pages, Hkv,
+    page_size, D) over every rank's pages."""
+    ps = pool.shape[2]
+    rows = [pool[int(table_row[j // ps]), :, j % ps] for j in range(int(n))]
+    return np.stack(rows) if rows else np.zeros((0, pool.shape[1], pool.shape[3]), pool.dtype)
+
+
+def attention(q, k, v, causal=True, scale=None):
+    """Softmax attention of one sequence.  q: (Lq, Hq, D), k, v: (Lk, Hkv, D)
+    float64.  Returns a dict: out, lse, and the error scales mag (sum of
+    weights times |v|) and smag (largest scale * sum |q k|)."""
+    q, k, v = (np.ascontiguousarray(a, np.float64) for a in (q, k, v))
+    Lq, Hq, D = q.shape
+    Lk, Hkv, _ = k.shape
+    assert Hq % Hkv == 0 and k.shape == v.shape
+    out, mag = np.empty((Lq, Hq, D)), np.empty((Lq, Hq, D))
+    lse, smag = np.empty((Lq, Hq)), np.empty((Lq, Hq))
+    _L().orc_attention(Lq, Lk, Hq, Hkv, D, int(causal), _p(q), _p(k), _p(v),
+                       float(1.0 / np.sqrt(D) if scale is None else scale), _p(out), _p(lse), _p(mag), _p(smag))
+    return dict(out=out, lse=lse, mag=mag, smag=smag)

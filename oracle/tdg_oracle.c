@@ -465,3 +465,139 @@ ORC_EXPORT void orc_attention_decode(int64_t B, int64_t Hq, int64_t Hkv, int64_t
         free(s);
     }
 }
+
+/* ------------------------------------------------------------------------ */
+/* 8-bit floats of the key-value cache: sign, 4 exponent bits (bias 7), 3     */
+/* fraction bits, no infinity, 0x7F / 0xFF not a number, largest value 448    */
+/* ------------------------------------------------------------------------ */
+
+ORC_EXPORT double orc_e4m3_to_f64(uint8_t b)
+{
+    const int e = (b >> 3) & 15, f = b & 7;
+    if ((b & 0x7F) == 0x7F)
+        return NAN;
+    const double m = e ? ldexp(8.0 + f, e - 10) : ldexp((double)f, -9);
+    return b & 0x80 ? -m : m;
+}
+
+/* Clamp to +-448, then nearest value, ties to the even code. */
+ORC_EXPORT uint8_t orc_f64_to_e4m3(double x)
+{
+    if (isnan(x))
+        return 0x7F;
+    const uint8_t sign = signbit(x) ? 0x80 : 0;
+    const double a = fabs(x);
+    if (a >= 448.0)
+        return sign | 0x7E;
+    int lo = 0; /* largest code not above a: codes 0 .. 0x7E ascend in value */
+    while (lo < 0x7E && orc_e4m3_to_f64((uint8_t)(lo + 1)) <= a)
+        ++lo;
+    const double down = a - orc_e4m3_to_f64((uint8_t)lo);
+    const double up = orc_e4m3_to_f64((uint8_t)(lo + 1)) - a;
+    if (up < down || (up == down && (lo & 1)))
+        ++lo;
+    return sign | (uint8_t)lo;
+}
+
+/* ------------------------------------------------------------------------ */
+/* Rotary positions                                                          */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * x: T x H x D (bf16 bits).  Pair i (0 <= i < rot/2) is elements (i, i + rot/2),
+ * or (2i, 2i+1) when interleaved; it turns by the table row of the position on
+ * its axis, pos[axis][t]:  (x, y) -> (c x - s y, c y + s x).  Elements from rot
+ * on are kept.  mag receives |c x| + |s y| of each output (an error scale).
+ */
+ORC_EXPORT void orc_rope(int64_t T, int64_t H, int64_t D, int rot, int interleaved, int axes, const int32_t *sections,
+                         const uint16_t *x, const float *cos_sin, const int32_t *pos, double *out, double *mag)
+{
+    for (int64_t t = 0; t < T; ++t)
+        for (int64_t h = 0; h < H; ++h) {
+            const uint16_t *r = x + (t * H + h) * D;
+            double *o = out + (t * H + h) * D, *m = mag + (t * H + h) * D;
+            for (int64_t d = 0; d < D; ++d) {
+                o[d] = orc_bf16_to_f64(r[d]);
+                m[d] = fabs(o[d]);
+            }
+            for (int i = 0; i < rot / 2; ++i) {
+                int a = 0, end = axes > 1 ? sections[0] : rot / 2;
+                while (i >= end)
+                    end += sections[++a];
+                const float *row = cos_sin + (int64_t)pos[a * T + t] * rot;
+                const double c = row[i], s = row[rot / 2 + i];
+                const int d0 = interleaved ? 2 * i : i, d1 = interleaved ? 2 * i + 1 : i + rot / 2;
+                const double p = orc_bf16_to_f64(r[d0]), q = orc_bf16_to_f64(r[d1]);
+                o[d0] = c * p - s * q;
+                o[d1] = c * q + s * p;
+                m[d0] = fabs(c * p) + fabs(s * q);
+                m[d1] = fabs(c * q) + fabs(s * p);
+            }
+        }
+}
+
+/* ------------------------------------------------------------------------ */
+/* Softmax attention of one sequence                                         */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * q: Lq x Hq x D, k and v: Lk x Hkv x D (double).  Query i sees key j when
+ * causal is 0 or j <= i + Lk - Lq.
+ *   out[i][h] = sum_j w_j v_j / sum_j w_j,  w_j = exp(scale q.k_j - max)
+ *   lse[i][h] = log sum_j exp(scale q.k_j)
+ *   mag[i][h][d] = sum_j w_j |v_j[d]| / sum_j w_j   (an error scale)
+ *   smag[i][h]  = max_j scale sum_d |q_d k_jd|        (an error scale)
+ * A row that sees no key: 0, lse = -inf.
+ */
+ORC_EXPORT void orc_attention(int64_t Lq, int64_t Lk, int64_t Hq, int64_t Hkv, int64_t D, int causal, const double *q,
+                              const double *k, const double *v, double scale, double *out, double *lse, double *mag,
+                              double *smag)
+{
+    const int64_t G = Hq / Hkv;
+#pragma omp parallel for schedule(dynamic, 4)
+    for (int64_t ih = 0; ih < Lq * Hq; ++ih) {
+        const int64_t i = ih / Hq, h = ih % Hq, g = h / G;
+        int64_t n = causal ? i + Lk - Lq + 1 : Lk;
+        if (n > Lk)
+            n = Lk;
+        if (n < 0)
+            n = 0;
+        double *o = out + ih * D, *m = mag + ih * D;
+        for (int64_t d = 0; d < D; ++d)
+            o[d] = m[d] = 0.0;
+        lse[ih] = -INFINITY;
+        smag[ih] = 0.0;
+        if (n == 0)
+            continue;
+        double *w = (double *)malloc(sizeof(double) * (size_t)n);
+        double top = -INFINITY, den = 0.0;
+        for (int64_t j = 0; j < n; ++j) {
+            double a = 0.0, b = 0.0;
+            for (int64_t d = 0; d < D; ++d) {
+                const double t = q[ih * D + d] * k[(j * Hkv + g) * D + d];
+                a += t;
+                b += fabs(t);
+            }
+            w[j] = scale * a;
+            if (w[j] > top)
+                top = w[j];
+            if (scale * b > smag[ih])
+                smag[ih] = scale * b;
+        }
+        for (int64_t j = 0; j < n; ++j) {
+            w[j] = exp(w[j] - top);
+            den += w[j];
+        }
+        for (int64_t j = 0; j < n; ++j)
+            for (int64_t d = 0; d < D; ++d) {
+                o[d] += w[j] * v[(j * Hkv + g) * D + d];
+                m[d] += w[j] * fabs(v[(j * Hkv + g) * D + d]);
+            }
+        for (int64_t d = 0; d < D; ++d) {
+            o[d] /= den;
+            m[d] /= den;
+        }
+        lse[ih] = top + log(den);
+        free(w);
+    }
+}

@@ -1,0 +1,199 @@
+"""GPU parity of the attention over packed prompts against the oracle."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from tile_centric_comm_gb300 import tdg
+from attn_util import bits, check_attention, check_lse, strided_rows, to_bits, to_dev_bf16
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def symm():
+    return tdg.Symm(1, 1024, 16)
+
+
+def _ends(n, gap=0):
+    return np.concatenate([[0], np.cumsum(n)]).astype(np.int32) + gap
+
+
+class Case:
+    def __init__(self, nq, nk, Hq, Hkv, D, seed=0, tail=0, q_mul=1.0):
+        g = np.random.default_rng(seed)
+        self.nq, self.nk, self.Hq, self.Hkv, self.D = list(nq), list(nk), Hq, Hkv, D
+        self.cu_q, self.cu_k = _ends(nq), _ends(nk)
+        Tq, Tk = sum(nq) + tail, sum(nk) + tail
+        self.q = bits(g.standard_normal((Tq, Hq, D)) * q_mul)
+        self.k, self.v = bits(g.standard_normal((Tk, Hkv, D))), bits(g.standard_normal((Tk, Hkv, D)) + 0.25)
+
+    def run(self, symm, causal=True, scale=0.0, lse=True, stream=None):
+        Tq = len(self.q)
+        _, (q, out) = strided_rows([self.q, np.full_like(self.q, 0x7FC1)])
+        _, (k, v) = strided_rows([self.k, self.v])
+        e = torch.full((Tq, self.Hq), float("nan"), device="cuda") if lse else None
+        cu_q, cu_k = (torch.from_numpy(c).cuda() for c in (self.cu_q, self.cu_k))
+        torch.cuda.synchronize()
+        tdg.prompt_attention(symm, q, k, v, out, cu_q, cu_k, lse=e, causal=causal, scale=scale, stream=stream)
+        torch.cuda.synchronize()
+        assert symm.status()["code"] == 0
+        return to_bits(out), e.cpu().numpy() if lse else None
+
+    def check(self, got, causal=True, scale=0.0, some=None, rows=None):
+        out, lse = got
+        for b in range(len(self.nq)) if some is None else some:
+            qs, ks = slice(self.cu_q[b], self.cu_q[b + 1]), slice(self.cu_k[b], self.cu_k[b + 1])
+            q, k, v = (oracle.bf16_to_f64(x) for x in (self.q[qs], self.k[ks], self.v[ks]))
+            o, e = out[qs], None if lse is None else lse[qs]
+            if rows is not None and len(q) > rows and causal:     # the last rows of a long one
+                q, o, e = q[-rows:], o[-rows:], None if e is None else e[-rows:]
+            want = oracle.attention(q, k, v, causal, scale or None)
+            check_attention(o, want, self.D, f"sequence {b} ({self.nq[b]} x {self.nk[b]})")
+            if e is not None:
+                check_lse(e, want, self.D, f"lse of sequence {b}")
+        assert np.all(out[self.cu_q[-1]:] == 0x7FC1)              # rows of no sequence
+
+
+LENS = [1, 2, 0, 127, 128, 129, 31, 255, 256, 257, 16, 300]
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (2, 1), (5, 1), (14, 2), (8, 1), (16, 1), (6, 2)])
+def test_packed_causal(symm, D, Hq, Hkv):
+    c = Case(LENS, LENS, Hq, Hkv, D, seed=Hq * D, tail=3)
+    got = c.run(symm)
+    c.check(got)
+    again = c.run(symm)
+    assert np.array_equal(got[0], again[0]) and np.array_equal(got[1], again[1], equal_nan=True)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("Hq,Hkv", [(8, 1), (3, 3), (128, 1), (33, 1)])
+def test_unlike_lengths(symm, D, causal, Hq, Hkv):
+    # pieces behind cached keys, more queries than keys (rows that see nothing), no keys, no queries
+    nq = [1, 64, 100, 40, 7, 0, 5, 130]
+    nk = [300, 64, 513, 13, 0, 50, 128, 129]
+    c = Case(nq, nk, Hq, Hkv, D, seed=Hq, tail=1)
+    c.check(c.run(symm, causal), causal)
+
+
+def test_no_lse_scale_and_stream(symm):
+    c = Case([70, 200], [70, 200], 4, 2, 128, seed=3)
+    s = torch.cuda.Stream()
+    c.check(c.run(symm, scale=0.2, lse=False, stream=s), scale=0.2)
+
+
+@pytest.mark.parametrize("q_mul", [1e-30, 20.0])
+def test_query_sizes(symm, q_mul):
+    c = Case([300, 257], [300, 600], 8, 2, 128, seed=4, q_mul=q_mul)
+    c.check(c.run(symm))
+
+
+def test_growing_scores(symm):
+    # every later key scores higher than all before it, by far more than the exponent's comfortable range
+    c = Case([640], [640], 2, 1, 128, seed=6)
+    k = np.zeros((640, 1, 128), np.float32)
+    k[:, 0, 0] = np.arange(640) * 0.5
+    q = np.zeros((640, 2, 128), np.float32)
+    q[..., 0] = 8.0
+    q[:, 1, 0] = -8.0                                    # and falling for the other head
+    c.q, c.k = bits(q), bits(k)
+    c.check(c.run(symm))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_what_others_hold_does_not_matter(symm, D):
+    # the neighbours of sequence 1 hold NaN and infinity in queries, keys and values, its own later keys too
+    c = Case([70, 130, 90], [70, 130, 90], 4, 2, D, seed=5, tail=2)
+    good = slice(70, 200)
+    for x in (c.q, c.k, c.v):
+        keep = x[good].copy()
+        x[:] = np.where(np.arange(x.size).reshape(x.shape) % 2, 0x7FC1, 0x7F80).astype(np.uint16)
+        x[good] = keep
+    got = c.run(symm)
+    c.check(got, some=[1])
+    # a key that a row does not see may hold anything: all rows but the last stay as they were
+    c.k[199] = 0x7FC1
+    bad = c.run(symm)
+    assert np.array_equal(bad[0][70:199], got[0][70:199]) and np.array_equal(bad[1][70:199], got[1][70:199])
+
+
+def test_many_sequences(symm):
+    g = np.random.default_rng(7)
+    n = g.integers(0, 40, 500).tolist()
+    c = Case(n, n, 4, 1, 64, seed=7)
+    c.check(c.run(symm))
+
+
+def test_nothing_to_do(symm):
+    q = torch.empty((0, 4, 128), dtype=torch.bfloat16, device="cuda")
+    k = torch.empty((0, 2, 128), dtype=torch.bfloat16, device="cuda")
+    cu = torch.zeros(2, dtype=torch.int32, device="cuda")
+    tdg.prompt_attention(symm, q, k, k, q, cu, cu)
+    # queries without a single key
+    c = Case([5], [0], 4, 2, 128)
+    out, lse = c.run(symm)
+    assert np.all(out == 0) and np.all(np.isneginf(lse))
+
+
+@pytest.mark.slow
+@pytest.mark.parametrize("Hq,Hkv,D,n", [(64, 8, 128, 8192), (40, 8, 128, 5001), (8, 8, 64, 12345)])
+def test_long(symm, Hq, Hkv, D, n):
+    c = Case([n], [n], Hq, Hkv, D, seed=n)
+    c.check(c.run(symm), rows=3)
+    # and rows at the beginning and in the middle
+    out, lse = c.run(symm)
+    for i in (0, 1, 127, 128, n // 2):
+        q, k, v = (oracle.bf16_to_f64(x) for x in (c.q[i:i + 1], c.k[:i + 1], c.v[:i + 1]))
+        want = oracle.attention(q, k, v)
+        check_attention(out[i:i + 1], want, D, f"row {i}")
+        check_lse(lse[i:i + 1], want, D, f"row {i}")
+
+
+@pytest.mark.parametrize("cu_q,cu_k", [([0, 50, 40, 90], [0, 50, 60, 90]), ([0, 30, 60, 91], [0, 30, 60, 90]),
+                                       ([-1, 30, 60, 90], [0, 30, 60, 90]), ([0, 30, 60, 90], [0, 30, 60, 95])])
+def test_bad_offsets_are_reported(symm, cu_q, cu_k):
+    c = Case([30, 30, 30], [30, 30, 30], 4, 2, 64)
+    q, k, v = (to_dev_bf16(x) for x in (c.q, c.k, c.v))
+    out = torch.full(q.shape, float("nan"), dtype=torch.bfloat16, device="cuda")
+    tdg.prompt_attention(symm, q, k, v, out, torch.tensor(cu_q, dtype=torch.int32, device="cuda"),
+                         torch.tensor(cu_k, dtype=torch.int32, device="cuda"))
+    torch.cuda.synchronize()
+    st = symm.status()
+    assert st["code"] == tdg.TDG_ERR_DEVICE and st["where"] == "cu"
+
+
+def test_refusals(symm):
+    c = Case([30], [30], 4, 2, 128)
+    q, k, v = (to_dev_bf16(x) for x in (c.q, c.k, c.v))
+    out = torch.empty_like(q)
+    cu = torch.from_numpy(c.cu_q).cuda()
+
+    def rc(**kw):
+        a = tdg.PromptAttentionArgs(Tq=30, Tk=30, B=1, Hq=4, Hkv=2, D=128, q=q.data_ptr(), k=k.data_ptr(),
+                                    v=v.data_ptr(), q_stride=512, k_stride=256, v_stride=256, out=out.data_ptr(),
+                                    out_stride=512, cu_q=cu.data_ptr(), cu_k=cu.data_ptr(), causal=1)
+        for key, x in kw.items():
+            setattr(a, key, x)
+        return tdg.lib().tdg_prompt_attention(symm.h, ctypes.byref(a), None)
+
+    bad = tdg.TDG_ERR_INVALID
+    assert rc() == tdg.TDG_OK
+    assert rc(Tq=-1) == bad and rc(Tk=-1) == bad and rc(Tq=1 << 31) == bad and rc(B=65536) == bad
+    assert rc(Hq=5) == bad and rc(Hkv=0) == bad and rc(D=96) == bad and rc(Hq=258, q_stride=1 << 16, out_stride=1 << 16) == bad
+    assert rc(q=None) == bad and rc(k=None) == bad and rc(out=None) == bad and rc(cu_q=None) == bad
+    assert rc(q=q.data_ptr() + 4) == bad and rc(q_stride=508) == bad and rc(k_stride=248) == bad and rc(v_stride=260) == bad
+    assert rc(out_stride=504) == bad and rc(out=q.data_ptr()) == bad and rc(out=v.data_ptr()) == bad
+    assert rc(causal=2) == bad and rc(scale=-0.5) == bad and rc(scale=float("nan")) == bad
+    with pytest.raises(ValueError, match="fit together"):
+        tdg.prompt_attention(symm, q, k, v[:29], out, cu, cu)
+    with pytest.raises(TypeError, match="bfloat16"):
+        tdg.prompt_attention(symm, q.float(), k, v, out, cu, cu)
+    with pytest.raises(TypeError, match="int32"):
+        tdg.prompt_attention(symm, q, k, v, out, cu.long(), cu)
+    torch.cuda.synchronize()
+    assert symm.status()["code"] == 0

@@ -27,7 +27,9 @@ MODE_SM, MODE_CE, MODE_LL, MODE_SERIAL = 0, 1, 2, 3
 MODES = {"sm": MODE_SM, "ce": MODE_CE, "ll": MODE_LL, "serial": MODE_SERIAL}
 B_KN, B_NK = 0, 1
 MOE_ROUTE, MOE_DISPATCH, MOE_COMBINE, MOE_ALL = 1, 2, 4, 7
-WHERE = {1: "ag_flag", 2: "pipe", 3: "ll", 4: "moe_expert", 5: "ring", 6: "rs_signal"}
+KV_BF16, KV_E4M3 = 0, 1
+WHERE = {1: "ag_flag", 2: "pipe", 3: "ll", 4: "moe_expert", 5: "ring", 6: "rs_signal",
+         7: "page", 8: "pos", 9: "cu"}
 
 # every symbol include/tdg.h declares
 EXPORTS = [
@@ -36,6 +38,8 @@ EXPORTS = [
     "tdg_device_info", "tdg_ag_gemm", "tdg_ag_gemm_all_ranks", "tdg_gemm_rs_stage_bytes", "tdg_gemm_rs",
     "tdg_moe_workspace_bytes", "tdg_moe_dispatch_combine", "tdg_moe_dispatch_combine_noalloc",
     "tdg_allreduce_recv_bytes", "tdg_allreduce", "tdg_flash_decode_part_bytes", "tdg_flash_decode",
+    "tdg_paged_pool_bytes", "tdg_rope_append", "tdg_prompt_attention",
+    "tdg_paged_decode_part_bytes", "tdg_paged_decode",
 ]
 MOE_STATIC_WORKSPACE_BYTES = 2 * 1024 * 1024
 
@@ -94,6 +98,37 @@ class FlashDecodeArgs(ctypes.Structure):
                 ("Hkv", _i64), ("D", _i64), ("S", _i64), ("k_off", _sz), ("v_off", _sz),
                 ("part_off", _sz), ("q", _vp), ("out", _vp), ("chunk", _i64),
                 ("scale", ctypes.c_float)]
+
+
+class PagedCacheDesc(ctypes.Structure):
+    _fields_ = [("pages", _i64), ("page_size", ctypes.c_int), ("kv_type", ctypes.c_int),
+                ("Hkv", _i64), ("D", _i64), ("k_off", _sz), ("v_off", _sz), ("k_scale", _vp),
+                ("v_scale", _vp)]
+
+
+class RopeAppendArgs(ctypes.Structure):
+    _fields_ = [("world", ctypes.c_int), ("cache", PagedCacheDesc), ("T", _i64), ("B", _i64),
+                ("Hq", _i64), ("q", _vp), ("k", _vp), ("v", _vp), ("q_stride", _i64),
+                ("k_stride", _i64), ("v_stride", _i64), ("q_out", _vp), ("k_out", _vp),
+                ("q_out_stride", _i64), ("k_out_stride", _i64), ("cos_sin", _vp),
+                ("max_pos", _i64), ("rot_dim", ctypes.c_int), ("interleaved", ctypes.c_int),
+                ("axes", ctypes.c_int), ("sections", ctypes.c_int * 3), ("pos", _vp),
+                ("pos_stride", _i64), ("cu", _vp), ("table", _vp), ("table_entries", _i64), ("table_stride", _i64),
+                ("lens", _vp)]
+
+
+class PromptAttentionArgs(ctypes.Structure):
+    _fields_ = [("Tq", _i64), ("Tk", _i64), ("B", _i64), ("Hq", _i64), ("Hkv", _i64), ("D", _i64),
+                ("q", _vp), ("k", _vp), ("v", _vp), ("q_stride", _i64), ("k_stride", _i64),
+                ("v_stride", _i64), ("out", _vp), ("out_stride", _i64), ("lse", _vp),
+                ("cu_q", _vp), ("cu_k", _vp), ("causal", ctypes.c_int), ("scale", ctypes.c_float)]
+
+
+class PagedDecodeArgs(ctypes.Structure):
+    _fields_ = [("world", ctypes.c_int), ("root", ctypes.c_int), ("cache", PagedCacheDesc),
+                ("B", _i64), ("Hq", _i64), ("q", _vp), ("q_stride", _i64), ("out", _vp),
+                ("out_stride", _i64), ("lse", _vp), ("table", _vp), ("table_entries", _i64), ("table_stride", _i64),
+                ("lens", _vp), ("part_off", _sz), ("scale", ctypes.c_float)]
 
 
 class TdgError(RuntimeError):
@@ -155,6 +190,16 @@ def lib():
             L.tdg_flash_decode_part_bytes.argtypes = [ctypes.c_int, _i64, _i64, _i64, _i64, _i64]
             L.tdg_flash_decode.restype = ctypes.c_int
             L.tdg_flash_decode.argtypes = [_vp, ctypes.POINTER(FlashDecodeArgs), _vp]
+            L.tdg_paged_pool_bytes.restype = _sz
+            L.tdg_paged_pool_bytes.argtypes = [_i64, ctypes.c_int, _i64, _i64, ctypes.c_int]
+            L.tdg_rope_append.restype = ctypes.c_int
+            L.tdg_rope_append.argtypes = [_vp, ctypes.POINTER(RopeAppendArgs), _vp]
+            L.tdg_prompt_attention.restype = ctypes.c_int
+            L.tdg_prompt_attention.argtypes = [_vp, ctypes.POINTER(PromptAttentionArgs), _vp]
+            L.tdg_paged_decode_part_bytes.restype = _sz
+            L.tdg_paged_decode_part_bytes.argtypes = [_i64, _i64, _i64]
+            L.tdg_paged_decode.restype = ctypes.c_int
+            L.tdg_paged_decode.argtypes = [_vp, ctypes.POINTER(PagedDecodeArgs), _vp]
             L.tdg_moe_dispatch_combine_noalloc.restype = ctypes.c_int
             L.tdg_moe_dispatch_combine_noalloc.argtypes = [_vp, ctypes.POINTER(MoeArgs), _vp]
             _lib = L
@@ -376,6 +421,182 @@ def flash_decode(symm: Symm, B: int, Hq: int, Hkv: int, D: int, S: int, k_off: i
                         out=_tensor(out, "out", torch.bfloat16, B * Hq * D, dev),
                         chunk=chunk, scale=scale)
     _check(lib().tdg_flash_decode(symm.h, ctypes.byref(a), _stream(stream)), "tdg_flash_decode")
+
+
+def paged_pool_bytes(pages: int, page_size: int, Hkv: int, D: int, e4m3: bool = False) -> int:
+    """Bytes of one pool (keys or values) in one rank's region."""
+    return lib().tdg_paged_pool_bytes(pages, page_size, Hkv, D, KV_E4M3 if e4m3 else KV_BF16)
+
+
+class PagedCache:
+    """A paged key-value cache in the heap: `pages` pages of `page_size` tokens
+    per rank, key pool at k_off and value pool at v_off of every region, each
+    (pages, Hkv, page_size, D) in bf16, or in 8 bits (e4m3=True) with one
+    float32 scale per key head for keys and for values.  Page id p is page
+    p % pages of rank p // pages."""
+
+    def __init__(self, pages: int, page_size: int, Hkv: int, D: int, k_off: int, v_off: int,
+                 e4m3: bool = False, k_scale=None, v_scale=None):
+        import torch
+        if e4m3 != (k_scale is not None) or e4m3 != (v_scale is not None):
+            raise ValueError("k_scale and v_scale belong to an 8-bit cache, and only to one")
+        self.pages, self.page_size, self.Hkv, self.D = pages, page_size, Hkv, D
+        self.k_off, self.v_off, self.e4m3 = k_off, v_off, e4m3
+        self.k_scale, self.v_scale = k_scale, v_scale       # kept alive with the description
+        self.desc = PagedCacheDesc(
+            pages=pages, page_size=page_size, kv_type=KV_E4M3 if e4m3 else KV_BF16, Hkv=Hkv, D=D,
+            k_off=k_off, v_off=v_off,
+            k_scale=_tensor(k_scale, "k_scale", torch.float32, Hkv) if e4m3 else None,
+            v_scale=_tensor(v_scale, "v_scale", torch.float32, Hkv) if e4m3 else None)
+
+    def pools(self, symm: Symm, rank: int):
+        """The key and the value pool of one rank, as tensors."""
+        import torch
+        shape = (self.pages, self.Hkv, self.page_size, self.D)
+        kind = torch.float8_e4m3fn if self.e4m3 else torch.bfloat16
+        return symm.view(rank, self.k_off, shape, kind), symm.view(rank, self.v_off, shape, kind)
+
+
+def _rows(t, name, device):
+    """Check rows of heads, (rows, heads, D) in bf16, whose rows may be strided
+    (columns of a wider buffer); returns (pointer, row stride in elements)."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name}: expected torch.bfloat16, got {t.dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{name}: expected (rows, heads, D), got {tuple(t.shape)}")
+    n, heads, D = t.shape
+    s0, s1, s2 = t.stride()
+    if n == 0 or heads == 0:
+        return t.data_ptr() or None, heads * D
+    if (s2 != 1 and D > 1) or (s1 != D and heads > 1):
+        raise ValueError(f"{name}: the heads of a row must be contiguous, strides {t.stride()}")
+    if n == 1:
+        s0 = heads * D          # one row has no stride
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, the heap is on {device}")
+    return t.data_ptr(), s0
+
+
+def _table(table, name, device):
+    """Check a page table (sequences, entries), int32, rows possibly strided."""
+    import torch
+    if not isinstance(table, torch.Tensor) or table.dtype != torch.int32:
+        raise TypeError(f"{name}: expected an int32 tensor")
+    if table.dim() != 2 or (table.shape[1] > 1 and table.stride(1) != 1):
+        raise ValueError(f"{name}: expected (sequences, entries) with contiguous rows")
+    if table.device != device:
+        raise ValueError(f"{name}: on {table.device}, the heap is on {device}")
+    n, entries = table.shape
+    return table.data_ptr(), entries, entries if n <= 1 else table.stride(0)
+
+
+def rope_append(symm: Symm, cache: PagedCache, q, k, v, q_out, cos_sin, pos, table, lens, cu=None,
+                k_out=None, sections=None, interleaved=False, stream=None):
+    """Turn the queries q (T, Hq, D) and keys k (T, Hkv, D) of T new tokens by
+    their positions into q_out and k_out, and write keys and values v into the
+    cache.  cos_sin: (positions, rot_dim) float32, cosines then sines (None: no
+    rotation); pos: (T,) or (axes, T) int32 with `sections` pairs per axis;
+    table: (B, entries) int32 page ids (None: no cache write); lens: (B,) int32
+    lengths with the new tokens; cu: (B + 1,) int32 row offsets (None: one row
+    per sequence).  q and q_out may be None, q_out may be q, k_out may be k."""
+    import torch
+    dev, i32 = symm.buf.device, torch.int32
+    T = k.shape[0]
+    a = RopeAppendArgs(world=symm.world, cache=cache.desc, T=T, interleaved=1 if interleaved else 0)
+    if tuple(k.shape[1:]) != (cache.Hkv, cache.D):
+        raise ValueError(f"k: expected heads ({cache.Hkv}, {cache.D}), got {tuple(k.shape[1:])}")
+    a.k, a.k_stride = _rows(k, "k", dev)
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    if q is not None:
+        if q.shape != q_out.shape or q.shape[0] != T or q.shape[2] != cache.D:
+            raise ValueError(f"q {tuple(q.shape)} and q_out {tuple(q_out.shape)} do not fit k {tuple(k.shape)}")
+        a.Hq = q.shape[1]
+        a.q, a.q_stride = _rows(q, "q", dev)
+        a.q_out, a.q_out_stride = _rows(q_out, "q_out", dev)
+    if k_out is not None:
+        if k_out.shape != k.shape:
+            raise ValueError(f"k_out {tuple(k_out.shape)} does not fit k {tuple(k.shape)}")
+        a.k_out, a.k_out_stride = _rows(k_out, "k_out", dev)
+    if cos_sin is not None:
+        axes = 1 if pos.dim() == 1 else pos.shape[0]
+        if pos.dim() > 2 or pos.shape[-1] != T or axes not in (1, 2, 3):
+            raise ValueError(f"pos: expected ({T},) or (1..3, {T}), got {tuple(pos.shape)}")
+        a.max_pos, a.rot_dim = cos_sin.shape
+        a.cos_sin = _tensor(cos_sin, "cos_sin", torch.float32, 0, dev)
+        a.axes, a.pos, a.pos_stride = axes, _tensor(pos, "pos", i32, axes * T, dev), T
+        if axes > 1:
+            if sections is None or len(sections) != axes:
+                raise ValueError(f"sections: expected {axes} numbers of pairs")
+            for i, n in enumerate(sections):
+                a.sections[i] = n
+    if table is not None:
+        B = table.shape[0]
+        if v.shape != k.shape:
+            raise ValueError(f"v {tuple(v.shape)} does not fit k {tuple(k.shape)}")
+        a.v, a.v_stride = _rows(v, "v", dev)
+        a.B = B
+        a.table, a.table_entries, a.table_stride = _table(table, "table", dev)
+        a.lens = _tensor(lens, "lens", i32, B, dev)
+        if cu is not None:
+            a.cu = _tensor(cu, "cu", i32, B + 1, dev)
+    _check(lib().tdg_rope_append(symm.h, ctypes.byref(a), _stream(stream)), "tdg_rope_append")
+
+
+def prompt_attention(symm: Symm, q, k, v, out, cu_q, cu_k, lse=None, causal=True, scale: float = 0.0,
+                     stream=None):
+    """Attention over whole prompts packed one after another: q and out (Tq,
+    Hq, D), k and v (Tk, Hkv, D), rows possibly strided; cu_q and cu_k (B + 1,)
+    int32 row offsets; lse (Tq, Hq) float32 or None."""
+    import torch
+    dev, i32 = symm.buf.device, torch.int32
+    Tq, Hq, D = q.shape
+    Tk, Hkv, _ = k.shape
+    if out.shape != q.shape or k.shape != v.shape or k.shape[2] != D:
+        raise ValueError(f"q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)} and out "
+                         f"{tuple(out.shape)} do not fit together")
+    B = cu_q.numel() - 1
+    a = PromptAttentionArgs(Tq=Tq, Tk=Tk, B=B, Hq=Hq, Hkv=Hkv, D=D, causal=1 if causal else 0,
+                            scale=scale)
+    a.q, a.q_stride = _rows(q, "q", dev)
+    a.k, a.k_stride = _rows(k, "k", dev)
+    a.v, a.v_stride = _rows(v, "v", dev)
+    a.out, a.out_stride = _rows(out, "out", dev)
+    a.cu_q = _tensor(cu_q, "cu_q", i32, 1, dev)
+    a.cu_k = _tensor(cu_k, "cu_k", i32, B + 1, dev)
+    if lse is not None:
+        a.lse = _tensor(lse, "lse", torch.float32, Tq * Hq, dev)
+    _check(lib().tdg_prompt_attention(symm.h, ctypes.byref(a), _stream(stream)), "tdg_prompt_attention")
+
+
+def paged_decode_part_bytes(Hq: int, Hkv: int, D: int) -> int:
+    return lib().tdg_paged_decode_part_bytes(Hq, Hkv, D)
+
+
+def paged_decode(symm: Symm, cache: PagedCache, q, out, table, lens, part_off: int, root: int = 0,
+                 lse=None, scale: float = 0.0, stream=None):
+    """Attention of one new token per sequence over the paged cache: q and out
+    (B, Hq, D), rows possibly strided; table (B, entries) int32 page ids; lens
+    (B,) int32 lengths with the new token; lse (B, Hq) float32 or None.  The
+    partial results (paged_decode_part_bytes) go to region(root) + part_off."""
+    import torch
+    dev, i32 = symm.buf.device, torch.int32
+    B, Hq, D = q.shape
+    if out.shape != q.shape or D != cache.D or table.shape[0] != B:
+        raise ValueError(f"q {tuple(q.shape)}, out {tuple(out.shape)} and table {tuple(table.shape)} "
+                         f"do not fit together")
+    a = PagedDecodeArgs(world=symm.world, root=root, cache=cache.desc, B=B, Hq=Hq, part_off=part_off,
+                        scale=scale)
+    a.q, a.q_stride = _rows(q, "q", dev)
+    a.out, a.out_stride = _rows(out, "out", dev)
+    a.table, a.table_entries, a.table_stride = _table(table, "table", dev)
+    a.lens = _tensor(lens, "lens", i32, B, dev)
+    if lse is not None:
+        a.lse = _tensor(lse, "lse", torch.float32, B * Hq, dev)
+    _check(lib().tdg_paged_decode(symm.h, ctypes.byref(a), _stream(stream)), "tdg_paged_decode")
 
 
 def _moe_args(symm, T, H, E, k, x_off, topk_off, gate_off, out_off, recv, counts, base, slot,
