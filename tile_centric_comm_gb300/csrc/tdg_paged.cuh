@@ -45,7 +45,8 @@ inline bool overlap(uint64_t a, uint64_t an, uint64_t b, uint64_t bn) { return a
 // Checks a cache description against the heap and fills the kernels' view.
 inline int paged_view(const tdg_symm *h, const tdg_paged_cache &c, tdg::PagedView &v)
 {
-    if (c.pages <= 0 || c.pages > INT32_MAX || (int64_t)h->world * c.pages > INT32_MAX || c.k_off % 1024 ||
+    if (c.pages <= 0 || c.pages > INT32_MAX || (int64_t)h->world * c.pages > INT32_MAX ||
+        c.Hkv <= 0 || c.pages > INT32_MAX / c.Hkv || c.k_off % 1024 ||
         c.v_off % 1024)
         return TDG_ERR_INVALID;
     const uint64_t pool = tdg_paged_pool_bytes(c.pages, c.page_size, c.Hkv, c.D, c.kv_type);

@@ -1,17 +1,58 @@
 // tdg_paged_decode.cu -- attention of one new token per sequence over the
 // paged cache: softmax(scale q K^T) V over lens[b] cached tokens.
 //
-// One CTA per (sequence, query head); its 4 warps take every fourth token, a
-// lane holds D/32 of the head's elements, and each warp keeps a running
-// maximum, sum and output (online softmax, float32), merged at the end.
+// Mathematics: with scores in base 2, a running maximum m and sum l per query
+// head, each group of 16 tokens updates  m' = max(m, s),  l' = l 2^(m - m') +
+// sum 2^(s - m'),  o' = o 2^(m - m') + P V;  partial results (m, l, o) join the
+// same way.  All of m, l, o are float32; P is rounded to bf16 for the
+// product, the only rounding besides the output's (keys and queries of an
+// 8-bit cache meet in f16, exactly but for elements 2^-14 below a query's
+// largest).
+//
+// Bound by HBM: K and V are read once, about 2 G flops per byte.  The G =
+// Hq/Hkv query heads of a key head are the 16 rows of mma.sync (m16n8k16), so
+// a page is read once for all of them.
+//
+// Split: the (sequence, key head) pairs' 64-token tiles form one long line, and
+// each of the two CTAs per SM takes an equal run of it, wherever it begins and
+// ends: ragged lengths leave no SM idle, and the partial results are at most
+// two per CTA whatever the lengths.  A second launch joins the split pairs.
+//
+// In a CTA, warp 4 looks up page ids and issues one TMA copy per page (or 64
+// tokens of one) for K and for V into a ring of stages; warps 0-3 each take 16
+// tokens of every tile.  The 5-D tensor map (64-token box, both 128-byte halves
+// of a 256-byte row in one copy) writes the 128-byte-swizzled layout that
+// ldmatrix reads without bank conflicts.
+#include <cuda_fp16.h>
+
 #include "tdg_paged.cuh"
 
 namespace tdg {
 
 namespace pd {
-constexpr int WARPS = 4;
-constexpr int MAX_CTAS = 512; // CTAs whose partial results the caller provides room for
-constexpr int ROWS = 16;      // query heads of a partial result
+constexpr int WARPS = 4;                      // consumer warps
+constexpr int THREADS = WARPS * 32 + 32;
+constexpr int TILE = 64;                      // tokens of a tile
+constexpr int MAX_CTAS = 512;                 // CTAs whose partial results the caller provides room for
+constexpr int ROWS = 16;                      // query heads of a partial result
+constexpr int JOIN_ROWS = 4;                  // rows of a join CTA
+constexpr int MERGE_COLS = 32;                // columns of one merge phase
+constexpr int BAR_BYTES = 384;
+
+template <int D, bool E4M3> struct Shape {
+    static constexpr int ESZ = E4M3 ? 1 : 2;
+    static constexpr int RB = D * ESZ < 128 ? D * ESZ : 128; // bytes of a block's row
+    static constexpr int NB = D * ESZ / RB;                   // blocks of a token's row
+    static constexpr int KV = TILE * D * ESZ;                 // bytes of a tile of K or of V
+    static constexpr int STAGES = KV >= 16384 ? 3 : KV >= 8192 ? 6 : 8;
+    static constexpr int Q_BYTES = ROWS * D * 2;
+    static constexpr int OFF_Q = STAGES * 2 * KV;
+    static constexpr int OFF_MERGE = OFF_Q + 2 * Q_BYTES;
+    static constexpr int OFF_ML = OFF_MERGE + WARPS * ROWS * MERGE_COLS * 4;
+    static constexpr int OFF_BAR = OFF_ML + WARPS * ROWS * 2 * 4;
+    static constexpr int SMEM = OFF_BAR + BAR_BYTES;
+};
+static_assert(2 * (Shape<128, false>::SMEM + 1024) <= 228 * 1024, "two CTAs per SM");
 } // namespace pd
 
 struct PagedDecodeParams {
@@ -19,86 +60,691 @@ struct PagedDecodeParams {
     uint32_t epoch;
     PagedView c;
     int64_t B, table_entries, table_stride, qs, os;
-    int Hq, G;
-    float scale;
+    int Hq, G, groups; // groups of 16 query heads per key head
+    int box;           // tokens of one TMA copy
+    float scale_log2;
+    uint64_t timeout_ns;
     const __nv_bfloat16 *q;
     __nv_bfloat16 *out;
     float *lse;
     const int32_t *table, *lens;
+    int4 *desc;     // [MAX_CTAS]: the split pair that ends in a CTA
+    float *part_ml; // [MAX_CTAS][2][ROWS][2]
+    float *part_o;  // [MAX_CTAS][2][ROWS][D]
 };
 
-template <int D, bool E4M3>
-__global__ void __launch_bounds__(pd::WARPS * 32) paged_decode_kernel(const __grid_constant__ PagedDecodeParams p)
+// A position on the line of tiles: tile `tile` of the pair (b, hg).
+struct PdWalk {
+    int64_t b;
+    int hg, tile, tiles;
+};
+
+struct PdBars {
+    uint64_t kfull[8], vfull[8], empty[8], qfull[2], qempty[2];
+    int64_t sums[pd::THREADS / 32];
+    PdWalk begin;
+};
+static_assert(sizeof(PdBars) <= pd::BAR_BYTES, "barrier block");
+
+__device__ __forceinline__ void pd_ldsm4(uint32_t addr, uint32_t (&r)[4])
 {
-    constexpr int N = D / 32;
-    __shared__ float sm[pd::WARPS], sl[pd::WARPS], so[pd::WARPS][D];
-    const int h = blockIdx.x, b = blockIdx.y, g = h / p.G;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int64_t len = p.lens[b];
-    if (len < 0 || len > p.table_entries << p.c.ps_log2) {
-        if (threadIdx.x == 0)
-            report_fault(p.status, TDG_ERR_DEVICE, TDG_WHERE_PAGE, (uint32_t)b, p.epoch);
-        len = 0;
-    }
-    float q[N], o[N], m = -INFINITY, l = 0.f;
-    const float ks = E4M3 ? p.c.k_scale[g] : 1.f, vs = E4M3 ? p.c.v_scale[g] : 1.f;
-    for (int i = 0; i < N; ++i) {
-        q[i] = __bfloat162float(p.q[b * p.qs + (int64_t)h * D + lane * N + i]) * p.scale * ks;
-        o[i] = 0.f;
-    }
-    for (int64_t t = warp; t < len; t += pd::WARPS) {
-        int32_t page = p.table[b * p.table_stride + (t >> p.c.ps_log2)];
-        if (page < 0 || page >= p.c.all_pages) {
-            if (lane == 0)
-                report_fault(p.status, TDG_ERR_DEVICE, TDG_WHERE_PAGE, (uint32_t)b, p.epoch);
-            continue;
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void pd_ldsm4_t(uint32_t addr, uint32_t (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+// c += a b, one m16n8k16 tile with bf16 or f16 inputs
+template <bool F16>
+__device__ __forceinline__ void pd_mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    if (F16)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                     "{%0, %1, %2, %3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                     "{%0, %1, %2, %3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// two 8-bit floats (the low or the high half of r) as two f16, exactly
+__device__ __forceinline__ uint32_t e4m3x2_lo(uint32_t r)
+{
+    uint32_t d;
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(d) : "r"(r));
+    return d;
+}
+__device__ __forceinline__ uint32_t e4m3x2_hi(uint32_t r)
+{
+    uint32_t d;
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}" : "=r"(d) : "r"(r));
+    return d;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
+{
+    uint32_t d;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+
+// two f16 that hold 8-bit floats, as bf16 (exact: 4 significant bits)
+__device__ __forceinline__ uint32_t f16x2_bf16x2(uint32_t r)
+{
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&r));
+    return pack_bf16x2(f.x, f.y);
+}
+
+// 2^-e for a row whose largest magnitude is `top`, so that the row scaled by it
+// lies within +-4: f16 then holds every bf16 value down to 2^-14 of the largest
+// exactly and the smaller ones to 2^-25 of it.
+__device__ __forceinline__ int pd_exponent(float top)
+{
+    const int e = (int)(__float_as_uint(top) >> 23) - 127;
+    return top > 0.f && top < INFINITY ? min(max(e, -126), 126) : 0;
+}
+__device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+// tiles of sequence b; a length that does not fit the table counts as none
+__device__ __forceinline__ int pd_tiles(const PagedDecodeParams &p, int64_t b)
+{
+    const int64_t len = p.lens[b];
+    return len <= 0 || len > p.table_entries << p.c.ps_log2 ? 0 : (int)((len + pd::TILE - 1) / pd::TILE);
+}
+
+// the first CTA whose run holds unit u, given total = base * ctas + rem
+__device__ __forceinline__ int pd_owner(int64_t u, int64_t base, int64_t rem)
+{
+    return (int)(u < rem * (base + 1) ? u / (base + 1) : rem + (u - rem * (base + 1)) / base);
+}
+
+// Scores, softmax update and output update of this warp's 16 tokens.  valid:
+// tokens of them that exist (16 unless TAIL); k and v: shared addresses of the
+// group's rows; blk: bytes between a row's 128-byte blocks.
+template <int D, bool E4M3, bool TAIL, class WaitV>
+__device__ __forceinline__ void pd_group(const uint32_t (&qa)[D / 16][4], float mul0, float mul1, uint32_t k, uint32_t v,
+                                         uint32_t blk, int valid, int lane, float (&m)[2], float (&l)[2],
+                                         float (&o)[D / 8][4], WaitV &&wait_v)
+{
+    using S = pd::Shape<D, E4M3>;
+    const int tig = lane & 3, mi = lane >> 3, ri = lane & 7;
+    float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+    auto swz = [](int row) -> uint32_t { return S::RB == 128 ? (uint32_t)(row & 7) << 4 : (uint32_t)((row >> 1) & 3) << 4; };
+    if constexpr (!E4M3) {
+        const int tok = (mi >> 1) * 8 + ri;
+        const uint32_t row = k + tok * S::RB, x = swz(tok) ^ ((mi & 1) * 16);
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+            uint32_t b[4];
+            pd_ldsm4(row + (ks / 4) * blk + (x ^ ((ks % 4) * 32)), b);
+            pd_mma<false>(s[0], qa[ks], b[0], b[1]);
+            pd_mma<false>(s[1], qa[ks], b[2], b[3]);
         }
-        const uint8_t *at = p.c.regions + (uint64_t)(page / p.c.pages) * p.c.region_bytes +
-                            paged_row(p.c, page % p.c.pages, g, (int)(t & ((1 << p.c.ps_log2) - 1)), E4M3 ? 1 : 2);
-        auto load = [&](const uint8_t *row, int i) -> float {
-            if (E4M3)
-                return (float)reinterpret_cast<const __nv_fp8_e4m3 *>(row)[lane * N + i];
-            return __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(row)[lane * N + i]);
-        };
-        float s = 0.f;
-        for (int i = 0; i < N; ++i)
-            s += q[i] * load(at + p.c.k_off, i);
-        for (int x = 16; x; x >>= 1)
-            s += __shfl_xor_sync(0xffffffffu, s, x);
-        const float mn = fmaxf(m, s), ms = mn == -INFINITY ? 0.f : mn;
-        const float al = expf(m - ms), w = expf(s - ms);
-        m = mn;
-        l = l * al + w;
-        for (int i = 0; i < N; ++i)
-            o[i] = o[i] * al + w * load(at + p.c.v_off, i);
+    } else {
+        // a lane's four bytes are four neighbouring dimensions of one token;
+        // the query's fragments are laid out in the same order
+        const int tok = (mi & 1) * 8 + ri;
+        const uint32_t row = k + tok * S::RB, x = swz(tok) ^ ((mi >> 1) * 16);
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ks += 2) {
+            uint32_t b[4];
+            pd_ldsm4(row + (x ^ (ks * 16)), b);
+            pd_mma<true>(s[0], qa[ks], e4m3x2_lo(b[0]), e4m3x2_hi(b[0]));
+            pd_mma<true>(s[1], qa[ks], e4m3x2_lo(b[1]), e4m3x2_hi(b[1]));
+            pd_mma<true>(s[0], qa[ks + 1], e4m3x2_lo(b[2]), e4m3x2_hi(b[2]));
+            pd_mma<true>(s[1], qa[ks + 1], e4m3x2_lo(b[3]), e4m3x2_hi(b[3]));
+        }
     }
-    if (lane == 0) {
-        sm[warp] = m;
-        sl[warp] = l;
+    // base-2 scores; tokens behind the length weigh nothing, whatever their key holds
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            s[nt][c] *= c < 2 ? mul0 : mul1;
+            if (TAIL && nt * 8 + tig * 2 + (c & 1) >= valid)
+                s[nt][c] = -INFINITY;
+        }
+    float al[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        float mx = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const float mn = fmaxf(m[r], mx), ms = mn == -INFINITY ? 0.f : mn;
+        al[r] = exp2_approx(m[r] - ms);
+        m[r] = mn;
+        float sum = 0.f;
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                s[nt][2 * r + c] = exp2_approx(s[nt][2 * r + c] - ms);
+                sum += s[nt][2 * r + c];
+            }
+        l[r] = l[r] * al[r] + sum; // this lane's share; the four lanes of a row are added at the end
     }
-    for (int i = 0; i < N; ++i)
-        so[warp][lane * N + i] = o[i];
+#pragma unroll
+    for (int n = 0; n < D / 8; ++n) {
+        o[n][0] *= al[0];
+        o[n][1] *= al[0];
+        o[n][2] *= al[1];
+        o[n][3] *= al[1];
+    }
+    // bf16 for an 8-bit cache too: f16 is finer, but it loses weights below
+    // 2^-24 of the largest, which carry an output whose heavy tokens hold 0
+    const uint32_t pa[4] = {pack_bf16x2(s[0][0], s[0][1]), pack_bf16x2(s[0][2], s[0][3]),
+                            pack_bf16x2(s[1][0], s[1][1]), pack_bf16x2(s[1][2], s[1][3])};
+    // a register of V holds tokens 2 tig, 2 tig + 1 (+ 8); those behind the
+    // length are cleared, since 0 times infinity or NaN is not 0
+    uint32_t keep[2] = {~0u, ~0u};
+    if (TAIL)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int t = i * 8 + tig * 2;
+            keep[i] = (t < valid ? 0x0000FFFFu : 0u) | (t + 1 < valid ? 0xFFFF0000u : 0u);
+        }
+    wait_v();
+    const int vtok = (mi & 1) * 8 + ri;
+    const uint32_t vrow = v + vtok * S::RB, vx = swz(vtok) ^ ((mi >> 1) * 16);
+    if constexpr (!E4M3) {
+#pragma unroll
+        for (int nd = 0; nd < D / 8; nd += 2) {
+            uint32_t b[4];
+            pd_ldsm4_t(vrow + (nd / 8) * blk + (vx ^ ((nd % 8) * 16)), b);
+            if (TAIL) {
+                b[0] &= keep[0];
+                b[1] &= keep[1];
+                b[2] &= keep[0];
+                b[3] &= keep[1];
+            }
+            pd_mma<false>(o[nd], pa, b[0], b[1]);
+            pd_mma<false>(o[nd + 1], pa, b[2], b[3]);
+        }
+    } else {
+        // 16 dimensions per matrix; a register holds two neighbouring
+        // dimensions of two tokens, sorted into one product of the even
+        // dimensions and one of the odd
+#pragma unroll
+        for (int j = 0; j < D / 16; j += 2) {
+            uint32_t b[4];
+            pd_ldsm4_t(vrow + (vx ^ (j * 16)), b);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                b[i] = __byte_perm(TAIL ? b[i] & keep[i & 1] : b[i], 0u, 0x3120);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                pd_mma<false>(o[2 * (j + i)], pa, f16x2_bf16x2(e4m3x2_lo(b[2 * i])), f16x2_bf16x2(e4m3x2_lo(b[2 * i + 1])));
+                pd_mma<false>(o[2 * (j + i) + 1], pa, f16x2_bf16x2(e4m3x2_hi(b[2 * i])), f16x2_bf16x2(e4m3x2_hi(b[2 * i + 1])));
+            }
+        }
+    }
+}
+
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(pd::THREADS, 2)
+    paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_constant__ CUtensorMap kmap,
+                        const __grid_constant__ CUtensorMap vmap)
+{
+    using S = pd::Shape<D, E4M3>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    PdBars *bar = reinterpret_cast<PdBars *>(smem + S::OFF_BAR);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int pairs = p.c.Hkv * p.groups; // lines of tiles per sequence
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S::STAGES; ++i) {
+            mbar_init(&bar->kfull[i], 1);
+            mbar_init(&bar->vfull[i], 1);
+            mbar_init(&bar->empty[i], pd::WARPS);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bar->qfull[i], 1);
+            mbar_init(&bar->qempty[i], pd::WARPS);
+        }
+        fence_mbar_init();
+        fence_proxy_async_smem();
+    }
+    // this CTA's run of the line: the warps' sums of tiles, then the sequence
+    // in which the run begins
+    const int64_t per = (p.B + pd::THREADS - 1) / pd::THREADS; // sequences of a thread
+    const int64_t b_lo = min((int64_t)threadIdx.x * per, p.B), b_hi = min(b_lo + per, p.B);
+    int64_t mine = 0;
+    for (int64_t b = b_lo; b < b_hi; ++b)
+        mine += pd_tiles(p, b);
+    int64_t upto = mine;
+    for (int d = 1; d < 32; d <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, upto, d);
+        if (lane >= d)
+            upto += x;
+    }
+    if (lane == 31)
+        bar->sums[warp] = upto;
+    // sequences without tokens (and those of a bad length) are nobody's run
+    for (int64_t b = blockIdx.x; b < p.B; b += gridDim.x)
+        if (pd_tiles(p, b) == 0) {
+            if (p.lens[b] != 0 && threadIdx.x == 0)
+                report_fault(p.status, TDG_ERR_DEVICE, TDG_WHERE_PAGE, (uint32_t)b, p.epoch);
+            for (int i = threadIdx.x; i < p.Hq * D / 8; i += pd::THREADS)
+                *reinterpret_cast<uint4 *>(p.out + b * p.os + (int64_t)i * 8) = make_uint4(0, 0, 0, 0);
+            if (p.lse)
+                for (int i = threadIdx.x; i < p.Hq; i += pd::THREADS)
+                    p.lse[b * p.Hq + i] = -INFINITY;
+        }
     __syncthreads();
-    float M = -INFINITY, L = 0.f;
-    for (int w = 0; w < pd::WARPS; ++w)
-        M = fmaxf(M, sm[w]);
-    const float Ms = M == -INFINITY ? 0.f : M;
-    for (int w = 0; w < pd::WARPS; ++w)
-        L += sl[w] * expf(sm[w] - Ms);
-    for (int d = threadIdx.x; d < D; d += blockDim.x) {
-        float a = 0.f;
-        for (int w = 0; w < pd::WARPS; ++w)
-            a += so[w][d] * expf(sm[w] - Ms);
-        p.out[b * p.os + (int64_t)h * D + d] = __float2bfloat16_rn(len > 0 ? a / L * vs : 0.f);
+    int64_t total = 0, before = 0;
+    for (int w = 0; w < pd::THREADS / 32; ++w) {
+        if (w < warp)
+            before += bar->sums[w];
+        total += bar->sums[w];
     }
-    if (p.lse && threadIdx.x == 0)
-        p.lse[(int64_t)b * p.Hq + h] = len > 0 ? M + logf(L) : -INFINITY;
+    upto += before;
+    const int64_t base = total * pairs / gridDim.x, rem = total * pairs % gridDim.x;
+    const int64_t u0 = blockIdx.x * base + min((int64_t)blockIdx.x, rem), u1 = u0 + base + (blockIdx.x < rem ? 1 : 0);
+    if ((upto - mine) * pairs <= u0 && u0 < upto * pairs && u0 < u1) {
+        int64_t at = u0 - (upto - mine) * pairs;
+        PdWalk w;
+        for (w.b = b_lo;; ++w.b) {
+            w.tiles = pd_tiles(p, w.b);
+            if (at < (int64_t)w.tiles * pairs)
+                break;
+            at -= (int64_t)w.tiles * pairs;
+        }
+        w.hg = (int)(at / w.tiles);
+        w.tile = (int)(at % w.tiles);
+        bar->begin = w;
+    }
+    __syncthreads();
+    if (u0 >= u1) {
+        if (threadIdx.x == 0)
+            p.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+        return;
+    }
+    PdWalk w = bar->begin;
+    int64_t u = u0;
+    // the next pair, of the next sequence that has tiles (there is one while u < u1)
+    auto next_pair = [&](PdWalk &x) {
+        x.tile = 0;
+        if (++x.hg == pairs) {
+            x.hg = 0;
+            do {
+                x.tiles = pd_tiles(p, ++x.b);
+            } while (x.tiles == 0);
+        }
+    };
+
+    if (warp == pd::WARPS) {
+        // ---- loads: a chunk is up to 32 copies of one pair, their page ids one per lane ----
+        const int per_tile = pd::TILE / p.box;               // copies of a tile
+        const int shift = p.c.ps_log2;
+        const int box_log2 = 31 - __clz(p.box);
+        const uint32_t copy_bytes = (uint32_t)p.box * D * S::ESZ;
+        auto chunk_ids = [&](const PdWalk &x, int tiles) -> int32_t {
+            const int64_t tok = (int64_t)x.tile * pd::TILE + ((int64_t)lane << box_log2);
+            if (lane >= tiles * per_tile || tok >= p.lens[x.b])
+                return 0;
+            const int32_t id = p.table[x.b * p.table_stride + (tok >> shift)];
+            if (id >= 0 && id < p.c.all_pages)
+                return id;
+            report_fault(p.status, TDG_ERR_DEVICE, TDG_WHERE_PAGE, (uint32_t)x.b, p.epoch);
+            return 0; // any page: the result is undefined, the access is not
+        };
+        auto chunk_tiles = [&](const PdWalk &x, int64_t at) -> int {
+            return (int)min(min((int64_t)(32 / per_tile), (int64_t)(x.tiles - x.tile)), u1 - at);
+        };
+        int n = chunk_tiles(w, u), stage = 0, pair = 0;
+        uint32_t phase = 0;
+        bool fresh = true, dead = false;
+        int32_t ids = chunk_ids(w, n);
+        int64_t issued = 0;
+        int queries = 0; // query copies issued
+        while (u < u1 && !dead) {
+            // look the next chunk up while this one's copies are issued
+            PdWalk y = w;
+            y.tile += n;
+            if (y.tile == y.tiles && u + n < u1)
+                next_pair(y);
+            const int n2 = u + n < u1 ? chunk_tiles(y, u + n) : 0;
+            const int32_t ids2 = n2 ? chunk_ids(y, n2) : 0;
+            const int64_t len = p.lens[w.b];
+            const int g = w.hg / p.groups;
+            if (fresh && lane == 0) { // a new pair: its queries
+                const int h0 = g * p.G + (w.hg % p.groups) * pd::ROWS;
+                const uint32_t bytes = (uint32_t)min(pd::ROWS, p.G - (w.hg % p.groups) * pd::ROWS) * D * 2;
+                const int qb = pair & 1;
+                if (!mbar_wait(&bar->qempty[qb], ((pair >> 1) & 1) ^ 1u, p.timeout_ns)) {
+                    report_fault(p.status, TDG_ERR_TIMEOUT, TDG_WHERE_PIPE, 0, p.epoch);
+                    dead = true;
+                } else {
+                    mbar_arrive_expect_tx(&bar->qfull[qb], bytes);
+                    bulk_load(smem + S::OFF_Q + qb * S::Q_BYTES, p.q + w.b * p.qs + (int64_t)h0 * D, bytes, &bar->qfull[qb]);
+                    queries = pair + 1;
+                }
+            }
+            dead = __shfl_sync(0xffffffffu, dead ? 1 : 0, 0) != 0;
+            for (int i = 0; i < n && !dead; ++i) {
+                const int64_t t0 = (int64_t)(w.tile + i) * pd::TILE;
+                const int copies = (int)min((int64_t)per_tile, (len - t0 + p.box - 1) >> box_log2);
+                if (lane == 0) {
+                    if (!mbar_wait(&bar->empty[stage], phase ^ 1u, p.timeout_ns)) {
+                        report_fault(p.status, TDG_ERR_TIMEOUT, TDG_WHERE_PIPE, 1, p.epoch);
+                        dead = true;
+                    } else {
+                        mbar_arrive_expect_tx(&bar->kfull[stage], copies * copy_bytes);
+                        mbar_arrive_expect_tx(&bar->vfull[stage], copies * copy_bytes);
+                    }
+                }
+                dead = __shfl_sync(0xffffffffu, dead ? 1 : 0, 0) != 0;
+                if (dead)
+                    break;
+                const int32_t id = __shfl_sync(0xffffffffu, ids, (i * per_tile + lane) & 31);
+                if (lane < copies) {
+                    const int row = (int)((t0 + ((int64_t)lane << box_log2)) & ((1 << shift) - 1)); // inside the page
+                    const int rank = id / (int)p.c.pages, local = id % (int)p.c.pages;
+                    uint8_t *dst = smem + stage * 2 * S::KV + lane * copy_bytes;
+                    tma_load_5d(dst, &kmap, &bar->kfull[stage], 0, row, 0, local * p.c.Hkv + g, rank);
+                    tma_load_5d(dst + S::KV, &vmap, &bar->vfull[stage], 0, row, 0, local * p.c.Hkv + g, rank);
+                }
+                ++issued;
+                if (++stage == S::STAGES) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+            fresh = y.tile == 0;
+            pair += fresh ? 1 : 0;
+            u += n;
+            w = y;
+            n = n2;
+            ids = ids2;
+        }
+        // after a timeout: leave only when the copies in flight have landed
+        if (dead && lane == 0) {
+            for (int f = max(0, queries - 2); f < queries; ++f)
+                (void)mbar_wait(&bar->qfull[f & 1], (uint32_t)(f >> 1) & 1u, p.timeout_ns);
+            for (int64_t f = max((int64_t)0, issued - S::STAGES); f < issued; ++f) {
+                (void)mbar_wait(&bar->kfull[f % S::STAGES], (uint32_t)(f / S::STAGES) & 1u, p.timeout_ns);
+                (void)mbar_wait(&bar->vfull[f % S::STAGES], (uint32_t)(f / S::STAGES) & 1u, p.timeout_ns);
+            }
+        }
+        return;
+    }
+
+    // ---- consumers ----
+    const int gid = lane >> 2, tig = lane & 3;
+    float *merge = reinterpret_cast<float *>(smem + S::OFF_MERGE); // [WARPS][ROWS][MERGE_COLS]
+    float *mls = reinterpret_cast<float *>(smem + S::OFF_ML);      // [WARPS][ROWS][2]
+    const uint32_t ring = smem_u32(smem);
+    const uint32_t blk = (uint32_t)p.box * S::RB;
+    // this warp's rows of a tile: which copy, and where in it
+    const int first = warp * 16;
+    const uint32_t group_off = (uint32_t)(first / p.box) * (p.box * D * S::ESZ) + (uint32_t)(first % p.box) * S::RB;
+    int stage = 0, pair = 0;
+    uint32_t phase = 0;
+    bool dead = false; // a wait ran out: wait no more, run on to the end (the call has reported it)
+    auto wait = [&](uint64_t *b, uint32_t ph, uint32_t what) {
+        if (!dead && !mbar_wait(b, ph, p.timeout_ns)) {
+            if (lane == 0)
+                report_fault(p.status, TDG_ERR_TIMEOUT, TDG_WHERE_PIPE, what, p.epoch);
+            dead = true;
+        }
+        __syncwarp(); // what follows (ldmatrix, mma, named barriers) wants the whole warp
+    };
+    int4 desc = make_int4(-1, 0, 0, 0);
+    while (u < u1) {
+        const int64_t len = p.lens[w.b];
+        const int g = w.hg / p.groups, mg = w.hg % p.groups;
+        const int rows = min(pd::ROWS, p.G - mg * pd::ROWS);
+        const int64_t pair_u0 = u - w.tile; // the pair's first unit
+        const int end = (int)min((int64_t)w.tiles, w.tile + (u1 - u));
+        // the queries as the A operand
+        const int qb = pair & 1;
+        wait(&bar->qfull[qb], (pair >> 1) & 1, 2);
+        uint32_t qa[D / 16][4];
+        float mul0 = p.scale_log2, mul1 = p.scale_log2;
+        const uint8_t *qs = smem + S::OFF_Q + qb * S::Q_BYTES;
+        if constexpr (!E4M3) {
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks)
+                pd_ldsm4(smem_u32(qs) + ((lane & 7) + ((lane >> 3) & 1) * 8) * D * 2 + ks * 32 + (lane >> 4) * 16, qa[ks]);
+        } else {
+            // f16, in the order in which the 8-bit keys arrive: four neighbours per lane
+            float x[2][D / 16][4], top[2] = {0.f, 0.f};
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    const uint2 y = *reinterpret_cast<const uint2 *>(qs + (gid + r * 8) * D * 2 + ks * 32 + tig * 8);
+                    x[r][ks][0] = __uint_as_float(y.x << 16);
+                    x[r][ks][1] = __uint_as_float(y.x & 0xFFFF0000u);
+                    x[r][ks][2] = __uint_as_float(y.y << 16);
+                    x[r][ks][3] = __uint_as_float(y.y & 0xFFFF0000u);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        top[r] = fmaxf(top[r], fabsf(x[r][ks][i]));
+                }
+            int e[2];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
+                top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
+                e[r] = pd_exponent(top[r]);
+            }
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const float f = pow2i(-e[r]);
+                    qa[ks][r] = pack_f16x2(x[r][ks][0] * f, x[r][ks][1] * f);
+                    qa[ks][2 + r] = pack_f16x2(x[r][ks][2] * f, x[r][ks][3] * f);
+                }
+            const float ks = p.c.k_scale[g];
+            mul0 *= ks * pow2i(e[0]);
+            mul1 *= ks * pow2i(e[1]);
+        }
+        ++pair;
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[D / 8][4];
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n)
+            o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+        for (int t = w.tile; t < end; ++t) {
+            const int64_t left = len - (int64_t)t * pd::TILE - first;
+            const uint32_t k = ring + stage * 2 * S::KV + group_off;
+            wait(&bar->kfull[stage], phase, 3);
+            auto wait_v = [&] { wait(&bar->vfull[stage], phase, 4); };
+            if (left >= 16)
+                pd_group<D, E4M3, false>(qa, mul0, mul1, k, k + S::KV, blk, 16, lane, m, l, o, wait_v);
+            else if (left > 0)
+                pd_group<D, E4M3, true>(qa, mul0, mul1, k, k + S::KV, blk, (int)left, lane, m, l, o, wait_v);
+            else
+                wait_v();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&bar->empty[stage]);
+            if (++stage == S::STAGES) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        }
+        // The queries' buffer is free once the products have read the
+        // fragments: released any earlier, right behind their ldmatrix, the next
+        // pair's queries were seen in them.
+        if (lane == 0)
+            mbar_arrive(&bar->qempty[qb]);
+        // join the four warps, MERGE_COLS columns at a time
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+            if (tig == 0) {
+                mls[(warp * pd::ROWS + gid + r * 8) * 2] = m[r];
+                mls[(warp * pd::ROWS + gid + r * 8) * 2 + 1] = l[r];
+            }
+        }
+        const bool whole = pair_u0 >= u0 && end == w.tiles;
+        const int slot = w.tile == 0 && pair_u0 > u0 ? 1 : 0; // 0: the pair that holds this CTA's first unit
+        const int row = threadIdx.x >> 3, col4 = (threadIdx.x & 7) * 4;
+        const int h = g * p.G + mg * pd::ROWS + row;
+        float M = -INFINITY, L = 0.f, wt[pd::WARPS];
+#pragma unroll
+        for (int c0 = 0; c0 < D; c0 += pd::MERGE_COLS) {
+            // columns xored by the row: no bank conflicts either way
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                float *dst = merge + (warp * pd::ROWS + gid + r * 8) * pd::MERGE_COLS;
+                if constexpr (!E4M3) {
+#pragma unroll
+                    for (int n = 0; n < pd::MERGE_COLS / 8; ++n)
+                        *reinterpret_cast<float2 *>(dst + ((n * 8 + tig * 2) ^ (gid * 4))) =
+                            make_float2(o[c0 / 8 + n][2 * r], o[c0 / 8 + n][2 * r + 1]);
+                } else {
+#pragma unroll
+                    for (int n = 0; n < pd::MERGE_COLS / 8; n += 2)
+                        *reinterpret_cast<float4 *>(dst + ((n * 8 + tig * 4) ^ (gid * 4))) =
+                            make_float4(o[c0 / 8 + n][2 * r], o[c0 / 8 + n + 1][2 * r], o[c0 / 8 + n][2 * r + 1],
+                                        o[c0 / 8 + n + 1][2 * r + 1]);
+                }
+            }
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+            if (c0 == 0) {
+#pragma unroll
+                for (int i = 0; i < pd::WARPS; ++i)
+                    M = fmaxf(M, mls[(i * pd::ROWS + row) * 2]);
+                const float Ms = M == -INFINITY ? 0.f : M;
+#pragma unroll
+                for (int i = 0; i < pd::WARPS; ++i) {
+                    wt[i] = exp2_approx(mls[(i * pd::ROWS + row) * 2] - Ms);
+                    L += mls[(i * pd::ROWS + row) * 2 + 1] * wt[i];
+                }
+            }
+            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < pd::WARPS; ++i) {
+                const float4 x = *reinterpret_cast<const float4 *>(merge + (i * pd::ROWS + row) * pd::MERGE_COLS +
+                                                                   (col4 ^ ((row & 7) * 4)));
+                a.x += x.x * wt[i];
+                a.y += x.y * wt[i];
+                a.z += x.z * wt[i];
+                a.w += x.w * wt[i];
+            }
+            if (row < rows) {
+                if (whole) {
+                    const float f = (E4M3 ? p.c.v_scale[g] : 1.f) / L;
+                    *reinterpret_cast<uint2 *>(p.out + w.b * p.os + (int64_t)h * D + c0 + col4) =
+                        make_uint2(pack_bf16x2(a.x * f, a.y * f), pack_bf16x2(a.z * f, a.w * f));
+                } else {
+                    __stcg(reinterpret_cast<float4 *>(p.part_o + ((size_t)(blockIdx.x * 2 + slot) * pd::ROWS + row) * D + c0 + col4), a);
+                }
+            }
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+        }
+        if (col4 == 0 && row < rows) {
+            if (!whole)
+                __stcg(reinterpret_cast<float2 *>(p.part_ml + ((size_t)(blockIdx.x * 2 + slot) * pd::ROWS + row) * 2), make_float2(M, L));
+            else if (p.lse)
+                p.lse[w.b * p.Hq + h] = (M + log2f(L)) * 0.6931471805599453f;
+        }
+        if (pair_u0 < u0 && end == w.tiles) { // a pair from earlier CTAs ends here
+            const int c0 = pd_owner(pair_u0, base, rem);
+            const int64_t c0_u0 = c0 * base + min((int64_t)c0, rem);
+            desc = make_int4((int)w.b, w.hg, c0, pair_u0 > c0_u0 ? 1 : 0);
+        }
+        u += end - w.tile;
+        w.tile = end;
+        if (end == w.tiles && u < u1)
+            next_pair(w);
+    }
+    if (threadIdx.x == 0)
+        p.desc[blockIdx.x] = desc;
+}
+
+// Joins the partial results of the pair that ends in CTA blockIdx.x (if one
+// does): rows blockIdx.y * JOIN_ROWS on, two columns per thread at D = 128.
+template <int D>
+__global__ void __launch_bounds__(pd::JOIN_ROWS *D / 2) paged_join_kernel(const __grid_constant__ PagedDecodeParams p)
+{
+    const int4 desc = p.desc[blockIdx.x];
+    if (desc.x < 0)
+        return;
+    const int g = desc.y / p.groups, mg = desc.y % p.groups;
+    const int row = blockIdx.y * pd::JOIN_ROWS + threadIdx.x / (D / 2), col = threadIdx.x % (D / 2) * 2;
+    if (row >= min(pd::ROWS, p.G - mg * pd::ROWS))
+        return;
+    const int h = g * p.G + mg * pd::ROWS + row;
+    const int c0 = desc.z, c1 = blockIdx.x;
+    // slot of CTA c: the first one's may be its second
+    auto at = [&](int c) -> size_t { return (size_t)(c * 2 + (c == c0 ? desc.w : 0)) * pd::ROWS + row; };
+    float M = -INFINITY;
+#pragma unroll 8
+    for (int c = c0; c <= c1; ++c)
+        M = fmaxf(M, __ldcg(p.part_ml + at(c) * 2));
+    const float Ms = M == -INFINITY ? 0.f : M;
+    float L = 0.f, a = 0.f, b = 0.f;
+#pragma unroll 8
+    for (int c = c0; c <= c1; ++c) {
+        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(p.part_ml + at(c) * 2));
+        const float2 x = __ldcg(reinterpret_cast<const float2 *>(p.part_o + at(c) * D + col));
+        const float wt = exp2_approx(ml.x - Ms);
+        L += ml.y * wt;
+        a += x.x * wt;
+        b += x.y * wt;
+    }
+    const float f = (p.c.v_scale ? p.c.v_scale[g] : 1.f) / L;
+    *reinterpret_cast<uint32_t *>(p.out + desc.x * p.os + (int64_t)h * D + col) = pack_bf16x2(a * f, b * f);
+    if (p.lse && col == 0)
+        p.lse[(int64_t)desc.x * p.Hq + h] = (M + log2f(L)) * 0.6931471805599453f;
 }
 
 } // namespace tdg
 
 using namespace tdg;
 using namespace tdg_host;
+
+namespace {
+
+// The pool as a 5-D tensor: {bytes of a 128-byte block, slot in the page, block
+// of the row, page and head, rank}; one box is `box` slots of every block.
+template <int D, bool E4M3> bool pool_map(CUtensorMap *m, const tdg_symm *h, const tdg_paged_cache &c, size_t off, int box)
+{
+    using S = pd::Shape<D, E4M3>;
+    const uint64_t row = (uint64_t)D * S::ESZ;
+    const uint64_t dims[5] = {S::RB / S::ESZ, (uint64_t)c.page_size, S::NB, (uint64_t)c.pages * c.Hkv, (uint64_t)h->world};
+    const uint64_t str[4] = {row, S::RB, row * c.page_size, h->region_bytes};
+    const uint32_t bx[5] = {S::RB / S::ESZ, (uint32_t)box, S::NB, 1, 1};
+    return encode_tiled(m, E4M3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, h->base + off, dims,
+                        str, bx, S::RB == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+}
+
+template <int D, bool E4M3> int launch_decode(const tdg_symm *h, const tdg_paged_decode_args *a, PagedDecodeParams &p, cudaStream_t st)
+{
+    using S = pd::Shape<D, E4M3>;
+    CUtensorMap km, vm;
+    if (!pool_map<D, E4M3>(&km, h, a->cache, a->cache.k_off, p.box) || !pool_map<D, E4M3>(&vm, h, a->cache, a->cache.v_off, p.box))
+        return TDG_ERR_CUDA;
+    const void *fn = reinterpret_cast<const void *>(&paged_decode_kernel<D, E4M3>);
+    if (const cudaError_t e = set_smem(fn, S::SMEM); e != cudaSuccess)
+        return cuda_err(e, "paged decode smem");
+    const unsigned ctas = (unsigned)(h->sm_count * 2 < pd::MAX_CTAS ? h->sm_count * 2 : pd::MAX_CTAS);
+    void *args[] = {&p, &km, &vm};
+    if (const int rc = cuda_err(launch(fn, dim3(ctas), dim3(pd::THREADS), S::SMEM, st, args, false), "paged decode launch"))
+        return rc;
+    void *jargs[] = {&p};
+    const int join_rows = p.G < pd::ROWS ? p.G : pd::ROWS;
+    return cuda_err(launch(reinterpret_cast<const void *>(&paged_join_kernel<D>),
+                           dim3(ctas, (unsigned)((join_rows + pd::JOIN_ROWS - 1) / pd::JOIN_ROWS)), dim3(pd::JOIN_ROWS * D / 2), 0, st,
+                           jargs, false),
+                    "paged join launch");
+}
+
+} // namespace
 
 extern "C" size_t tdg_paged_decode_part_bytes(int64_t Hq, int64_t Hkv, int64_t D)
 {
@@ -147,19 +793,22 @@ extern "C" int tdg_paged_decode(tdg_symm *h, const tdg_paged_decode_args *a, voi
     p.os = a->out_stride;
     p.Hq = (int)Hq;
     p.G = (int)(Hq / Hkv);
-    p.scale = a->scale > 0.f ? a->scale : 1.0f / sqrtf((float)D);
+    p.groups = (p.G + pd::ROWS - 1) / pd::ROWS;
+    p.box = a->cache.page_size < pd::TILE ? a->cache.page_size : pd::TILE;
+    p.scale_log2 = (a->scale > 0.f ? a->scale : 1.0f / sqrtf((float)D)) * 1.4426950408889634f; // scores live in base 2
+    p.timeout_ns = timeout_or_default(0);
     p.q = static_cast<const __nv_bfloat16 *>(a->q);
     p.out = static_cast<__nv_bfloat16 *>(a->out);
     p.lse = a->lse;
     p.table = a->table;
     p.lens = a->lens;
+    uint8_t *part_at = h->base + (uint64_t)a->root * h->region_bytes + a->part_off;
+    p.desc = reinterpret_cast<int4 *>(part_at);
+    p.part_ml = reinterpret_cast<float *>(p.desc + pd::MAX_CTAS);
+    p.part_o = p.part_ml + (size_t)pd::MAX_CTAS * 2 * pd::ROWS * 2;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool e4m3 = a->cache.kv_type == TDG_KV_E4M3;
-    const void *fn = D == 128 ? (e4m3 ? reinterpret_cast<const void *>(&paged_decode_kernel<128, true>)
-                                      : reinterpret_cast<const void *>(&paged_decode_kernel<128, false>))
-                              : (e4m3 ? reinterpret_cast<const void *>(&paged_decode_kernel<64, true>)
-                                      : reinterpret_cast<const void *>(&paged_decode_kernel<64, false>));
-    void *args[] = {&p};
-    return cuda_err(launch(fn, dim3((unsigned)Hq, (unsigned)a->B), dim3(pd::WARPS * 32), 0,
-                           static_cast<cudaStream_t>(stream), args, false),
-                    "paged decode launch");
+    if (D == 128)
+        return e4m3 ? launch_decode<128, true>(h, a, p, st) : launch_decode<128, false>(h, a, p, st);
+    return e4m3 ? launch_decode<64, true>(h, a, p, st) : launch_decode<64, false>(h, a, p, st);
 }
