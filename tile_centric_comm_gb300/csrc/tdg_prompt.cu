@@ -1,73 +1,658 @@
 // tdg_prompt.cu -- attention over whole prompts packed one after another:
 // softmax(scale Q K^T) V per sequence, causal from the last key back.
 //
-// One warp per (query row, head): a lane holds D/32 of the head's elements and
-// the warp keeps a running maximum, sum and output in float32.
+// Mathematics: per query row a running maximum m and sum l over blocks of 128
+// keys, in base 2:  P = 2^(c s - m),  l += sum P,  O += P V,  c = scale log2 e.
+// m follows the row's true maximum only when that has grown by more than 8
+// (a factor of 256): until then P stays below 2^8 and the old m serves as
+// well, so the output, which lives in TMEM, is rarely rescaled.  S, m, l and O
+// are float32; P is rounded to bf16 for its product.
+//
+// Work: an item is 256 rows of one key head -- two tiles of 128, each 128/G
+// tokens times the G = Hq/Hkv query heads that share the key head, so a block
+// of keys and values is fetched once for all of them and a tile's causal edge
+// is only 128/G tokens wide.  One persistent CTA per SM:
+//   warps 0-3, 4-7  softmax of tile 0 and 1: a thread owns a row
+//   warp 8          one thread issues tcgen05.mma: S_t = Q_t K^T from shared
+//                   memory, O_t += P_t V with P_t read from TMEM, where the
+//                   softmax left it in S_t's own columns
+//   warp 9          looks items up and loads Q, K and V by TMA
+//   warps 10, 11    idle: they complete the warpgroup that gives registers up
+// TMEM holds S_0, S_1 (128 columns each) and O_0, O_1 (D each).  While the
+// softmax works on one tile, the tensor cores work on the other.
 #include "tdg_paged.cuh"
 
 namespace tdg {
 
+namespace pa {
+constexpr int THREADS = 384;
+// registers a thread: 168 at launch; 2 x 208 + 88 = 3 x 168, so the split asks
+// for no more than the launch holds
+constexpr int REGS_SOFTMAX = 208, REGS_OTHER = 88;
+constexpr int MMA_WARP = 8, LOAD_WARP = 9;
+constexpr int BN = 128;       // keys of a block
+constexpr int CHUNKS = 256;   // entries of the item table
+constexpr int SLOTS = 2;      // items in hand
+constexpr uint32_t TMEM_COLS = 512;
+
+template <int D> struct Shape {
+    static constexpr int HALVES = D / 64;
+    static constexpr int Q_BYTES = 128 * D * 2;
+    static constexpr int KV_BYTES = BN * D * 2;
+    static constexpr int STAGES = D == 128 ? 5 : 8;
+    static constexpr int OFF_KV = 2 * Q_BYTES;
+    static constexpr int OFF_CTL = OFF_KV + STAGES * KV_BYTES;
+};
+} // namespace pa
+
 struct PromptParams {
     DevStatus *status;
     uint32_t epoch;
-    int64_t Tq, Tk, B, qs, ks, vs, os;
-    int Hq, Hkv, G, causal;
-    float scale;
-    const __nv_bfloat16 *q, *k, *v;
+    uint64_t timeout_ns;
+    int64_t Tq, Tk, B, os;
+    int Hq, Hkv, G, NT; // NT: tokens of a tile, 128 / G
+    int causal;
+    float scale_log2;
     __nv_bfloat16 *out;
     float *lse;
     const int32_t *cu_q, *cu_k;
 };
 
-// Rows of sequence b; false (and a report by one thread) when the offsets are
-// out of order or range.
-__device__ __forceinline__ bool prompt_sequence(const PromptParams &p, int64_t b, bool report, int64_t &q0, int &Lq,
-                                                int64_t &k0, int &Lk)
+// Tokens [t0, t0 + 2 NT) of a sequence and key head g.
+struct PromptItem {
+    int q0, Lq, k0, Lk, g, t0, valid, pad;
+};
+
+struct PromptCtl {
+    uint64_t kvfull[8], kvempty[8], qfull[2], qempty[2], sfull[2], pfull[2], ofull[2];
+    uint64_t ifull[pa::SLOTS], iempty[pa::SLOTS], tail, drain;
+    PromptItem item[pa::SLOTS];
+    uint32_t tmem_base;
+    volatile int abort;
+    int issued;                        // ring fills issued
+    uint32_t first[pa::CHUNKS + 1];    // first item of every table entry
+    uint16_t order[pa::CHUNKS];        // the sequence of an entry, longest first
+};
+template <int D> constexpr int prompt_smem() { return pa::Shape<D>::OFF_CTL + (int)sizeof(PromptCtl); }
+static_assert(prompt_smem<128>() <= 227 * 1024, "shared memory");
+
+// Rows of sequence b; false when the offsets are out of order or range (the
+// sequence then counts as empty).
+__device__ __forceinline__ bool prompt_sequence(const PromptParams &p, int64_t b, PromptItem &it)
 {
     const int64_t qa = p.cu_q[b], qb = p.cu_q[b + 1], ka = p.cu_k[b], kb = p.cu_k[b + 1];
     const bool ok = qa >= 0 && qb >= qa && qb <= p.Tq && ka >= 0 && kb >= ka && kb <= p.Tk;
-    if (!ok && report)
-        report_fault(p.status, TDG_ERR_DEVICE, TDG_WHERE_CU, (uint32_t)b, p.epoch);
-    q0 = qa;
-    k0 = ka;
-    Lq = ok ? (int)(qb - qa) : 0;
-    Lk = ok ? (int)(kb - ka) : 0;
+    it.q0 = (int)qa;
+    it.k0 = (int)ka;
+    it.Lq = ok ? (int)(qb - qa) : 0;
+    it.Lk = ok ? (int)(kb - ka) : 0;
     return ok;
 }
 
-template <int D>
-__global__ void __launch_bounds__(128) prompt_kernel(const __grid_constant__ PromptParams p)
+// Keys that token `tok` of the item's sequence sees.
+__device__ __forceinline__ int prompt_limit(const PromptParams &p, const PromptItem &it, int tok)
 {
-    constexpr int N = D / 32;
-    const int lane = threadIdx.x & 31;
-    const int h = blockIdx.x, g = h / p.G;
-    int64_t q0, k0;
-    int Lq, Lk;
-    prompt_sequence(p, blockIdx.y, threadIdx.x == 0, q0, Lq, k0, Lk);
-    for (int i = blockIdx.z * 4 + (threadIdx.x >> 5); i < Lq; i += gridDim.z * 4) {
-        const int n = p.causal ? min(Lk, i + Lk - Lq + 1) : Lk;
-        float q[N], o[N], m = -INFINITY, l = 0.f;
-        for (int x = 0; x < N; ++x) {
-            q[x] = __bfloat162float(p.q[(q0 + i) * p.qs + (int64_t)h * D + lane * N + x]) * p.scale;
-            o[x] = 0.f;
+    return p.causal ? min(it.Lk, max(0, tok + it.Lk - it.Lq + 1)) : it.Lk;
+}
+
+// Key blocks of tile t (0 or 1): up to the last one its last token sees.
+__device__ __forceinline__ int prompt_blocks(const PromptParams &p, const PromptItem &it, int t)
+{
+    const int lo = it.t0 + t * p.NT, hi = min(lo + p.NT, it.Lq);
+    return hi > lo ? (prompt_limit(p, it, hi - 1) + pa::BN - 1) / pa::BN : 0;
+}
+
+// Shared-memory matrix descriptors (128-byte swizzle, 8 rows 1 KB apart) by
+// halves: the low word holds the address and the leading offset, the high word
+// is the same for all.  The steps' offsets are added inside the asm: added
+// outside, the compiler keeps every sum of the unrolled loops in a register.
+constexpr uint32_t SDESC_HI = (1024u >> 4) | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint32_t sdesc_lo(uint32_t saddr, uint32_t lbo) { return (saddr & 0x3FFFFu) >> 4 | (lbo >> 4) << 16; }
+
+// D[tmem] (+)= A[smem] B[smem], operands `off` 16-byte units behind a and b
+__device__ __forceinline__ void umma_ss(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t off, uint32_t idesc,
+                                        uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b32 x, y;\n\t.reg .b64 da, db;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "add.u32 x, %1, %3;\n\tadd.u32 y, %2, %3;\n\t"
+        "mov.b64 da, {x, %6};\n\tmov.b64 db, {y, %6};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, p;\n\t}" ::"r"(d_tmem),
+        "r"(a), "r"(b), "r"(off), "r"(idesc), "r"(accumulate), "r"(SDESC_HI)
+        : "memory");
+}
+
+// D[tmem] (+)= A[tmem] B[smem]
+__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b, uint32_t off, uint32_t idesc,
+                                        uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b32 y;\n\t.reg .b64 db;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "add.u32 y, %2, %3;\n\t"
+        "mov.b64 db, {y, %6};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b), "r"(off), "r"(idesc), "r"(accumulate), "r"(SDESC_HI)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+                 "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+                 "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// (a.x, a.y) * (b.x, b.y) + (c.x, c.y) in one instruction
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z, w;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, w;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "add.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+template <int D>
+__global__ void __launch_bounds__(pa::THREADS, 1)
+    prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant__ CUtensorMap qmap,
+                  const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap)
+{
+    using S = pa::Shape<D>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    PromptCtl *ctl = reinterpret_cast<PromptCtl *>(smem + S::OFF_CTL);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S::STAGES; ++i) {
+            mbar_init(&ctl->kvfull[i], 1);
+            mbar_init(&ctl->kvempty[i], 1);
         }
-        for (int j = 0; j < n; ++j) {
-            float s = 0.f;
-            for (int x = 0; x < N; ++x)
-                s += q[x] * __bfloat162float(p.k[(k0 + j) * p.ks + (int64_t)g * D + lane * N + x]);
-            for (int x = 16; x; x >>= 1)
-                s += __shfl_xor_sync(0xffffffffu, s, x);
-            const float mn = fmaxf(m, s), ms = mn == -INFINITY ? 0.f : mn;
-            const float al = expf(m - ms), w = expf(s - ms);
-            m = mn;
-            l = l * al + w;
-            for (int x = 0; x < N; ++x)
-                o[x] = o[x] * al + w * __bfloat162float(p.v[(k0 + j) * p.vs + (int64_t)g * D + lane * N + x]);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&ctl->qfull[i], 1);
+            mbar_init(&ctl->qempty[i], 1);
+            mbar_init(&ctl->sfull[i], 1);
+            mbar_init(&ctl->pfull[i], 4);
+            mbar_init(&ctl->ofull[i], 1);
         }
-        for (int x = 0; x < N; ++x)
-            p.out[(q0 + i) * p.os + (int64_t)h * D + lane * N + x] = __float2bfloat16_rn(n > 0 ? o[x] / l : 0.f);
-        if (p.lse && lane == 0)
-            p.lse[(q0 + i) * p.Hq + h] = n > 0 ? m + logf(l) : -INFINITY;
+        for (int i = 0; i < pa::SLOTS; ++i) {
+            mbar_init(&ctl->ifull[i], 1);
+            mbar_init(&ctl->iempty[i], 9); // the issuer and eight softmax warps
+        }
+        mbar_init(&ctl->tail, 1);
+        mbar_init(&ctl->drain, 1);
+        ctl->abort = 0;
+        ctl->issued = 0;
+        fence_mbar_init();
+        fence_proxy_async_smem();
+    }
+    if (warp == pa::MMA_WARP) {
+        tmem_alloc(&ctl->tmem_base, pa::TMEM_COLS);
+        tmem_relinquish();
+        tc_fence_before();
+    }
+    // The item table.  Up to CHUNKS sequences: one entry each, the longest
+    // first, so that what is left at the end is short; more: runs of
+    // sequences in their own order (each is then a small part of the whole).
+    const int64_t per = (p.B + pa::CHUNKS - 1) / pa::CHUNKS;
+    const int span = 2 * p.NT; // tokens of an item
+    {
+        const int i = threadIdx.x;
+        const int64_t lo = min(i * per, p.B), hi = i < pa::CHUNKS ? min(lo + per, p.B) : lo;
+        int64_t n = 0;
+        for (int64_t b = lo; b < hi; ++b) {
+            PromptItem it;
+            if (!prompt_sequence(p, b, it) && blockIdx.x == 0)
+                report_fault(p.status, TDG_ERR_DEVICE, TDG_WHERE_CU, (uint32_t)b, p.epoch);
+            n += (it.Lq + span - 1) / span;
+        }
+        if (i < pa::CHUNKS)
+            ctl->first[i] = (uint32_t)n;
+        __syncthreads();
+        if (i < pa::CHUNKS) {
+            int rank = 0;
+            if (per == 1) {
+                for (int j = 0; j < (int)p.B; ++j) {
+                    const uint32_t x = ctl->first[j];
+                    rank += x > (uint32_t)n || (x == (uint32_t)n && j < i) ? 1 : 0;
+                }
+                if (i >= p.B)
+                    rank = i;
+            } else {
+                rank = i;
+            }
+            ctl->order[rank] = (uint16_t)i;
+        }
+        __syncthreads();
+        if (warp == 0) { // exclusive sums in that order, 8 entries a lane
+            uint32_t x[8], sum = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                x[j] = sum;
+                sum += ctl->first[ctl->order[lane * 8 + j]];
+            }
+            uint32_t upto = sum;
+            for (int d = 1; d < 32; d <<= 1) {
+                const uint32_t y = __shfl_up_sync(0xffffffffu, upto, d);
+                if (lane >= d)
+                    upto += y;
+            }
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                ctl->first[lane * 8 + j] = upto - sum + x[j];
+            if (lane == 31)
+                ctl->first[pa::CHUNKS] = upto;
+        }
+    }
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = ctl->tmem_base;
+    const uint32_t items = ctl->first[pa::CHUNKS] * (uint32_t)p.Hkv;
+    const uint64_t tmo = p.timeout_ns;
+    auto wait = [&](uint64_t *b, uint32_t phase, uint32_t what) -> bool {
+        if (mbar_wait(b, phase, tmo))
+            return true;
+        report_fault(p.status, TDG_ERR_TIMEOUT, TDG_WHERE_PIPE, what, p.epoch);
+        ctl->abort = 1;
+        return false;
+    };
+
+    if (warp < pa::MMA_WARP) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(pa::REGS_SOFTMAX));
+        const int t = warp >> 2; // tile
+        const int r = (warp & 3) * 32 + lane;
+        const int row_tok = r / p.G, row_head = r % p.G;
+        const bool row_used = r < p.NT * p.G;
+        const uint32_t lanes = (uint32_t)(warp & 3) * 32 << 16;
+        const uint32_t s_addr = tmem + lanes + t * 128, o_addr = tmem + lanes + 256 + t * 128;
+        int slot = 0;
+        uint32_t slot_phase = 0, s_phase = 0, o_phase = 0;
+        while (true) {
+            bool ok = wait(&ctl->ifull[slot], slot_phase, 30);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok)
+                break;
+            const PromptItem it = ctl->item[slot];
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&ctl->iempty[slot]);
+            if (++slot == pa::SLOTS) {
+                slot = 0;
+                slot_phase ^= 1u;
+            }
+            if (!it.valid)
+                break;
+            const int tile_tok = it.t0 + t * p.NT, tok = tile_tok + row_tok;
+            const int nb = prompt_blocks(p, it, t);
+            const int limit = prompt_limit(p, it, tok);          // keys this row sees
+            const int open = prompt_limit(p, it, tile_tok);      // keys every row of the tile sees
+            float m = -INFINITY, l = 0.f;                        // m: in units of s
+            for (int j = 0; j < nb; ++j) {
+                ok = __all_sync(0xffffffffu, wait(&ctl->sfull[t], s_phase, 31));
+                if (!ok)
+                    break;
+                s_phase ^= 1u;
+                tc_fence_after();
+                uint32_t s[4][32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    tmem_ld_32x32b_x32(s_addr + c * 32, s[c]);
+                tmem_ld_wait();
+                if ((j + 1) * pa::BN > open) { // the causal edge or the sequence's end runs through this block
+                    const int lim = limit - j * pa::BN;
+#pragma unroll
+                    for (int c = 0; c < 128; ++c)
+                        s[c / 32][c % 32] = c < lim ? s[c / 32][c % 32] : 0xFF800000u; // -inf
+                }
+                float mx[4] = {__uint_as_float(s[0][0]), __uint_as_float(s[1][0]), __uint_as_float(s[2][0]), __uint_as_float(s[3][0])};
+#pragma unroll
+                for (int c = 1; c < 32; ++c)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        mx[i] = fmaxf(mx[i], __uint_as_float(s[i][c]));
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                if (j == 0) {
+                    m = top;
+                } else {
+                    const bool grown = (top - m) * p.scale_log2 > 8.f; // also from -inf
+                    if (__any_sync(0xffffffffu, grown)) {
+                        const float al = grown ? exp2_approx((m - top) * p.scale_log2) : 1.f;
+                        if (grown) {
+                            m = top;
+                            l *= al;
+                        }
+                        // the block before has left the tensor cores: its
+                        // product was issued ahead of this block's scores
+#pragma unroll
+                        for (int c = 0; c < D; c += 16) {
+                            uint32_t o[16];
+                            tmem_ld_32x32b_x16(o_addr + c, o);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
+                            tmem_st_32x32b_x16(o_addr + c, o);
+                        }
+                    }
+                }
+                const float ms = m == -INFINITY ? 0.f : m * p.scale_log2;
+                const float2 c2 = make_float2(p.scale_log2, p.scale_log2), m2 = make_float2(-ms, -ms);
+                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float2 x = fma2(make_float2(__uint_as_float(s[c][2 * i]), __uint_as_float(s[c][2 * i + 1])), c2, m2);
+                        const float2 e = make_float2(exp2_approx(x.x), exp2_approx(x.y));
+                        sum[i & 1] = add2(sum[i & 1], e);
+                        w[i] = pack_bf16x2(e.x, e.y);
+                    }
+                    tmem_st_32x32b_x16(s_addr + c * 16, w);
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&ctl->pfull[t]);
+                sum[0] = add2(sum[0], sum[1]);
+                l += sum[0].x + sum[0].y;
+            }
+            if (!ok)
+                break;
+            if (nb) {
+                ok = __all_sync(0xffffffffu, wait(&ctl->ofull[t], o_phase, 32));
+                if (!ok)
+                    break;
+                o_phase ^= 1u;
+                tc_fence_after();
+            }
+            const bool mine = row_used && tok < it.Lq;
+            const bool sees = limit > 0;
+            const float f = sees ? 1.f / l : 0.f;
+            const int64_t row = (int64_t)it.q0 + tok;
+            const int h = it.g * p.G + row_head;
+            __nv_bfloat16 *dst = p.out + row * p.os + (int64_t)h * D;
+#pragma unroll
+            for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                if (nb) {
+                    tmem_ld_32x32b_x32(o_addr + c, o);
+                    tmem_ld_wait();
+                }
+                if (mine)
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8) {
+                        uint4 v = make_uint4(0, 0, 0, 0);
+                        if (sees) {
+                            v.x = pack_bf16x2(__uint_as_float(o[i]) * f, __uint_as_float(o[i + 1]) * f);
+                            v.y = pack_bf16x2(__uint_as_float(o[i + 2]) * f, __uint_as_float(o[i + 3]) * f);
+                            v.z = pack_bf16x2(__uint_as_float(o[i + 4]) * f, __uint_as_float(o[i + 5]) * f);
+                            v.w = pack_bf16x2(__uint_as_float(o[i + 6]) * f, __uint_as_float(o[i + 7]) * f);
+                        }
+                        *reinterpret_cast<uint4 *>(dst + c + i) = v;
+                    }
+            }
+            tc_fence_before(); // the next item's first product writes O after this tile's next pfull
+            if (p.lse && mine)
+                p.lse[row * p.Hq + h] = sees ? (m * p.scale_log2 + log2f(l)) * 0.6931471805599453f : -INFINITY;
+        }
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(pa::REGS_OTHER));
+        if (warp == pa::LOAD_WARP) {
+            int slot = 0, stage = 0;
+            uint32_t slot_phase = 0, phase = 0, q_phase[2] = {0, 0}, tail_phase = 0;
+            int issued = 0;
+            bool ok = true;
+            for (uint32_t idx = blockIdx.x; ok; idx += gridDim.x) {
+                PromptItem it;
+                it.valid = idx < items ? 1 : 0;
+                if (it.valid) {
+                    // the table entry: the last one whose first item is not behind
+                    const uint32_t unit = idx / (uint32_t)p.Hkv;
+                    int e = 0;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        e += __popc(__ballot_sync(0xffffffffu, ctl->first[j * 32 + lane] <= unit));
+                    --e;
+                    int left = (int)(unit - ctl->first[e]);
+                    int64_t b = (int64_t)ctl->order[e] * per;
+                    const int64_t end = min(b + per, p.B);
+                    int n = 0;
+                    for (; b < end; ++b) {
+                        prompt_sequence(p, b, it);
+                        n = (it.Lq + span - 1) / span;
+                        if (left < n)
+                            break;
+                        left -= n;
+                    }
+                    if (b == end) // only with offsets that cover rows again and again: nothing to do
+                        it.Lq = it.Lk = n = left = 0;
+                    it.g = (int)(idx % (uint32_t)p.Hkv);
+                    it.t0 = max(0, n - 1 - left) * span; // the last tokens, which see the most, first
+                }
+                if (lane == 0) {
+                    ok = wait(&ctl->iempty[slot], slot_phase ^ 1u, 10);
+                    if (ok) {
+                        ctl->item[slot] = it;
+                        mbar_arrive(&ctl->ifull[slot]);
+                    }
+                }
+                ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+                if (++slot == pa::SLOTS) {
+                    slot = 0;
+                    slot_phase ^= 1u;
+                }
+                if (!it.valid || !ok)
+                    break;
+                const int nb0 = prompt_blocks(p, it, 0), nb1 = prompt_blocks(p, it, 1), nb = max(nb0, nb1);
+                if (lane == 0) {
+                    for (int t = 0; t < 2 && ok; ++t)
+                        if (t == 0 ? nb0 : nb1) {
+                            ok = wait(&ctl->qempty[t], q_phase[t] ^ 1u, 11);
+                            if (!ok)
+                                break;
+                            q_phase[t] ^= 1u;
+                            mbar_arrive_expect_tx(&ctl->qfull[t], (uint32_t)(p.NT * p.G * D * 2));
+#pragma unroll
+                            for (int hf = 0; hf < S::HALVES; ++hf)
+                                tma_load_3d_addr(smem + t * S::Q_BYTES + hf * 16384, &qmap, smem_u32(&ctl->qfull[t]), hf * 64,
+                                                 it.g * p.G, it.q0 + it.t0 + t * p.NT);
+                        }
+                }
+                ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+                for (int j = 0; j < nb && ok; ++j)
+                    for (int kv = 0; kv < 2 && ok; ++kv) {
+                        uint8_t *dst = smem + S::OFF_KV + stage * S::KV_BYTES;
+                        const int rows = it.Lk - j * pa::BN; // keys of this block that are the sequence's own
+                        // values behind the sequence's end are cleared: weight 0 times
+                        // whatever the neighbour holds must be 0
+                        const bool clear = kv == 1 && rows < pa::BN;
+                        if (lane == 0) {
+                            ok = wait(&ctl->kvempty[stage], phase ^ 1u, 12);
+                            if (ok) {
+                                uint64_t *bar = clear ? &ctl->tail : &ctl->kvfull[stage];
+                                mbar_arrive_expect_tx(bar, S::KV_BYTES);
+#pragma unroll
+                                for (int hf = 0; hf < S::HALVES; ++hf)
+                                    tma_load_3d_addr(dst + hf * 16384, kv ? &vmap : &kmap, smem_u32(bar), hf * 64, it.g,
+                                                     it.k0 + j * pa::BN);
+                            }
+                        }
+                        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+                        if (!ok)
+                            break;
+                        if (clear) {
+                            const bool landed = wait(&ctl->tail, tail_phase, 13);
+                            tail_phase ^= 1u;
+                            __syncwarp();
+                            for (int i = rows * 8 + lane; i < pa::BN * 8; i += 32)
+#pragma unroll
+                                for (int hf = 0; hf < S::HALVES; ++hf)
+                                    *reinterpret_cast<uint4 *>(dst + hf * 16384 + i * 16) = make_uint4(0, 0, 0, 0);
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane == 0)
+                                mbar_arrive(&ctl->kvfull[stage]);
+                            ok = landed;
+                        }
+                        ++issued;
+                        if (++stage == S::STAGES) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
+                    }
+            }
+            if (lane == 0)
+                ctl->issued = issued;
+            if (ctl->abort && lane == 0) {
+                // leave only when the copies in flight have landed
+                for (int t = 0; t < 2; ++t)
+                    if (q_phase[t] || issued)
+                        (void)mbar_wait(&ctl->qfull[t], q_phase[t] ^ 1u, tmo);
+                for (int f = max(0, issued - S::STAGES); f < issued; ++f)
+                    (void)mbar_wait(&ctl->kvfull[f % S::STAGES], (uint32_t)(f / S::STAGES) & 1u, tmo);
+            }
+            __syncwarp();
+        } else if (warp == pa::MMA_WARP) {
+            if (lane == 0) {
+                constexpr uint32_t idesc_s = idesc_bf16(128, pa::BN, 0), idesc_o = idesc_bf16(128, D, 1);
+                const uint32_t base = smem_u32(smem);
+                int slot = 0, stage = 0;
+                uint32_t slot_phase = 0, phase = 0, q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
+                // S_t = Q_t K^T: both K-major, 16 elements are 32 bytes, 64 are a half
+                auto qk = [&](int t, int st) {
+                    const uint32_t a = sdesc_lo(base + t * S::Q_BYTES, 16), b = sdesc_lo(base + S::OFF_KV + st * S::KV_BYTES, 16);
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k)
+                        umma_ss(tmem + t * 128, a, b, (k / 4) * 1024 + (k % 4) * 2, idesc_s, k != 0 ? 1u : 0u);
+                    umma_commit(&ctl->sfull[t]);
+                };
+                // O_t += P_t V: P_t is 64 columns of bf16 pairs over S_t; V is
+                // MN-major: halves of 64 dimensions 16 KB apart, 16 keys are 2 KB
+                auto pv = [&](int t, int st, bool first) {
+                    const uint32_t b = sdesc_lo(base + S::OFF_KV + st * S::KV_BYTES, 16384);
+#pragma unroll
+                    for (int k = 0; k < pa::BN / 16; ++k)
+                        umma_ts(tmem + 256 + t * 128, tmem + t * 128 + k * 8, b, k * 128, idesc_o, !first || k != 0 ? 1u : 0u);
+                };
+                auto next = [&](int &st, uint32_t &ph) {
+                    if (++st == S::STAGES) {
+                        st = 0;
+                        ph ^= 1u;
+                    }
+                };
+                bool ok = true;
+                while (ok) {
+                    ok = wait(&ctl->ifull[slot], slot_phase, 20);
+                    if (!ok)
+                        break;
+                    const PromptItem it = ctl->item[slot];
+                    mbar_arrive(&ctl->iempty[slot]);
+                    if (++slot == pa::SLOTS) {
+                        slot = 0;
+                        slot_phase ^= 1u;
+                    }
+                    if (!it.valid)
+                        break;
+                    const int nb[2] = {prompt_blocks(p, it, 0), prompt_blocks(p, it, 1)};
+                    const int most = max(nb[0], nb[1]);
+                    if (!most)
+                        continue;
+                    ok = wait(&ctl->kvfull[stage], phase, 21);
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+                        if (ok && nb[t]) {
+                            ok = wait(&ctl->qfull[t], q_phase[t], 22);
+                            if (!ok)
+                                break;
+                            q_phase[t] ^= 1u;
+                            tc_fence_after();
+                            qk(t, stage);
+                            if (nb[t] == 1)
+                                umma_commit(&ctl->qempty[t]);
+                        }
+                    if (!ok)
+                        break;
+                    umma_commit(&ctl->kvempty[stage]);
+                    next(stage, phase);
+                    for (int j = 0; j < most && ok; ++j) {
+                        const int vst = stage;
+                        const uint32_t vph = phase;
+                        next(stage, phase);
+                        const bool more = j + 1 < most; // there is a next block of keys: it is in `stage`
+                        ok = wait(&ctl->kvfull[vst], vph, 23);
+                        bool have_k = false;
+#pragma unroll
+                        for (int t = 0; t < 2; ++t)
+                            if (ok && j < nb[t]) {
+                                ok = wait(&ctl->pfull[t], p_phase[t], 24);
+                                if (!ok)
+                                    break;
+                                p_phase[t] ^= 1u;
+                                tc_fence_after();
+                                pv(t, vst, j == 0);
+                                if (j + 1 < nb[t]) {
+                                    if (!have_k) {
+                                        ok = wait(&ctl->kvfull[stage], phase, 25);
+                                        if (!ok)
+                                            break;
+                                        have_k = true;
+                                        tc_fence_after();
+                                    }
+                                    qk(t, stage);
+                                    if (j + 2 == nb[t])
+                                        umma_commit(&ctl->qempty[t]);
+                                } else {
+                                    umma_commit(&ctl->ofull[t]);
+                                }
+                            }
+                        if (!ok)
+                            break;
+                        umma_commit(&ctl->kvempty[vst]);
+                        if (more) {
+                            umma_commit(&ctl->kvempty[stage]);
+                            next(stage, phase);
+                        }
+                    }
+                }
+                if (ctl->abort) { // every MMA issued finishes before TMEM is freed
+                    umma_commit(&ctl->drain);
+                    (void)mbar_wait(&ctl->drain, 0, tmo);
+                }
+            }
+            __syncwarp();
+        }
+    }
+    __syncthreads();
+    if (warp == pa::MMA_WARP) {
+        tc_fence_after();
+        tmem_dealloc(tmem, pa::TMEM_COLS);
     }
 }
 
@@ -101,29 +686,40 @@ extern "C" int tdg_prompt_attention(tdg_symm *h, const tdg_prompt_attention_args
     PromptParams p;
     memset(&p, 0, sizeof p);
     p.status = h->status;
+    p.G = (int)(Hq / Hkv);
+    p.NT = 128 / p.G;
+    // items: at most one per 2 NT tokens and one more per sequence, of every key head
+    const int64_t items = (a->Tq / (2 * p.NT) + a->B) * Hkv;
+    if (items > INT32_MAX)
+        return TDG_ERR_INVALID;
     p.epoch = next_epoch(h);
+    p.timeout_ns = timeout_or_default(0);
     p.Tq = a->Tq;
     p.Tk = a->Tk;
     p.B = a->B;
-    p.qs = a->q_stride;
-    p.ks = a->k_stride;
-    p.vs = a->v_stride;
     p.os = a->out_stride;
     p.Hq = (int)Hq;
     p.Hkv = (int)Hkv;
-    p.G = (int)(Hq / Hkv);
     p.causal = a->causal;
-    p.scale = a->scale > 0.f ? a->scale : 1.0f / sqrtf((float)D);
-    p.q = static_cast<const __nv_bfloat16 *>(a->q);
-    p.k = static_cast<const __nv_bfloat16 *>(a->k);
-    p.v = static_cast<const __nv_bfloat16 *>(a->v);
+    p.scale_log2 = (a->scale > 0.f ? a->scale : 1.0f / sqrtf((float)D)) * 1.4426950408889634f;
     p.out = static_cast<__nv_bfloat16 *>(a->out);
     p.lse = a->lse;
     p.cu_q = a->cu_q;
     p.cu_k = a->cu_k;
+    CUtensorMap qm, km, vm;
+    // rows of heads: {D, heads, rows}; a box is 64 dimensions of a tile's heads and tokens
+    if (!map_bf16_3d(&qm, a->q, D, Hq, a->Tq, D * 2, a->q_stride * 2, 64, (uint32_t)p.G, (uint32_t)p.NT))
+        return TDG_ERR_CUDA;
+    km = vm = qm; // no keys: nothing is loaded through them
+    if (a->Tk && (!map_bf16_3d(&km, a->k, D, Hkv, a->Tk, D * 2, a->k_stride * 2, 64, 1, pa::BN) ||
+                  !map_bf16_3d(&vm, a->v, D, Hkv, a->Tk, D * 2, a->v_stride * 2, 64, 1, pa::BN)))
+        return TDG_ERR_CUDA;
     const void *fn = D == 128 ? reinterpret_cast<const void *>(&prompt_kernel<128>) : reinterpret_cast<const void *>(&prompt_kernel<64>);
-    void *args[] = {&p};
-    const unsigned z = (unsigned)(a->Tq < 1024 ? (a->Tq + 3) / 4 : 256);
-    return cuda_err(launch(fn, dim3((unsigned)Hq, (unsigned)a->B, z), dim3(128), 0, static_cast<cudaStream_t>(stream), args, false),
+    const int smem = D == 128 ? prompt_smem<128>() : prompt_smem<64>();
+    if (const cudaError_t e = set_smem(fn, smem); e != cudaSuccess)
+        return cuda_err(e, "prompt attention smem");
+    void *args[] = {&p, &qm, &km, &vm};
+    const unsigned ctas = (unsigned)(items < h->sm_count ? items : h->sm_count);
+    return cuda_err(launch(fn, dim3(ctas), dim3(pa::THREADS), smem, static_cast<cudaStream_t>(stream), args, false),
                     "prompt attention launch");
 }
