@@ -53,3 +53,36 @@ def test_null_handles(L):
     assert L.tdg_rope_append(None, None, None) == tdg.TDG_ERR_INVALID
     assert L.tdg_prompt_attention(None, None, None) == tdg.TDG_ERR_INVALID
     assert L.tdg_paged_decode(None, None, None) == tdg.TDG_ERR_INVALID
+
+
+def test_packed_arguments_match_the_structures():
+    """The binding packs arguments with one struct call: same layout as the structures."""
+    import random
+
+    def values(cls):
+        for name, kind in cls._fields_:
+            if isinstance(kind, type) and issubclass(kind, ctypes.Structure):
+                yield from values(kind)
+            elif hasattr(kind, "_length_"):
+                yield from (random.randrange(1, 1 << 20) for _ in range(kind._length_))
+            elif kind is ctypes.c_float:
+                yield 0.25
+            else:
+                yield random.randrange(1, 1 << 20)
+
+    def fill(obj, it):
+        for name, kind in obj._fields_:
+            if isinstance(kind, type) and issubclass(kind, ctypes.Structure):
+                fill(getattr(obj, name), it)
+            elif hasattr(kind, "_length_"):
+                for i in range(kind._length_):
+                    getattr(obj, name)[i] = next(it)
+            else:
+                setattr(obj, name, next(it))
+
+    for cls, pack in ((tdg.RopeAppendArgs, tdg._pack_rope), (tdg.PromptAttentionArgs, tdg._pack_prompt),
+                      (tdg.PagedDecodeArgs, tdg._pack_decode)):
+        v = list(values(cls))
+        obj = cls()
+        fill(obj, iter(v))
+        assert pack(*v) == bytes(obj), cls.__name__

@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -261,6 +262,7 @@ class Symm:
             buffer = torch.empty(nbytes + 1024, dtype=torch.uint8, device=device or "cuda")
         _tensor(buffer, "buffer", torch.uint8, nbytes + 1024)
         self.buf = buffer
+        self.device = buffer.device
         self.base_off = (-buffer.data_ptr()) % 1024
         self.base = buffer.data_ptr() + self.base_off
         self.nbytes = nbytes
@@ -448,6 +450,9 @@ class PagedCache:
             k_off=k_off, v_off=v_off,
             k_scale=_tensor(k_scale, "k_scale", torch.float32, Hkv) if e4m3 else None,
             v_scale=_tensor(v_scale, "v_scale", torch.float32, Hkv) if e4m3 else None)
+        # the description's fields as the packed calls take them
+        self.packed = (pages, page_size, self.desc.kv_type, Hkv, D, k_off, v_off,
+                       self.desc.k_scale or 0, self.desc.v_scale or 0)
 
     def pools(self, symm: Symm, rank: int):
         """The key and the value pool of one rank, as tensors."""
@@ -457,40 +462,81 @@ class PagedCache:
         return symm.view(rank, self.k_off, shape, kind), symm.view(rank, self.v_off, shape, kind)
 
 
+_torch = None
+
+
+def _attn():
+    """torch, and the library's attention entry points taking packed arguments
+    (one struct.pack call costs a fraction of filling a ctypes structure field
+    by field, and these calls are short)."""
+    global _torch
+    import torch
+    L = lib()
+    fast = ctypes.CDLL(LIB_PATH)
+    for name in ("tdg_rope_append", "tdg_prompt_attention", "tdg_paged_decode"):
+        f = getattr(fast, name)
+        f.restype, f.argtypes = ctypes.c_int, [_vp, ctypes.c_char_p, _vp]
+        globals()["_" + name] = f
+    _torch = torch
+    return L
+
+
+_DESC = "qiiqqNNPP"                                          # tdg_paged_cache
+_pack_rope = struct.Struct("@i4x" + _DESC + "qqqPPPqqqPPqqPqiiiiiiPqPPqqP").pack
+_pack_prompt = struct.Struct("@qqqqqqPPPqqqPqPPPif").pack
+_pack_decode = struct.Struct("@ii" + _DESC + "qqPqPqPPqqPNf0q").pack
+
+
+def _raw_stream(stream, device):
+    if stream is None:
+        return _torch.cuda.current_stream(device).cuda_stream
+    return stream.cuda_stream
+
+
 def _rows(t, name, device):
     """Check rows of heads, (rows, heads, D) in bf16, whose rows may be strided
-    (columns of a wider buffer); returns (pointer, row stride in elements)."""
-    import torch
-    if not isinstance(t, torch.Tensor):
+    (columns of a wider buffer); returns (pointer, row stride in elements, rows,
+    heads, D)."""
+    if not isinstance(t, _torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not _torch.bfloat16:
         raise TypeError(f"{name}: expected torch.bfloat16, got {t.dtype}")
-    if t.dim() != 3:
-        raise ValueError(f"{name}: expected (rows, heads, D), got {tuple(t.shape)}")
-    n, heads, D = t.shape
+    shape = t.shape
+    if len(shape) != 3:
+        raise ValueError(f"{name}: expected (rows, heads, D), got {tuple(shape)}")
+    n, heads, D = shape
     s0, s1, s2 = t.stride()
-    if n == 0 or heads == 0:
-        return t.data_ptr() or None, heads * D
+    if n <= 1 or not heads:
+        s0 = heads * D          # no second row, no stride
+        if not n or not heads:
+            return t.data_ptr(), s0, n, heads, D
     if (s2 != 1 and D > 1) or (s1 != D and heads > 1):
         raise ValueError(f"{name}: the heads of a row must be contiguous, strides {t.stride()}")
-    if n == 1:
-        s0 = heads * D          # one row has no stride
     if t.device != device:
         raise ValueError(f"{name}: on {t.device}, the heap is on {device}")
-    return t.data_ptr(), s0
+    return t.data_ptr(), s0, n, heads, D
 
 
 def _table(table, name, device):
-    """Check a page table (sequences, entries), int32, rows possibly strided."""
-    import torch
-    if not isinstance(table, torch.Tensor) or table.dtype != torch.int32:
+    """Check a page table (sequences, entries), int32, rows possibly strided;
+    returns (pointer, entries, row stride, sequences)."""
+    if not isinstance(table, _torch.Tensor) or table.dtype is not _torch.int32:
         raise TypeError(f"{name}: expected an int32 tensor")
-    if table.dim() != 2 or (table.shape[1] > 1 and table.stride(1) != 1):
+    shape, stride = table.shape, table.stride()
+    if len(shape) != 2 or (shape[1] > 1 and stride[1] != 1):
         raise ValueError(f"{name}: expected (sequences, entries) with contiguous rows")
     if table.device != device:
         raise ValueError(f"{name}: on {table.device}, the heap is on {device}")
-    n, entries = table.shape
-    return table.data_ptr(), entries, entries if n <= 1 else table.stride(0)
+    n, entries = shape
+    return table.data_ptr(), entries, entries if n <= 1 else stride[0], n
+
+
+def _flat(t, name, dtype, numel, device):
+    """_tensor's checks, in the order in which they are cheap."""
+    if isinstance(t, _torch.Tensor) and t.dtype is dtype and t.device == device and t.is_contiguous() \
+            and t.numel() >= numel:
+        return t.data_ptr()
+    return _tensor(t, name, dtype, numel, device)
 
 
 def rope_append(symm: Symm, cache: PagedCache, q, k, v, q_out, cos_sin, pos, table, lens, cu=None,
@@ -502,48 +548,50 @@ def rope_append(symm: Symm, cache: PagedCache, q, k, v, q_out, cos_sin, pos, tab
     table: (B, entries) int32 page ids (None: no cache write); lens: (B,) int32
     lengths with the new tokens; cu: (B + 1,) int32 row offsets (None: one row
     per sequence).  q and q_out may be None, q_out may be q, k_out may be k."""
-    import torch
-    dev, i32 = symm.buf.device, torch.int32
-    T = k.shape[0]
-    a = RopeAppendArgs(world=symm.world, cache=cache.desc, T=T, interleaved=1 if interleaved else 0)
-    if tuple(k.shape[1:]) != (cache.Hkv, cache.D):
-        raise ValueError(f"k: expected heads ({cache.Hkv}, {cache.D}), got {tuple(k.shape[1:])}")
-    a.k, a.k_stride = _rows(k, "k", dev)
-    if (q is None) != (q_out is None):
-        raise ValueError("q and q_out go together")
-    if q is not None:
-        if q.shape != q_out.shape or q.shape[0] != T or q.shape[2] != cache.D:
+    if _torch is None:
+        _attn()
+    dev, i32 = symm.device, _torch.int32
+    kp, ks, T, Hkv, D = _rows(k, "k", dev)
+    if Hkv != cache.Hkv or D != cache.D:
+        raise ValueError(f"k: expected heads ({cache.Hkv}, {cache.D}), got ({Hkv}, {D})")
+    Hq = qp = qs = qop = qos = kop = kos = B = vp = vs = tp = te = ts = lp = cp = 0
+    csp = max_pos = rot = axes = pp = s0 = s1 = s2 = 0
+    if q is not None and q_out is not None:
+        qp, qs, n, Hq, qD = _rows(q, "q", dev)
+        qop, qos, *like = _rows(q_out, "q_out", dev)
+        if like != [n, Hq, qD] or n != T or qD != D:
             raise ValueError(f"q {tuple(q.shape)} and q_out {tuple(q_out.shape)} do not fit k {tuple(k.shape)}")
-        a.Hq = q.shape[1]
-        a.q, a.q_stride = _rows(q, "q", dev)
-        a.q_out, a.q_out_stride = _rows(q_out, "q_out", dev)
+    elif q is not q_out:
+        raise ValueError("q and q_out go together")
     if k_out is not None:
-        if k_out.shape != k.shape:
+        kop, kos, *like = _rows(k_out, "k_out", dev)
+        if like != [T, Hkv, D]:
             raise ValueError(f"k_out {tuple(k_out.shape)} does not fit k {tuple(k.shape)}")
-        a.k_out, a.k_out_stride = _rows(k_out, "k_out", dev)
     if cos_sin is not None:
-        axes = 1 if pos.dim() == 1 else pos.shape[0]
-        if pos.dim() > 2 or pos.shape[-1] != T or axes not in (1, 2, 3):
+        csp = _flat(cos_sin, "cos_sin", _torch.float32, 0, dev)
+        max_pos, rot = cos_sin.shape
+        shape = pos.shape
+        axes = 1 if len(shape) == 1 else shape[0]
+        if len(shape) not in (1, 2) or shape[-1] != T or not 1 <= axes <= 3:
             raise ValueError(f"pos: expected ({T},) or (1..3, {T}), got {tuple(pos.shape)}")
-        a.max_pos, a.rot_dim = cos_sin.shape
-        a.cos_sin = _tensor(cos_sin, "cos_sin", torch.float32, 0, dev)
-        a.axes, a.pos, a.pos_stride = axes, _tensor(pos, "pos", i32, axes * T, dev), T
+        pp = _flat(pos, "pos", i32, axes * T, dev)
         if axes > 1:
             if sections is None or len(sections) != axes:
                 raise ValueError(f"sections: expected {axes} numbers of pairs")
-            for i, n in enumerate(sections):
-                a.sections[i] = n
+            s0, s1, s2 = (*sections, 0)[:3]
     if table is not None:
-        B = table.shape[0]
-        if v.shape != k.shape:
+        vp, vs, *like = _rows(v, "v", dev)
+        if like != [T, Hkv, D]:
             raise ValueError(f"v {tuple(v.shape)} does not fit k {tuple(k.shape)}")
-        a.v, a.v_stride = _rows(v, "v", dev)
-        a.B = B
-        a.table, a.table_entries, a.table_stride = _table(table, "table", dev)
-        a.lens = _tensor(lens, "lens", i32, B, dev)
+        tp, te, ts, B = _table(table, "table", dev)
+        lp = _flat(lens, "lens", i32, B, dev)
         if cu is not None:
-            a.cu = _tensor(cu, "cu", i32, B + 1, dev)
-    _check(lib().tdg_rope_append(symm.h, ctypes.byref(a), _stream(stream)), "tdg_rope_append")
+            cp = _flat(cu, "cu", i32, B + 1, dev)
+    a = _pack_rope(symm.world, *cache.packed, T, B, Hq, qp, kp, vp, qs, ks, vs, qop, kop, qos, kos, csp,
+                   max_pos, rot, 1 if interleaved else 0, axes, s0, s1, s2, pp, T, cp, tp, te, ts, lp)
+    rc = _tdg_rope_append(symm.h, a, _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "tdg_rope_append")
 
 
 def prompt_attention(symm: Symm, q, k, v, out, cu_q, cu_k, lse=None, causal=True, scale: float = 0.0,
@@ -551,25 +599,25 @@ def prompt_attention(symm: Symm, q, k, v, out, cu_q, cu_k, lse=None, causal=True
     """Attention over whole prompts packed one after another: q and out (Tq,
     Hq, D), k and v (Tk, Hkv, D), rows possibly strided; cu_q and cu_k (B + 1,)
     int32 row offsets; lse (Tq, Hq) float32 or None."""
-    import torch
-    dev, i32 = symm.buf.device, torch.int32
-    Tq, Hq, D = q.shape
-    Tk, Hkv, _ = k.shape
-    if out.shape != q.shape or k.shape != v.shape or k.shape[2] != D:
+    if _torch is None:
+        _attn()
+    dev, i32 = symm.device, _torch.int32
+    qp, qs, Tq, Hq, D = _rows(q, "q", dev)
+    kp, ks, Tk, Hkv, kD = _rows(k, "k", dev)
+    vp, vs, *vlike = _rows(v, "v", dev)
+    op, os_, *olike = _rows(out, "out", dev)
+    if olike != [Tq, Hq, D] or vlike != [Tk, Hkv, kD] or kD != D:
         raise ValueError(f"q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)} and out "
                          f"{tuple(out.shape)} do not fit together")
+    cqp = _flat(cu_q, "cu_q", i32, 1, dev)
     B = cu_q.numel() - 1
-    a = PromptAttentionArgs(Tq=Tq, Tk=Tk, B=B, Hq=Hq, Hkv=Hkv, D=D, causal=1 if causal else 0,
-                            scale=scale)
-    a.q, a.q_stride = _rows(q, "q", dev)
-    a.k, a.k_stride = _rows(k, "k", dev)
-    a.v, a.v_stride = _rows(v, "v", dev)
-    a.out, a.out_stride = _rows(out, "out", dev)
-    a.cu_q = _tensor(cu_q, "cu_q", i32, 1, dev)
-    a.cu_k = _tensor(cu_k, "cu_k", i32, B + 1, dev)
-    if lse is not None:
-        a.lse = _tensor(lse, "lse", torch.float32, Tq * Hq, dev)
-    _check(lib().tdg_prompt_attention(symm.h, ctypes.byref(a), _stream(stream)), "tdg_prompt_attention")
+    ckp = _flat(cu_k, "cu_k", i32, B + 1, dev)
+    lp = 0 if lse is None else _flat(lse, "lse", _torch.float32, Tq * Hq, dev)
+    a = _pack_prompt(Tq, Tk, B, Hq, Hkv, D, qp, kp, vp, qs, ks, vs, op, os_, lp, cqp, ckp,
+                     1 if causal else 0, scale)
+    rc = _tdg_prompt_attention(symm.h, a, _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "tdg_prompt_attention")
 
 
 def paged_decode_part_bytes(Hq: int, Hkv: int, D: int) -> int:
@@ -582,21 +630,21 @@ def paged_decode(symm: Symm, cache: PagedCache, q, out, table, lens, part_off: i
     (B, Hq, D), rows possibly strided; table (B, entries) int32 page ids; lens
     (B,) int32 lengths with the new token; lse (B, Hq) float32 or None.  The
     partial results (paged_decode_part_bytes) go to region(root) + part_off."""
-    import torch
-    dev, i32 = symm.buf.device, torch.int32
-    B, Hq, D = q.shape
-    if out.shape != q.shape or D != cache.D or table.shape[0] != B:
+    if _torch is None:
+        _attn()
+    dev = symm.device
+    qp, qs, B, Hq, D = _rows(q, "q", dev)
+    op, os_, *like = _rows(out, "out", dev)
+    tp, te, ts, n = _table(table, "table", dev)
+    if like != [B, Hq, D] or D != cache.D or n != B:
         raise ValueError(f"q {tuple(q.shape)}, out {tuple(out.shape)} and table {tuple(table.shape)} "
                          f"do not fit together")
-    a = PagedDecodeArgs(world=symm.world, root=root, cache=cache.desc, B=B, Hq=Hq, part_off=part_off,
-                        scale=scale)
-    a.q, a.q_stride = _rows(q, "q", dev)
-    a.out, a.out_stride = _rows(out, "out", dev)
-    a.table, a.table_entries, a.table_stride = _table(table, "table", dev)
-    a.lens = _tensor(lens, "lens", i32, B, dev)
-    if lse is not None:
-        a.lse = _tensor(lse, "lse", torch.float32, B * Hq, dev)
-    _check(lib().tdg_paged_decode(symm.h, ctypes.byref(a), _stream(stream)), "tdg_paged_decode")
+    np_ = _flat(lens, "lens", _torch.int32, B, dev)
+    lp = 0 if lse is None else _flat(lse, "lse", _torch.float32, B * Hq, dev)
+    a = _pack_decode(symm.world, root, *cache.packed, B, Hq, qp, qs, op, os_, lp, tp, te, ts, np_, part_off, scale)
+    rc = _tdg_paged_decode(symm.h, a, _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "tdg_paged_decode")
 
 
 def _moe_args(symm, T, H, E, k, x_off, topk_off, gate_off, out_off, recv, counts, base, slot,
