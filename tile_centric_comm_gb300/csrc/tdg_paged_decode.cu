@@ -312,7 +312,12 @@ __global__ void __launch_bounds__(pd::THREADS, 2)
         }
         fence_mbar_init();
         fence_proxy_async_smem();
+        prefetch_tensormap(&kmap);
+        prefetch_tensormap(&vmap);
     }
+    // launched while the kernel before may still run: nothing above touches memory
+    griddep_launch_dependents();
+    griddep_wait();
     // this CTA's run of the line: the warps' sums of tiles, then the sequence
     // in which the run begins
     const int64_t per = (p.B + pd::THREADS - 1) / pd::THREADS; // sequences of a thread
@@ -671,6 +676,8 @@ __global__ void __launch_bounds__(pd::THREADS, 2)
 template <int D>
 __global__ void __launch_bounds__(pd::JOIN_ROWS *D / 2) paged_join_kernel(const __grid_constant__ PagedDecodeParams p)
 {
+    griddep_launch_dependents();
+    griddep_wait();
     const int4 desc = p.desc[blockIdx.x];
     if (desc.x < 0)
         return;
@@ -734,13 +741,13 @@ template <int D, bool E4M3> int launch_decode(const tdg_symm *h, const tdg_paged
         return cuda_err(e, "paged decode smem");
     const unsigned ctas = (unsigned)(h->sm_count * 2 < pd::MAX_CTAS ? h->sm_count * 2 : pd::MAX_CTAS);
     void *args[] = {&p, &km, &vm};
-    if (const int rc = cuda_err(launch(fn, dim3(ctas), dim3(pd::THREADS), S::SMEM, st, args, false), "paged decode launch"))
+    if (const int rc = cuda_err(launch(fn, dim3(ctas), dim3(pd::THREADS), S::SMEM, st, args, false, 1, true), "paged decode launch"))
         return rc;
     void *jargs[] = {&p};
     const int join_rows = p.G < pd::ROWS ? p.G : pd::ROWS;
     return cuda_err(launch(reinterpret_cast<const void *>(&paged_join_kernel<D>),
                            dim3(ctas, (unsigned)((join_rows + pd::JOIN_ROWS - 1) / pd::JOIN_ROWS)), dim3(pd::JOIN_ROWS * D / 2), 0, st,
-                           jargs, false),
+                           jargs, false, 1, true),
                     "paged join launch");
 }
 

@@ -209,12 +209,18 @@ __global__ void __launch_bounds__(pa::THREADS, 1)
         ctl->issued = 0;
         fence_mbar_init();
         fence_proxy_async_smem();
+        prefetch_tensormap(&qmap);
+        prefetch_tensormap(&kmap);
+        prefetch_tensormap(&vmap);
     }
     if (warp == pa::MMA_WARP) {
         tmem_alloc(&ctl->tmem_base, pa::TMEM_COLS);
         tmem_relinquish();
         tc_fence_before();
     }
+    // launched while the kernel before may still run: nothing above touches memory
+    griddep_launch_dependents();
+    griddep_wait();
     // The item table.  Up to CHUNKS sequences: one entry each, the longest
     // first, so that what is left at the end is short; more: runs of
     // sequences in their own order (each is then a small part of the whole).
@@ -720,6 +726,6 @@ extern "C" int tdg_prompt_attention(tdg_symm *h, const tdg_prompt_attention_args
         return cuda_err(e, "prompt attention smem");
     void *args[] = {&p, &qm, &km, &vm};
     const unsigned ctas = (unsigned)(items < h->sm_count ? items : h->sm_count);
-    return cuda_err(launch(fn, dim3(ctas), dim3(pa::THREADS), smem, static_cast<cudaStream_t>(stream), args, false),
+    return cuda_err(launch(fn, dim3(ctas), dim3(pa::THREADS), smem, static_cast<cudaStream_t>(stream), args, false, 1, true),
                     "prompt attention launch");
 }

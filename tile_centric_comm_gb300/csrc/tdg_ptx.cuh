@@ -214,6 +214,12 @@ __device__ __forceinline__ bool wait_flag(const uint32_t *p, uint32_t epoch, uin
 }
 
 // ------------------------------------------------------------------ TMA ----
+// Fetch a tensor map (a kernel parameter) ahead of the first copy through it.
+__device__ __forceinline__ void prefetch_tensormap(const CUtensorMap *map)
+{
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
 // 2-D tile load, with the barrier given as a shared-window address
 __device__ __forceinline__ void tma_load_2d_addr(void *smem_dst, const CUtensorMap *map, uint32_t bar,
                                                  int x, int y)

@@ -2,24 +2,31 @@
 // new tokens' keys and values into the pages of the symmetric heap's cache.
 //
 // Per head and pair i: (x, y) -> (c x - s y, c y + s x) with (c, s) from a
-// table row chosen by the position on the pair's axis.  One CTA handles one
-// row (token); a thread keeps the cosines and sines of 8 pairs and walks over
-// the row's heads with them.
+// table row chosen by the position on the pair's axis.
+//
+// Bound by memory: every row is read once and written once (keys twice: to
+// k_out and to the cache).  One CTA handles a group of up to 8 rows.  First
+// its threads look the rows up (sequence, page, slot, positions: chains of
+// dependent loads, paid once per group) and put the rows' cosines and sines
+// into shared memory; then they walk over all (row, head) pairs of the group,
+// 16 elements a thread, four pairs' loads in flight at a time.
 #include "tdg_paged.cuh"
 
 namespace tdg {
 
 namespace rp {
 constexpr int THREADS = 256;
+constexpr int MAX_ROWS = 8; // rows of a group
+constexpr int DEPTH = 4;    // units whose loads a thread has in flight
 } // namespace rp
 
 struct RopeParams {
     DevStatus *status;
     uint32_t epoch;
     PagedView c;
-    int64_t B, max_pos, pos_stride, table_entries, table_stride;
+    int64_t T, B, max_pos, pos_stride, table_entries, table_stride;
     int64_t qs, ks, vs, qos, kos;
-    int Hq, rot, axes, sec0, sec01;
+    int Hq, rot, axes, sec0, sec01, rows; // rows: of a group
     const __nv_bfloat16 *q, *k, *v;
     __nv_bfloat16 *q_out, *k_out;
     const float *cos_sin;
@@ -42,137 +49,204 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8])
     return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
 }
 
-// 8 values divided by the head's scale, in e4m3 (clamped to +-448, NaN kept)
-__device__ __forceinline__ uint2 pack8_e4m3(const float (&f)[8], float scale)
+// 8 values times 1/scale, in e4m3 (clamped to +-448, NaN kept)
+__device__ __forceinline__ uint2 pack8_e4m3(const float (&f)[8], float inv)
 {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        w[i] = __nv_cvt_float2_to_fp8x2(make_float2(f[2 * i] / scale, f[2 * i + 1] / scale), __NV_SATFINITE, __NV_E4M3);
+        w[i] = __nv_cvt_float2_to_fp8x2(make_float2(f[2 * i] * inv, f[2 * i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
     return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
 }
 
-template <bool INTER, bool E4M3>
+// rows are read once: past L1 (and not through the read-only path, since an
+// output may be its own input)
+__device__ __forceinline__ uint4 ld_once(const __nv_bfloat16 *p)
+{
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+
+template <int D, bool INTER, bool E4M3>
 __global__ void __launch_bounds__(rp::THREADS) rope_append_kernel(const __grid_constant__ RopeParams p)
 {
-    const int t = blockIdx.x;
-    const int D = p.c.D, units = D / 16; // 16-element units of a head
-    // the sequence of this row: the first b with cu[b + 1] > t
-    bool store = p.table != nullptr;
-    int b = t;
-    int64_t newer = 1; // rows of the sequence from this one on
-    if (store && p.cu) {
-        b = 0;
-        for (int64_t i = threadIdx.x; i - threadIdx.x < p.B; i += rp::THREADS)
-            b += __syncthreads_count(i < p.B && p.cu[i + 1] <= t);
-        store = b < p.B && p.cu[b] <= t && p.cu[b + 1] > t; // offsets out of order cover no row
-        if (store)
-            newer = (int64_t)p.cu[b + 1] - t;
-    }
-    // the axes' positions
-    int32_t pos[3] = {0, 0, 0};
-    if (p.rot) {
-        bool ok = true;
-        for (int a = 0; a < 3; ++a)
-            if (a < p.axes) {
-                pos[a] = p.pos[(int64_t)a * p.pos_stride + t];
-                ok = ok && pos[a] >= 0 && pos[a] < p.max_pos;
-            }
-        if (!ok) {
-            if (threadIdx.x == 0)
-                report_fault(p.status, TDG_ERR_DEVICE, TDG_WHERE_POS, (uint32_t)t, p.epoch);
-            return;
-        }
-    }
-    uint8_t *kc = nullptr, *vc = nullptr; // head 0's slot in the cache
+    constexpr int UNITS = D / 16; // 16-element units of a head
     constexpr int ESZ = E4M3 ? 1 : 2;
-    if (store) {
-        const int64_t len = p.lens[b], at = len - newer;
-        const int64_t first = p.cu ? len - ((int64_t)p.cu[b + 1] - p.cu[b]) : at;
-        int32_t page = -1;
-        if (first >= 0 && at >= 0 && len <= p.table_entries << p.c.ps_log2)
-            page = p.table[b * p.table_stride + (at >> p.c.ps_log2)];
-        if (page < 0 || page >= p.c.all_pages) {
-            if (threadIdx.x == 0)
-                report_fault(p.status, TDG_ERR_DEVICE, TDG_WHERE_PAGE, (uint32_t)t, p.epoch);
-            store = false;
-        } else {
-            const int slot = (int)(at & ((1 << p.c.ps_log2) - 1));
-            uint8_t *base = p.c.regions + (uint64_t)(page / p.c.pages) * p.c.region_bytes +
-                            paged_row(p.c, page % p.c.pages, 0, slot, ESZ);
-            kc = base + p.c.k_off;
-            vc = base + p.c.v_off;
+    constexpr int LANES = rp::THREADS / UNITS;
+    __shared__ __align__(16) float turn[rp::MAX_ROWS][D]; // cosines, then sines, of a row's pairs
+    __shared__ uint8_t *slot_k[rp::MAX_ROWS], *slot_v[rp::MAX_ROWS]; // head 0's slot in the cache, or NULL
+    __shared__ int skip[rp::MAX_ROWS]; // a row with a position outside the table
+    __shared__ int seq[rp::MAX_ROWS];
+    griddep_launch_dependents();
+    griddep_wait();
+    const int64_t first = (int64_t)blockIdx.x * p.rows;
+    const int rows = (int)min((int64_t)p.rows, p.T - first);
+    // the sequence of each row: the first b with cu[b + 1] > t.  All threads
+    // scan cu at once; with offsets in order the rows' counts ascend.
+    if (p.table && p.cu) {
+        if (threadIdx.x < rp::MAX_ROWS)
+            seq[threadIdx.x] = 0;
+        __syncthreads();
+        int count[rp::MAX_ROWS] = {};
+        for (int64_t i = threadIdx.x; i < p.B; i += rp::THREADS) {
+            const int64_t end = p.cu[i + 1];
+#pragma unroll
+            for (int r = 0; r < rp::MAX_ROWS; ++r)
+                count[r] += end <= first + r ? 1 : 0;
+        }
+#pragma unroll
+        for (int r = 0; r < rp::MAX_ROWS; ++r) {
+            const int n = __reduce_add_sync(0xffffffffu, count[r]);
+            if (n && (threadIdx.x & 31) == 0)
+                atomicAdd(&seq[r], n);
+        }
+        __syncthreads();
+    }
+    if ((int)threadIdx.x < rows) {
+        const int r = threadIdx.x;
+        const int64_t t = first + r;
+        int bad = 0;
+        for (int a = 0; p.rot && a < p.axes; ++a) {
+            const int32_t pos = p.pos[(int64_t)a * p.pos_stride + t];
+            bad |= pos < 0 || pos >= p.max_pos ? 1 : 0;
+        }
+        if (bad)
+            report_fault(p.status, TDG_ERR_DEVICE, TDG_WHERE_POS, (uint32_t)t, p.epoch);
+        skip[r] = bad;
+        uint8_t *at_slot = nullptr;
+        if (p.table && !bad) {
+            const int64_t b = p.cu ? seq[r] : t;
+            int64_t lo = t, hi = t + 1; // the sequence's new rows
+            if (p.cu) {
+                lo = b < p.B ? p.cu[b] : t + 1;
+                hi = b < p.B ? p.cu[b + 1] : t + 1;
+            }
+            if (lo <= t && t < hi) { // else the row belongs to no sequence (or the offsets are out of order)
+                const int64_t len = p.lens[b], at = len - (hi - t);
+                int32_t page = -1;
+                if (len >= hi - lo && len <= p.table_entries << p.c.ps_log2)
+                    page = p.table[b * p.table_stride + (at >> p.c.ps_log2)];
+                if (page < 0 || page >= p.c.all_pages)
+                    report_fault(p.status, TDG_ERR_DEVICE, TDG_WHERE_PAGE, (uint32_t)t, p.epoch);
+                else
+                    at_slot = p.c.regions + (uint64_t)(page / p.c.pages) * p.c.region_bytes +
+                              paged_row(p.c, page % p.c.pages, 0, (int)(at & ((1 << p.c.ps_log2) - 1)), ESZ);
+            }
+        }
+        slot_k[r] = at_slot ? at_slot + p.c.k_off : nullptr;
+        slot_v[r] = at_slot ? at_slot + p.c.v_off : nullptr;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < rows * p.rot; i += rp::THREADS) {
+        const int r = i / p.rot, c = i % p.rot, pair = c < p.rot / 2 ? c : c - p.rot / 2;
+        if (!skip[r]) {
+            const int a = (pair >= p.sec0 ? 1 : 0) + (pair >= p.sec01 ? 1 : 0);
+            turn[r][c] = p.cos_sin[(int64_t)p.pos[(int64_t)a * p.pos_stride + first + r] * p.rot + c];
         }
     }
-    const uint64_t head_bytes = (uint64_t)(D * ESZ) << p.c.ps_log2; // from one head's slot to the next one's
+    __syncthreads();
 
-    const int u = threadIdx.x % units;       // this thread's unit in every head
+    const int u = threadIdx.x % UNITS; // this thread's unit in every head
     const bool turned = u * 16 < p.rot;
-    int lo, hi;                               // its two runs of 8 elements
-    if (INTER || !turned) {
-        lo = u * 16;
-        hi = lo + 8;
-    } else {
-        lo = u * 8;
-        hi = p.rot / 2 + u * 8;
+    // its two runs of 8 elements
+    const int lo = INTER || !turned ? u * 16 : u * 8;
+    const int hi = INTER || !turned ? lo + 8 : p.rot / 2 + u * 8;
+    const uint64_t head_bytes = (uint64_t)(D * ESZ) << p.c.ps_log2; // from one head's slot to the next one's
+    const int heads = p.Hq + 2 * p.c.Hkv, kv_end = p.Hq + p.c.Hkv;
+    const int pairs = rows * heads;
+    int r = 0, hh = threadIdx.x / UNITS;
+    while (hh >= heads) {
+        hh -= heads;
+        ++r;
     }
-    float cs[8], sn[8];
-    if (turned) {
+    for (int i = threadIdx.x / UNITS; i < pairs; i += rp::DEPTH * LANES) {
+        uint4 x4[rp::DEPTH], y4[rp::DEPTH];
+        int rr[rp::DEPTH], hd[rp::DEPTH];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int i = u * 8 + j;
-            const int a = (i >= p.sec0 ? 1 : 0) + (i >= p.sec01 ? 1 : 0);
-            const float *row = p.cos_sin + (int64_t)(a == 0 ? pos[0] : a == 1 ? pos[1] : pos[2]) * p.rot;
-            cs[j] = row[i];
-            sn[j] = row[p.rot / 2 + i];
-        }
-    }
-    const int heads = p.Hq + 2 * p.c.Hkv;
-    for (int hh = threadIdx.x / units; hh < heads; hh += rp::THREADS / units) {
-        const bool is_q = hh < p.Hq;
-        const bool is_v = hh >= p.Hq + p.c.Hkv;
-        const int h = is_q ? hh : is_v ? hh - p.Hq - p.c.Hkv : hh - p.Hq;
-        if (is_v && !store)
-            break;
-        const __nv_bfloat16 *src = (is_q ? p.q + (int64_t)t * p.qs : is_v ? p.v + (int64_t)t * p.vs : p.k + (int64_t)t * p.ks) + (int64_t)h * D;
-        float x[8], y[8];
-        unpack8(*reinterpret_cast<const uint4 *>(src + lo), x);
-        unpack8(*reinterpret_cast<const uint4 *>(src + hi), y);
-        if (turned && !is_v) {
-            if (INTER) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float a0 = x[2 * j], a1 = x[2 * j + 1], b0 = y[2 * j], b1 = y[2 * j + 1];
-                    x[2 * j] = cs[j] * a0 - sn[j] * a1;
-                    x[2 * j + 1] = cs[j] * a1 + sn[j] * a0;
-                    y[2 * j] = cs[j + 4] * b0 - sn[j + 4] * b1;
-                    y[2 * j + 1] = cs[j + 4] * b1 + sn[j + 4] * b0;
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float a = x[j], c = y[j];
-                    x[j] = cs[j] * a - sn[j] * c;
-                    y[j] = cs[j] * c + sn[j] * a;
-                }
+        for (int d = 0; d < rp::DEPTH; ++d) {
+            rr[d] = -1;
+            hd[d] = hh;
+            if (i + d * LANES < pairs && !skip[r] && (hh < kv_end || slot_v[r])) {
+                rr[d] = r;
+                const int64_t t = first + r;
+                const __nv_bfloat16 *src = hh < p.Hq ? p.q + t * p.qs + (int64_t)hh * D
+                                           : hh < kv_end ? p.k + t * p.ks + (int64_t)(hh - p.Hq) * D
+                                                         : p.v + t * p.vs + (int64_t)(hh - kv_end) * D;
+                x4[d] = ld_once(src + lo);
+                y4[d] = ld_once(src + hi);
+            }
+            hh += LANES;
+            while (hh >= heads) {
+                hh -= heads;
+                ++r;
             }
         }
-        if (!is_v) {
-            __nv_bfloat16 *dst = is_q ? p.q_out + (int64_t)t * p.qos : p.k_out ? p.k_out + (int64_t)t * p.kos : nullptr;
-            if (dst) {
-                *reinterpret_cast<uint4 *>(dst + (int64_t)h * D + lo) = pack8(x);
-                *reinterpret_cast<uint4 *>(dst + (int64_t)h * D + hi) = pack8(y);
+#pragma unroll
+        for (int d = 0; d < rp::DEPTH; ++d) {
+            if (rr[d] < 0)
+                continue;
+            const int row = rr[d], head = hd[d];
+            const bool is_v = head >= kv_end;
+            if (is_v && !E4M3) { // a copy
+                uint8_t *dst = slot_v[row] + (uint64_t)(head - kv_end) * head_bytes;
+                *reinterpret_cast<uint4 *>(dst + lo * 2) = x4[d];
+                *reinterpret_cast<uint4 *>(dst + hi * 2) = y4[d];
+                continue;
             }
-        }
-        if (!is_q && store) {
-            uint8_t *dst = (is_v ? vc : kc) + (uint64_t)h * head_bytes;
-            if (E4M3) {
-                const float scale = (is_v ? p.c.v_scale : p.c.k_scale)[h];
-                *reinterpret_cast<uint2 *>(dst + lo) = pack8_e4m3(x, scale);
-                *reinterpret_cast<uint2 *>(dst + hi) = pack8_e4m3(y, scale);
-            } else {
-                *reinterpret_cast<uint4 *>(dst + lo * 2) = pack8(x);
-                *reinterpret_cast<uint4 *>(dst + hi * 2) = pack8(y);
+            float x[8], y[8];
+            unpack8(x4[d], x);
+            unpack8(y4[d], y);
+            if (turned && !is_v) {
+                const float *cs = &turn[row][u * 8], *sn = &turn[row][p.rot / 2 + u * 8];
+                float c[8], s[8];
+#pragma unroll
+                for (int j = 0; j < 8; j += 4) {
+                    *reinterpret_cast<float4 *>(&c[j]) = *reinterpret_cast<const float4 *>(cs + j);
+                    *reinterpret_cast<float4 *>(&s[j]) = *reinterpret_cast<const float4 *>(sn + j);
+                }
+                if (INTER) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float a0 = x[2 * j], a1 = x[2 * j + 1], b0 = y[2 * j], b1 = y[2 * j + 1];
+                        x[2 * j] = c[j] * a0 - s[j] * a1;
+                        x[2 * j + 1] = c[j] * a1 + s[j] * a0;
+                        y[2 * j] = c[j + 4] * b0 - s[j + 4] * b1;
+                        y[2 * j + 1] = c[j + 4] * b1 + s[j + 4] * b0;
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float a = x[j], b = y[j];
+                        x[j] = c[j] * a - s[j] * b;
+                        y[j] = c[j] * b + s[j] * a;
+                    }
+                }
+                x4[d] = pack8(x);
+                y4[d] = pack8(y);
+            }
+            const int64_t t = first + row;
+            if (!is_v) {
+                __nv_bfloat16 *dst = head < p.Hq ? p.q_out + t * p.qos + (int64_t)head * D
+                                     : p.k_out   ? p.k_out + t * p.kos + (int64_t)(head - p.Hq) * D
+                                                 : nullptr;
+                if (dst) {
+                    *reinterpret_cast<uint4 *>(dst + lo) = x4[d];
+                    *reinterpret_cast<uint4 *>(dst + hi) = y4[d];
+                }
+            }
+            uint8_t *slot = is_v ? slot_v[row] : slot_k[row];
+            if (head >= p.Hq && slot) {
+                const int h = head - (is_v ? kv_end : p.Hq);
+                uint8_t *dst = slot + (uint64_t)h * head_bytes;
+                if (E4M3) {
+                    const float inv = 1.f / (is_v ? p.c.v_scale : p.c.k_scale)[h];
+                    *reinterpret_cast<uint2 *>(dst + lo) = pack8_e4m3(x, inv);
+                    *reinterpret_cast<uint2 *>(dst + hi) = pack8_e4m3(y, inv);
+                } else {
+                    *reinterpret_cast<uint4 *>(dst + lo * 2) = x4[d];
+                    *reinterpret_cast<uint4 *>(dst + hi * 2) = y4[d];
+                }
             }
         }
     }
@@ -182,6 +256,16 @@ __global__ void __launch_bounds__(rp::THREADS) rope_append_kernel(const __grid_c
 
 using namespace tdg;
 using namespace tdg_host;
+
+namespace {
+template <int D> const void *pick(bool inter, bool e4m3)
+{
+    return inter ? (e4m3 ? reinterpret_cast<const void *>(&rope_append_kernel<D, true, true>)
+                         : reinterpret_cast<const void *>(&rope_append_kernel<D, true, false>))
+                 : (e4m3 ? reinterpret_cast<const void *>(&rope_append_kernel<D, false, true>)
+                         : reinterpret_cast<const void *>(&rope_append_kernel<D, false, false>));
+}
+} // namespace
 
 extern "C" size_t tdg_paged_pool_bytes(int64_t pages, int page_size, int64_t Hkv, int64_t D, int kv_type)
 {
@@ -260,6 +344,7 @@ extern "C" int tdg_rope_append(tdg_symm *h, const tdg_rope_append_args *a, void 
     }
     p.status = h->status;
     p.epoch = next_epoch(h);
+    p.T = T;
     p.B = a->B;
     p.max_pos = a->max_pos;
     p.pos_stride = a->pos_stride;
@@ -285,12 +370,13 @@ extern "C" int tdg_rope_append(tdg_symm *h, const tdg_rope_append_args *a, void 
     p.cu = a->cu;
     p.table = a->table;
     p.lens = a->lens;
+    // rows of a group: up to 8, as long as that leaves every SM four CTAs
+    const int64_t rows = T / ((int64_t)h->sm_count * 4);
+    p.rows = (int)(rows < 1 ? 1 : rows > rp::MAX_ROWS ? rp::MAX_ROWS : rows);
     const bool e4m3 = a->table && a->cache.kv_type == TDG_KV_E4M3;
-    const void *fn = a->interleaved ? (e4m3 ? reinterpret_cast<const void *>(&rope_append_kernel<true, true>)
-                                            : reinterpret_cast<const void *>(&rope_append_kernel<true, false>))
-                                    : (e4m3 ? reinterpret_cast<const void *>(&rope_append_kernel<false, true>)
-                                            : reinterpret_cast<const void *>(&rope_append_kernel<false, false>));
+    const void *fn = D == 128 ? pick<128>(a->interleaved, e4m3) : pick<64>(a->interleaved, e4m3);
     void *args[] = {&p};
-    return cuda_err(launch(fn, dim3((unsigned)T), dim3(rp::THREADS), 0, static_cast<cudaStream_t>(stream), args, false),
+    return cuda_err(launch(fn, dim3((unsigned)((T + p.rows - 1) / p.rows)), dim3(rp::THREADS), 0,
+                           static_cast<cudaStream_t>(stream), args, false, 1, true),
                     "rope append launch");
 }
