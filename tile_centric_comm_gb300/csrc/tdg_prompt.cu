@@ -102,39 +102,55 @@ __device__ __forceinline__ int prompt_blocks(const PromptParams &p, const Prompt
     return hi > lo ? (prompt_limit(p, it, hi - 1) + pa::BN - 1) / pa::BN : 0;
 }
 
-// Shared-memory matrix descriptors (128-byte swizzle, 8 rows 1 KB apart) by
-// halves: the low word holds the address and the leading offset, the high word
-// is the same for all.  The steps' offsets are added inside the asm: added
-// outside, the compiler keeps every sum of the unrolled loops in a register.
+// The MMA warp runs its whole loop converged and the instructions themselves
+// are predicated on one elected lane: their operands then stay in uniform
+// registers.  (Issued from a branch that only one lane takes, each instruction
+// of 64 cycles' tensor work costs more than 64 cycles to issue.)
+// Shared-memory matrix descriptors (128-byte swizzle, 8 rows 1 KB apart) come
+// by halves: the low word holds the address and the leading offset, the high
+// word is the same for all.
 constexpr uint32_t SDESC_HI = (1024u >> 4) | 1u << 14 | 2u << 29;
 __device__ __forceinline__ uint32_t sdesc_lo(uint32_t saddr, uint32_t lbo) { return (saddr & 0x3FFFFu) >> 4 | (lbo >> 4) << 16; }
 
-// D[tmem] (+)= A[smem] B[smem], operands `off` 16-byte units behind a and b
-__device__ __forceinline__ void umma_ss(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t off, uint32_t idesc,
+__device__ __forceinline__ uint32_t elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r;
+}
+
+// D[tmem] (+)= A[smem] B[smem], by the lane with `leader`
+__device__ __forceinline__ void umma_ss(uint32_t leader, uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t idesc,
                                         uint32_t accumulate)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b32 x, y;\n\t.reg .b64 da, db;\n\t"
-        "setp.ne.b32 p, %5, 0;\n\t"
-        "add.u32 x, %1, %3;\n\tadd.u32 y, %2, %3;\n\t"
-        "mov.b64 da, {x, %6};\n\tmov.b64 db, {y, %6};\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, p;\n\t}" ::"r"(d_tmem),
-        "r"(a), "r"(b), "r"(off), "r"(idesc), "r"(accumulate), "r"(SDESC_HI)
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 da, db;\n\t"
+        "setp.ne.b32 e, %0, 0;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+        "mov.b64 da, {%2, %6};\n\tmov.b64 db, {%3, %6};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%1], da, db, %4, p;\n\t}" ::"r"(leader),
+        "r"(d_tmem), "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(SDESC_HI)
         : "memory");
 }
 
 // D[tmem] (+)= A[tmem] B[smem]
-__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b, uint32_t off, uint32_t idesc,
+__device__ __forceinline__ void umma_ts(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem, uint32_t b, uint32_t idesc,
                                         uint32_t accumulate)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b32 y;\n\t.reg .b64 db;\n\t"
-        "setp.ne.b32 p, %5, 0;\n\t"
-        "add.u32 y, %2, %3;\n\t"
-        "mov.b64 db, {y, %6};\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "r"(b), "r"(off), "r"(idesc), "r"(accumulate), "r"(SDESC_HI)
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 db;\n\t"
+        "setp.ne.b32 e, %0, 0;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+        "mov.b64 db, {%3, %6};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%1], [%2], db, %4, p;\n\t}" ::"r"(leader),
+        "r"(d_tmem), "r"(a_tmem), "r"(b), "r"(idesc), "r"(accumulate), "r"(SDESC_HI)
         : "memory");
+}
+
+__device__ __forceinline__ void umma_commit_if(uint32_t leader, uint64_t *bar)
+{
+    asm volatile("{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %0, 0;\n\t"
+                 "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%1];\n\t}" ::"r"(leader),
+                 "r"(smem_u32(bar))
+                 : "memory");
 }
 
 __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16])
@@ -546,111 +562,112 @@ __global__ void __launch_bounds__(pa::THREADS, 1)
             }
             __syncwarp();
         } else if (warp == pa::MMA_WARP) {
-            if (lane == 0) {
-                constexpr uint32_t idesc_s = idesc_bf16(128, pa::BN, 0), idesc_o = idesc_bf16(128, D, 1);
-                const uint32_t base = smem_u32(smem);
-                int slot = 0, stage = 0;
-                uint32_t slot_phase = 0, phase = 0, q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
-                // S_t = Q_t K^T: both K-major, 16 elements are 32 bytes, 64 are a half
-                auto qk = [&](int t, int st) {
-                    const uint32_t a = sdesc_lo(base + t * S::Q_BYTES, 16), b = sdesc_lo(base + S::OFF_KV + st * S::KV_BYTES, 16);
+            constexpr uint32_t idesc_s = idesc_bf16(128, pa::BN, 0), idesc_o = idesc_bf16(128, D, 1);
+            const uint32_t base = smem_u32(smem), leader = elect_one();
+            int slot = 0, stage = 0;
+            uint32_t slot_phase = 0, phase = 0, q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
+            // (all 512 columns of TMEM are this CTA's: they begin at column 0)
+            // S_t = Q_t K^T: both K-major, 16 elements are 32 bytes, 64 are a half
+            auto qk = [&](int t, int st) {
+                const uint32_t a = sdesc_lo(base + t * S::Q_BYTES, 16), b = sdesc_lo(base + S::OFF_KV + st * S::KV_BYTES, 16);
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k)
-                        umma_ss(tmem + t * 128, a, b, (k / 4) * 1024 + (k % 4) * 2, idesc_s, k != 0 ? 1u : 0u);
-                    umma_commit(&ctl->sfull[t]);
-                };
-                // O_t += P_t V: P_t is 64 columns of bf16 pairs over S_t; V is
-                // MN-major: halves of 64 dimensions 16 KB apart, 16 keys are 2 KB
-                auto pv = [&](int t, int st, bool first) {
-                    const uint32_t b = sdesc_lo(base + S::OFF_KV + st * S::KV_BYTES, 16384);
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t off = (k / 4) * 1024 + (k % 4) * 2;
+                    umma_ss(leader, t * 128, a + off, b + off, idesc_s, k != 0 ? 1u : 0u);
+                }
+                umma_commit_if(leader, &ctl->sfull[t]);
+            };
+            // O_t += P_t V: P_t is 64 columns of bf16 pairs over S_t; V is
+            // MN-major: halves of 64 dimensions 16 KB apart, 16 keys are 2 KB
+            auto pv = [&](int t, int st, bool first) {
+                const uint32_t b = sdesc_lo(base + S::OFF_KV + st * S::KV_BYTES, 16384);
 #pragma unroll
-                    for (int k = 0; k < pa::BN / 16; ++k)
-                        umma_ts(tmem + 256 + t * 128, tmem + t * 128 + k * 8, b, k * 128, idesc_o, !first || k != 0 ? 1u : 0u);
-                };
-                auto next = [&](int &st, uint32_t &ph) {
-                    if (++st == S::STAGES) {
-                        st = 0;
-                        ph ^= 1u;
-                    }
-                };
-                bool ok = true;
-                while (ok) {
-                    ok = wait(&ctl->ifull[slot], slot_phase, 20);
-                    if (!ok)
-                        break;
-                    const PromptItem it = ctl->item[slot];
+                for (int k = 0; k < pa::BN / 16; ++k)
+                    umma_ts(leader, 256 + t * 128, t * 128 + k * 8, b + k * 128, idesc_o, !first || k != 0 ? 1u : 0u);
+            };
+            auto next = [&](int &st, uint32_t &ph) {
+                if (++st == S::STAGES) {
+                    st = 0;
+                    ph ^= 1u;
+                }
+            };
+            auto all_wait = [&](uint64_t *b, uint32_t ph, uint32_t what) -> bool {
+                const bool ok = __all_sync(0xffffffffu, wait(b, ph, what));
+                tc_fence_after();
+                return ok;
+            };
+            bool ok = true;
+            while (ok) {
+                ok = all_wait(&ctl->ifull[slot], slot_phase, 20);
+                if (!ok)
+                    break;
+                const PromptItem it = ctl->item[slot];
+                __syncwarp();
+                if (lane == 0)
                     mbar_arrive(&ctl->iempty[slot]);
-                    if (++slot == pa::SLOTS) {
-                        slot = 0;
-                        slot_phase ^= 1u;
-                    }
-                    if (!it.valid)
-                        break;
-                    const int nb[2] = {prompt_blocks(p, it, 0), prompt_blocks(p, it, 1)};
-                    const int most = max(nb[0], nb[1]);
-                    if (!most)
-                        continue;
-                    ok = wait(&ctl->kvfull[stage], phase, 21);
+                if (++slot == pa::SLOTS) {
+                    slot = 0;
+                    slot_phase ^= 1u;
+                }
+                if (!__any_sync(0xffffffffu, it.valid))
+                    break;
+                const int nb[2] = {__reduce_max_sync(0xffffffffu, prompt_blocks(p, it, 0)),
+                                   __reduce_max_sync(0xffffffffu, prompt_blocks(p, it, 1))};
+                const int most = max(nb[0], nb[1]);
+                if (!most)
+                    continue;
+                ok = all_wait(&ctl->kvfull[stage], phase, 21);
 #pragma unroll
-                    for (int t = 0; t < 2; ++t)
-                        if (ok && nb[t]) {
-                            ok = wait(&ctl->qfull[t], q_phase[t], 22);
-                            if (!ok)
-                                break;
-                            q_phase[t] ^= 1u;
-                            tc_fence_after();
-                            qk(t, stage);
-                            if (nb[t] == 1)
-                                umma_commit(&ctl->qempty[t]);
-                        }
-                    if (!ok)
-                        break;
-                    umma_commit(&ctl->kvempty[stage]);
-                    next(stage, phase);
-                    for (int j = 0; j < most && ok; ++j) {
-                        const int vst = stage;
-                        const uint32_t vph = phase;
-                        next(stage, phase);
-                        const bool more = j + 1 < most; // there is a next block of keys: it is in `stage`
-                        ok = wait(&ctl->kvfull[vst], vph, 23);
-                        bool have_k = false;
-#pragma unroll
-                        for (int t = 0; t < 2; ++t)
-                            if (ok && j < nb[t]) {
-                                ok = wait(&ctl->pfull[t], p_phase[t], 24);
-                                if (!ok)
-                                    break;
-                                p_phase[t] ^= 1u;
-                                tc_fence_after();
-                                pv(t, vst, j == 0);
-                                if (j + 1 < nb[t]) {
-                                    if (!have_k) {
-                                        ok = wait(&ctl->kvfull[stage], phase, 25);
-                                        if (!ok)
-                                            break;
-                                        have_k = true;
-                                        tc_fence_after();
-                                    }
-                                    qk(t, stage);
-                                    if (j + 2 == nb[t])
-                                        umma_commit(&ctl->qempty[t]);
-                                } else {
-                                    umma_commit(&ctl->ofull[t]);
-                                }
-                            }
+                for (int t = 0; t < 2; ++t)
+                    if (ok && nb[t]) {
+                        ok = all_wait(&ctl->qfull[t], q_phase[t], 22);
                         if (!ok)
                             break;
-                        umma_commit(&ctl->kvempty[vst]);
-                        if (more) {
-                            umma_commit(&ctl->kvempty[stage]);
-                            next(stage, phase);
+                        q_phase[t] ^= 1u;
+                        qk(t, stage);
+                        if (nb[t] == 1)
+                            umma_commit_if(leader, &ctl->qempty[t]);
+                    }
+                if (!ok)
+                    break;
+                umma_commit_if(leader, &ctl->kvempty[stage]);
+                next(stage, phase);
+                for (int j = 0; j < most && ok; ++j) {
+                    const int vst = stage;
+                    const uint32_t vph = phase;
+                    next(stage, phase);
+                    const bool more = j + 1 < most; // there is a next block of keys: it is in `stage`
+                    ok = all_wait(&ctl->kvfull[vst], vph, 23);
+                    if (ok && more)
+                        ok = all_wait(&ctl->kvfull[stage], phase, 25);
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+                        if (ok && j < nb[t]) {
+                            ok = all_wait(&ctl->pfull[t], p_phase[t], 24);
+                            if (!ok)
+                                break;
+                            p_phase[t] ^= 1u;
+                            pv(t, vst, j == 0);
+                            if (j + 1 < nb[t]) {
+                                qk(t, stage);
+                                if (j + 2 == nb[t])
+                                    umma_commit_if(leader, &ctl->qempty[t]);
+                            } else {
+                                umma_commit_if(leader, &ctl->ofull[t]);
+                            }
                         }
+                    if (!ok)
+                        break;
+                    umma_commit_if(leader, &ctl->kvempty[vst]);
+                    if (more) {
+                        umma_commit_if(leader, &ctl->kvempty[stage]);
+                        next(stage, phase);
                     }
                 }
-                if (ctl->abort) { // every MMA issued finishes before TMEM is freed
-                    umma_commit(&ctl->drain);
-                    (void)mbar_wait(&ctl->drain, 0, tmo);
-                }
+            }
+            if (__any_sync(0xffffffffu, ctl->abort)) { // every MMA issued finishes before TMEM is freed
+                umma_commit_if(leader, &ctl->drain);
+                (void)mbar_wait(&ctl->drain, 0, tmo);
             }
             __syncwarp();
         }
