@@ -65,8 +65,9 @@ struct PromptItem {
 
 struct PromptCtl {
     uint64_t kvfull[8], kvempty[8], qfull[2], qempty[2], sfull[2], pfull[2], ofull[2];
-    uint64_t ifull[pa::SLOTS], iempty[pa::SLOTS], tail, drain;
+    uint64_t ifull[pa::SLOTS], iempty[pa::SLOTS], tail, drain, steal;
     PromptItem item[pa::SLOTS];
+    uint4 stolen;                      // answer to the request for a further item
     uint32_t tmem_base;
     volatile int abort;
     int issued;                        // ring fills issued
@@ -111,6 +112,31 @@ __device__ __forceinline__ int prompt_blocks(const PromptParams &p, const Prompt
 // word is the same for all.
 constexpr uint32_t SDESC_HI = (1024u >> 4) | 1u << 14 | 2u << 29;
 __device__ __forceinline__ uint32_t sdesc_lo(uint32_t saddr, uint32_t lbo) { return (saddr & 0x3FFFFu) >> 4 | (lbo >> 4) << 16; }
+
+// Items are CTAs of the grid: a running CTA takes over one that has not been
+// launched yet (cluster launch control), so every SM is busy until the items
+// run out, whatever they cost, and no counter in memory is needed.
+__device__ __forceinline__ void steal_request(uint4 *answer, uint64_t *bar)
+{
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                     smem_u32(answer)),
+                 "r"(smem_u32(bar))
+                 : "memory");
+}
+// the index of the CTA taken over, or -1 when none is left
+__device__ __forceinline__ int64_t steal_answer(const uint4 *answer)
+{
+    uint32_t ok, x;
+    asm volatile("{\n\t.reg .b128 r;\n\t.reg .pred p;\n\t"
+                 "ld.shared.b128 r, [%2];\n\t"
+                 "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+                 "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t}"
+                 : "=r"(ok), "=r"(x)
+                 : "r"(smem_u32(answer))
+                 : "memory");
+    return ok ? (int64_t)x : -1;
+}
 
 __device__ __forceinline__ uint32_t elect_one()
 {
@@ -221,6 +247,7 @@ __global__ void __launch_bounds__(pa::THREADS, 1)
         }
         mbar_init(&ctl->tail, 1);
         mbar_init(&ctl->drain, 1);
+        mbar_init(&ctl->steal, 1);
         ctl->abort = 0;
         ctl->issued = 0;
         fence_mbar_init();
@@ -451,12 +478,16 @@ __global__ void __launch_bounds__(pa::THREADS, 1)
             uint32_t slot_phase = 0, phase = 0, q_phase[2] = {0, 0}, tail_phase = 0;
             int issued = 0;
             bool ok = true;
-            for (uint32_t idx = blockIdx.x; ok; idx += gridDim.x) {
+            uint32_t steal_phase = 0;
+            int64_t idx = blockIdx.x;
+            while (true) {
                 PromptItem it;
-                it.valid = idx < items ? 1 : 0;
-                if (it.valid) {
+                it.valid = idx >= 0 && idx < items ? 1 : 0;
+                if (idx >= items) {
+                    it.Lq = it.Lk = it.t0 = 0; // the grid is an upper bound of the items: skip
+                } else if (it.valid) {
                     // the table entry: the last one whose first item is not behind
-                    const uint32_t unit = idx / (uint32_t)p.Hkv;
+                    const uint32_t unit = (uint32_t)idx / (uint32_t)p.Hkv;
                     int e = 0;
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
@@ -475,23 +506,31 @@ __global__ void __launch_bounds__(pa::THREADS, 1)
                     }
                     if (b == end) // only with offsets that cover rows again and again: nothing to do
                         it.Lq = it.Lk = n = left = 0;
-                    it.g = (int)(idx % (uint32_t)p.Hkv);
+                    it.g = (int)((uint32_t)idx % (uint32_t)p.Hkv);
                     it.t0 = max(0, n - 1 - left) * span; // the last tokens, which see the most, first
                 }
-                if (lane == 0) {
-                    ok = wait(&ctl->iempty[slot], slot_phase ^ 1u, 10);
-                    if (ok) {
-                        ctl->item[slot] = it;
-                        mbar_arrive(&ctl->ifull[slot]);
+                if (idx < items) { // the item, or the end
+                    if (lane == 0) {
+                        ok = wait(&ctl->iempty[slot], slot_phase ^ 1u, 10);
+                        if (ok) {
+                            ctl->item[slot] = it;
+                            mbar_arrive(&ctl->ifull[slot]);
+                        }
                     }
+                    ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+                    if (++slot == pa::SLOTS) {
+                        slot = 0;
+                        slot_phase ^= 1u;
+                    }
+                    if (!it.valid || !ok)
+                        break;
                 }
-                ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-                if (++slot == pa::SLOTS) {
-                    slot = 0;
-                    slot_phase ^= 1u;
+                // ask for the next item now, take the answer once this one's loads are under way
+                if (lane == 0) {
+                    fence_proxy_async_smem(); // the last answer has been read
+                    mbar_arrive_expect_tx(&ctl->steal, sizeof(uint4));
+                    steal_request(&ctl->stolen, &ctl->steal);
                 }
-                if (!it.valid || !ok)
-                    break;
                 const int nb0 = prompt_blocks(p, it, 0), nb1 = prompt_blocks(p, it, 1), nb = max(nb0, nb1);
                 if (lane == 0) {
                     for (int t = 0; t < 2 && ok; ++t)
@@ -549,6 +588,14 @@ __global__ void __launch_bounds__(pa::THREADS, 1)
                             phase ^= 1u;
                         }
                     }
+                // (also after a timeout: the answer must have landed before the CTA leaves)
+                const bool answered = wait(&ctl->steal, steal_phase, 14);
+                steal_phase ^= 1u;
+                ok = __all_sync(0xffffffffu, ok && answered);
+                if (!ok)
+                    break;
+                idx = steal_answer(&ctl->stolen);
+                __syncwarp();
             }
             if (lane == 0)
                 ctl->issued = issued;
@@ -742,7 +789,6 @@ extern "C" int tdg_prompt_attention(tdg_symm *h, const tdg_prompt_attention_args
     if (const cudaError_t e = set_smem(fn, smem); e != cudaSuccess)
         return cuda_err(e, "prompt attention smem");
     void *args[] = {&p, &qm, &km, &vm};
-    const unsigned ctas = (unsigned)(items < h->sm_count ? items : h->sm_count);
-    return cuda_err(launch(fn, dim3(ctas), dim3(pa::THREADS), smem, static_cast<cudaStream_t>(stream), args, false, 1, true),
+    return cuda_err(launch(fn, dim3((unsigned)items), dim3(pa::THREADS), smem, static_cast<cudaStream_t>(stream), args, false, 1, true),
                     "prompt attention launch");
 }
