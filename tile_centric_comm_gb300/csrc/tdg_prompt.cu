@@ -52,6 +52,7 @@ struct PromptParams {
     int64_t Tq, Tk, B, os;
     int Hq, Hkv, G, NT; // NT: tokens of a tile, 128 / G
     int causal;
+    int out32; // rows of out are 32-byte aligned
     float scale_log2;
     __nv_bfloat16 *out;
     float *lse;
@@ -196,6 +197,14 @@ __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)
                  : "r"(taddr));
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// 32 bytes in one store (32-byte aligned)
+__device__ __forceinline__ void st_global_32(void *p, const uint32_t *w)
+{
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
 
 // (a.x, a.y) * (b.x, b.y) + (c.x, c.y) in one instruction
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
@@ -454,18 +463,18 @@ __global__ void __launch_bounds__(pa::THREADS, 1)
                     tmem_ld_32x32b_x32(o_addr + c, o);
                     tmem_ld_wait();
                 }
-                if (mine)
+                uint32_t w[16];
 #pragma unroll
-                    for (int i = 0; i < 32; i += 8) {
-                        uint4 v = make_uint4(0, 0, 0, 0);
-                        if (sees) {
-                            v.x = pack_bf16x2(__uint_as_float(o[i]) * f, __uint_as_float(o[i + 1]) * f);
-                            v.y = pack_bf16x2(__uint_as_float(o[i + 2]) * f, __uint_as_float(o[i + 3]) * f);
-                            v.z = pack_bf16x2(__uint_as_float(o[i + 4]) * f, __uint_as_float(o[i + 5]) * f);
-                            v.w = pack_bf16x2(__uint_as_float(o[i + 6]) * f, __uint_as_float(o[i + 7]) * f);
-                        }
-                        *reinterpret_cast<uint4 *>(dst + c + i) = v;
-                    }
+                for (int i = 0; i < 16; ++i)
+                    w[i] = sees ? pack_bf16x2(__uint_as_float(o[2 * i]) * f, __uint_as_float(o[2 * i + 1]) * f) : 0u;
+                if (mine && p.out32) { // whole 32-byte sectors
+                    st_global_32(dst + c, w);
+                    st_global_32(dst + c + 16, w + 8);
+                } else if (mine) {
+#pragma unroll
+                    for (int i = 0; i < 16; i += 4)
+                        *reinterpret_cast<uint4 *>(dst + c + 2 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+                }
             }
             tc_fence_before(); // the next item's first product writes O after this tile's next pfull
             if (p.lse && mine)
@@ -773,6 +782,7 @@ extern "C" int tdg_prompt_attention(tdg_symm *h, const tdg_prompt_attention_args
     p.causal = a->causal;
     p.scale_log2 = (a->scale > 0.f ? a->scale : 1.0f / sqrtf((float)D)) * 1.4426950408889634f;
     p.out = static_cast<__nv_bfloat16 *>(a->out);
+    p.out32 = (reinterpret_cast<uintptr_t>(a->out) & 31u) == 0 && a->out_stride % 16 == 0;
     p.lse = a->lse;
     p.cu_q = a->cu_q;
     p.cu_k = a->cu_k;
