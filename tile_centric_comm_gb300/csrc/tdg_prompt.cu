@@ -20,6 +20,8 @@
 //   warps 10, 11    idle: they complete the warpgroup that gives registers up
 // TMEM holds S_0, S_1 (128 columns each) and O_0, O_1 (D each).  While the
 // softmax works on one tile, the tensor cores work on the other.
+#include <type_traits>
+
 #include "tdg_paged.cuh"
 
 namespace tdg {
@@ -39,7 +41,7 @@ template <int D> struct Shape {
     static constexpr int HALVES = D / 64;
     static constexpr int Q_BYTES = 128 * D * 2;
     static constexpr int KV_BYTES = BN * D * 2;
-    static constexpr int STAGES = D == 128 ? 5 : 8;
+    static constexpr int STAGES = 4; // an item takes 2 slots a block: it begins in slot 0 or 2
     static constexpr int OFF_KV = 2 * Q_BYTES;
     static constexpr int OFF_CTL = OFF_KV + STAGES * KV_BYTES;
 };
@@ -97,11 +99,15 @@ __device__ __forceinline__ int prompt_limit(const PromptParams &p, const PromptI
     return p.causal ? min(it.Lk, max(0, tok + it.Lk - it.Lq + 1)) : it.Lk;
 }
 
-// Key blocks of tile t (0 or 1): up to the last one its last token sees.
-__device__ __forceinline__ int prompt_blocks(const PromptParams &p, const PromptItem &it, int t)
+// Keys that the last token of tile t (0 or 1) sees: the tile's key blocks end there.
+__device__ __forceinline__ int prompt_most(const PromptParams &p, const PromptItem &it, int t)
 {
     const int lo = it.t0 + t * p.NT, hi = min(lo + p.NT, it.Lq);
-    return hi > lo ? (prompt_limit(p, it, hi - 1) + pa::BN - 1) / pa::BN : 0;
+    return hi > lo ? prompt_limit(p, it, hi - 1) : 0;
+}
+__device__ __forceinline__ int prompt_blocks(const PromptParams &p, const PromptItem &it, int t)
+{
+    return (prompt_most(p, it, t) + pa::BN - 1) / pa::BN;
 }
 
 // The MMA warp runs its whole loop converged and the instructions themselves
@@ -635,11 +641,28 @@ __global__ void __launch_bounds__(pa::THREADS, 1)
             };
             // O_t += P_t V: P_t is 64 columns of bf16 pairs over S_t; V is
             // MN-major: halves of 64 dimensions 16 KB apart, 16 keys are 2 KB
-            auto pv = [&](int t, int st, bool first) {
+            auto pv = [&](int t, int st, uint32_t first) {
                 const uint32_t b = sdesc_lo(base + S::OFF_KV + st * S::KV_BYTES, 16384);
 #pragma unroll
                 for (int k = 0; k < pa::BN / 16; ++k)
-                    umma_ts(leader, 256 + t * 128, t * 128 + k * 8, b + k * 128, idesc_o, !first || k != 0 ? 1u : 0u);
+                    umma_ts(leader, 256 + t * 128, t * 128 + k * 8, b + k * 128, idesc_o, k != 0 ? 1u : first ^ 1u);
+            };
+            // the same for the first `cols` keys of a block (a multiple of 16)
+            auto qk_part = [&](int t, int st, int cols) {
+                const uint32_t a = sdesc_lo(base + t * S::Q_BYTES, 16), b = sdesc_lo(base + S::OFF_KV + st * S::KV_BYTES, 16);
+                const uint32_t idesc = (idesc_s & ~(0x3Fu << 17)) | (uint32_t)(cols >> 3) << 17;
+#pragma unroll 1
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t off = (k / 4) * 1024 + (k % 4) * 2;
+                    umma_ss(leader, t * 128, a + off, b + off, idesc, k != 0 ? 1u : 0u);
+                }
+                umma_commit_if(leader, &ctl->sfull[t]);
+            };
+            auto pv_part = [&](int t, int st, uint32_t first, int cols) {
+                const uint32_t b = sdesc_lo(base + S::OFF_KV + st * S::KV_BYTES, 16384);
+#pragma unroll 1
+                for (int k = 0; k < cols / 16; ++k)
+                    umma_ts(leader, 256 + t * 128, t * 128 + k * 8, b + k * 128, idesc_o, k != 0 ? 1u : first ^ 1u);
             };
             auto next = [&](int &st, uint32_t &ph) {
                 if (++st == S::STAGES) {
@@ -667,8 +690,10 @@ __global__ void __launch_bounds__(pa::THREADS, 1)
                 }
                 if (!__any_sync(0xffffffffu, it.valid))
                     break;
-                const int nb[2] = {__reduce_max_sync(0xffffffffu, prompt_blocks(p, it, 0)),
-                                   __reduce_max_sync(0xffffffffu, prompt_blocks(p, it, 1))};
+                const int keys[2] = {__reduce_max_sync(0xffffffffu, prompt_most(p, it, 0)),
+                                     __reduce_max_sync(0xffffffffu, prompt_most(p, it, 1))};
+                const int nb[2] = {(keys[0] + pa::BN - 1) / pa::BN, (keys[1] + pa::BN - 1) / pa::BN};
+                auto cols = [&](int t, int j) -> int { return min(pa::BN, (keys[t] - j * pa::BN + 15) & ~15); };
                 const int most = max(nb[0], nb[1]);
                 if (!most)
                     continue;
@@ -680,7 +705,7 @@ __global__ void __launch_bounds__(pa::THREADS, 1)
                         if (!ok)
                             break;
                         q_phase[t] ^= 1u;
-                        qk(t, stage);
+                        qk_part(t, stage, cols(t, 0));
                         if (nb[t] == 1)
                             umma_commit_if(leader, &ctl->qempty[t]);
                     }
@@ -688,7 +713,8 @@ __global__ void __launch_bounds__(pa::THREADS, 1)
                     break;
                 umma_commit_if(leader, &ctl->kvempty[stage]);
                 next(stage, phase);
-                for (int j = 0; j < most && ok; ++j) {
+                // any block: what the tiles need of it
+                auto any_block = [&](int j) {
                     const int vst = stage;
                     const uint32_t vph = phase;
                     next(stage, phase);
@@ -703,9 +729,9 @@ __global__ void __launch_bounds__(pa::THREADS, 1)
                             if (!ok)
                                 break;
                             p_phase[t] ^= 1u;
-                            pv(t, vst, j == 0);
+                            pv_part(t, vst, j == 0 ? 1u : 0u, cols(t, j));
                             if (j + 1 < nb[t]) {
-                                qk(t, stage);
+                                qk_part(t, stage, cols(t, j + 1));
                                 if (j + 2 == nb[t])
                                     umma_commit_if(leader, &ctl->qempty[t]);
                             } else {
@@ -713,13 +739,46 @@ __global__ void __launch_bounds__(pa::THREADS, 1)
                             }
                         }
                     if (!ok)
-                        break;
+                        return;
                     umma_commit_if(leader, &ctl->kvempty[vst]);
                     if (more) {
                         umma_commit_if(leader, &ctl->kvempty[stage]);
                         next(stage, phase);
                     }
-                }
+                };
+                // a block followed by two more of both tiles, its values in slot V
+                // and the next keys in the slot behind: no conditions between the
+                // instructions, and every descriptor and barrier a constant
+                auto whole_block = [&](auto vslot, int j) {
+                    constexpr int V = decltype(vslot)::value, K = (V + 1) % S::STAGES;
+                    const uint32_t vph = phase, kph = phase ^ (K == 0 ? 1u : 0u);
+                    ok = all_wait(&ctl->kvfull[V], vph, 23) && all_wait(&ctl->kvfull[K], kph, 25) &&
+                         all_wait(&ctl->pfull[0], p_phase[0], 24);
+                    if (!ok)
+                        return;
+                    pv(0, V, j == 0 ? 1u : 0u);
+                    qk(0, K);
+                    ok = all_wait(&ctl->pfull[1], p_phase[1], 24);
+                    if (!ok)
+                        return;
+                    pv(1, V, j == 0 ? 1u : 0u);
+                    qk(1, K);
+                    umma_commit_if(leader, &ctl->kvempty[V]);
+                    umma_commit_if(leader, &ctl->kvempty[K]);
+                    p_phase[0] ^= 1u;
+                    p_phase[1] ^= 1u;
+                    stage = (V + 2) % S::STAGES;
+                    phase = kph;
+                };
+                int j = 0;
+                const int both = min(nb[0], nb[1]) - 2;
+                for (; ok && j < both; ++j)
+                    if (stage == 1)
+                        whole_block(std::integral_constant<int, 1>{}, j);
+                    else
+                        whole_block(std::integral_constant<int, 3>{}, j);
+                for (; ok && j < most; ++j)
+                    any_block(j);
             }
             if (__any_sync(0xffffffffu, ctl->abort)) { // every MMA issued finishes before TMEM is freed
                 umma_commit_if(leader, &ctl->drain);
