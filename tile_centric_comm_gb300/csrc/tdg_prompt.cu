@@ -400,30 +400,9 @@ __global__ void __launch_bounds__(pa::THREADS, 1)
                     for (int i = 0; i < 4; ++i)
                         mx[i] = fmaxf(mx[i], __uint_as_float(s[i][c]));
                 const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                if (j == 0) {
-                    m = top;
-                } else {
-                    const bool grown = (top - m) * p.scale_log2 > 8.f; // also from -inf
-                    if (__any_sync(0xffffffffu, grown)) {
-                        const float al = grown ? exp2_approx((m - top) * p.scale_log2) : 1.f;
-                        if (grown) {
-                            m = top;
-                            l *= al;
-                        }
-                        // the block before has left the tensor cores: its
-                        // product was issued ahead of this block's scores
-#pragma unroll
-                        for (int c = 0; c < D; c += 16) {
-                            uint32_t o[16];
-                            tmem_ld_32x32b_x16(o_addr + c, o);
-                            tmem_ld_wait();
-#pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
-                            tmem_st_32x32b_x16(o_addr + c, o);
-                        }
-                    }
-                }
+                const bool grown = j > 0 && (top - m) * p.scale_log2 > 8.f; // also from -inf
+                const float al = grown ? exp2_approx((m - top) * p.scale_log2) : 1.f;
+                m = j == 0 || grown ? top : m;
                 const float ms = m == -INFINITY ? 0.f : m * p.scale_log2;
                 const float2 c2 = make_float2(p.scale_log2, p.scale_log2), m2 = make_float2(-ms, -ms);
                 float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
@@ -438,6 +417,22 @@ __global__ void __launch_bounds__(pa::THREADS, 1)
                         w[i] = pack_bf16x2(e.x, e.y);
                     }
                     tmem_st_32x32b_x16(s_addr + c * 16, w);
+                }
+                // O follows a new m only now, off the weights' path.  The block
+                // before has left the tensor cores: its product was issued ahead
+                // of this block's scores.
+                if (__any_sync(0xffffffffu, grown)) {
+                    l *= al;
+#pragma unroll
+                    for (int c = 0; c < D; c += 16) {
+                        uint32_t o[16];
+                        tmem_ld_32x32b_x16(o_addr + c, o);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
+                        tmem_st_32x32b_x16(o_addr + c, o);
+                    }
                 }
                 tmem_st_wait();
                 tc_fence_before();
