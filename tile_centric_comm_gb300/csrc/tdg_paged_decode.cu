@@ -13,14 +13,16 @@
 // Hq/Hkv query heads of a key head are the 16 rows of mma.sync (m16n8k16), so
 // a page is read once for all of them.
 //
-// Split: the (sequence, key head) pairs' 64-token tiles form one long line, and
+// Split: the (sequence, key head) pairs' tiles (64 tokens; 128 of an 8-bit
+// cache) form one long line, and
 // each of the two CTAs per SM takes an equal run of it, wherever it begins and
 // ends: ragged lengths leave no SM idle, and the partial results are at most
 // two per CTA whatever the lengths.  A second launch joins the split pairs.
 //
-// In a CTA, warp 4 looks up page ids and issues one TMA copy per page (or 64
-// tokens of one) for K and for V into a ring of stages; warps 0-3 each take 16
-// tokens of every tile.  The 5-D tensor map (64-token box, both 128-byte halves
+// In a CTA, warp 4 looks up page ids and issues one TMA copy per page (or
+// tile) for K and for V into a ring of stages; warps 0-3 each take 16
+// tokens of every tile (32 of an 8-bit cache: two chains of work to interleave).  The 5-D tensor map (one box is a tile's
+// tokens of the page, both 128-byte halves
 // of a 256-byte row in one copy) writes the 128-byte-swizzled layout that
 // ldmatrix reads without bank conflicts.
 #include <cuda_fp16.h>
@@ -32,7 +34,6 @@ namespace tdg {
 namespace pd {
 constexpr int WARPS = 4;                      // consumer warps
 constexpr int THREADS = WARPS * 32 + 32;
-constexpr int TILE = 64;                      // tokens of a tile
 constexpr int MAX_CTAS = 512;                 // CTAs whose partial results the caller provides room for
 constexpr int ROWS = 16;                      // query heads of a partial result
 constexpr int JOIN_ROWS = 4;                  // rows of a join CTA
@@ -41,10 +42,12 @@ constexpr int BAR_BYTES = 384;
 
 template <int D, bool E4M3> struct Shape {
     static constexpr int ESZ = E4M3 ? 1 : 2;
+    static constexpr int NG = E4M3 ? 2 : 1;                   // groups of 16 tokens that a warp takes at once
+    static constexpr int TILE = WARPS * NG * 16;              // tokens of a tile
     static constexpr int RB = D * ESZ < 128 ? D * ESZ : 128; // bytes of a block's row
     static constexpr int NB = D * ESZ / RB;                   // blocks of a token's row
     static constexpr int KV = TILE * D * ESZ;                 // bytes of a tile of K or of V
-    static constexpr int STAGES = KV >= 16384 ? 3 : KV >= 8192 ? 6 : 8;
+    static constexpr int STAGES = KV >= 16384 ? 3 : 6;
     static constexpr int Q_BYTES = ROWS * D * 2;
     static constexpr int OFF_Q = STAGES * 2 * KV;
     static constexpr int OFF_MERGE = OFF_Q + 2 * Q_BYTES;
@@ -52,7 +55,8 @@ template <int D, bool E4M3> struct Shape {
     static constexpr int OFF_BAR = OFF_ML + WARPS * ROWS * 2 * 4;
     static constexpr int SMEM = OFF_BAR + BAR_BYTES;
 };
-static_assert(2 * (Shape<128, false>::SMEM + 1024) <= 228 * 1024, "two CTAs per SM");
+static_assert(2 * (Shape<128, false>::SMEM + 1024) <= 228 * 1024 && 2 * (Shape<128, true>::SMEM + 1024) <= 228 * 1024,
+              "two CTAs per SM");
 } // namespace pd
 
 struct PagedDecodeParams {
@@ -155,10 +159,10 @@ __device__ __forceinline__ int pd_exponent(float top)
 __device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
 // tiles of sequence b; a length that does not fit the table counts as none
-__device__ __forceinline__ int pd_tiles(const PagedDecodeParams &p, int64_t b)
+template <int TILE> __device__ __forceinline__ int pd_tiles(const PagedDecodeParams &p, int64_t b)
 {
     const int64_t len = p.lens[b];
-    return len <= 0 || len > p.table_entries << p.c.ps_log2 ? 0 : (int)((len + pd::TILE - 1) / pd::TILE);
+    return len <= 0 || len > p.table_entries << p.c.ps_log2 ? 0 : (int)((len + TILE - 1) / TILE);
 }
 
 // the first CTA whose run holds unit u, given total = base * ctas + rem
@@ -167,123 +171,151 @@ __device__ __forceinline__ int pd_owner(int64_t u, int64_t base, int64_t rem)
     return (int)(u < rem * (base + 1) ? u / (base + 1) : rem + (u - rem * (base + 1)) / base);
 }
 
-// Scores, softmax update and output update of this warp's 16 tokens.  valid:
-// tokens of them that exist (16 unless TAIL); k and v: shared addresses of the
-// group's rows; blk: bytes between a row's 128-byte blocks.
+// Scores, softmax update and output update of this warp's NG groups of 16
+// tokens of a tile.  valid: tokens of them that exist (all unless TAIL); at:
+// shared addresses of the groups' key rows, the value rows S::KV behind; blk:
+// bytes between a row's 128-byte blocks.
 template <int D, bool E4M3, bool TAIL, class WaitV>
-__device__ __forceinline__ void pd_group(const uint32_t (&qa)[D / 16][4], float mul0, float mul1, uint32_t k, uint32_t v,
-                                         uint32_t blk, int valid, int lane, float (&m)[2], float (&l)[2],
-                                         float (&o)[D / 8][4], WaitV &&wait_v)
+__device__ __forceinline__ void pd_group(const uint32_t (&qa)[D / 16][4], const float (&mul)[2],
+                                         const uint32_t (&at)[pd::Shape<D, E4M3>::NG], uint32_t blk, int valid, int lane,
+                                         float (&m)[2], float (&l)[2], float (&o)[D / 8][4], WaitV &&wait_v)
 {
     using S = pd::Shape<D, E4M3>;
+    constexpr int NG = S::NG;
     const int tig = lane & 3, mi = lane >> 3, ri = lane & 7;
-    float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+    float s[NG][2][4];
     auto swz = [](int row) -> uint32_t { return S::RB == 128 ? (uint32_t)(row & 7) << 4 : (uint32_t)((row >> 1) & 3) << 4; };
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            s[g][i / 4][i % 4] = 0.f;
     if constexpr (!E4M3) {
         const int tok = (mi >> 1) * 8 + ri;
-        const uint32_t row = k + tok * S::RB, x = swz(tok) ^ ((mi & 1) * 16);
+        const uint32_t row = tok * S::RB, x = swz(tok) ^ ((mi & 1) * 16);
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-            uint32_t b[4];
-            pd_ldsm4(row + (ks / 4) * blk + (x ^ ((ks % 4) * 32)), b);
-            pd_mma<false>(s[0], qa[ks], b[0], b[1]);
-            pd_mma<false>(s[1], qa[ks], b[2], b[3]);
-        }
+        for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                uint32_t b[4];
+                pd_ldsm4(at[g] + row + (ks / 4) * blk + (x ^ ((ks % 4) * 32)), b);
+                pd_mma<false>(s[g][0], qa[ks], b[0], b[1]);
+                pd_mma<false>(s[g][1], qa[ks], b[2], b[3]);
+            }
     } else {
         // a lane's four bytes are four neighbouring dimensions of one token;
         // the query's fragments are laid out in the same order
         const int tok = (mi & 1) * 8 + ri;
-        const uint32_t row = k + tok * S::RB, x = swz(tok) ^ ((mi >> 1) * 16);
+        const uint32_t row = tok * S::RB, x = swz(tok) ^ ((mi >> 1) * 16);
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ks += 2) {
-            uint32_t b[4];
-            pd_ldsm4(row + (x ^ (ks * 16)), b);
-            pd_mma<true>(s[0], qa[ks], e4m3x2_lo(b[0]), e4m3x2_hi(b[0]));
-            pd_mma<true>(s[1], qa[ks], e4m3x2_lo(b[1]), e4m3x2_hi(b[1]));
-            pd_mma<true>(s[0], qa[ks + 1], e4m3x2_lo(b[2]), e4m3x2_hi(b[2]));
-            pd_mma<true>(s[1], qa[ks + 1], e4m3x2_lo(b[3]), e4m3x2_hi(b[3]));
-        }
+        for (int ks = 0; ks < D / 16; ks += 2)
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                uint32_t b[4];
+                pd_ldsm4(at[g] + row + (x ^ (ks * 16)), b);
+                pd_mma<true>(s[g][0], qa[ks], e4m3x2_lo(b[0]), e4m3x2_hi(b[0]));
+                pd_mma<true>(s[g][1], qa[ks], e4m3x2_lo(b[1]), e4m3x2_hi(b[1]));
+                pd_mma<true>(s[g][0], qa[ks + 1], e4m3x2_lo(b[2]), e4m3x2_hi(b[2]));
+                pd_mma<true>(s[g][1], qa[ks + 1], e4m3x2_lo(b[3]), e4m3x2_hi(b[3]));
+            }
     }
     // base-2 scores; tokens behind the length weigh nothing, whatever their key holds
 #pragma unroll
-    for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            s[nt][c] *= c < 2 ? mul0 : mul1;
-            if (TAIL && nt * 8 + tig * 2 + (c & 1) >= valid)
-                s[nt][c] = -INFINITY;
-        }
-    float al[2];
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        float mx = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const float mn = fmaxf(m[r], mx), ms = mn == -INFINITY ? 0.f : mn;
-        al[r] = exp2_approx(m[r] - ms);
-        m[r] = mn;
-        float sum = 0.f;
+    for (int g = 0; g < NG; ++g)
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                s[nt][2 * r + c] = exp2_approx(s[nt][2 * r + c] - ms);
-                sum += s[nt][2 * r + c];
+            for (int c = 0; c < 4; ++c) {
+                s[g][nt][c] *= mul[c / 2];
+                if (TAIL && g * 16 + nt * 8 + tig * 2 + (c & 1) >= valid)
+                    s[g][nt][c] = -INFINITY;
             }
+    // m follows the row's true maximum only when that has grown by more than 8
+    // (a factor of 256), so the output is rarely rescaled; weights stay below
+    // 2^8, and any m serves the sums as well as another
+    bool grown = false;
+    float al[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        float mx = -INFINITY;
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+            mx = fmaxf(mx, fmaxf(fmaxf(s[g][0][2 * r], s[g][0][2 * r + 1]), fmaxf(s[g][1][2 * r], s[g][1][2 * r + 1])));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const bool up = mx - m[r] > 8.f; // also from -inf
+        al[r] = up ? exp2_approx(m[r] - mx) : 1.f;
+        m[r] = up ? mx : m[r];
+        grown = grown || up;
+        const float ms = m[r] == -INFINITY ? 0.f : m[r];
+        float sum = 0.f;
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    s[g][nt][2 * r + c] = exp2_approx(s[g][nt][2 * r + c] - ms);
+                    sum += s[g][nt][2 * r + c];
+                }
         l[r] = l[r] * al[r] + sum; // this lane's share; the four lanes of a row are added at the end
     }
+    if (__any_sync(0xffffffffu, grown))
 #pragma unroll
-    for (int n = 0; n < D / 8; ++n) {
-        o[n][0] *= al[0];
-        o[n][1] *= al[0];
-        o[n][2] *= al[1];
-        o[n][3] *= al[1];
-    }
-    // bf16 for an 8-bit cache too: f16 is finer, but it loses weights below
-    // 2^-24 of the largest, which carry an output whose heavy tokens hold 0
-    const uint32_t pa[4] = {pack_bf16x2(s[0][0], s[0][1]), pack_bf16x2(s[0][2], s[0][3]),
-                            pack_bf16x2(s[1][0], s[1][1]), pack_bf16x2(s[1][2], s[1][3])};
-    // a register of V holds tokens 2 tig, 2 tig + 1 (+ 8); those behind the
-    // length are cleared, since 0 times infinity or NaN is not 0
-    uint32_t keep[2] = {~0u, ~0u};
-    if (TAIL)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int t = i * 8 + tig * 2;
-            keep[i] = (t < valid ? 0x0000FFFFu : 0u) | (t + 1 < valid ? 0xFFFF0000u : 0u);
+        for (int n = 0; n < D / 8; ++n) {
+            o[n][0] *= al[0];
+            o[n][1] *= al[0];
+            o[n][2] *= al[1];
+            o[n][3] *= al[1];
         }
     wait_v();
     const int vtok = (mi & 1) * 8 + ri;
-    const uint32_t vrow = v + vtok * S::RB, vx = swz(vtok) ^ ((mi >> 1) * 16);
-    if constexpr (!E4M3) {
+    const uint32_t vrow = S::KV + vtok * S::RB, vx = swz(vtok) ^ ((mi >> 1) * 16);
 #pragma unroll
-        for (int nd = 0; nd < D / 8; nd += 2) {
-            uint32_t b[4];
-            pd_ldsm4_t(vrow + (nd / 8) * blk + (vx ^ ((nd % 8) * 16)), b);
-            if (TAIL) {
-                b[0] &= keep[0];
-                b[1] &= keep[1];
-                b[2] &= keep[0];
-                b[3] &= keep[1];
-            }
-            pd_mma<false>(o[nd], pa, b[0], b[1]);
-            pd_mma<false>(o[nd + 1], pa, b[2], b[3]);
-        }
-    } else {
-        // 16 dimensions per matrix; a register holds two neighbouring
-        // dimensions of two tokens, sorted into one product of the even
-        // dimensions and one of the odd
-#pragma unroll
-        for (int j = 0; j < D / 16; j += 2) {
-            uint32_t b[4];
-            pd_ldsm4_t(vrow + (vx ^ (j * 16)), b);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                b[i] = __byte_perm(TAIL ? b[i] & keep[i & 1] : b[i], 0u, 0x3120);
+    for (int g = 0; g < NG; ++g) {
+        // bf16 for an 8-bit cache too: f16 is finer, but it loses weights below
+        // 2^-24 of the largest, which carry an output whose heavy tokens hold 0
+        const uint32_t pa[4] = {pack_bf16x2(s[g][0][0], s[g][0][1]), pack_bf16x2(s[g][0][2], s[g][0][3]),
+                                pack_bf16x2(s[g][1][0], s[g][1][1]), pack_bf16x2(s[g][1][2], s[g][1][3])};
+        // a register of V holds tokens 2 tig, 2 tig + 1 (+ 8); those behind the
+        // length are cleared, since 0 times infinity or NaN is not 0
+        uint32_t keep[2] = {~0u, ~0u};
+        if (TAIL)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                pd_mma<false>(o[2 * (j + i)], pa, f16x2_bf16x2(e4m3x2_lo(b[2 * i])), f16x2_bf16x2(e4m3x2_lo(b[2 * i + 1])));
-                pd_mma<false>(o[2 * (j + i) + 1], pa, f16x2_bf16x2(e4m3x2_hi(b[2 * i])), f16x2_bf16x2(e4m3x2_hi(b[2 * i + 1])));
+                const int t = g * 16 + i * 8 + tig * 2;
+                keep[i] = (t < valid ? 0x0000FFFFu : 0u) | (t + 1 < valid ? 0xFFFF0000u : 0u);
+            }
+        if constexpr (!E4M3) {
+#pragma unroll
+            for (int nd = 0; nd < D / 8; nd += 2) {
+                uint32_t b[4];
+                pd_ldsm4_t(at[g] + vrow + (nd / 8) * blk + (vx ^ ((nd % 8) * 16)), b);
+                if (TAIL) {
+                    b[0] &= keep[0];
+                    b[1] &= keep[1];
+                    b[2] &= keep[0];
+                    b[3] &= keep[1];
+                }
+                pd_mma<false>(o[nd], pa, b[0], b[1]);
+                pd_mma<false>(o[nd + 1], pa, b[2], b[3]);
+            }
+        } else {
+            // 16 dimensions per matrix; a register holds two neighbouring
+            // dimensions of two tokens, sorted into one product of the even
+            // dimensions and one of the odd
+#pragma unroll
+            for (int j = 0; j < D / 16; j += 2) {
+                uint32_t b[4];
+                pd_ldsm4_t(at[g] + vrow + (vx ^ (j * 16)), b);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    b[i] = __byte_perm(TAIL ? b[i] & keep[i & 1] : b[i], 0u, 0x3120);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    pd_mma<false>(o[2 * (j + i)], pa, f16x2_bf16x2(e4m3x2_lo(b[2 * i])), f16x2_bf16x2(e4m3x2_lo(b[2 * i + 1])));
+                    pd_mma<false>(o[2 * (j + i) + 1], pa, f16x2_bf16x2(e4m3x2_hi(b[2 * i])), f16x2_bf16x2(e4m3x2_hi(b[2 * i + 1])));
+                }
             }
         }
     }
@@ -324,7 +356,7 @@ __global__ void __launch_bounds__(pd::THREADS, 2)
     const int64_t b_lo = min((int64_t)threadIdx.x * per, p.B), b_hi = min(b_lo + per, p.B);
     int64_t mine = 0;
     for (int64_t b = b_lo; b < b_hi; ++b)
-        mine += pd_tiles(p, b);
+        mine += pd_tiles<S::TILE>(p, b);
     int64_t upto = mine;
     for (int d = 1; d < 32; d <<= 1) {
         const int64_t x = __shfl_up_sync(0xffffffffu, upto, d);
@@ -335,7 +367,7 @@ __global__ void __launch_bounds__(pd::THREADS, 2)
         bar->sums[warp] = upto;
     // sequences without tokens (and those of a bad length) are nobody's run
     for (int64_t b = blockIdx.x; b < p.B; b += gridDim.x)
-        if (pd_tiles(p, b) == 0) {
+        if (pd_tiles<S::TILE>(p, b) == 0) {
             if (p.lens[b] != 0 && threadIdx.x == 0)
                 report_fault(p.status, TDG_ERR_DEVICE, TDG_WHERE_PAGE, (uint32_t)b, p.epoch);
             for (int i = threadIdx.x; i < p.Hq * D / 8; i += pd::THREADS)
@@ -358,7 +390,7 @@ __global__ void __launch_bounds__(pd::THREADS, 2)
         int64_t at = u0 - (upto - mine) * pairs;
         PdWalk w;
         for (w.b = b_lo;; ++w.b) {
-            w.tiles = pd_tiles(p, w.b);
+            w.tiles = pd_tiles<S::TILE>(p, w.b);
             if (at < (int64_t)w.tiles * pairs)
                 break;
             at -= (int64_t)w.tiles * pairs;
@@ -381,19 +413,19 @@ __global__ void __launch_bounds__(pd::THREADS, 2)
         if (++x.hg == pairs) {
             x.hg = 0;
             do {
-                x.tiles = pd_tiles(p, ++x.b);
+                x.tiles = pd_tiles<S::TILE>(p, ++x.b);
             } while (x.tiles == 0);
         }
     };
 
     if (warp == pd::WARPS) {
         // ---- loads: a chunk is up to 32 copies of one pair, their page ids one per lane ----
-        const int per_tile = pd::TILE / p.box;               // copies of a tile
+        const int per_tile = S::TILE / p.box;               // copies of a tile
         const int shift = p.c.ps_log2;
         const int box_log2 = 31 - __clz(p.box);
         const uint32_t copy_bytes = (uint32_t)p.box * D * S::ESZ;
         auto chunk_ids = [&](const PdWalk &x, int tiles) -> int32_t {
-            const int64_t tok = (int64_t)x.tile * pd::TILE + ((int64_t)lane << box_log2);
+            const int64_t tok = (int64_t)x.tile * S::TILE + ((int64_t)lane << box_log2);
             if (lane >= tiles * per_tile || tok >= p.lens[x.b])
                 return 0;
             const int32_t id = p.table[x.b * p.table_stride + (tok >> shift)];
@@ -436,7 +468,7 @@ __global__ void __launch_bounds__(pd::THREADS, 2)
             }
             dead = __shfl_sync(0xffffffffu, dead ? 1 : 0, 0) != 0;
             for (int i = 0; i < n && !dead; ++i) {
-                const int64_t t0 = (int64_t)(w.tile + i) * pd::TILE;
+                const int64_t t0 = (int64_t)(w.tile + i) * S::TILE;
                 const int copies = (int)min((int64_t)per_tile, (len - t0 + p.box - 1) >> box_log2);
                 if (lane == 0) {
                     if (!mbar_wait(&bar->empty[stage], phase ^ 1u, p.timeout_ns)) {
@@ -490,8 +522,11 @@ __global__ void __launch_bounds__(pd::THREADS, 2)
     const uint32_t ring = smem_u32(smem);
     const uint32_t blk = (uint32_t)p.box * S::RB;
     // this warp's rows of a tile: which copy, and where in it
-    const int first = warp * 16;
-    const uint32_t group_off = (uint32_t)(first / p.box) * (p.box * D * S::ESZ) + (uint32_t)(first % p.box) * S::RB;
+    const int first = warp * S::NG * 16;
+    uint32_t group_off[S::NG];
+#pragma unroll
+    for (int i = 0; i < S::NG; ++i)
+        group_off[i] = (uint32_t)((first + i * 16) / p.box) * (p.box * D * S::ESZ) + (uint32_t)((first + i * 16) % p.box) * S::RB;
     int stage = 0, pair = 0;
     uint32_t phase = 0;
     bool dead = false; // a wait ran out: wait no more, run on to the end (the call has reported it)
@@ -514,7 +549,7 @@ __global__ void __launch_bounds__(pd::THREADS, 2)
         const int qb = pair & 1;
         wait(&bar->qfull[qb], (pair >> 1) & 1, 2);
         uint32_t qa[D / 16][4];
-        float mul0 = p.scale_log2, mul1 = p.scale_log2;
+        float mul[2] = {p.scale_log2, p.scale_log2};
         const uint8_t *qs = smem + S::OFF_Q + qb * S::Q_BYTES;
         if constexpr (!E4M3) {
 #pragma unroll
@@ -552,8 +587,8 @@ __global__ void __launch_bounds__(pd::THREADS, 2)
                     qa[ks][2 + r] = pack_f16x2(x[r][ks][2] * f, x[r][ks][3] * f);
                 }
             const float ks = p.c.k_scale[g];
-            mul0 *= ks * pow2i(e[0]);
-            mul1 *= ks * pow2i(e[1]);
+            mul[0] *= ks * pow2i(e[0]);
+            mul[1] *= ks * pow2i(e[1]);
         }
         ++pair;
         float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[D / 8][4];
@@ -561,14 +596,17 @@ __global__ void __launch_bounds__(pd::THREADS, 2)
         for (int n = 0; n < D / 8; ++n)
             o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
         for (int t = w.tile; t < end; ++t) {
-            const int64_t left = len - (int64_t)t * pd::TILE - first;
-            const uint32_t k = ring + stage * 2 * S::KV + group_off;
+            const int64_t left = len - (int64_t)t * S::TILE - first;
+            uint32_t at[S::NG];
+#pragma unroll
+            for (int i = 0; i < S::NG; ++i)
+                at[i] = ring + stage * 2 * S::KV + group_off[i];
             wait(&bar->kfull[stage], phase, 3);
             auto wait_v = [&] { wait(&bar->vfull[stage], phase, 4); };
-            if (left >= 16)
-                pd_group<D, E4M3, false>(qa, mul0, mul1, k, k + S::KV, blk, 16, lane, m, l, o, wait_v);
+            if (left >= S::NG * 16)
+                pd_group<D, E4M3, false>(qa, mul, at, blk, S::NG * 16, lane, m, l, o, wait_v);
             else if (left > 0)
-                pd_group<D, E4M3, true>(qa, mul0, mul1, k, k + S::KV, blk, (int)left, lane, m, l, o, wait_v);
+                pd_group<D, E4M3, true>(qa, mul, at, blk, (int)left, lane, m, l, o, wait_v);
             else
                 wait_v();
             __syncwarp();
@@ -733,6 +771,7 @@ template <int D, bool E4M3> bool pool_map(CUtensorMap *m, const tdg_symm *h, con
 template <int D, bool E4M3> int launch_decode(const tdg_symm *h, const tdg_paged_decode_args *a, PagedDecodeParams &p, cudaStream_t st)
 {
     using S = pd::Shape<D, E4M3>;
+    p.box = a->cache.page_size < S::TILE ? a->cache.page_size : S::TILE;
     CUtensorMap km, vm;
     if (!pool_map<D, E4M3>(&km, h, a->cache, a->cache.k_off, p.box) || !pool_map<D, E4M3>(&vm, h, a->cache, a->cache.v_off, p.box))
         return TDG_ERR_CUDA;
@@ -801,7 +840,6 @@ extern "C" int tdg_paged_decode(tdg_symm *h, const tdg_paged_decode_args *a, voi
     p.Hq = (int)Hq;
     p.G = (int)(Hq / Hkv);
     p.groups = (p.G + pd::ROWS - 1) / pd::ROWS;
-    p.box = a->cache.page_size < pd::TILE ? a->cache.page_size : pd::TILE;
     p.scale_log2 = (a->scale > 0.f ? a->scale : 1.0f / sqrtf((float)D)) * 1.4426950408889634f; // scores live in base 2
     p.timeout_ns = timeout_or_default(0);
     p.q = static_cast<const __nv_bfloat16 *>(a->q);
