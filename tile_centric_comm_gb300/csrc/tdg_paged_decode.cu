@@ -727,20 +727,36 @@ __global__ void __launch_bounds__(pd::JOIN_ROWS *D / 2) paged_join_kernel(const 
     const int c0 = desc.z, c1 = blockIdx.x;
     // slot of CTA c: the first one's may be its second
     auto at = [&](int c) -> size_t { return (size_t)(c * 2 + (c == c0 ? desc.w : 0)) * pd::ROWS + row; };
-    float M = -INFINITY;
-#pragma unroll 8
-    for (int c = c0; c <= c1; ++c)
-        M = fmaxf(M, __ldcg(p.part_ml + at(c) * 2));
-    const float Ms = M == -INFINITY ? 0.f : M;
-    float L = 0.f, a = 0.f, b = 0.f;
-#pragma unroll 8
-    for (int c = c0; c <= c1; ++c) {
-        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(p.part_ml + at(c) * 2));
-        const float2 x = __ldcg(reinterpret_cast<const float2 *>(p.part_o + at(c) * D + col));
-        const float wt = exp2_approx(ml.x - Ms);
-        L += ml.y * wt;
-        a += x.x * wt;
-        b += x.y * wt;
+    // eight partial results at a time, their maxima, sums and outputs in one
+    // round of loads
+    float M = -INFINITY, L = 0.f, a = 0.f, b = 0.f;
+    for (int c = c0; c <= c1; c += 8) {
+        float2 ml[8], x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            ml[i] = make_float2(-INFINITY, 0.f);
+            x[i] = make_float2(0.f, 0.f);
+            if (c + i <= c1) {
+                ml[i] = __ldcg(reinterpret_cast<const float2 *>(p.part_ml + at(c + i) * 2));
+                x[i] = __ldcg(reinterpret_cast<const float2 *>(p.part_o + at(c + i) * D + col));
+            }
+        }
+        float top = M;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            top = fmaxf(top, ml[i].x);
+        const float ms = top == -INFINITY ? 0.f : top, al = exp2_approx(M - ms);
+        M = top;
+        L *= al;
+        a *= al;
+        b *= al;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float wt = exp2_approx(ml[i].x - ms);
+            L += ml[i].y * wt;
+            a += x[i].x * wt;
+            b += x[i].y * wt;
+        }
     }
     const float f = (p.c.v_scale ? p.c.v_scale[g] : 1.f) / L;
     *reinterpret_cast<uint32_t *>(p.out + desc.x * p.os + (int64_t)h * D + col) = pack_bf16x2(a * f, b * f);

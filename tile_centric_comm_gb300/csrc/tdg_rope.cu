@@ -68,8 +68,10 @@ __device__ __forceinline__ uint4 ld_once(const __nv_bfloat16 *p)
     return v;
 }
 
+// (four CTAs per SM rather than three are worth 5 % of a long bf16 write; the
+// 8-bit kernel does not fit the registers that this leaves)
 template <int D, bool INTER, bool E4M3>
-__global__ void __launch_bounds__(rp::THREADS) rope_append_kernel(const __grid_constant__ RopeParams p)
+__global__ void __launch_bounds__(rp::THREADS, E4M3 ? 3 : 4) rope_append_kernel(const __grid_constant__ RopeParams p)
 {
     constexpr int UNITS = D / 16; // 16-element units of a head
     constexpr int ESZ = E4M3 ? 1 : 2;
