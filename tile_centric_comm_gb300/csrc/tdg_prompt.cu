@@ -590,7 +590,7 @@ __global__ void __launch_bounds__(pa::THREADS, 1)
                             __syncwarp();
                             if (lane == 0)
                                 mbar_arrive(&ctl->kvfull[stage]);
-                            ok = landed;
+                            ok = __all_sync(0xffffffffu, landed);
                         }
                         ++issued;
                         if (++stage == S::STAGES) {
