@@ -197,3 +197,21 @@ def test_refusals(symm):
         tdg.prompt_attention(symm, q, k, v, out, cu.long(), cu)
     torch.cuda.synchronize()
     assert symm.status()["code"] == 0
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_output_rows_off_the_32_byte_grid(symm, D):
+    # an output that starts 16 bytes off, with a row stride of an odd number of 16-byte units
+    c = Case([70, 200], [70, 200], 4, 2, D, seed=3)
+    T, n = len(c.q), 4 * D
+    buf = torch.full(((T + 1) * (n + 8),), float("nan"), dtype=torch.bfloat16, device="cuda")
+    out = torch.as_strided(buf, (T, 4, D), (n + 8, D, 1), 8)
+    q, k, v = (to_dev_bf16(x) for x in (c.q, c.k, c.v))
+    cu = torch.from_numpy(c.cu_q).cuda()
+    tdg.prompt_attention(symm, q, k, v, out, cu, cu)
+    torch.cuda.synchronize()
+    assert symm.status()["code"] == 0
+    c.check((to_bits(out), None))
+    rest = torch.ones_like(buf, dtype=torch.bool)
+    torch.as_strided(rest, (T, 4, D), (n + 8, D, 1), 8).fill_(False)
+    assert torch.isnan(buf[rest].float()).all()

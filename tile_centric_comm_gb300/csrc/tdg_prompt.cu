@@ -73,7 +73,6 @@ struct PromptCtl {
     uint4 stolen;                      // answer to the request for a further item
     uint32_t tmem_base;
     volatile int abort;
-    int issued;                        // ring fills issued
     uint32_t first[pa::CHUNKS + 1];    // first item of every table entry
     uint16_t order[pa::CHUNKS];        // the sequence of an entry, longest first
 };
@@ -264,7 +263,6 @@ __global__ void __launch_bounds__(pa::THREADS, 1)
         mbar_init(&ctl->drain, 1);
         mbar_init(&ctl->steal, 1);
         ctl->abort = 0;
-        ctl->issued = 0;
         fence_mbar_init();
         fence_proxy_async_smem();
         prefetch_tensormap(&qmap);
@@ -607,8 +605,6 @@ __global__ void __launch_bounds__(pa::THREADS, 1)
                 idx = steal_answer(&ctl->stolen);
                 __syncwarp();
             }
-            if (lane == 0)
-                ctl->issued = issued;
             if (ctl->abort && lane == 0) {
                 // leave only when the copies in flight have landed
                 for (int t = 0; t < 2; ++t)
