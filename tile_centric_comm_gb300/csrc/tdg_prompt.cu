@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(pa::THREADS, 1)
                 // of this block's scores.
                 if (__any_sync(0xffffffffu, grown)) {
                     l *= al;
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < D; c += 16) {
                         uint32_t o[16];
                         tmem_ld_32x32b_x16(o_addr + c, o);
@@ -455,7 +455,7 @@ __global__ void __launch_bounds__(pa::THREADS, 1)
             const int64_t row = (int64_t)it.q0 + tok;
             const int h = it.g * p.G + row_head;
             __nv_bfloat16 *dst = p.out + row * p.os + (int64_t)h * D;
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < D; c += 32) {
                 uint32_t o[32];
                 if (nb) {
