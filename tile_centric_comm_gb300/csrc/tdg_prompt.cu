@@ -388,8 +388,13 @@ __global__ void __launch_bounds__(pa::THREADS, 1)
                 if ((j + 1) * pa::BN > open) { // the causal edge or the sequence's end runs through this block
                     const int lim = limit - j * pa::BN;
 #pragma unroll
-                    for (int c = 0; c < 128; ++c)
-                        s[c / 32][c % 32] = c < lim ? s[c / 32][c % 32] : 0xFF800000u; // -inf
+                    for (int c = 0; c < 4; ++c) {
+                        const int n = lim - c * 32; // of this chunk's 32
+                        const uint32_t sees = n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            s[c][i] = sees >> i & 1 ? s[c][i] : 0xFF800000u; // -inf
+                    }
                 }
                 float mx[4] = {__uint_as_float(s[0][0]), __uint_as_float(s[1][0]), __uint_as_float(s[2][0]), __uint_as_float(s[3][0])};
 #pragma unroll
