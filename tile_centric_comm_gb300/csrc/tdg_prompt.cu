@@ -746,6 +746,7 @@ __global__ void __launch_bounds__(pa::THREADS, 1)
                 // and the next keys in the slot behind: no conditions between the
                 // instructions, and every descriptor and barrier a constant
                 auto whole_block = [&](auto vslot, int j) {
+                    static_assert(S::STAGES == 4, "values lie in slots 1 and 3, and the ring wraps at K only");
                     constexpr int V = decltype(vslot)::value, K = (V + 1) % S::STAGES;
                     const uint32_t vph = phase, kph = phase ^ (K == 0 ? 1u : 0u);
                     ok = all_wait(&ctl->kvfull[V], vph, 23) && all_wait(&ctl->kvfull[K], kph, 25) &&
