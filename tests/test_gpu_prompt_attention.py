@@ -215,3 +215,20 @@ def test_output_rows_off_the_32_byte_grid(symm, D):
     rest = torch.ones_like(buf, dtype=torch.bool)
     torch.as_strided(rest, (T, 4, D), (n + 8, D, 1), 8).fill_(False)
     assert torch.isnan(buf[rest].float()).all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("Hq,Hkv,nq,nk", [
+    (8, 1, [1], [5000]),                                   # few rows, long keys: 8 CTAs share an item
+    (7, 1, [1, 17, 40], [3000, 2177, 4000]),
+    (4, 2, [3, 0, 64, 5], [2500, 3000, 64, 2]),            # beside sequences of few keys, and rows that see nothing
+    (16, 2, [130, 9], [1500, 1300]),
+    (2, 2, [700], [700]),
+])
+def test_keys_shared_by_ctas(symm, D, causal, Hq, Hkv, nq, nk):
+    c = Case(nq, nk, Hq, Hkv, D, seed=sum(nk) + D, tail=1)
+    got = c.run(symm, causal)
+    c.check(got, causal)
+    again = c.run(symm, causal)
+    assert np.array_equal(got[0], again[0]) and np.array_equal(got[1], again[1], equal_nan=True)

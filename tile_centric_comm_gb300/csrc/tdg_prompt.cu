@@ -35,6 +35,7 @@ constexpr int MMA_WARP = 8, LOAD_WARP = 9;
 constexpr int BN = 128;       // keys of a block
 constexpr int CHUNKS = 256;   // entries of the item table
 constexpr int SLOTS = 2;      // items in hand
+constexpr int MAX_SPLIT = 8;  // CTAs that share an item's keys
 constexpr uint32_t TMEM_COLS = 512;
 
 template <int D> struct Shape {
@@ -54,6 +55,7 @@ struct PromptParams {
     int64_t Tq, Tk, B, os;
     int Hq, Hkv, G, NT; // NT: tokens of a tile, 128 / G
     int causal;
+    int split; // CTAs of a cluster that share an item's keys (SPLIT)
     int out32; // rows of out are 32-byte aligned
     float scale_log2;
     __nv_bfloat16 *out;
@@ -66,11 +68,18 @@ struct PromptItem {
     int q0, Lq, k0, Lk, g, t0, valid, pad;
 };
 
+// The key blocks [lo, hi) of a SPLIT item that are this CTA's.
+struct PromptShare {
+    int lo, hi;
+};
+
 struct PromptCtl {
     uint64_t kvfull[8], kvempty[8], qfull[2], qempty[2], sfull[2], pfull[2], ofull[2];
     uint64_t ifull[pa::SLOTS], iempty[pa::SLOTS], tail, drain, steal;
     PromptItem item[pa::SLOTS];
     uint4 stolen;                      // answer to the request for a further item
+    float2 stat[2][128];               // SPLIT: maximum and sum of this CTA's rows
+    PromptShare share;
     uint32_t tmem_base;
     volatile int abort;
     uint32_t first[pa::CHUNKS + 1];    // first item of every table entry
@@ -104,9 +113,12 @@ __device__ __forceinline__ int prompt_most(const PromptParams &p, const PromptIt
     const int lo = it.t0 + t * p.NT, hi = min(lo + p.NT, it.Lq);
     return hi > lo ? prompt_limit(p, it, hi - 1) : 0;
 }
-__device__ __forceinline__ int prompt_blocks(const PromptParams &p, const PromptItem &it, int t)
+// The tile's key blocks (SPLIT: those that are this CTA's).
+template <bool SPLIT>
+__device__ __forceinline__ int prompt_blocks(const PromptParams &p, const PromptItem &it, int t, const PromptShare &share)
 {
-    return (prompt_most(p, it, t) + pa::BN - 1) / pa::BN;
+    const int all = (prompt_most(p, it, t) + pa::BN - 1) / pa::BN;
+    return SPLIT ? max(0, min(all, share.hi) - share.lo) : all;
 }
 
 // The MMA warp runs its whole loop converged and the instructions themselves
@@ -142,6 +154,19 @@ __device__ __forceinline__ int64_t steal_answer(const uint4 *answer)
                  : "r"(smem_u32(answer))
                  : "memory");
     return ok ? (int64_t)x : -1;
+}
+
+__device__ __forceinline__ float2 ld_cluster_f2(uint32_t a)
+{
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t a)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+    return v;
 }
 
 __device__ __forceinline__ uint32_t elect_one()
@@ -233,7 +258,7 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b)
     return d;
 }
 
-template <int D>
+template <int D, bool SPLIT>
 __global__ void __launch_bounds__(pa::THREADS, 1)
     prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant__ CUtensorMap qmap,
                   const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap)
@@ -369,8 +394,9 @@ __global__ void __launch_bounds__(pa::THREADS, 1)
             }
             if (!it.valid)
                 break;
+            const PromptShare share = SPLIT ? ctl->share : PromptShare{0, 0};
             const int tile_tok = it.t0 + t * p.NT, tok = tile_tok + row_tok;
-            const int nb = prompt_blocks(p, it, t);
+            const int nb = prompt_blocks<SPLIT>(p, it, t, share);
             const int limit = prompt_limit(p, it, tok);          // keys this row sees
             const int open = prompt_limit(p, it, tile_tok);      // keys every row of the tile sees
             float m = -INFINITY, l = 0.f;                        // m: in units of s
@@ -385,8 +411,9 @@ __global__ void __launch_bounds__(pa::THREADS, 1)
                 for (int c = 0; c < 4; ++c)
                     tmem_ld_32x32b_x32(s_addr + c * 32, s[c]);
                 tmem_ld_wait();
-                if ((j + 1) * pa::BN > open) { // the causal edge or the sequence's end runs through this block
-                    const int lim = limit - j * pa::BN;
+                const int key0 = ((SPLIT ? share.lo : 0) + j) * pa::BN; // the block's first key
+                if (key0 + pa::BN > open) { // the causal edge or the sequence's end runs through this block
+                    const int lim = limit - key0;
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         const int n = lim - c * 32; // of this chunk's 32
@@ -454,6 +481,27 @@ __global__ void __launch_bounds__(pa::THREADS, 1)
                 o_phase ^= 1u;
                 tc_fence_after();
             }
+            if constexpr (SPLIT) {
+                // This CTA's maximum, sum and output of the row go to shared
+                // memory, the output over the ring, once nothing reads the ring.
+                if (prompt_blocks<SPLIT>(p, it, t ^ 1, share))
+                    ok = __all_sync(0xffffffffu, wait(&ctl->ofull[t ^ 1], 0, 32));
+                tc_fence_after();
+                ctl->stat[t][r] = make_float2(nb ? m * p.scale_log2 : -INFINITY, l);
+                float *dst = reinterpret_cast<float *>(smem + S::OFF_KV) + (t * 128 + r) * D;
+                const bool wanted = row_used && tok < it.Lq;
+#pragma unroll 1
+                for (int c = 0; nb && c < D; c += 32) {
+                    uint32_t o[32];
+                    tmem_ld_32x32b_x32(o_addr + c, o);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; wanted && i < 8; ++i) // chunks of 16 bytes xored by the row: no bank conflicts
+                        *reinterpret_cast<uint4 *>(dst + (((c / 4 + i) ^ (r & (D / 4 - 1))) * 4)) =
+                            make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                }
+                continue; // the next item is the end
+            }
             const bool mine = row_used && tok < it.Lq;
             const bool sees = limit > 0;
             const float f = sees ? 1.f / l : 0.f;
@@ -492,7 +540,8 @@ __global__ void __launch_bounds__(pa::THREADS, 1)
             int issued = 0;
             bool ok = true;
             uint32_t steal_phase = 0;
-            int64_t idx = blockIdx.x;
+            int64_t idx = SPLIT ? blockIdx.x / p.split : blockIdx.x;
+            PromptShare share = {0, 0};
             while (true) {
                 PromptItem it;
                 it.valid = idx >= 0 && idx < items ? 1 : 0;
@@ -521,12 +570,19 @@ __global__ void __launch_bounds__(pa::THREADS, 1)
                         it.Lq = it.Lk = n = left = 0;
                     it.g = (int)((uint32_t)idx % (uint32_t)p.Hkv);
                     it.t0 = max(0, n - 1 - left) * span; // the last tokens, which see the most, first
+                    if (SPLIT) { // this CTA's share of the key blocks
+                        const int all = max(prompt_blocks<false>(p, it, 0, share), prompt_blocks<false>(p, it, 1, share)), rank = (int)cluster_ctarank();
+                        share.lo = all * rank / p.split;
+                        share.hi = all * (rank + 1) / p.split;
+                    }
                 }
                 if (idx < items) { // the item, or the end
                     if (lane == 0) {
                         ok = wait(&ctl->iempty[slot], slot_phase ^ 1u, 10);
                         if (ok) {
                             ctl->item[slot] = it;
+                            if (SPLIT && it.valid)
+                                ctl->share = share;
                             mbar_arrive(&ctl->ifull[slot]);
                         }
                     }
@@ -539,12 +595,12 @@ __global__ void __launch_bounds__(pa::THREADS, 1)
                         break;
                 }
                 // ask for the next item now, take the answer once this one's loads are under way
-                if (lane == 0) {
+                if (!SPLIT && lane == 0) {
                     fence_proxy_async_smem(); // the last answer has been read
                     mbar_arrive_expect_tx(&ctl->steal, sizeof(uint4));
                     steal_request(&ctl->stolen, &ctl->steal);
                 }
-                const int nb0 = prompt_blocks(p, it, 0), nb1 = prompt_blocks(p, it, 1), nb = max(nb0, nb1);
+                const int nb0 = prompt_blocks<SPLIT>(p, it, 0, share), nb1 = prompt_blocks<SPLIT>(p, it, 1, share), nb = max(nb0, nb1);
                 if (lane == 0) {
                     for (int t = 0; t < 2 && ok; ++t)
                         if (t == 0 ? nb0 : nb1) {
@@ -563,7 +619,7 @@ __global__ void __launch_bounds__(pa::THREADS, 1)
                 for (int j = 0; j < nb && ok; ++j)
                     for (int kv = 0; kv < 2 && ok; ++kv) {
                         uint8_t *dst = smem + S::OFF_KV + stage * S::KV_BYTES;
-                        const int rows = it.Lk - j * pa::BN; // keys of this block that are the sequence's own
+                        const int key0 = ((SPLIT ? share.lo : 0) + j) * pa::BN, rows = it.Lk - key0; // keys of this block that are the sequence's own
                         // values behind the sequence's end are cleared: weight 0 times
                         // whatever the neighbour holds must be 0
                         const bool clear = kv == 1 && rows < pa::BN;
@@ -575,7 +631,7 @@ __global__ void __launch_bounds__(pa::THREADS, 1)
 #pragma unroll
                                 for (int hf = 0; hf < S::HALVES; ++hf)
                                     tma_load_3d_addr(dst + hf * 16384, kv ? &vmap : &kmap, smem_u32(bar), hf * 64, it.g,
-                                                     it.k0 + j * pa::BN);
+                                                     it.k0 + key0);
                             }
                         }
                         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
@@ -601,6 +657,12 @@ __global__ void __launch_bounds__(pa::THREADS, 1)
                             phase ^= 1u;
                         }
                     }
+                if (SPLIT) { // one item a cluster
+                    idx = -1;
+                    if (!ok)
+                        break;
+                    continue;
+                }
                 // (also after a timeout: the answer must have landed before the CTA leaves)
                 const bool answered = wait(&ctl->steal, steal_phase, 14);
                 steal_phase ^= 1u;
@@ -688,8 +750,14 @@ __global__ void __launch_bounds__(pa::THREADS, 1)
                     break;
                 const int keys[2] = {__reduce_max_sync(0xffffffffu, prompt_most(p, it, 0)),
                                      __reduce_max_sync(0xffffffffu, prompt_most(p, it, 1))};
-                const int nb[2] = {(keys[0] + pa::BN - 1) / pa::BN, (keys[1] + pa::BN - 1) / pa::BN};
-                auto cols = [&](int t, int j) -> int { return min(pa::BN, (keys[t] - j * pa::BN + 15) & ~15); };
+                int lo = 0, nb[2] = {(keys[0] + pa::BN - 1) / pa::BN, (keys[1] + pa::BN - 1) / pa::BN};
+                if constexpr (SPLIT) {
+                    lo = __reduce_max_sync(0xffffffffu, ctl->share.lo);
+                    const int hi = __reduce_max_sync(0xffffffffu, ctl->share.hi);
+                    nb[0] = max(0, min(nb[0], hi) - lo);
+                    nb[1] = max(0, min(nb[1], hi) - lo);
+                }
+                auto cols = [&](int t, int j) -> int { return min(pa::BN, (keys[t] - (lo + j) * pa::BN + 15) & ~15); };
                 const int most = max(nb[0], nb[1]);
                 if (!most)
                     continue;
@@ -789,6 +857,52 @@ __global__ void __launch_bounds__(pa::THREADS, 1)
         tc_fence_after();
         tmem_dealloc(tmem, pa::TMEM_COLS);
     }
+    if constexpr (SPLIT) {
+        // join the cluster's shares: every CTA takes 256 / split rows, four
+        // dimensions a thread, and reads the others' shared memory
+        cluster_sync();
+        const PromptItem it = ctl->item[0];
+        if (it.valid && threadIdx.x < 256) {
+            const int per = 256 / p.split, row0 = (int)cluster_ctarank() * per;
+            const uint32_t stat0 = smem_u32(&ctl->stat[0][0]), out0 = smem_u32(smem + S::OFF_KV);
+            for (int u = threadIdx.x; u < per * (D / 4); u += 256) {
+                const int row = row0 + u / (D / 4), ch = u % (D / 4), t = row >> 7, r = row & 127;
+                const int tok = it.t0 + t * p.NT + r / p.G;
+                if (r >= p.NT * p.G || tok >= it.Lq)
+                    continue;
+                float2 st[pa::MAX_SPLIT];
+                float M = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < pa::MAX_SPLIT; ++c) {
+                    st[c] = make_float2(-INFINITY, 0.f);
+                    if (c < p.split)
+                        st[c] = ld_cluster_f2(mapa_shared(stat0 + row * 8, c));
+                    M = fmaxf(M, st[c].x);
+                }
+                float L = 0.f;
+                float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int c = 0; c < pa::MAX_SPLIT; ++c)
+                    if (st[c].x != -INFINITY) { // a share that the row sees something of
+                        const float w = exp2_approx(st[c].x - M);
+                        const float4 x = ld_cluster_f4(mapa_shared(out0 + (row * D + (ch ^ (r & (D / 4 - 1))) * 4) * 4, c));
+                        L += st[c].y * w;
+                        a.x += x.x * w;
+                        a.y += x.y * w;
+                        a.z += x.z * w;
+                        a.w += x.w * w;
+                    }
+                const float f = prompt_limit(p, it, tok) > 0 ? 1.f / L : 0.f;
+                const int64_t at = (int64_t)it.q0 + tok;
+                const int h = it.g * p.G + r % p.G;
+                *reinterpret_cast<uint2 *>(p.out + at * p.os + (int64_t)h * D + ch * 4) =
+                    make_uint2(pack_bf16x2(a.x * f, a.y * f), pack_bf16x2(a.z * f, a.w * f));
+                if (p.lse && ch == 0)
+                    p.lse[at * p.Hq + h] = f != 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+            }
+        }
+        cluster_sync(); // no CTA leaves while another reads its shared memory
+    }
 }
 
 } // namespace tdg
@@ -850,11 +964,22 @@ extern "C" int tdg_prompt_attention(tdg_symm *h, const tdg_prompt_attention_args
     if (a->Tk && (!map_bf16_3d(&km, a->k, D, Hkv, a->Tk, D * 2, a->k_stride * 2, 64, 1, pa::BN) ||
                   !map_bf16_3d(&vm, a->v, D, Hkv, a->Tk, D * 2, a->v_stride * 2, 64, 1, pa::BN)))
         return TDG_ERR_CUDA;
-    const void *fn = D == 128 ? reinterpret_cast<const void *>(&prompt_kernel<128>) : reinterpret_cast<const void *>(&prompt_kernel<64>);
+    // Few items of many keys: up to 8 CTAs share an item's keys, as many as the
+    // SMs allow, if an average sequence's item is spared 8 blocks by it (a block
+    // is 1.2 us of an item, the cluster and its join cost 5 to 6 us).
+    const int64_t room = h->sm_count / items, blocks = a->Tk / a->B / pa::BN;
+    p.split = room >= 8 ? 8 : room >= 4 ? 4 : room >= 2 ? 2 : 1;
+    if (blocks - blocks / p.split < 8)
+        p.split = 1;
+    const void *fn = D == 128 ? (p.split > 1 ? reinterpret_cast<const void *>(&prompt_kernel<128, true>)
+                                             : reinterpret_cast<const void *>(&prompt_kernel<128, false>))
+                              : (p.split > 1 ? reinterpret_cast<const void *>(&prompt_kernel<64, true>)
+                                             : reinterpret_cast<const void *>(&prompt_kernel<64, false>));
     const int smem = D == 128 ? prompt_smem<128>() : prompt_smem<64>();
     if (const cudaError_t e = set_smem(fn, smem); e != cudaSuccess)
         return cuda_err(e, "prompt attention smem");
     void *args[] = {&p, &qm, &km, &vm};
-    return cuda_err(launch(fn, dim3((unsigned)items), dim3(pa::THREADS), smem, static_cast<cudaStream_t>(stream), args, false, 1, true),
+    return cuda_err(launch(fn, dim3((unsigned)(items * p.split)), dim3(pa::THREADS), smem, static_cast<cudaStream_t>(stream), args,
+                           false, p.split, true),
                     "prompt attention launch");
 }
