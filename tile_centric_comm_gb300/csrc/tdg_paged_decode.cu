@@ -36,7 +36,8 @@ constexpr int WARPS = 4;                      // consumer warps
 constexpr int THREADS = WARPS * 32 + 32;
 constexpr int MAX_CTAS = 512;                 // CTAs whose partial results the caller provides room for
 constexpr int ROWS = 16;                      // query heads of a partial result
-constexpr int JOIN_ROWS = 4;                  // rows of a join CTA
+constexpr int JOIN_ROWS = 2;                  // rows of a join CTA
+constexpr int JOIN_THREADS = 256;
 constexpr int MERGE_COLS = 32;                // columns of one merge phase
 constexpr int BAR_BYTES = 384;
 
@@ -710,57 +711,90 @@ __global__ void __launch_bounds__(pd::THREADS, 2)
 }
 
 // Joins the partial results of the pair that ends in CTA blockIdx.x (if one
-// does): rows blockIdx.y * JOIN_ROWS on, two columns per thread at D = 128.
-template <int D>
-__global__ void __launch_bounds__(pd::JOIN_ROWS *D / 2) paged_join_kernel(const __grid_constant__ PagedDecodeParams p)
+// does): rows blockIdx.y * JOIN_ROWS on.  A pair may be split over every CTA,
+// so groups of D/4 threads (four columns each) share the partial results of a
+// row, each group four at a time, maxima, sums and outputs in one round of
+// loads; the first group of a row then joins the groups.  The order is fixed by
+// the split alone.
+template <int D> __global__ void __launch_bounds__(pd::JOIN_THREADS) paged_join_kernel(const __grid_constant__ PagedDecodeParams p)
 {
+    constexpr int LANES = D / 4, GROUPS = pd::JOIN_THREADS / LANES, U = 4;
+    __shared__ float2 gml[GROUPS];
+    __shared__ float4 go[GROUPS][LANES];
     griddep_launch_dependents();
     griddep_wait();
     const int4 desc = p.desc[blockIdx.x];
     if (desc.x < 0)
         return;
     const int g = desc.y / p.groups, mg = desc.y % p.groups;
-    const int row = blockIdx.y * pd::JOIN_ROWS + threadIdx.x / (D / 2), col = threadIdx.x % (D / 2) * 2;
-    if (row >= min(pd::ROWS, p.G - mg * pd::ROWS))
+    const int rows = min(pd::JOIN_ROWS, min(pd::ROWS, p.G - mg * pd::ROWS) - (int)blockIdx.y * pd::JOIN_ROWS);
+    if (rows <= 0)
         return;
-    const int h = g * p.G + mg * pd::ROWS + row;
+    const int per = GROUPS / (rows == 1 ? 1 : 2); // groups of a row
+    const int group = threadIdx.x / LANES, lane = threadIdx.x % LANES;
+    const int row = blockIdx.y * pd::JOIN_ROWS + group / per, part = group % per;
+    const bool used = group / per < rows;
     const int c0 = desc.z, c1 = blockIdx.x;
     // slot of CTA c: the first one's may be its second
     auto at = [&](int c) -> size_t { return (size_t)(c * 2 + (c == c0 ? desc.w : 0)) * pd::ROWS + row; };
-    // eight partial results at a time, their maxima, sums and outputs in one
-    // round of loads
-    float M = -INFINITY, L = 0.f, a = 0.f, b = 0.f;
-    for (int c = c0; c <= c1; c += 8) {
-        float2 ml[8], x[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            ml[i] = make_float2(-INFINITY, 0.f);
-            x[i] = make_float2(0.f, 0.f);
-            if (c + i <= c1) {
-                ml[i] = __ldcg(reinterpret_cast<const float2 *>(p.part_ml + at(c + i) * 2));
-                x[i] = __ldcg(reinterpret_cast<const float2 *>(p.part_o + at(c + i) * D + col));
-            }
-        }
-        float top = M;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            top = fmaxf(top, ml[i].x);
+    float M = -INFINITY, L = 0.f;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](const float2 &ml, const float4 &x, float ms) {
+        const float w = exp2_approx(ml.x - ms);
+        L += ml.y * w;
+        a.x += x.x * w;
+        a.y += x.y * w;
+        a.z += x.z * w;
+        a.w += x.w * w;
+    };
+    auto raise = [&](float top) -> float { // brings M, L and a to a new maximum
         const float ms = top == -INFINITY ? 0.f : top, al = exp2_approx(M - ms);
         M = top;
         L *= al;
-        a *= al;
-        b *= al;
+        a.x *= al;
+        a.y *= al;
+        a.z *= al;
+        a.w *= al;
+        return ms;
+    };
+    for (int c = c0 + part; used && c <= c1; c += per * U) {
+        float2 ml[U];
+        float4 x[U];
+        float top = M;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float wt = exp2_approx(ml[i].x - ms);
-            L += ml[i].y * wt;
-            a += x[i].x * wt;
-            b += x[i].y * wt;
+        for (int i = 0; i < U; ++i) {
+            ml[i] = make_float2(-INFINITY, 0.f);
+            x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (c + i * per <= c1) {
+                ml[i] = __ldcg(reinterpret_cast<const float2 *>(p.part_ml + at(c + i * per) * 2));
+                x[i] = __ldcg(reinterpret_cast<const float4 *>(p.part_o + at(c + i * per) * D + lane * 4));
+            }
         }
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+            top = fmaxf(top, ml[i].x);
+        const float ms = raise(top);
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+            add(ml[i], x[i], ms);
     }
+    if (lane == 0)
+        gml[group] = make_float2(M, L);
+    go[group][lane] = a;
+    __syncthreads();
+    if (!used || part != 0)
+        return;
+    float top = M;
+    for (int i = 1; i < per; ++i)
+        top = fmaxf(top, gml[group + i].x);
+    const float ms = raise(top);
+    for (int i = 1; i < per; ++i)
+        add(gml[group + i], go[group + i][lane], ms);
+    const int h = g * p.G + mg * pd::ROWS + row;
     const float f = (p.c.v_scale ? p.c.v_scale[g] : 1.f) / L;
-    *reinterpret_cast<uint32_t *>(p.out + desc.x * p.os + (int64_t)h * D + col) = pack_bf16x2(a * f, b * f);
-    if (p.lse && col == 0)
+    *reinterpret_cast<uint2 *>(p.out + desc.x * p.os + (int64_t)h * D + lane * 4) =
+        make_uint2(pack_bf16x2(a.x * f, a.y * f), pack_bf16x2(a.z * f, a.w * f));
+    if (p.lse && lane == 0)
         p.lse[(int64_t)desc.x * p.Hq + h] = (M + log2f(L)) * 0.6931471805599453f;
 }
 
@@ -801,7 +835,7 @@ template <int D, bool E4M3> int launch_decode(const tdg_symm *h, const tdg_paged
     void *jargs[] = {&p};
     const int join_rows = p.G < pd::ROWS ? p.G : pd::ROWS;
     return cuda_err(launch(reinterpret_cast<const void *>(&paged_join_kernel<D>),
-                           dim3(ctas, (unsigned)((join_rows + pd::JOIN_ROWS - 1) / pd::JOIN_ROWS)), dim3(pd::JOIN_ROWS * D / 2), 0, st,
+                           dim3(ctas, (unsigned)((join_rows + pd::JOIN_ROWS - 1) / pd::JOIN_ROWS)), dim3(pd::JOIN_THREADS), 0, st,
                            jargs, false, 1, true),
                     "paged join launch");
 }
