@@ -171,9 +171,11 @@ cudaError_t launch(const void *fn, dim3 grid, dim3 block, size_t smem, cudaStrea
     cfg.stream = s;
     cudaLaunchAttribute attr[3];
     int n = 0;
-    attr[n].id = cudaLaunchAttributeCooperative;
-    attr[n].val.cooperative = cooperative ? 1 : 0;
-    ++n;
+    if (cooperative) {
+        attr[n].id = cudaLaunchAttributeCooperative;
+        attr[n].val.cooperative = 1;
+        ++n;
+    }
     if (cluster > 1) {
         attr[n].id = cudaLaunchAttributeClusterDimension;
         attr[n].val.clusterDim.x = (unsigned)cluster;

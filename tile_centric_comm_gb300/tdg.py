@@ -469,7 +469,7 @@ def _attn():
     """torch, and the library's attention entry points taking packed arguments
     (one struct.pack call costs a fraction of filling a ctypes structure field
     by field, and these calls are short)."""
-    global _torch, _current_raw_stream
+    global _torch, _current_raw_stream, _Tensor, _t_bf16, _t_i32, _t_f32
     import torch
     L = lib()
     fast = ctypes.CDLL(LIB_PATH)
@@ -478,6 +478,7 @@ def _attn():
         f.restype, f.argtypes = ctypes.c_int, [_vp, ctypes.c_char_p, _vp]
         globals()["_" + name] = f
     _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    _Tensor, _t_bf16, _t_i32, _t_f32 = torch.Tensor, torch.bfloat16, torch.int32, torch.float32
     _torch = torch
     return L
 
@@ -501,22 +502,22 @@ def _rows(t, name, device):
     """Check rows of heads, (rows, heads, D) in bf16, whose rows may be strided
     (columns of a wider buffer); returns (pointer, row stride in elements, rows,
     heads, D)."""
-    if not isinstance(t, _torch.Tensor):
+    if not isinstance(t, _Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
-    if t.dtype is not _torch.bfloat16:
+    if t.dtype is not _t_bf16:
         raise TypeError(f"{name}: expected torch.bfloat16, got {t.dtype}")
-    shape = t.shape
-    if len(shape) != 3:
-        raise ValueError(f"{name}: expected (rows, heads, D), got {tuple(shape)}")
-    n, heads, D = shape
-    s0, s1, s2 = t.stride()
+    stride = t.stride()
+    if len(stride) != 3:
+        raise ValueError(f"{name}: expected (rows, heads, D), got {tuple(t.shape)}")
+    n, heads, D = t.shape
+    s0, s1, s2 = stride
     if n <= 1 or not heads:
         s0 = heads * D          # no second row, no stride
         if not n or not heads:
             return t.data_ptr(), s0, n, heads, D
     if (s2 != 1 and D > 1) or (s1 != D and heads > 1):
-        raise ValueError(f"{name}: the heads of a row must be contiguous, strides {t.stride()}")
-    if t.device != device:
+        raise ValueError(f"{name}: the heads of a row must be contiguous, strides {stride}")
+    if t.get_device() != device.index:
         raise ValueError(f"{name}: on {t.device}, the heap is on {device}")
     return t.data_ptr(), s0, n, heads, D
 
@@ -524,20 +525,22 @@ def _rows(t, name, device):
 def _table(table, name, device):
     """Check a page table (sequences, entries), int32, rows possibly strided;
     returns (pointer, entries, row stride, sequences)."""
-    if not isinstance(table, _torch.Tensor) or table.dtype is not _torch.int32:
+    if not isinstance(table, _Tensor) or table.dtype is not _t_i32:
         raise TypeError(f"{name}: expected an int32 tensor")
-    shape, stride = table.shape, table.stride()
-    if len(shape) != 2 or (shape[1] > 1 and stride[1] != 1):
+    stride = table.stride()
+    if len(stride) != 2:
+        raise ValueError(f"{name}: expected (sequences, entries)")
+    n, entries = table.shape
+    if entries > 1 and stride[1] != 1:
         raise ValueError(f"{name}: expected (sequences, entries) with contiguous rows")
-    if table.device != device:
+    if table.get_device() != device.index:
         raise ValueError(f"{name}: on {table.device}, the heap is on {device}")
-    n, entries = shape
     return table.data_ptr(), entries, entries if n <= 1 else stride[0], n
 
 
 def _flat(t, name, dtype, numel, device):
     """_tensor's checks, in the order in which they are cheap."""
-    if isinstance(t, _torch.Tensor) and t.dtype is dtype and t.device == device and t.is_contiguous() \
+    if isinstance(t, _Tensor) and t.dtype is dtype and t.get_device() == device.index and t.is_contiguous() \
             and t.numel() >= numel:
         return t.data_ptr()
     return _tensor(t, name, dtype, numel, device)
@@ -554,7 +557,7 @@ def rope_append(symm: Symm, cache: PagedCache, q, k, v, q_out, cos_sin, pos, tab
     per sequence).  q and q_out may be None, q_out may be q, k_out may be k."""
     if _torch is None:
         _attn()
-    dev, i32 = symm.device, _torch.int32
+    dev, i32 = symm.device, _t_i32
     kp, ks, T, Hkv, D = _rows(k, "k", dev)
     if Hkv != cache.Hkv or D != cache.D:
         raise ValueError(f"k: expected heads ({cache.Hkv}, {cache.D}), got ({Hkv}, {D})")
@@ -572,7 +575,7 @@ def rope_append(symm: Symm, cache: PagedCache, q, k, v, q_out, cos_sin, pos, tab
         if like != [T, Hkv, D]:
             raise ValueError(f"k_out {tuple(k_out.shape)} does not fit k {tuple(k.shape)}")
     if cos_sin is not None:
-        csp = _flat(cos_sin, "cos_sin", _torch.float32, 0, dev)
+        csp = _flat(cos_sin, "cos_sin", _t_f32, 0, dev)
         max_pos, rot = cos_sin.shape
         shape = pos.shape
         axes = 1 if len(shape) == 1 else shape[0]
@@ -605,7 +608,7 @@ def prompt_attention(symm: Symm, q, k, v, out, cu_q, cu_k, lse=None, causal=True
     int32 row offsets; lse (Tq, Hq) float32 or None."""
     if _torch is None:
         _attn()
-    dev, i32 = symm.device, _torch.int32
+    dev, i32 = symm.device, _t_i32
     qp, qs, Tq, Hq, D = _rows(q, "q", dev)
     kp, ks, Tk, Hkv, kD = _rows(k, "k", dev)
     vp, vs, *vlike = _rows(v, "v", dev)
@@ -616,7 +619,7 @@ def prompt_attention(symm: Symm, q, k, v, out, cu_q, cu_k, lse=None, causal=True
     cqp = _flat(cu_q, "cu_q", i32, 1, dev)
     B = cu_q.numel() - 1
     ckp = _flat(cu_k, "cu_k", i32, B + 1, dev)
-    lp = 0 if lse is None else _flat(lse, "lse", _torch.float32, Tq * Hq, dev)
+    lp = 0 if lse is None else _flat(lse, "lse", _t_f32, Tq * Hq, dev)
     a = _pack_prompt(Tq, Tk, B, Hq, Hkv, D, qp, kp, vp, qs, ks, vs, op, os_, lp, cqp, ckp,
                      1 if causal else 0, scale)
     rc = _tdg_prompt_attention(symm.h, a, _raw_stream(stream, dev))
@@ -643,8 +646,8 @@ def paged_decode(symm: Symm, cache: PagedCache, q, out, table, lens, part_off: i
     if like != [B, Hq, D] or D != cache.D or n != B:
         raise ValueError(f"q {tuple(q.shape)}, out {tuple(out.shape)} and table {tuple(table.shape)} "
                          f"do not fit together")
-    np_ = _flat(lens, "lens", _torch.int32, B, dev)
-    lp = 0 if lse is None else _flat(lse, "lse", _torch.float32, B * Hq, dev)
+    np_ = _flat(lens, "lens", _t_i32, B, dev)
+    lp = 0 if lse is None else _flat(lse, "lse", _t_f32, B * Hq, dev)
     a = _pack_decode(symm.world, root, *cache.packed, B, Hq, qp, qs, op, os_, lp, tp, te, ts, np_, part_off, scale)
     rc = _tdg_paged_decode(symm.h, a, _raw_stream(stream, dev))
     if rc:
