@@ -232,3 +232,22 @@ def test_keys_shared_by_ctas(symm, D, causal, Hq, Hkv, nq, nk):
     c.check(got, causal)
     again = c.run(symm, causal)
     assert np.array_equal(got[0], again[0]) and np.array_equal(got[1], again[1], equal_nan=True)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("Hq,Hkv,nq,nk", [
+    (48, 48, LENS + [511, 64, 65, 63, 1000], LENS + [511, 64, 65, 63, 1000]),
+    (128, 64, [1, 70, 300, 0, 129, 64, 2, 90, 33, 5, 200, 17], [700, 70, 100, 50, 1000, 0, 65, 222, 33, 64, 1, 128]),
+    (32, 8, [1 + 7 * i % 41 for i in range(300)], [1 + 7 * i % 41 for i in range(300)]),  # more than the table's entries
+])
+def test_many_items(symm, D, causal, Hq, Hkv, nq, nk):
+    # several items for each SM: taken by length, and with heads of 64 by two CTAs an SM
+    c = Case(nq, nk, Hq, Hkv, D, seed=Hq + D, tail=2)
+    bad = 4                              # what one sequence holds is no other's business
+    c.k[c.cu_k[bad]:c.cu_k[bad + 1]] = 0x7FC0
+    c.v[c.cu_k[bad]:c.cu_k[bad + 1]] = 0x7F80
+    got = c.run(symm, causal)
+    c.check(got, causal, some=[b for b in range(len(nq)) if b != bad])
+    again = c.run(symm, causal)
+    assert np.array_equal(got[0], again[0]) and np.array_equal(got[1], again[1], equal_nan=True)

@@ -1,7 +1,7 @@
 // tdg_prompt.cu -- attention over whole prompts packed one after another:
 // softmax(scale Q K^T) V per sequence, causal from the last key back.
 //
-// Mathematics: per query row a running maximum m and sum l over blocks of 128
+// Mathematics: per query row a running maximum m and sum l over blocks of
 // keys, in base 2:  P = 2^(c s - m),  l += sum P,  O += P V,  c = scale log2 e.
 // m follows the row's true maximum only when that has grown by more than 8
 // (a factor of 256): until then P stays below 2^8 and the old m serves as
@@ -11,15 +11,34 @@
 // Work: an item is 256 rows of one key head -- two tiles of 128, each 128/G
 // tokens times the G = Hq/Hkv query heads that share the key head, so a block
 // of keys and values is fetched once for all of them and a tile's causal edge
-// is only 128/G tokens wide.  One persistent CTA per SM:
+// is only 128/G tokens wide.  The grid has a CTA per item, and a CTA that is
+// done takes over one that has not been launched (cluster launch control): no
+// counter in memory, and SMs are busy until the items run out.  Roles:
 //   warps 0-3, 4-7  softmax of tile 0 and 1: a thread owns a row
-//   warp 8          one thread issues tcgen05.mma: S_t = Q_t K^T from shared
-//                   memory, O_t += P_t V with P_t read from TMEM, where the
-//                   softmax left it in S_t's own columns
-//   warp 9          looks items up and loads Q, K and V by TMA
-//   warps 10, 11    idle: they complete the warpgroup that gives registers up
-// TMEM holds S_0, S_1 (128 columns each) and O_0, O_1 (D each).  While the
-// softmax works on one tile, the tensor cores work on the other.
+//   warp 8          issues tcgen05.mma: S_t = Q_t K^T from shared memory,
+//                   O_t += P_t V with P_t read from TMEM, where the softmax
+//                   left it in S_t's own columns
+//   warp 9          finds items, loads Q, K and V by TMA into a ring of 4 slots
+//   warps 10, 11    (one CTA an SM) idle: they complete the warpgroup that
+//                   gives registers up
+// While the softmax works on one tile, the tensor cores work on the other.
+// Blocks are 128 keys with one CTA on an SM.  Heads of 64 with many items take
+// 64 keys and two CTAs an SM instead: their products are half as long, and one
+// CTA's two tiles leave the tensor cores waiting.  Few items of many keys:
+// a cluster of up to 8 CTAs shares an item's keys and joins through
+// distributed shared memory.
+//
+// Bound: 4 D flops per query, key and head on the tensor cores.  Measured on
+// one GB300 (dense peak measured there: 1876 TFLOP/s):
+//   8192 tokens, 64 / 8 heads of 128           635 us, 1730 TFLOP/s, 92 %
+//   1000 behind 7000, 2 x, same heads          333 us, 1505 TFLOP/s; 3.4 items
+//                                              an SM: 85 % of what 4 would take
+//   12 of 17..2311, 40 / 8 heads of 128        214 us, 1200 TFLOP/s: short items,
+//                                              the first and the last block of each
+//   4 of 2048..4096, 32 heads of 64            240 us, 830 TFLOP/s: with weights
+//                                              left as they are 167 us, that is what
+//                                              products of 64 columns reach here
+//   119 tokens, 64 / 8 heads of 128            8.1 us: launch, table, one block
 #include <type_traits>
 
 #include "tdg_paged.cuh"
@@ -27,18 +46,32 @@
 namespace tdg {
 
 namespace pa {
-constexpr int THREADS = 384;
-// registers a thread: 168 at launch; 2 x 208 + 88 = 3 x 168, so the split asks
-// for no more than the launch holds
+// registers a thread, one CTA an SM: 168 at launch; 2 x 208 + 88 = 3 x 168, so
+// the split asks for no more than the launch holds (two CTAs: 96 for all)
 constexpr int REGS_SOFTMAX = 208, REGS_OTHER = 88;
 constexpr int MMA_WARP = 8, LOAD_WARP = 9;
-constexpr int BN = 128;       // keys of a block
 constexpr int CHUNKS = 256;   // entries of the item table
 constexpr int SLOTS = 2;      // items in hand
+// Items go by their length, the longest of all sequences first, when there are
+// several sequences, more items than SMs, and K and V take less than this; else
+// by sequences, the longest first, which share what they read.  By sequence and
+// by length: 8 of 1700 tokens, 8 heads of 64 (28 MB) 57 -> 45 us, 24 of 790, 14 / 2
+// heads of 128 (19 MB) 72 -> 66; but 12 of 17..2311, 8 key heads of 128 (54 MB)
+// 214 -> 219, 16 of 4096 (268 MB) 2880 -> 3460.
+constexpr int64_t BY_LENGTH_BYTES = (int64_t)32 << 20;
+// Heads of 64: two CTAs an SM from this many items for each SM.  One and two:
+// 46 of 350 tokens, 32 / 4 heads (13 items) 84 -> 72 us, 32 of 300..3000, 32 / 8 heads
+// (43 items) 700 -> 555; but 8 of 1700, 8 heads (3 items) 45 -> 58.
+constexpr int TWO_CTAS_ITEMS = 6;
 constexpr int MAX_SPLIT = 8;  // CTAs that share an item's keys
-constexpr uint32_t TMEM_COLS = 512;
 
-template <int D> struct Shape {
+// BLOCK: keys of a block, 128, or 64 where two CTAs share an SM
+template <int D, int BLOCK> struct Shape {
+    static constexpr int BN = BLOCK;
+    static constexpr int CTAS = BN == 64 ? 2 : 1; // of an SM
+    static constexpr int THREADS = BN == 64 ? 320 : 384;
+    static constexpr int O_COL = 2 * BN; // columns of TMEM: S_t begins at t BN, O_t at O_COL + t D
+    static constexpr uint32_t TMEM_COLS = BN == 64 ? 256 : 512;
     static constexpr int HALVES = D / 64;
     static constexpr int Q_BYTES = 128 * D * 2;
     static constexpr int KV_BYTES = BN * D * 2;
@@ -57,6 +90,7 @@ struct PromptParams {
     int causal;
     int split; // CTAs of a cluster that share an item's keys (SPLIT)
     int out32; // rows of out are 32-byte aligned
+    int by_length; // items in the order of their lengths
     float scale_log2;
     __nv_bfloat16 *out;
     float *lse;
@@ -84,9 +118,10 @@ struct PromptCtl {
     volatile int abort;
     uint32_t first[pa::CHUNKS + 1];    // first item of every table entry
     uint16_t order[pa::CHUNKS];        // the sequence of an entry, longest first
+    uint32_t top[pa::CHUNKS];          // length of an entry's longest item, in spans of an item
 };
-template <int D> constexpr int prompt_smem() { return pa::Shape<D>::OFF_CTL + (int)sizeof(PromptCtl); }
-static_assert(prompt_smem<128>() <= 227 * 1024, "shared memory");
+template <int D, int BN> constexpr int prompt_smem() { return pa::Shape<D, BN>::OFF_CTL + (int)sizeof(PromptCtl); }
+static_assert(prompt_smem<128, 128>() <= 227 * 1024 && prompt_smem<64, 64>() <= 113 * 1024, "shared memory");
 
 // Rows of sequence b; false when the offsets are out of order or range (the
 // sequence then counts as empty).
@@ -114,10 +149,10 @@ __device__ __forceinline__ int prompt_most(const PromptParams &p, const PromptIt
     return hi > lo ? prompt_limit(p, it, hi - 1) : 0;
 }
 // The tile's key blocks (SPLIT: those that are this CTA's).
-template <bool SPLIT>
+template <int BN, bool SPLIT>
 __device__ __forceinline__ int prompt_blocks(const PromptParams &p, const PromptItem &it, int t, const PromptShare &share)
 {
-    const int all = (prompt_most(p, it, t) + pa::BN - 1) / pa::BN;
+    const int all = (prompt_most(p, it, t) + BN - 1) / BN;
     return SPLIT ? max(0, min(all, share.hi) - share.lo) : all;
 }
 
@@ -218,6 +253,12 @@ __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_
                  "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
                  : "memory");
 }
+__device__ __forceinline__ void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
 __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16])
 {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
@@ -258,12 +299,13 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b)
     return d;
 }
 
-template <int D, bool SPLIT>
-__global__ void __launch_bounds__(pa::THREADS, 1)
+template <int D, int BN, bool SPLIT>
+__global__ void __launch_bounds__(pa::Shape<D, BN>::THREADS, pa::Shape<D, BN>::CTAS)
     prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant__ CUtensorMap qmap,
                   const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap)
 {
-    using S = pa::Shape<D>;
+    using S = pa::Shape<D, BN>;
+    static_assert(!SPLIT || S::STAGES * S::KV_BYTES >= 256 * D * 4, "the join's rows lie over the ring");
     extern __shared__ __align__(1024) uint8_t smem[];
     PromptCtl *ctl = reinterpret_cast<PromptCtl *>(smem + S::OFF_CTL);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -295,7 +337,7 @@ __global__ void __launch_bounds__(pa::THREADS, 1)
         prefetch_tensormap(&vmap);
     }
     if (warp == pa::MMA_WARP) {
-        tmem_alloc(&ctl->tmem_base, pa::TMEM_COLS);
+        tmem_alloc(&ctl->tmem_base, S::TMEM_COLS);
         tmem_relinquish();
         tc_fence_before();
     }
@@ -305,17 +347,21 @@ __global__ void __launch_bounds__(pa::THREADS, 1)
     // The item table.  Up to CHUNKS sequences: one entry each, the longest
     // first, so that what is left at the end is short; more: runs of
     // sequences in their own order (each is then a small part of the whole).
+    // An entry's items are numbered from its last tokens, and each is one span
+    // shorter than the one before.
     const int64_t per = (p.B + pa::CHUNKS - 1) / pa::CHUNKS;
     const int span = 2 * p.NT; // tokens of an item
     {
         const int i = threadIdx.x;
         const int64_t lo = min(i * per, p.B), hi = i < pa::CHUNKS ? min(lo + per, p.B) : lo;
-        int64_t n = 0;
+        int64_t n = 0, past = 0;
         for (int64_t b = lo; b < hi; ++b) {
             PromptItem it;
             if (!prompt_sequence(p, b, it) && blockIdx.x == 0)
                 report_fault(p.status, TDG_ERR_DEVICE, TDG_WHERE_CU, (uint32_t)b, p.epoch);
             n += (it.Lq + span - 1) / span;
+            if (p.by_length)
+                past = max(0, it.Lk - it.Lq) / span;
         }
         if (i < pa::CHUNKS)
             ctl->first[i] = (uint32_t)n;
@@ -333,6 +379,7 @@ __global__ void __launch_bounds__(pa::THREADS, 1)
                 rank = i;
             }
             ctl->order[rank] = (uint16_t)i;
+            ctl->top[rank] = (uint32_t)(n + past);
         }
         __syncthreads();
         if (warp == 0) { // exclusive sums in that order, 8 entries a lane
@@ -370,13 +417,14 @@ __global__ void __launch_bounds__(pa::THREADS, 1)
     };
 
     if (warp < pa::MMA_WARP) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(pa::REGS_SOFTMAX));
+        if constexpr (S::CTAS == 1)
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(pa::REGS_SOFTMAX));
         const int t = warp >> 2; // tile
         const int r = (warp & 3) * 32 + lane;
-        const int row_tok = r / p.G, row_head = r % p.G;
+        const int row_tok = r / p.G;
         const bool row_used = r < p.NT * p.G;
         const uint32_t lanes = (uint32_t)(warp & 3) * 32 << 16;
-        const uint32_t s_addr = tmem + lanes + t * 128, o_addr = tmem + lanes + 256 + t * 128;
+        const uint32_t s_addr = tmem + lanes + t * BN, o_addr = tmem + lanes + S::O_COL + t * D;
         int slot = 0;
         uint32_t slot_phase = 0, s_phase = 0, o_phase = 0;
         while (true) {
@@ -384,21 +432,12 @@ __global__ void __launch_bounds__(pa::THREADS, 1)
             ok = __all_sync(0xffffffffu, ok);
             if (!ok)
                 break;
-            const PromptItem it = ctl->item[slot];
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&ctl->iempty[slot]);
-            if (++slot == pa::SLOTS) {
-                slot = 0;
-                slot_phase ^= 1u;
-            }
+            const PromptItem &it = ctl->item[slot]; // held to its end: registers are short
             if (!it.valid)
                 break;
             const PromptShare share = SPLIT ? ctl->share : PromptShare{0, 0};
-            const int tile_tok = it.t0 + t * p.NT, tok = tile_tok + row_tok;
-            const int nb = prompt_blocks<SPLIT>(p, it, t, share);
-            const int limit = prompt_limit(p, it, tok);          // keys this row sees
-            const int open = prompt_limit(p, it, tile_tok);      // keys every row of the tile sees
+            const int nb = prompt_blocks<BN, SPLIT>(p, it, t, share);
+            const int open = prompt_limit(p, it, it.t0 + t * p.NT); // keys every row of the tile sees
             float m = -INFINITY, l = 0.f;                        // m: in units of s
             for (int j = 0; j < nb; ++j) {
                 ok = __all_sync(0xffffffffu, wait(&ctl->sfull[t], s_phase, 31));
@@ -406,16 +445,16 @@ __global__ void __launch_bounds__(pa::THREADS, 1)
                     break;
                 s_phase ^= 1u;
                 tc_fence_after();
-                uint32_t s[4][32];
+                uint32_t s[BN / 32][32];
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
+                for (int c = 0; c < BN / 32; ++c)
                     tmem_ld_32x32b_x32(s_addr + c * 32, s[c]);
                 tmem_ld_wait();
-                const int key0 = ((SPLIT ? share.lo : 0) + j) * pa::BN; // the block's first key
-                if (key0 + pa::BN > open) { // the causal edge or the sequence's end runs through this block
-                    const int lim = limit - key0;
+                const int key0 = ((SPLIT ? share.lo : 0) + j) * BN; // the block's first key
+                if (key0 + BN > open) { // the causal edge or the sequence's end runs through this block
+                    const int lim = prompt_limit(p, it, it.t0 + t * p.NT + row_tok) - key0;
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
+                    for (int c = 0; c < BN / 32; ++c) {
                         const int n = lim - c * 32; // of this chunk's 32
                         const uint32_t sees = n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1;
 #pragma unroll
@@ -423,12 +462,15 @@ __global__ void __launch_bounds__(pa::THREADS, 1)
                             s[c][i] = sees >> i & 1 ? s[c][i] : 0xFF800000u; // -inf
                     }
                 }
-                float mx[4] = {__uint_as_float(s[0][0]), __uint_as_float(s[1][0]), __uint_as_float(s[2][0]), __uint_as_float(s[3][0])};
+                float mx[4];
 #pragma unroll
-                for (int c = 1; c < 32; ++c)
+                for (int i = 0; i < 4; ++i)
+                    mx[i] = __uint_as_float(s[i * BN / 128][i * BN / 4 % 32]);
+#pragma unroll
+                for (int c = 1; c < BN / 4; ++c)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        mx[i] = fmaxf(mx[i], __uint_as_float(s[i][c]));
+                        mx[i] = fmaxf(mx[i], __uint_as_float(s[i * BN / 128][i * BN / 4 % 32 + c]));
                 const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                 const bool grown = j > 0 && (top - m) * p.scale_log2 > 8.f; // also from -inf
                 const float al = grown ? exp2_approx((m - top) * p.scale_log2) : 1.f;
@@ -437,16 +479,17 @@ __global__ void __launch_bounds__(pa::THREADS, 1)
                 const float2 c2 = make_float2(p.scale_log2, p.scale_log2), m2 = make_float2(-ms, -ms);
                 float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t w[16];
+                for (int c = 0; c < BN / 16; ++c) {
+                    uint32_t w[8];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float2 x = fma2(make_float2(__uint_as_float(s[c][2 * i]), __uint_as_float(s[c][2 * i + 1])), c2, m2);
+                    for (int i = 0; i < 8; ++i) {
+                        const uint32_t *sc = s[c / 2] + c % 2 * 16 + 2 * i;
+                        const float2 x = fma2(make_float2(__uint_as_float(sc[0]), __uint_as_float(sc[1])), c2, m2);
                         const float2 e = make_float2(exp2_approx(x.x), exp2_approx(x.y));
                         sum[i & 1] = add2(sum[i & 1], e);
                         w[i] = pack_bf16x2(e.x, e.y);
                     }
-                    tmem_st_32x32b_x16(s_addr + c * 16, w);
+                    tmem_st_32x32b_x8(s_addr + c * 8, w);
                 }
                 // O follows a new m only now, off the weights' path.  The block
                 // before has left the tensor cores: its product was issued ahead
@@ -484,12 +527,12 @@ __global__ void __launch_bounds__(pa::THREADS, 1)
             if constexpr (SPLIT) {
                 // This CTA's maximum, sum and output of the row go to shared
                 // memory, the output over the ring, once nothing reads the ring.
-                if (prompt_blocks<SPLIT>(p, it, t ^ 1, share))
+                if (prompt_blocks<BN, SPLIT>(p, it, t ^ 1, share))
                     ok = __all_sync(0xffffffffu, wait(&ctl->ofull[t ^ 1], 0, 32));
                 tc_fence_after();
                 ctl->stat[t][r] = make_float2(nb ? m * p.scale_log2 : -INFINITY, l);
                 float *dst = reinterpret_cast<float *>(smem + S::OFF_KV) + (t * 128 + r) * D;
-                const bool wanted = row_used && tok < it.Lq;
+                const bool wanted = row_used && it.t0 + t * p.NT + row_tok < it.Lq;
 #pragma unroll 1
                 for (int c = 0; nb && c < D; c += 32) {
                     uint32_t o[32];
@@ -500,40 +543,52 @@ __global__ void __launch_bounds__(pa::THREADS, 1)
                         *reinterpret_cast<uint4 *>(dst + (((c / 4 + i) ^ (r & (D / 4 - 1))) * 4)) =
                             make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                 }
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&ctl->iempty[slot]);
+                slot = 1;
                 continue; // the next item is the end
             }
+            const int tok = it.t0 + t * p.NT + row_tok;
             const bool mine = row_used && tok < it.Lq;
-            const bool sees = limit > 0;
+            const bool sees = prompt_limit(p, it, tok) > 0;
             const float f = sees ? 1.f / l : 0.f;
             const int64_t row = (int64_t)it.q0 + tok;
-            const int h = it.g * p.G + row_head;
+            const int h = it.g * p.G + r - row_tok * p.G;
             __nv_bfloat16 *dst = p.out + row * p.os + (int64_t)h * D;
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-                uint32_t o[32];
+            for (int c = 0; c < D; c += 16) {
+                uint32_t o[16];
                 if (nb) {
-                    tmem_ld_32x32b_x32(o_addr + c, o);
+                    tmem_ld_32x32b_x16(o_addr + c, o);
                     tmem_ld_wait();
                 }
-                uint32_t w[16];
+                uint32_t w[8];
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
+                for (int i = 0; i < 8; ++i)
                     w[i] = sees ? pack_bf16x2(__uint_as_float(o[2 * i]) * f, __uint_as_float(o[2 * i + 1]) * f) : 0u;
                 if (mine && p.out32) { // whole 32-byte sectors
                     st_global_32(dst + c, w);
-                    st_global_32(dst + c + 16, w + 8);
                 } else if (mine) {
 #pragma unroll
-                    for (int i = 0; i < 16; i += 4)
+                    for (int i = 0; i < 8; i += 4)
                         *reinterpret_cast<uint4 *>(dst + c + 2 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
                 }
             }
             tc_fence_before(); // the next item's first product writes O after this tile's next pfull
             if (p.lse && mine)
                 p.lse[row * p.Hq + h] = sees ? (m * p.scale_log2 + log2f(l)) * 0.6931471805599453f : -INFINITY;
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&ctl->iempty[slot]);
+            if (++slot == pa::SLOTS) {
+                slot = 0;
+                slot_phase ^= 1u;
+            }
         }
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(pa::REGS_OTHER));
+        if constexpr (S::CTAS == 1)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(pa::REGS_OTHER));
         if (warp == pa::LOAD_WARP) {
             int slot = 0, stage = 0;
             uint32_t slot_phase = 0, phase = 0, q_phase[2] = {0, 0}, tail_phase = 0;
@@ -541,6 +596,10 @@ __global__ void __launch_bounds__(pa::THREADS, 1)
             bool ok = true;
             uint32_t steal_phase = 0;
             int64_t idx = SPLIT ? blockIdx.x / p.split : blockIdx.x;
+            int longest = 0;
+            for (int j = lane; p.by_length && j < (int)p.B; j += 32)
+                longest = max(longest, (int)ctl->top[j]);
+            longest = __reduce_max_sync(0xffffffffu, longest);
             PromptShare share = {0, 0};
             while (true) {
                 PromptItem it;
@@ -548,14 +607,52 @@ __global__ void __launch_bounds__(pa::THREADS, 1)
                 if (idx >= items) {
                     it.Lq = it.Lk = it.t0 = 0; // the grid is an upper bound of the items: skip
                 } else if (it.valid) {
-                    // the table entry: the last one whose first item is not behind
                     const uint32_t unit = (uint32_t)idx / (uint32_t)p.Hkv;
-                    int e = 0;
+                    int e = 0, left;
+                    if (p.by_length) {
+                        // items of at least x spans, in all entries
+                        auto count = [&](int x) -> uint32_t {
+                            int n = 0;
+                            for (int j = lane; j < (int)p.B; j += 32)
+                                n += max(0, min((int)ctl->top[j] - x + 1, (int)(ctl->first[j + 1] - ctl->first[j])));
+                            return __reduce_add_sync(0xffffffffu, (uint32_t)n);
+                        };
+                        // the item's length: the largest x with more than `unit` items
+                        int x = 1, hi = longest;
+                        uint32_t longer = 0;
+                        while (x < hi) {
+                            const int mid = (x + hi + 1) / 2;
+                            const uint32_t c = count(mid);
+                            if (c > unit) {
+                                x = mid;
+                            } else {
+                                hi = mid - 1;
+                                longer = c;
+                            }
+                        }
+                        // the entry: one of those that have an item of this length
+                        int skip = (int)(unit - longer);
+                        for (int j = 0; j < (int)p.B; j += 32) {
+                            const int top = (int)ctl->top[j + lane], n = (int)(ctl->first[j + lane + 1] - ctl->first[j + lane]);
+                            const bool has = top - n < x && x <= top;
+                            const uint32_t own = __ballot_sync(0xffffffffu, has);
+                            const bool it_is = has && __popc(own & ((1u << lane) - 1)) == skip;
+                            const uint32_t found = __ballot_sync(0xffffffffu, it_is);
+                            if (found) {
+                                e = j + __ffs(found) - 1;
+                                break;
+                            }
+                            skip -= __popc(own);
+                        }
+                        left = (int)ctl->top[e] - x;
+                    } else {
+                        // the table entry: the last one whose first item is not behind
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        e += __popc(__ballot_sync(0xffffffffu, ctl->first[j * 32 + lane] <= unit));
-                    --e;
-                    int left = (int)(unit - ctl->first[e]);
+                        for (int j = 0; j < 8; ++j)
+                            e += __popc(__ballot_sync(0xffffffffu, ctl->first[j * 32 + lane] <= unit));
+                        --e;
+                        left = (int)(unit - ctl->first[e]);
+                    }
                     int64_t b = (int64_t)ctl->order[e] * per;
                     const int64_t end = min(b + per, p.B);
                     int n = 0;
@@ -571,7 +668,8 @@ __global__ void __launch_bounds__(pa::THREADS, 1)
                     it.g = (int)((uint32_t)idx % (uint32_t)p.Hkv);
                     it.t0 = max(0, n - 1 - left) * span; // the last tokens, which see the most, first
                     if (SPLIT) { // this CTA's share of the key blocks
-                        const int all = max(prompt_blocks<false>(p, it, 0, share), prompt_blocks<false>(p, it, 1, share)), rank = (int)cluster_ctarank();
+                        const int all = max(prompt_blocks<BN, false>(p, it, 0, share), prompt_blocks<BN, false>(p, it, 1, share));
+                        const int rank = (int)cluster_ctarank();
                         share.lo = all * rank / p.split;
                         share.hi = all * (rank + 1) / p.split;
                     }
@@ -600,7 +698,8 @@ __global__ void __launch_bounds__(pa::THREADS, 1)
                     mbar_arrive_expect_tx(&ctl->steal, sizeof(uint4));
                     steal_request(&ctl->stolen, &ctl->steal);
                 }
-                const int nb0 = prompt_blocks<SPLIT>(p, it, 0, share), nb1 = prompt_blocks<SPLIT>(p, it, 1, share), nb = max(nb0, nb1);
+                const int nb0 = prompt_blocks<BN, SPLIT>(p, it, 0, share), nb1 = prompt_blocks<BN, SPLIT>(p, it, 1, share);
+                const int nb = max(nb0, nb1);
                 if (lane == 0) {
                     for (int t = 0; t < 2 && ok; ++t)
                         if (t == 0 ? nb0 : nb1) {
@@ -619,10 +718,11 @@ __global__ void __launch_bounds__(pa::THREADS, 1)
                 for (int j = 0; j < nb && ok; ++j)
                     for (int kv = 0; kv < 2 && ok; ++kv) {
                         uint8_t *dst = smem + S::OFF_KV + stage * S::KV_BYTES;
-                        const int key0 = ((SPLIT ? share.lo : 0) + j) * pa::BN, rows = it.Lk - key0; // keys of this block that are the sequence's own
+                        const int key0 = ((SPLIT ? share.lo : 0) + j) * BN;
+                        const int rows = it.Lk - key0; // keys of this block that are the sequence's own
                         // values behind the sequence's end are cleared: weight 0 times
                         // whatever the neighbour holds must be 0
-                        const bool clear = kv == 1 && rows < pa::BN;
+                        const bool clear = kv == 1 && rows < BN;
                         if (lane == 0) {
                             ok = wait(&ctl->kvempty[stage], phase ^ 1u, 12);
                             if (ok) {
@@ -641,7 +741,7 @@ __global__ void __launch_bounds__(pa::THREADS, 1)
                             const bool landed = wait(&ctl->tail, tail_phase, 13);
                             tail_phase ^= 1u;
                             __syncwarp();
-                            for (int i = rows * 8 + lane; i < pa::BN * 8; i += 32)
+                            for (int i = rows * 8 + lane; i < BN * 8; i += 32)
 #pragma unroll
                                 for (int hf = 0; hf < S::HALVES; ++hf)
                                     *reinterpret_cast<uint4 *>(dst + hf * 16384 + i * 16) = make_uint4(0, 0, 0, 0);
@@ -682,28 +782,29 @@ __global__ void __launch_bounds__(pa::THREADS, 1)
             }
             __syncwarp();
         } else if (warp == pa::MMA_WARP) {
-            constexpr uint32_t idesc_s = idesc_bf16(128, pa::BN, 0), idesc_o = idesc_bf16(128, D, 1);
+            constexpr uint32_t idesc_s = idesc_bf16(128, BN, 0), idesc_o = idesc_bf16(128, D, 1);
             const uint32_t base = smem_u32(smem), leader = elect_one();
             int slot = 0, stage = 0;
             uint32_t slot_phase = 0, phase = 0, q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
-            // (all 512 columns of TMEM are this CTA's: they begin at column 0)
+            // (a CTA that has all 512 columns of TMEM has them from column 0)
+            const uint32_t s_col = S::CTAS == 1 ? 0u : __reduce_max_sync(0xffffffffu, tmem), o_col = s_col + S::O_COL;
             // S_t = Q_t K^T: both K-major, 16 elements are 32 bytes, 64 are a half
             auto qk = [&](int t, int st) {
                 const uint32_t a = sdesc_lo(base + t * S::Q_BYTES, 16), b = sdesc_lo(base + S::OFF_KV + st * S::KV_BYTES, 16);
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
                     const uint32_t off = (k / 4) * 1024 + (k % 4) * 2;
-                    umma_ss(leader, t * 128, a + off, b + off, idesc_s, k != 0 ? 1u : 0u);
+                    umma_ss(leader, s_col + t * BN, a + off, b + off, idesc_s, k != 0 ? 1u : 0u);
                 }
                 umma_commit_if(leader, &ctl->sfull[t]);
             };
-            // O_t += P_t V: P_t is 64 columns of bf16 pairs over S_t; V is
+            // O_t += P_t V: P_t is bf16 pairs over S_t; V is
             // MN-major: halves of 64 dimensions 16 KB apart, 16 keys are 2 KB
             auto pv = [&](int t, int st, uint32_t first) {
                 const uint32_t b = sdesc_lo(base + S::OFF_KV + st * S::KV_BYTES, 16384);
 #pragma unroll
-                for (int k = 0; k < pa::BN / 16; ++k)
-                    umma_ts(leader, 256 + t * 128, t * 128 + k * 8, b + k * 128, idesc_o, k != 0 ? 1u : first ^ 1u);
+                for (int k = 0; k < BN / 16; ++k)
+                    umma_ts(leader, o_col + t * D, s_col + t * BN + k * 8, b + k * 128, idesc_o, k != 0 ? 1u : first ^ 1u);
             };
             // the same for the first `cols` keys of a block (a multiple of 16)
             auto qk_part = [&](int t, int st, int cols) {
@@ -712,7 +813,7 @@ __global__ void __launch_bounds__(pa::THREADS, 1)
 #pragma unroll 1
                 for (int k = 0; k < D / 16; ++k) {
                     const uint32_t off = (k / 4) * 1024 + (k % 4) * 2;
-                    umma_ss(leader, t * 128, a + off, b + off, idesc, k != 0 ? 1u : 0u);
+                    umma_ss(leader, s_col + t * BN, a + off, b + off, idesc, k != 0 ? 1u : 0u);
                 }
                 umma_commit_if(leader, &ctl->sfull[t]);
             };
@@ -720,7 +821,7 @@ __global__ void __launch_bounds__(pa::THREADS, 1)
                 const uint32_t b = sdesc_lo(base + S::OFF_KV + st * S::KV_BYTES, 16384);
 #pragma unroll 1
                 for (int k = 0; k < cols / 16; ++k)
-                    umma_ts(leader, 256 + t * 128, t * 128 + k * 8, b + k * 128, idesc_o, k != 0 ? 1u : first ^ 1u);
+                    umma_ts(leader, o_col + t * D, s_col + t * BN + k * 8, b + k * 128, idesc_o, k != 0 ? 1u : first ^ 1u);
             };
             auto next = [&](int &st, uint32_t &ph) {
                 if (++st == S::STAGES) {
@@ -750,14 +851,14 @@ __global__ void __launch_bounds__(pa::THREADS, 1)
                     break;
                 const int keys[2] = {__reduce_max_sync(0xffffffffu, prompt_most(p, it, 0)),
                                      __reduce_max_sync(0xffffffffu, prompt_most(p, it, 1))};
-                int lo = 0, nb[2] = {(keys[0] + pa::BN - 1) / pa::BN, (keys[1] + pa::BN - 1) / pa::BN};
+                int lo = 0, nb[2] = {(keys[0] + BN - 1) / BN, (keys[1] + BN - 1) / BN};
                 if constexpr (SPLIT) {
                     lo = __reduce_max_sync(0xffffffffu, ctl->share.lo);
                     const int hi = __reduce_max_sync(0xffffffffu, ctl->share.hi);
                     nb[0] = max(0, min(nb[0], hi) - lo);
                     nb[1] = max(0, min(nb[1], hi) - lo);
                 }
-                auto cols = [&](int t, int j) -> int { return min(pa::BN, (keys[t] - (lo + j) * pa::BN + 15) & ~15); };
+                auto cols = [&](int t, int j) -> int { return min(BN, (keys[t] - (lo + j) * BN + 15) & ~15); };
                 const int most = max(nb[0], nb[1]);
                 if (!most)
                     continue;
@@ -855,7 +956,7 @@ __global__ void __launch_bounds__(pa::THREADS, 1)
     __syncthreads();
     if (warp == pa::MMA_WARP) {
         tc_fence_after();
-        tmem_dealloc(tmem, pa::TMEM_COLS);
+        tmem_dealloc(tmem, S::TMEM_COLS);
     }
     if constexpr (SPLIT) {
         // join the cluster's shares: every CTA takes 256 / split rows, four
@@ -956,30 +1057,36 @@ extern "C" int tdg_prompt_attention(tdg_symm *h, const tdg_prompt_attention_args
     p.lse = a->lse;
     p.cu_q = a->cu_q;
     p.cu_k = a->cu_k;
+    const bool two = D == 64 && items >= (int64_t)pa::TWO_CTAS_ITEMS * h->sm_count;
+    const uint32_t bn = two ? 64 : 128;
+    p.by_length = a->B > 1 && a->B <= pa::CHUNKS && items > h->sm_count && a->Tk * Hkv * D * 4 < pa::BY_LENGTH_BYTES;
     CUtensorMap qm, km, vm;
     // rows of heads: {D, heads, rows}; a box is 64 dimensions of a tile's heads and tokens
     if (!map_bf16_3d(&qm, a->q, D, Hq, a->Tq, D * 2, a->q_stride * 2, 64, (uint32_t)p.G, (uint32_t)p.NT))
         return TDG_ERR_CUDA;
     km = vm = qm; // no keys: nothing is loaded through them
-    if (a->Tk && (!map_bf16_3d(&km, a->k, D, Hkv, a->Tk, D * 2, a->k_stride * 2, 64, 1, pa::BN) ||
-                  !map_bf16_3d(&vm, a->v, D, Hkv, a->Tk, D * 2, a->v_stride * 2, 64, 1, pa::BN)))
+    if (a->Tk && (!map_bf16_3d(&km, a->k, D, Hkv, a->Tk, D * 2, a->k_stride * 2, 64, 1, bn) ||
+                  !map_bf16_3d(&vm, a->v, D, Hkv, a->Tk, D * 2, a->v_stride * 2, 64, 1, bn)))
         return TDG_ERR_CUDA;
     // Few items of many keys: up to 8 CTAs share an item's keys, as many as the
     // SMs allow, if an average sequence's item is spared 8 blocks by it (a block
     // is 1.2 us of an item, the cluster and its join cost 5 to 6 us).
-    const int64_t room = h->sm_count / items, blocks = a->Tk / a->B / pa::BN;
+    const int64_t room = h->sm_count / items, blocks = a->Tk / a->B / 128;
     p.split = room >= 8 ? 8 : room >= 4 ? 4 : room >= 2 ? 2 : 1;
     if (blocks - blocks / p.split < 8)
         p.split = 1;
-    const void *fn = D == 128 ? (p.split > 1 ? reinterpret_cast<const void *>(&prompt_kernel<128, true>)
-                                             : reinterpret_cast<const void *>(&prompt_kernel<128, false>))
-                              : (p.split > 1 ? reinterpret_cast<const void *>(&prompt_kernel<64, true>)
-                                             : reinterpret_cast<const void *>(&prompt_kernel<64, false>));
-    const int smem = D == 128 ? prompt_smem<128>() : prompt_smem<64>();
+    const bool split = p.split > 1;
+    const void *fn = D == 128 ? (split ? reinterpret_cast<const void *>(&prompt_kernel<128, 128, true>)
+                                       : reinterpret_cast<const void *>(&prompt_kernel<128, 128, false>))
+                     : two    ? reinterpret_cast<const void *>(&prompt_kernel<64, 64, false>)
+                     : split  ? reinterpret_cast<const void *>(&prompt_kernel<64, 128, true>)
+                              : reinterpret_cast<const void *>(&prompt_kernel<64, 128, false>);
+    const int smem = D == 128 ? prompt_smem<128, 128>() : two ? prompt_smem<64, 64>() : prompt_smem<64, 128>();
     if (const cudaError_t e = set_smem(fn, smem); e != cudaSuccess)
         return cuda_err(e, "prompt attention smem");
     void *args[] = {&p, &qm, &km, &vm};
-    return cuda_err(launch(fn, dim3((unsigned)(items * p.split)), dim3(pa::THREADS), smem, static_cast<cudaStream_t>(stream), args,
-                           false, p.split, true),
+    const int threads = two ? pa::Shape<64, 64>::THREADS : pa::Shape<64, 128>::THREADS;
+    return cuda_err(launch(fn, dim3((unsigned)(items * p.split)), dim3(threads), smem, static_cast<cudaStream_t>(stream), args, false,
+                           p.split, true),
                     "prompt attention launch");
 }
