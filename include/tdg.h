@@ -1,6 +1,8 @@
 /*
  * tdg.h -- C ABI of libtdg: tile-centric overlapped AllGather+GEMM,
- * GEMM+ReduceScatter and MoE dispatch/combine on one GB300 (sm_103a).
+ * GEMM+ReduceScatter and MoE dispatch/combine, and the attention of a serving
+ * step (rotary positions, packed prompts, a paged cache) on one GB300
+ * (sm_103a).
  *
  * Model.  W logical ranks live in ONE device allocation that the caller owns:
  * W equal "regions" (rank r's symmetric heap) followed by W signal areas and
@@ -518,7 +520,8 @@ TDG_API size_t tdg_paged_pool_bytes(int64_t pages, int page_size, int64_t Hkv, i
  * rot_dim a multiple of 16, at most D; sections non-negative with the sum
  * rot_dim/2; strides multiples of 8 elements and at least the row's extent;
  * device pointers 16-byte aligned (pos, cu, table, lens, scales 4-byte); the
- * table as for tdg_paged_decode.  T == 0 is a no-op.  The cache's D and Hkv describe k also when table is NULL.
+ * table as for tdg_paged_decode.  T == 0 is a no-op.  The cache's D and Hkv
+ * describe k also when table is NULL.
  */
 typedef struct {
     int world;
@@ -589,11 +592,12 @@ TDG_API int tdg_prompt_attention(tdg_symm *h, const tdg_prompt_attention_args *a
  *   out[b][h] = sum_j softmax_j(scale * q[b][h] . k_j) v_j,  g = h / (Hq/Hkv).
  * A sequence of length 0 gives 0, and -inf in lse (NULL or B x Hq float32, the
  * natural logarithm of the sum of exponentials).  The work is divided evenly
- * over the GPU whatever the lengths: it is cut into 64-token tiles, and every
- * CTA takes an equal run of them, so long sequences are split and short ones
- * grouped.  Partial results (row maximum, row sum, unnormalised output,
- * float32) go to region(root) + part_off (tdg_paged_decode_part_bytes), and a
- * second, stream-ordered launch joins the split ones in a fixed order.
+ * over the GPU whatever the lengths: it is cut into tiles of 64 tokens (128 of
+ * an 8-bit cache), and every CTA takes an equal run of them, so long sequences
+ * are split and short ones grouped.  Partial results (row maximum, row sum,
+ * unnormalised output, float32) go to region(root) + part_off
+ * (tdg_paged_decode_part_bytes), and a second, stream-ordered launch joins the
+ * split ones in a fixed order.
  * What the pages hold behind a sequence's length never reaches a result.
  * A negative length, one that does not fit the table row, or a page id
  * outside the pools is reported as TDG_ERR_DEVICE (TDG_WHERE_PAGE, index b);

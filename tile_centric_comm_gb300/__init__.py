@@ -1,5 +1,6 @@
 """tile_centric_comm_gb300 -- tile-centric overlapped AllGather+GEMM,
-GEMM+ReduceScatter and MoE dispatch/combine for GB300 (sm_103a).
+GEMM+ReduceScatter, MoE dispatch/combine and the attention of a serving step
+for GB300 (sm_103a).
 
 The compute path is the CUDA library ``libtdg.so`` (C ABI declared in
 ``include/tdg.h``); ``tile_centric_comm_gb300.tdg`` is its thin ctypes binding.

@@ -10,6 +10,10 @@
 // dependent loads, paid once per group) and put the rows' cosines and sines
 // into shared memory; then they walk over all (row, head) pairs of the group,
 // 16 elements a thread, four pairs' loads in flight at a time.
+//
+// Measured on one GB300, 64 / 8 heads of 128: 9 prompts of 301..4093 tokens (927 MB)
+// 159 us, 5.8 TB/s (a copy makes 6.8 here, a stream that is half writes 6.0);
+// 256 tokens into an 8-bit cache 4.9 us and one token 3.8 us: launch and lookups.
 #include "tdg_paged.cuh"
 
 namespace tdg {
