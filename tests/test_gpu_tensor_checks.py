@@ -1,0 +1,45 @@
+"""The binding's native tensor checks give what the Python ones give, value or error."""
+import pytest
+import torch
+
+from tile_centric_comm_gb300 import tdg
+
+pytestmark = pytest.mark.gpu
+
+
+def _both(native, checked, *args):
+    def outcome(f):
+        try:
+            return f(*args)
+        except (TypeError, ValueError) as e:
+            return type(e), str(e)
+    got, want = outcome(native), outcome(checked)
+    assert got == want
+    return got
+
+
+def test_same_outcomes():
+    tdg._attn()
+    dev = tdg.Symm(1, 1024, 16).device
+    bf, i32, f32 = torch.bfloat16, torch.int32, torch.float32
+    x = torch.zeros(6, 12, 64, dtype=bf, device="cuda")
+    wide = torch.zeros(6, 12 * 64 + 8, dtype=bf, device="cuda")[:, :768].unflatten(1, (12, 64))
+    good = [x, wide, wide[:1], wide[:0], x[:, 2:5], x[:, :1], x[::2], x[1:], torch.nn.Parameter(x),
+            torch.zeros(0, 12, 64, dtype=bf, device="cuda"), torch.zeros(6, 0, 64, dtype=bf, device="cuda"),
+            x.expand(6, 12, 64), x[:1].expand(6, 12, 64)]
+    bad = [x.float(), x.cpu(), x[0], x.transpose(0, 1), x[:, ::2], x[:, :, ::2], x[:, :, :1], None, 3, x.unsqueeze(0), [1.0]]
+    for t in good:
+        assert isinstance(_both(tdg._rows, tdg._checked_rows, t, "x", dev)[0], int)
+    for t in bad:
+        assert isinstance(_both(tdg._rows, tdg._checked_rows, t, "x", dev)[0], type)
+
+    m = torch.zeros(5, 9, dtype=i32, device="cuda")
+    for t in [m, m[:, :4], m[:1], m[:, :1], m[:0], m[::2], m[:1, 3:]]:
+        assert isinstance(_both(tdg._table, tdg._checked_table, t, "m", dev)[0], int)
+    for t in [m.long(), m.cpu(), m[0], m.t(), m[:, ::2], None]:
+        assert isinstance(_both(tdg._table, tdg._checked_table, t, "m", dev)[0], type)
+
+    for t, kind, n in [(m, i32, 45), (m[0], i32, 9), (m[1:3], i32, 0), (m[:0], i32, 0), (x.float(), f32, 1)]:
+        assert isinstance(_both(tdg._flat, tdg._checked_flat, t, "t", kind, n, dev), int)
+    for t, kind, n in [(m, i32, 46), (m, f32, 1), (m[:, :4], i32, 1), (m.cpu(), i32, 1), (None, i32, 0), ("m", i32, 0)]:
+        assert isinstance(_both(tdg._flat, tdg._checked_flat, t, "t", kind, n, dev), tuple)

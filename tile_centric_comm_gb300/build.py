@@ -5,22 +5,27 @@
 Each .cu under csrc/ is compiled in parallel with nvcc (one -gencode, sm_103a),
 then linked into tile_centric_comm_gb300/_build/libtdg.so with the static CUDA
 runtime, so the library has no load-time dependency on libcuda (the driver
-entry points it needs are looked up at run time).
+entry points it needs are looked up at run time).  csrc/tdg_tensors.cpp,
+the binding's tensor checks, becomes a CPython module beside it (g++, against
+torch's headers).
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libtdg.so")
+TENSORS = os.path.join(BUILD, "tdg_tensors.so")
 INCLUDE = os.path.join(ROOT, "include")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -51,12 +56,29 @@ def _stale(target, inputs):
     return any(os.path.getmtime(i) > t for i in inputs)
 
 
+def build_tensors(force: bool = False) -> str:
+    src = os.path.join(CSRC, "tdg_tensors.cpp")
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    headers = os.path.join(torch, "include")
+    if force or _stale(TENSORS, [src, os.path.join(torch, "version.py")]):
+        tmp = TENSORS + f".tmp{os.getpid()}"
+        cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-w", "-I", sysconfig.get_path("include"),
+               "-I", headers, "-I", os.path.join(headers, "torch", "csrc", "api", "include"), src, "-o", tmp,
+               "-L", os.path.join(torch, "lib"), "-lc10", "-ltorch_cpu", "-ltorch_python"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"g++ failed for tdg_tensors.cpp:\n{r.stderr}")
+        os.replace(tmp, TENSORS)
+    return TENSORS
+
+
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = _sources()
     deps = _deps()
     objs = [os.path.join(BUILD, os.path.basename(s)[:-3] + ".o") for s in srcs]
     if not force and not _stale(LIB, srcs + deps):
+        build_tensors(force)
         return LIB
     cc = nvcc()
 
@@ -70,10 +92,12 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
             raise RuntimeError(f"nvcc failed for {os.path.basename(src)}:\n{r.stderr}")
         return obj, r.stderr
 
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 4))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 4))) as ex:
+        tensors = ex.submit(build_tensors, force)
         for obj, err in ex.map(compile_one, zip(srcs, objs)):
             if verbose and err:
                 print(err, file=sys.stderr)
+        tensors.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [cc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)

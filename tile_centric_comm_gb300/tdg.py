@@ -9,12 +9,15 @@ is no fallback.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import struct
 import threading
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "_build", "libtdg.so")
+TENSORS_PATH = os.path.join(HERE, "_build", "tdg_tensors.so")
 
 TDG_OK = 0
 TDG_ERR_INVALID = -1
@@ -462,16 +465,24 @@ class PagedCache:
         return symm.view(rank, self.k_off, shape, kind), symm.view(rank, self.v_off, shape, kind)
 
 
-_torch = _current_raw_stream = None
+_torch = _current_raw_stream = _rows = _table = _flat = None
 
 
 def _attn():
     """torch, and the library's attention entry points taking packed arguments
     (one struct.pack call costs a fraction of filling a ctypes structure field
     by field, and these calls are short)."""
-    global _torch, _current_raw_stream, _Tensor, _t_bf16, _t_i32, _t_f32
+    global _torch, _current_raw_stream, _rows, _table, _flat, _Tensor, _t_bf16, _t_i32, _t_f32
     import torch
     L = lib()
+    if not os.path.exists(TENSORS_PATH):
+        raise RuntimeError(f"tdg_tensors.so not found at {TENSORS_PATH}: build it with "
+                           "`python -m tile_centric_comm_gb300.build`")
+    loader = importlib.machinery.ExtensionFileLoader("tdg_tensors", TENSORS_PATH)
+    checks = importlib.util.module_from_spec(importlib.util.spec_from_loader("tdg_tensors", loader))
+    loader.exec_module(checks)
+    checks.setup(torch.Tensor, _checked_rows, _checked_table, _checked_flat)
+    _rows, _table, _flat = checks.rows, checks.table, checks.flat
     fast = ctypes.CDLL(LIB_PATH)
     for name in ("tdg_rope_append", "tdg_prompt_attention", "tdg_paged_decode"):
         f = getattr(fast, name)
@@ -498,7 +509,9 @@ def _raw_stream(stream, device):
         _torch.cuda.current_stream(device).cuda_stream
 
 
-def _rows(t, name, device):
+# csrc/tdg_tensors.cpp does the same checks for tensors that pass them and calls
+# these for those that do not
+def _checked_rows(t, name, device):
     """Check rows of heads, (rows, heads, D) in bf16, whose rows may be strided
     (columns of a wider buffer); returns (pointer, row stride in elements, rows,
     heads, D)."""
@@ -522,7 +535,7 @@ def _rows(t, name, device):
     return t.data_ptr(), s0, n, heads, D
 
 
-def _table(table, name, device):
+def _checked_table(table, name, device):
     """Check a page table (sequences, entries), int32, rows possibly strided;
     returns (pointer, entries, row stride, sequences)."""
     if not isinstance(table, _Tensor) or table.dtype is not _t_i32:
@@ -538,7 +551,7 @@ def _table(table, name, device):
     return table.data_ptr(), entries, entries if n <= 1 else stride[0], n
 
 
-def _flat(t, name, dtype, numel, device):
+def _checked_flat(t, name, dtype, numel, device):
     """_tensor's checks, in the order in which they are cheap."""
     if isinstance(t, _Tensor) and t.dtype is dtype and t.get_device() == device.index and t.is_contiguous() \
             and t.numel() >= numel:
