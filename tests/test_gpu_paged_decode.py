@@ -195,3 +195,47 @@ def test_refusals():
         tdg.paged_decode(c.symm, c.cache, q.half(), out, c.table_d, c.lens_d, c.part_off)
     torch.cuda.synchronize()
     assert c.symm.status()["code"] == 0
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("page,Hq,Hkv", [(16, 8, 1), (64, 14, 2), (256, 40, 2), (32, 24, 24)])
+def test_lengths_in_a_wide_table(D, e4m3, page, Hq, Hkv):
+    # a table for far longer sequences: no cluster takes a pair, equal runs of the line are taken
+    lens = [0, 1, 2, 15, 16, 17, 31, 63, 64, 65, 127, 128, 129, 200, 0, 257, 500, 900, 3, 64, 0]
+    c = Cache(2, lens, Hkv, D, page, e4m3, seed=Hq + D, extra_entries=16384 // page)
+    got = run_case(c, Hq, seed=Hq)
+    check_case(c, Hq, got)
+    again = run_case(c, Hq, seed=Hq)
+    assert all(np.array_equal(a, b) for a, b in zip(got, again))
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("Hkv,lens", [
+    (1, [1]), (1, [65]), (1, [128]), (1, [129]), (1, [500]), (2, [511, 64]), (3, [1000, 0, 1, 777]),
+    (8, [100] * 9 + [0, 128]), (19, [130, 64]), (37, [300, 0]), (150, [70, 129]),
+])
+def test_clusters(e4m3, Hkv, lens):
+    # from 8 CTAs a pair to one, with more CTAs than tiles, and with empty sequences
+    c = Cache(1, lens, Hkv, 128, 16, e4m3, seed=Hkv)
+    got = run_case(c, 4 * Hkv, seed=Hkv)
+    check_case(c, 4 * Hkv, got)
+
+
+@pytest.mark.parametrize("what", ["negative", "long", "page"])
+def test_bad_indices_in_a_wide_table(what):
+    c = Cache(2, [90, 300], 2, 128, 16, seed=8, extra_entries=1024)
+    if what == "negative":
+        c.lens_d[0] = -5
+    elif what == "long":
+        c.lens_d[0] = 16 * c.table.shape[1] + 1
+    else:
+        c.table_d[0, 2] = 2 * c.pages
+    q = torch.zeros((2, 8, 128), dtype=torch.bfloat16, device="cuda")
+    out = torch.empty_like(q)
+    tdg.paged_decode(c.symm, c.cache, q, out, c.table_d, c.lens_d, c.part_off)
+    torch.cuda.synchronize()
+    st = c.symm.status()
+    assert st["code"] == tdg.TDG_ERR_DEVICE and st["where"] == "page" and st["index"] == 0
+    k, v = c.sequence(1)
+    check_attention(to_bits(out)[1:], oracle.attention(np.zeros((1, 8, 128)), k, v), 128)

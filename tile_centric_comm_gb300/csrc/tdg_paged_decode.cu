@@ -14,10 +14,12 @@
 // a page is read once for all of them.
 //
 // Split: the (sequence, key head) pairs' tiles (64 tokens; 128 of an 8-bit
-// cache) form one long line, and each of the two CTAs per SM takes an equal run
-// of it, wherever it begins and ends: ragged lengths leave no SM idle, and the
-// partial results are at most two per CTA whatever the lengths.  A second
-// launch joins the split pairs.
+// cache) form one long line, in which a pair also counts for the tiles that its
+// beginning and end cost, and each of the two CTAs per SM takes an equal run of
+// it, wherever it begins and ends: ragged lengths leave no SM idle, and the
+// partial results are at most two per CTA whatever the lengths.  A second launch
+// joins the split pairs.  When the pairs are few and short, a cluster takes each
+// one and joins through distributed shared memory, in one launch.
 //
 // In a CTA, warp 4 looks up page ids and issues one TMA copy per page (or
 // tile) for K and for V into a ring of stages; warps 0-3 each take 16 tokens
@@ -28,12 +30,12 @@
 //
 // Measured on one GB300 (copy rate 6.79 TB/s), 64 / 8 heads of 128, both launches:
 //   2 sequences of 200,000..262,144          288 us, 7.0 TB/s
-//   64 of 1..8192, pages of 16               176 us, 6.6 TB/s
-//   128 of 2048..4096, 8-bit                 149 us, 5.3 TB/s: the conversions
+//   64 of 1..8192, pages of 16               174 us, 6.6 TB/s
+//   128 of 2048..4096, 8-bit                 144 us, 5.5 TB/s: the conversions
 //                                            e4m3 -> f16 -> bf16 and what waits
 //                                            for them; three CTAs an SM spill
-//   one sequence of 1000                     8.5 to 9.4 us: two launches, two
-//                                            dependent round trips in each
+//   64 of 1..512                             19 us, 4.3 TB/s: pairs of a few tiles
+//   one sequence of 1000 (a cluster a pair)  7.3 us: launch, lookups, two tiles
 #include <cuda_fp16.h>
 
 #include "tdg_paged.cuh"
@@ -47,8 +49,13 @@ constexpr int MAX_CTAS = 512;                 // CTAs whose partial results the 
 constexpr int ROWS = 16;                      // query heads of a partial result
 constexpr int JOIN_ROWS = 2;                  // rows of a join CTA
 constexpr int JOIN_THREADS = 256;
-constexpr int MERGE_COLS = 32;                // columns of one merge phase
 constexpr int BAR_BYTES = 384;
+constexpr int MAX_SPLIT = 8;                  // CTAs of a cluster (PAIRS)
+// What a pair costs beside its tiles, in tiles: its queries and the join of the
+// four warps.  With runs equal in tiles alone the CTAs of the short sequences were
+// the last: 64 sequences of 1..512 27.5 us, 19 with 2 (20.9 with 1, 18.7 with 3),
+// 128 of 2048..4096 in 8 bits 144.5 (146.1 with 3).
+constexpr int PAIR_UNITS = 2;
 
 template <int D, bool E4M3> struct Shape {
     static constexpr int ESZ = E4M3 ? 1 : 2;
@@ -60,9 +67,13 @@ template <int D, bool E4M3> struct Shape {
     static constexpr int STAGES = KV >= 16384 ? 3 : 6;
     static constexpr int Q_BYTES = ROWS * D * 2;
     static constexpr int OFF_Q = STAGES * 2 * KV;
-    static constexpr int OFF_MERGE = OFF_Q + 2 * Q_BYTES;
-    static constexpr int OFF_ML = OFF_MERGE + WARPS * ROWS * MERGE_COLS * 4;
-    static constexpr int OFF_BAR = OFF_ML + WARPS * ROWS * 2 * 4;
+    static constexpr int ML_FLOATS = WARPS * ROWS * 2;        // the warps' maxima and sums of a pair
+    static constexpr int OFF_ML = OFF_Q + 2 * Q_BYTES;
+    static constexpr int OFF_BAR = OFF_ML + 2 * ML_FLOATS * 4;
+    // A warp's own keys and values of a tile are as many bytes as its 16 rows
+    // of output, in pieces of 16 rows: a piece takes COLS columns.
+    static constexpr int PIECES = 2 * NG * NB, COLS = D / PIECES;
+    static_assert(COLS * 4 == RB, "a piece's rows are a block's");
     static constexpr int SMEM = OFF_BAR + BAR_BYTES;
 };
 static_assert(2 * (Shape<128, false>::SMEM + 1024) <= 228 * 1024 && 2 * (Shape<128, true>::SMEM + 1024) <= 228 * 1024,
@@ -76,6 +87,7 @@ struct PagedDecodeParams {
     int64_t B, table_entries, table_stride, qs, os;
     int Hq, G, groups; // groups of 16 query heads per key head
     int box;           // tokens of one TMA copy
+    int split;         // CTAs that share a pair (PAIRS)
     float scale_log2;
     uint64_t timeout_ns;
     const __nv_bfloat16 *q;
@@ -173,6 +185,14 @@ template <int TILE> __device__ __forceinline__ int pd_tiles(const PagedDecodePar
 {
     const int64_t len = p.lens[b];
     return len <= 0 || len > p.table_entries << p.c.ps_log2 ? 0 : (int)((len + TILE - 1) / TILE);
+}
+
+// what one pair of sequence b is on the line: its tiles, behind what a pair costs
+// beside them (its queries, and the join of the four warps)
+template <int TILE> __device__ __forceinline__ int64_t pd_units(const PagedDecodeParams &p, int64_t b)
+{
+    const int tiles = pd_tiles<TILE>(p, b);
+    return tiles ? tiles + pd::PAIR_UNITS : 0;
 }
 
 // the first CTA whose run holds unit u, given total = base * ctas + rem
@@ -331,8 +351,63 @@ __device__ __forceinline__ void pd_group(const uint32_t (&qa)[D / 16][4], const 
     }
 }
 
-template <int D, bool E4M3>
-__global__ void __launch_bounds__(pd::THREADS, 2)
+// Joins the shares of a cluster's pair: each CTA takes some of its rows, four
+// columns a thread, and reads all shares' maxima, sums and outputs in one round
+// of loads.
+template <int D, bool E4M3> __device__ void pd_join_pair(const PagedDecodeParams &p, uint8_t *smem, const PdWalk &w)
+{
+    if (p.split == 1 || w.tiles <= 1) // one CTA had it all (the same for all of the cluster)
+        return;
+    __syncwarp();
+    cluster_sync();
+    const int g = w.hg / p.groups, mg = w.hg % p.groups, rows = min(pd::ROWS, p.G - mg * pd::ROWS);
+    const int per = pd::ROWS / p.split, row0 = (int)cluster_ctarank() * per;
+    using S = pd::Shape<D, E4M3>;
+    const uint32_t out_at = smem_u32(smem + S::OFF_Q), ml_at = smem_u32(smem + S::OFF_ML); // (pair is 1 when they are left)
+    for (int u = threadIdx.x; u < per * (D / 4); u += pd::THREADS) {
+        const int row = row0 + u / (D / 4), c4 = u % (D / 4) * 4;
+        if (row >= rows)
+            break;
+        float2 ml[pd::MAX_SPLIT];
+        float4 x[pd::MAX_SPLIT];
+        float M = -INFINITY, L = 0.f;
+#pragma unroll
+        for (int c = 0; c < pd::MAX_SPLIT; ++c) {
+            ml[c] = make_float2(-INFINITY, 0.f);
+            x[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (c < p.split && w.tiles * (c + 1) / p.split > w.tiles * c / p.split) { // a share that has tiles
+                ml[c] = ld_cluster_f2(mapa_shared(ml_at + row * 8, (uint32_t)c));
+                x[c] = ld_cluster_f4(mapa_shared(out_at + (row * D + c4) * 4, (uint32_t)c));
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < pd::MAX_SPLIT; ++c)
+            M = fmaxf(M, ml[c].x);
+        const float Ms = M == -INFINITY ? 0.f : M;
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int c = 0; c < pd::MAX_SPLIT; ++c) {
+            const float wt = exp2_approx(ml[c].x - Ms);
+            L += ml[c].y * wt;
+            a.x += x[c].x * wt;
+            a.y += x[c].y * wt;
+            a.z += x[c].z * wt;
+            a.w += x[c].w * wt;
+        }
+        const int h = g * p.G + mg * pd::ROWS + row;
+        const float f = (E4M3 ? p.c.v_scale[g] : 1.f) / L;
+        *reinterpret_cast<uint2 *>(p.out + w.b * p.os + (int64_t)h * D + c4) =
+            make_uint2(pack_bf16x2(a.x * f, a.y * f), pack_bf16x2(a.z * f, a.w * f));
+        if (p.lse && c4 == 0)
+            p.lse[w.b * p.Hq + h] = (M + log2f(L)) * 0.6931471805599453f;
+    }
+    __syncwarp();
+    cluster_sync(); // no CTA leaves while another reads its shared memory
+}
+
+// PAIRS: a cluster of p.split CTAs takes one pair and joins through distributed
+// shared memory; otherwise a CTA takes its run of the line.
+template <int D, bool E4M3, bool PAIRS> __global__ void __launch_bounds__(pd::THREADS, 2)
     paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_constant__ CUtensorMap kmap,
                         const __grid_constant__ CUtensorMap vmap)
 {
@@ -360,63 +435,93 @@ __global__ void __launch_bounds__(pd::THREADS, 2)
     // launched while the kernel before may still run: nothing above touches memory
     griddep_launch_dependents();
     griddep_wait();
-    // this CTA's run of the line: the warps' sums of tiles, then the sequence
-    // in which the run begins
-    const int64_t per = (p.B + pd::THREADS - 1) / pd::THREADS; // sequences of a thread
-    const int64_t b_lo = min((int64_t)threadIdx.x * per, p.B), b_hi = min(b_lo + per, p.B);
-    int64_t mine = 0;
-    for (int64_t b = b_lo; b < b_hi; ++b)
-        mine += pd_tiles<S::TILE>(p, b);
-    int64_t upto = mine;
-    for (int d = 1; d < 32; d <<= 1) {
-        const int64_t x = __shfl_up_sync(0xffffffffu, upto, d);
-        if (lane >= d)
-            upto += x;
-    }
-    if (lane == 31)
-        bar->sums[warp] = upto;
-    // sequences without tokens (and those of a bad length) are nobody's run
-    for (int64_t b = blockIdx.x; b < p.B; b += gridDim.x)
-        if (pd_tiles<S::TILE>(p, b) == 0) {
-            if (p.lens[b] != 0 && threadIdx.x == 0)
-                report_fault(p.status, TDG_ERR_DEVICE, TDG_WHERE_PAGE, (uint32_t)b, p.epoch);
-            for (int i = threadIdx.x; i < p.Hq * D / 8; i += pd::THREADS)
-                *reinterpret_cast<uint4 *>(p.out + b * p.os + (int64_t)i * 8) = make_uint4(0, 0, 0, 0);
-            if (p.lse)
-                for (int i = threadIdx.x; i < p.Hq; i += pd::THREADS)
-                    p.lse[b * p.Hq + i] = -INFINITY;
+    int64_t u0, u1, base = 0, rem = 0;
+    PdWalk w;
+    if constexpr (PAIRS) {
+        // this CTA's share of its pair; u counts the pair's own tiles
+        const int pair = (int)(blockIdx.x / (unsigned)p.split), rank = (int)(blockIdx.x % (unsigned)p.split);
+        w.b = pair / pairs;
+        w.hg = pair % pairs;
+        w.tiles = pd_tiles<S::TILE>(p, w.b);
+        u0 = w.tiles * rank / p.split;
+        u1 = w.tiles * (rank + 1) / p.split;
+        w.tile = (int)u0;
+        if (w.tiles == 0 && rank == 0) { // no tokens, or a bad length
+            if (w.hg == 0 && threadIdx.x == 0 && p.lens[w.b] != 0)
+                report_fault(p.status, TDG_ERR_DEVICE, TDG_WHERE_PAGE, (uint32_t)w.b, p.epoch);
+            const int h0 = w.hg / p.groups * p.G + w.hg % p.groups * pd::ROWS, rows = min(pd::ROWS, p.G - w.hg % p.groups * pd::ROWS);
+            for (int i = threadIdx.x; i < rows * D / 8; i += pd::THREADS)
+                *reinterpret_cast<uint4 *>(p.out + w.b * p.os + (int64_t)h0 * D + (int64_t)i * 8) = make_uint4(0, 0, 0, 0);
+            if (p.lse && (int)threadIdx.x < rows)
+                p.lse[w.b * p.Hq + h0 + threadIdx.x] = -INFINITY;
         }
-    __syncthreads();
-    int64_t total = 0, before = 0;
-    for (int w = 0; w < pd::THREADS / 32; ++w) {
-        if (w < warp)
-            before += bar->sums[w];
-        total += bar->sums[w];
-    }
-    upto += before;
-    const int64_t base = total * pairs / gridDim.x, rem = total * pairs % gridDim.x;
-    const int64_t u0 = blockIdx.x * base + min((int64_t)blockIdx.x, rem), u1 = u0 + base + (blockIdx.x < rem ? 1 : 0);
-    if ((upto - mine) * pairs <= u0 && u0 < upto * pairs && u0 < u1) {
-        int64_t at = u0 - (upto - mine) * pairs;
-        PdWalk w;
-        for (w.b = b_lo;; ++w.b) {
-            w.tiles = pd_tiles<S::TILE>(p, w.b);
-            if (at < (int64_t)w.tiles * pairs)
-                break;
-            at -= (int64_t)w.tiles * pairs;
+        __syncthreads(); // the barriers are ready
+    } else {
+        // this CTA's run of the line: the warps' sums of tiles, then the sequence
+        // in which the run begins
+        const int64_t per = (p.B + pd::THREADS - 1) / pd::THREADS; // sequences of a thread
+        const int64_t b_lo = min((int64_t)threadIdx.x * per, p.B), b_hi = min(b_lo + per, p.B);
+        int64_t mine = 0;
+        for (int64_t b = b_lo; b < b_hi; ++b)
+            mine += pd_units<S::TILE>(p, b);
+        int64_t upto = mine;
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t x = __shfl_up_sync(0xffffffffu, upto, d);
+            if (lane >= d)
+                upto += x;
         }
-        w.hg = (int)(at / w.tiles);
-        w.tile = (int)(at % w.tiles);
-        bar->begin = w;
+        if (lane == 31)
+            bar->sums[warp] = upto;
+        // sequences without tokens (and those of a bad length) are nobody's run
+        for (int64_t b = blockIdx.x; b < p.B; b += gridDim.x)
+            if (pd_tiles<S::TILE>(p, b) == 0) {
+                if (p.lens[b] != 0 && threadIdx.x == 0)
+                    report_fault(p.status, TDG_ERR_DEVICE, TDG_WHERE_PAGE, (uint32_t)b, p.epoch);
+                for (int i = threadIdx.x; i < p.Hq * D / 8; i += pd::THREADS)
+                    *reinterpret_cast<uint4 *>(p.out + b * p.os + (int64_t)i * 8) = make_uint4(0, 0, 0, 0);
+                if (p.lse)
+                    for (int i = threadIdx.x; i < p.Hq; i += pd::THREADS)
+                        p.lse[b * p.Hq + i] = -INFINITY;
+            }
+        __syncthreads();
+        int64_t total = 0, before = 0;
+        for (int i = 0; i < pd::THREADS / 32; ++i) {
+            if (i < warp)
+                before += bar->sums[i];
+            total += bar->sums[i];
+        }
+        upto += before;
+        base = total * pairs / gridDim.x;
+        rem = total * pairs % gridDim.x;
+        u0 = blockIdx.x * base + min((int64_t)blockIdx.x, rem);
+        u1 = u0 + base + (blockIdx.x < rem ? 1 : 0);
+        if ((upto - mine) * pairs <= u0 && u0 < upto * pairs && u0 < u1) {
+            int64_t at = u0 - (upto - mine) * pairs;
+            for (w.b = b_lo;; ++w.b) {
+                const int64_t units = pd_units<S::TILE>(p, w.b);
+                if (at < units * pairs) {
+                    w.tiles = (int)(units - pd::PAIR_UNITS);
+                    w.hg = (int)(at / units);
+                    w.tile = (int)(at % units) - pd::PAIR_UNITS; // below 0: the pair's tiles begin so far on
+                    break;
+                }
+                at -= units * pairs;
+            }
+            bar->begin = w;
+        }
+        __syncthreads();
+        if (u0 >= u1) {
+            if (threadIdx.x == 0)
+                p.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+            return;
+        }
+        w = bar->begin;
     }
-    __syncthreads();
-    if (u0 >= u1) {
-        if (threadIdx.x == 0)
-            p.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
-        return;
-    }
-    PdWalk w = bar->begin;
     int64_t u = u0;
+    if (w.tile < 0) {
+        u -= w.tile;
+        w.tile = 0;
+    }
     // the next pair, of the next sequence that has tiles (there is one while u < u1)
     auto next_pair = [&](PdWalk &x) {
         x.tile = 0;
@@ -447,19 +552,22 @@ __global__ void __launch_bounds__(pd::THREADS, 2)
         auto chunk_tiles = [&](const PdWalk &x, int64_t at) -> int {
             return (int)min(min((int64_t)(32 / per_tile), (int64_t)(x.tiles - x.tile)), u1 - at);
         };
-        int n = chunk_tiles(w, u), stage = 0, pair = 0;
+        int n = u < u1 ? chunk_tiles(w, u) : 0, stage = 0, pair = 0;
         uint32_t phase = 0;
         bool fresh = true, dead = false;
-        int32_t ids = chunk_ids(w, n);
+        int32_t ids = n ? chunk_ids(w, n) : 0;
         int64_t issued = 0;
         int queries = 0; // query copies issued
-        while (u < u1 && !dead) {
+        while (n && !dead) {
             // look the next chunk up while this one's copies are issued
             PdWalk y = w;
             y.tile += n;
-            if (y.tile == y.tiles && u + n < u1)
+            u += n;
+            if (y.tile == y.tiles && u < u1) {
                 next_pair(y);
-            const int n2 = u + n < u1 ? chunk_tiles(y, u + n) : 0;
+                u += pd::PAIR_UNITS;
+            }
+            const int n2 = u < u1 ? chunk_tiles(y, u) : 0;
             const int32_t ids2 = n2 ? chunk_ids(y, n2) : 0;
             const int64_t len = p.lens[w.b];
             const int g = w.hg / p.groups;
@@ -508,7 +616,6 @@ __global__ void __launch_bounds__(pd::THREADS, 2)
             }
             fresh = y.tile == 0;
             pair += fresh ? 1 : 0;
-            u += n;
             w = y;
             n = n2;
             ids = ids2;
@@ -522,103 +629,209 @@ __global__ void __launch_bounds__(pd::THREADS, 2)
                 (void)mbar_wait(&bar->vfull[f % S::STAGES], (uint32_t)(f / S::STAGES) & 1u, p.timeout_ns);
             }
         }
-        return;
-    }
-
-    // ---- consumers ----
-    const int gid = lane >> 2, tig = lane & 3;
-    float *merge = reinterpret_cast<float *>(smem + S::OFF_MERGE); // [WARPS][ROWS][MERGE_COLS]
-    float *mls = reinterpret_cast<float *>(smem + S::OFF_ML);      // [WARPS][ROWS][2]
-    const uint32_t ring = smem_u32(smem);
-    const uint32_t blk = (uint32_t)p.box * S::RB;
-    // this warp's rows of a tile: which copy, and where in it
-    const int first = warp * S::NG * 16;
-    uint32_t group_off[S::NG];
+    } else {
+        // ---- consumers ----
+        const int gid = lane >> 2, tig = lane & 3;
+        const uint32_t ring = smem_u32(smem);
+        const uint32_t blk = (uint32_t)p.box * S::RB;
+        // this warp's rows of a tile: which copy, and where in it
+        const int first = warp * S::NG * 16;
+        const int box_log2 = 31 - __clz(p.box);
+        auto group_at = [&](int token) -> uint32_t { // where a group's rows begin, in a tile's keys or values
+            return (uint32_t)((token >> box_log2 << box_log2) * (D * S::ESZ) + (token & (p.box - 1)) * S::RB);
+        };
+        uint32_t group_off[S::NG];
 #pragma unroll
-    for (int i = 0; i < S::NG; ++i)
-        group_off[i] = (uint32_t)((first + i * 16) / p.box) * (p.box * D * S::ESZ) + (uint32_t)((first + i * 16) % p.box) * S::RB;
-    int stage = 0, pair = 0;
-    uint32_t phase = 0;
-    bool dead = false; // a wait ran out: wait no more, run on to the end (the call has reported it)
-    auto wait = [&](uint64_t *b, uint32_t ph, uint32_t what) {
-        if (!dead && !mbar_wait(b, ph, p.timeout_ns)) {
-            if (lane == 0)
-                report_fault(p.status, TDG_ERR_TIMEOUT, TDG_WHERE_PIPE, what, p.epoch);
-            dead = true;
-        }
-        __syncwarp(); // what follows (ldmatrix, mma, named barriers) wants the whole warp
-    };
-    int4 desc = make_int4(-1, 0, 0, 0);
-    while (u < u1) {
-        const int64_t len = p.lens[w.b];
-        const int g = w.hg / p.groups, mg = w.hg % p.groups;
-        const int rows = min(pd::ROWS, p.G - mg * pd::ROWS);
-        const int64_t pair_u0 = u - w.tile; // the pair's first unit
-        const int end = (int)min((int64_t)w.tiles, w.tile + (u1 - u));
-        // the queries as the A operand
-        const int qb = pair & 1;
-        wait(&bar->qfull[qb], (pair >> 1) & 1, 2);
-        uint32_t qa[D / 16][4];
-        float mul[2] = {p.scale_log2, p.scale_log2};
-        const uint8_t *qs = smem + S::OFF_Q + qb * S::Q_BYTES;
-        if constexpr (!E4M3) {
-#pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks)
-                pd_ldsm4(smem_u32(qs) + ((lane & 7) + ((lane >> 3) & 1) * 8) * D * 2 + ks * 32 + (lane >> 4) * 16, qa[ks]);
-        } else {
-            // f16, in the order in which the 8-bit keys arrive: four neighbours per lane
-            float x[2][D / 16][4], top[2] = {0.f, 0.f};
-#pragma unroll
-            for (int r = 0; r < 2; ++r)
-#pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks) {
-                    const uint2 y = *reinterpret_cast<const uint2 *>(qs + (gid + r * 8) * D * 2 + ks * 32 + tig * 8);
-                    x[r][ks][0] = __uint_as_float(y.x << 16);
-                    x[r][ks][1] = __uint_as_float(y.x & 0xFFFF0000u);
-                    x[r][ks][2] = __uint_as_float(y.y << 16);
-                    x[r][ks][3] = __uint_as_float(y.y & 0xFFFF0000u);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        top[r] = fmaxf(top[r], fabsf(x[r][ks][i]));
+        for (int i = 0; i < S::NG; ++i)
+            group_off[i] = group_at(first + i * 16);
+        int stage = 0, pair = 0;
+        uint32_t phase = 0;
+        bool dead = false; // a wait ran out: wait no more, run on to the end (the call has reported it)
+        auto wait = [&](uint64_t *b, uint32_t ph, uint32_t what) {
+            if (!dead && !mbar_wait(b, ph, p.timeout_ns)) {
+                if (lane == 0)
+                    report_fault(p.status, TDG_ERR_TIMEOUT, TDG_WHERE_PIPE, what, p.epoch);
+                dead = true;
+            }
+            __syncwarp(); // what follows (ldmatrix, mma, named barriers) wants the whole warp
+        };
+        int4 desc = make_int4(-1, 0, 0, 0);
+        while (u < u1) {
+            const int64_t len = p.lens[w.b];
+            const int g = w.hg / p.groups, mg = w.hg % p.groups;
+            const int rows = min(pd::ROWS, p.G - mg * pd::ROWS);
+            const int64_t pair_u0 = u - w.tile; // the pair's first unit
+            const int end = (int)min((int64_t)w.tiles, w.tile + (u1 - u));
+            // the queries as the A operand
+            const int qb = pair & 1;
+            wait(&bar->qfull[qb], (pair >> 1) & 1, 2);
+            uint32_t qa[D / 16][4];
+            float mul[2] = {p.scale_log2, p.scale_log2};
+            const uint8_t *qs = smem + S::OFF_Q + qb * S::Q_BYTES;
+            if constexpr (!E4M3) {
+    #pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks)
+                    pd_ldsm4(smem_u32(qs) + ((lane & 7) + ((lane >> 3) & 1) * 8) * D * 2 + ks * 32 + (lane >> 4) * 16, qa[ks]);
+            } else {
+                // f16, in the order in which the 8-bit keys arrive: four neighbours per lane
+                float x[2][D / 16][4], top[2] = {0.f, 0.f};
+    #pragma unroll
+                for (int r = 0; r < 2; ++r)
+    #pragma unroll
+                    for (int ks = 0; ks < D / 16; ++ks) {
+                        const uint2 y = *reinterpret_cast<const uint2 *>(qs + (gid + r * 8) * D * 2 + ks * 32 + tig * 8);
+                        x[r][ks][0] = __uint_as_float(y.x << 16);
+                        x[r][ks][1] = __uint_as_float(y.x & 0xFFFF0000u);
+                        x[r][ks][2] = __uint_as_float(y.y << 16);
+                        x[r][ks][3] = __uint_as_float(y.y & 0xFFFF0000u);
+    #pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            top[r] = fmaxf(top[r], fabsf(x[r][ks][i]));
+                    }
+                int e[2];
+    #pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
+                    top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
+                    e[r] = pd_exponent(top[r]);
                 }
-            int e[2];
+    #pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks)
+    #pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const float f = pow2i(-e[r]);
+                        qa[ks][r] = pack_f16x2(x[r][ks][0] * f, x[r][ks][1] * f);
+                        qa[ks][2 + r] = pack_f16x2(x[r][ks][2] * f, x[r][ks][3] * f);
+                    }
+                const float ks = p.c.k_scale[g];
+                mul[0] *= ks * pow2i(e[0]);
+                mul[1] *= ks * pow2i(e[1]);
+            }
+            ++pair;
+            float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[D / 8][4];
+    #pragma unroll
+            for (int n = 0; n < D / 8; ++n)
+                o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+            for (int t = w.tile; t < end; ++t) {
+                const int64_t left = len - (int64_t)t * S::TILE - first;
+                uint32_t at[S::NG];
+    #pragma unroll
+                for (int i = 0; i < S::NG; ++i)
+                    at[i] = ring + stage * 2 * S::KV + group_off[i];
+                wait(&bar->kfull[stage], phase, 3);
+                auto wait_v = [&] { wait(&bar->vfull[stage], phase, 4); };
+                if (left >= S::NG * 16)
+                    pd_group<D, E4M3, false>(qa, mul, at, blk, S::NG * 16, lane, m, l, o, wait_v);
+                else if (left > 0)
+                    pd_group<D, E4M3, true>(qa, mul, at, blk, (int)left, lane, m, l, o, wait_v);
+                else
+                    wait_v();
+                if (t + 1 == end)
+                    break; // the last tile's slot is kept for the join
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&bar->empty[stage]);
+                if (++stage == S::STAGES) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+            // The queries' buffer is free once the products have read the
+            // fragments: released any earlier, right behind their ldmatrix, the next
+            // pair's queries were seen in them.
+            if (lane == 0)
+                mbar_arrive(&bar->qempty[qb]);
+            // Join the four warps.  Each leaves its output where its own keys and
+            // values of the last tile were, which nobody else reads; the slot is
+            // released when all that has been read.
+            float *mls = reinterpret_cast<float *>(smem + S::OFF_ML) + (pair & 1) * S::ML_FLOATS; // [WARPS][ROWS][2]
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
-                top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
-                e[r] = pd_exponent(top[r]);
+                l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+                l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+                if (tig == 0) {
+                    mls[(warp * pd::ROWS + gid + r * 8) * 2] = m[r];
+                    mls[(warp * pd::ROWS + gid + r * 8) * 2 + 1] = l[r];
+                }
             }
+            uint8_t *slot_at = smem + stage * 2 * S::KV;
+            auto piece = [&](uint32_t group, int i) -> float * { // piece i: values or keys, group, block
+                return reinterpret_cast<float *>(slot_at + i / (S::NG * S::NB) * S::KV + i % S::NB * blk + group);
+            };
+            constexpr int SWIZZLE = S::COLS / 4 - 1; // columns xored by the row: no bank conflicts either way
 #pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks)
+            for (int i = 0; i < S::PIECES; ++i)
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    const float f = pow2i(-e[r]);
-                    qa[ks][r] = pack_f16x2(x[r][ks][0] * f, x[r][ks][1] * f);
-                    qa[ks][2 + r] = pack_f16x2(x[r][ks][2] * f, x[r][ks][3] * f);
+                    float *dst = piece(group_off[i / S::NB % S::NG], i) + (gid + r * 8) * S::COLS;
+                    const int c8 = i * S::COLS / 8;
+                    if constexpr (!E4M3) {
+#pragma unroll
+                        for (int n = 0; n < S::COLS / 8; ++n)
+                            *reinterpret_cast<float2 *>(dst + ((n * 8 + tig * 2) ^ ((gid & SWIZZLE) * 4))) =
+                                make_float2(o[c8 + n][2 * r], o[c8 + n][2 * r + 1]);
+                    } else {
+#pragma unroll
+                        for (int n = 0; n < S::COLS / 8; n += 2)
+                            *reinterpret_cast<float4 *>(dst + ((n * 8 + tig * 4) ^ ((gid & SWIZZLE) * 4))) = make_float4(
+                                o[c8 + n][2 * r], o[c8 + n + 1][2 * r], o[c8 + n][2 * r + 1], o[c8 + n + 1][2 * r + 1]);
+                    }
                 }
-            const float ks = p.c.k_scale[g];
-            mul[0] *= ks * pow2i(e[0]);
-            mul[1] *= ks * pow2i(e[1]);
-        }
-        ++pair;
-        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[D / 8][4];
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+            const bool whole = pair_u0 >= u0 && end == w.tiles;
+            const int slot = w.tile == 0 && pair_u0 > u0 ? 1 : 0; // 0: the pair that holds this CTA's first unit
+            // 16 rows of COLS / 4 chunks a piece; the threads take AT_ONCE pieces at a time
+            constexpr int CHUNKS = S::COLS / 4, AT_ONCE = 128 / (pd::ROWS * CHUNKS);
+            const int row = threadIdx.x / CHUNKS % pd::ROWS, col4 = threadIdx.x % CHUNKS * 4, p0 = threadIdx.x / (pd::ROWS * CHUNKS);
+            const int h = g * p.G + mg * pd::ROWS + row;
+            float M = -INFINITY, L = 0.f, wt[pd::WARPS];
 #pragma unroll
-        for (int n = 0; n < D / 8; ++n)
-            o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
-        for (int t = w.tile; t < end; ++t) {
-            const int64_t left = len - (int64_t)t * S::TILE - first;
-            uint32_t at[S::NG];
+            for (int i = 0; i < pd::WARPS; ++i)
+                M = fmaxf(M, mls[(i * pd::ROWS + row) * 2]);
+            const float Ms = M == -INFINITY ? 0.f : M;
 #pragma unroll
-            for (int i = 0; i < S::NG; ++i)
-                at[i] = ring + stage * 2 * S::KV + group_off[i];
-            wait(&bar->kfull[stage], phase, 3);
-            auto wait_v = [&] { wait(&bar->vfull[stage], phase, 4); };
-            if (left >= S::NG * 16)
-                pd_group<D, E4M3, false>(qa, mul, at, blk, S::NG * 16, lane, m, l, o, wait_v);
-            else if (left > 0)
-                pd_group<D, E4M3, true>(qa, mul, at, blk, (int)left, lane, m, l, o, wait_v);
-            else
-                wait_v();
+            for (int i = 0; i < pd::WARPS; ++i) {
+                wt[i] = exp2_approx(mls[(i * pd::ROWS + row) * 2] - Ms);
+                L += mls[(i * pd::ROWS + row) * 2 + 1] * wt[i];
+            }
+            const float f = whole ? (E4M3 ? p.c.v_scale[g] : 1.f) / L : 1.f;
+            // (rolled for bf16, whose code is short enough to fetch: 17 against 19.5 us
+            // for 64 sequences of 1..512; unrolled for 8 bits: 145 against 148.5 us for
+            // 128 of 2048..4096)
+            constexpr int STEPS = E4M3 ? S::PIECES / AT_ONCE : 1;
+            if (row < rows) {
+#pragma unroll STEPS
+                for (int q = 0; q < S::PIECES / AT_ONCE; ++q) {
+                    const int pc = q * AT_ONCE + p0, c = pc * S::COLS + col4;
+                    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                    for (int i = 0; i < pd::WARPS; ++i) {
+                        const float4 x = *reinterpret_cast<const float4 *>(
+                            piece(group_at((i * S::NG + pc / S::NB % S::NG) * 16), pc) + row * S::COLS + (col4 ^ ((row & SWIZZLE) * 4)));
+                        a.x += x.x * wt[i];
+                        a.y += x.y * wt[i];
+                        a.z += x.z * wt[i];
+                        a.w += x.w * wt[i];
+                    }
+                    if (whole)
+                        *reinterpret_cast<uint2 *>(p.out + w.b * p.os + (int64_t)h * D + c) =
+                            make_uint2(pack_bf16x2(a.x * f, a.y * f), pack_bf16x2(a.z * f, a.w * f));
+                    else if constexpr (PAIRS) // over the queries, which all warps have read
+                        *reinterpret_cast<float4 *>(smem + S::OFF_Q + (row * D + c) * 4) = a;
+                    else
+                        __stcg(reinterpret_cast<float4 *>(p.part_o + ((size_t)(blockIdx.x * 2 + slot) * pd::ROWS + row) * D + c), a);
+                }
+                if (col4 == 0 && p0 == 0) {
+                    if (PAIRS && !whole) // (the other pair's place: there is none)
+                        *reinterpret_cast<float2 *>(smem + S::OFF_ML + (((pair & 1) ^ 1) * S::ML_FLOATS + row * 2) * 4) = make_float2(M, L);
+                    else if (!whole)
+                        __stcg(reinterpret_cast<float2 *>(p.part_ml + ((size_t)(blockIdx.x * 2 + slot) * pd::ROWS + row) * 2),
+                               make_float2(M, L));
+                    else if (p.lse)
+                        p.lse[w.b * p.Hq + h] = (M + log2f(L)) * 0.6931471805599453f;
+                }
+            }
+            fence_proxy_async_smem(); // the slot's next tile comes by TMA
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(&bar->empty[stage]);
@@ -626,97 +839,23 @@ __global__ void __launch_bounds__(pd::THREADS, 2)
                 stage = 0;
                 phase ^= 1u;
             }
-        }
-        // The queries' buffer is free once the products have read the
-        // fragments: released any earlier, right behind their ldmatrix, the next
-        // pair's queries were seen in them.
-        if (lane == 0)
-            mbar_arrive(&bar->qempty[qb]);
-        // join the four warps, MERGE_COLS columns at a time
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-            if (tig == 0) {
-                mls[(warp * pd::ROWS + gid + r * 8) * 2] = m[r];
-                mls[(warp * pd::ROWS + gid + r * 8) * 2 + 1] = l[r];
+            if (!PAIRS && pair_u0 < u0 && end == w.tiles) { // a pair from earlier CTAs ends here
+                const int c0 = pd_owner(pair_u0, base, rem);
+                const int64_t c0_u0 = c0 * base + min((int64_t)c0, rem);
+                desc = make_int4((int)w.b, w.hg, c0, pair_u0 > c0_u0 ? 1 : 0);
+            }
+            u += end - w.tile;
+            w.tile = end;
+            if (end == w.tiles && u < u1) {
+                next_pair(w);
+                u += pd::PAIR_UNITS;
             }
         }
-        const bool whole = pair_u0 >= u0 && end == w.tiles;
-        const int slot = w.tile == 0 && pair_u0 > u0 ? 1 : 0; // 0: the pair that holds this CTA's first unit
-        const int row = threadIdx.x >> 3, col4 = (threadIdx.x & 7) * 4;
-        const int h = g * p.G + mg * pd::ROWS + row;
-        float M = -INFINITY, L = 0.f, wt[pd::WARPS];
-#pragma unroll
-        for (int c0 = 0; c0 < D; c0 += pd::MERGE_COLS) {
-            // columns xored by the row: no bank conflicts either way
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                float *dst = merge + (warp * pd::ROWS + gid + r * 8) * pd::MERGE_COLS;
-                if constexpr (!E4M3) {
-#pragma unroll
-                    for (int n = 0; n < pd::MERGE_COLS / 8; ++n)
-                        *reinterpret_cast<float2 *>(dst + ((n * 8 + tig * 2) ^ (gid * 4))) =
-                            make_float2(o[c0 / 8 + n][2 * r], o[c0 / 8 + n][2 * r + 1]);
-                } else {
-#pragma unroll
-                    for (int n = 0; n < pd::MERGE_COLS / 8; n += 2)
-                        *reinterpret_cast<float4 *>(dst + ((n * 8 + tig * 4) ^ (gid * 4))) =
-                            make_float4(o[c0 / 8 + n][2 * r], o[c0 / 8 + n + 1][2 * r], o[c0 / 8 + n][2 * r + 1],
-                                        o[c0 / 8 + n + 1][2 * r + 1]);
-                }
-            }
-            asm volatile("bar.sync 1, 128;" ::: "memory");
-            if (c0 == 0) {
-#pragma unroll
-                for (int i = 0; i < pd::WARPS; ++i)
-                    M = fmaxf(M, mls[(i * pd::ROWS + row) * 2]);
-                const float Ms = M == -INFINITY ? 0.f : M;
-#pragma unroll
-                for (int i = 0; i < pd::WARPS; ++i) {
-                    wt[i] = exp2_approx(mls[(i * pd::ROWS + row) * 2] - Ms);
-                    L += mls[(i * pd::ROWS + row) * 2 + 1] * wt[i];
-                }
-            }
-            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int i = 0; i < pd::WARPS; ++i) {
-                const float4 x = *reinterpret_cast<const float4 *>(merge + (i * pd::ROWS + row) * pd::MERGE_COLS +
-                                                                   (col4 ^ ((row & 7) * 4)));
-                a.x += x.x * wt[i];
-                a.y += x.y * wt[i];
-                a.z += x.z * wt[i];
-                a.w += x.w * wt[i];
-            }
-            if (row < rows) {
-                if (whole) {
-                    const float f = (E4M3 ? p.c.v_scale[g] : 1.f) / L;
-                    *reinterpret_cast<uint2 *>(p.out + w.b * p.os + (int64_t)h * D + c0 + col4) =
-                        make_uint2(pack_bf16x2(a.x * f, a.y * f), pack_bf16x2(a.z * f, a.w * f));
-                } else {
-                    __stcg(reinterpret_cast<float4 *>(p.part_o + ((size_t)(blockIdx.x * 2 + slot) * pd::ROWS + row) * D + c0 + col4), a);
-                }
-            }
-            asm volatile("bar.sync 1, 128;" ::: "memory");
-        }
-        if (col4 == 0 && row < rows) {
-            if (!whole)
-                __stcg(reinterpret_cast<float2 *>(p.part_ml + ((size_t)(blockIdx.x * 2 + slot) * pd::ROWS + row) * 2), make_float2(M, L));
-            else if (p.lse)
-                p.lse[w.b * p.Hq + h] = (M + log2f(L)) * 0.6931471805599453f;
-        }
-        if (pair_u0 < u0 && end == w.tiles) { // a pair from earlier CTAs ends here
-            const int c0 = pd_owner(pair_u0, base, rem);
-            const int64_t c0_u0 = c0 * base + min((int64_t)c0, rem);
-            desc = make_int4((int)w.b, w.hg, c0, pair_u0 > c0_u0 ? 1 : 0);
-        }
-        u += end - w.tile;
-        w.tile = end;
-        if (end == w.tiles && u < u1)
-            next_pair(w);
+        if (!PAIRS && threadIdx.x == 0)
+            p.desc[blockIdx.x] = desc;
     }
-    if (threadIdx.x == 0)
-        p.desc[blockIdx.x] = desc;
+    if constexpr (PAIRS)
+        pd_join_pair<D, E4M3>(p, smem, w);
 }
 
 // Joins the partial results of the pair that ends in CTA blockIdx.x (if one
@@ -736,14 +875,52 @@ template <int D> __global__ void __launch_bounds__(pd::JOIN_THREADS) paged_join_
     if (desc.x < 0)
         return;
     const int g = desc.y / p.groups, mg = desc.y % p.groups;
-    const int rows = min(pd::JOIN_ROWS, min(pd::ROWS, p.G - mg * pd::ROWS) - (int)blockIdx.y * pd::JOIN_ROWS);
+    const int all = min(pd::ROWS, p.G - mg * pd::ROWS);
+    const int c0 = desc.z, c1 = blockIdx.x;
+    if (c1 - c0 < U) { // few partial results: one CTA takes all rows, a group of threads a row
+        for (int row = threadIdx.x / LANES; blockIdx.y == 0 && row < all; row += GROUPS) {
+            const int col = threadIdx.x % LANES * 4;
+            float2 ml[U];
+            float4 x[U];
+            float M = -INFINITY, L = 0.f;
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                ml[i] = make_float2(-INFINITY, 0.f);
+                x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (c0 + i <= c1) {
+                    const size_t at = (size_t)((c0 + i) * 2 + (i == 0 ? desc.w : 0)) * pd::ROWS + row;
+                    ml[i] = __ldcg(reinterpret_cast<const float2 *>(p.part_ml + at * 2));
+                    x[i] = __ldcg(reinterpret_cast<const float4 *>(p.part_o + at * D + col));
+                }
+                M = fmaxf(M, ml[i].x);
+            }
+            const float Ms = M == -INFINITY ? 0.f : M;
+            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const float w = exp2_approx(ml[i].x - Ms);
+                L += ml[i].y * w;
+                a.x += x[i].x * w;
+                a.y += x[i].y * w;
+                a.z += x[i].z * w;
+                a.w += x[i].w * w;
+            }
+            const int h = g * p.G + mg * pd::ROWS + row;
+            const float f = (p.c.v_scale ? p.c.v_scale[g] : 1.f) / L;
+            *reinterpret_cast<uint2 *>(p.out + desc.x * p.os + (int64_t)h * D + col) =
+                make_uint2(pack_bf16x2(a.x * f, a.y * f), pack_bf16x2(a.z * f, a.w * f));
+            if (p.lse && col == 0)
+                p.lse[(int64_t)desc.x * p.Hq + h] = (M + log2f(L)) * 0.6931471805599453f;
+        }
+        return;
+    }
+    const int rows = min(pd::JOIN_ROWS, all - (int)blockIdx.y * pd::JOIN_ROWS);
     if (rows <= 0)
         return;
     const int per = GROUPS / (rows == 1 ? 1 : 2); // groups of a row
     const int group = threadIdx.x / LANES, lane = threadIdx.x % LANES;
     const int row = blockIdx.y * pd::JOIN_ROWS + group / per, part = group % per;
     const bool used = group / per < rows;
-    const int c0 = desc.z, c1 = blockIdx.x;
     // slot of CTA c: the first one's may be its second
     auto at = [&](int c) -> size_t { return (size_t)(c * 2 + (c == c0 ? desc.w : 0)) * pd::ROWS + row; };
     float M = -INFINITY, L = 0.f;
@@ -834,17 +1011,36 @@ template <int D, bool E4M3> int launch_decode(const tdg_symm *h, const tdg_paged
     CUtensorMap km, vm;
     if (!pool_map<D, E4M3>(&km, h, a->cache, a->cache.k_off, p.box) || !pool_map<D, E4M3>(&vm, h, a->cache, a->cache.v_off, p.box))
         return TDG_ERR_CUDA;
-    const void *fn = reinterpret_cast<const void *>(&paged_decode_kernel<D, E4M3>);
+    // Few short sequences: a cluster of up to 8 CTAs for each pair, and no second
+    // launch, when its longest share is at most CAP tiles and at most SAVED (what
+    // the launch costs, in tiles) longer than an equal run of the line.
+    // By the line and so: one of 1000, 64 / 8 heads, 8.6 -> 7.3 us, 30 of 100
+    // 9.1 -> 6.1, 8-bit 32 of 200 11.3 -> 8.0; but one of 4000 on one key head 8.9 ->
+    // 9.9, 8-bit one of 4000 10.4 -> 11.4.
+    const int64_t pairs = a->B * a->cache.Hkv * p.groups, most = (a->table_entries * a->cache.page_size + S::TILE - 1) / S::TILE;
+    constexpr int64_t CAP = E4M3 ? 4 : 8, SAVED_HALVES = E4M3 ? 5 : 11;
+    const int64_t ctas = h->sm_count * 2 < pd::MAX_CTAS ? h->sm_count * 2 : pd::MAX_CTAS;
+    p.split = pairs > ctas ? 0 : pd::MAX_SPLIT;
+    while (p.split > 1 && (pairs * p.split > ctas || p.split / 2 >= most))
+        p.split /= 2;
+    if (most > CAP * p.split || 2 * most * ctas > p.split * (SAVED_HALVES * ctas + 2 * pairs * most))
+        p.split = 0;
+    const void *fn = p.split ? reinterpret_cast<const void *>(&paged_decode_kernel<D, E4M3, true>)
+                             : reinterpret_cast<const void *>(&paged_decode_kernel<D, E4M3, false>);
     if (const cudaError_t e = set_smem(fn, S::SMEM); e != cudaSuccess)
         return cuda_err(e, "paged decode smem");
-    const unsigned ctas = (unsigned)(h->sm_count * 2 < pd::MAX_CTAS ? h->sm_count * 2 : pd::MAX_CTAS);
+    if (p.split) {
+        void *args[] = {&p, &km, &vm};
+        return cuda_err(launch(fn, dim3((unsigned)(pairs * p.split)), dim3(pd::THREADS), S::SMEM, st, args, false, p.split, true),
+                        "paged decode launch");
+    }
     void *args[] = {&p, &km, &vm};
-    if (const int rc = cuda_err(launch(fn, dim3(ctas), dim3(pd::THREADS), S::SMEM, st, args, false, 1, true), "paged decode launch"))
-        return rc;
+    if (const cudaError_t e = launch(fn, dim3((unsigned)ctas), dim3(pd::THREADS), S::SMEM, st, args, false, 1, true); e != cudaSuccess)
+        return cuda_err(e, "paged decode launch");
     void *jargs[] = {&p};
     const int join_rows = p.G < pd::ROWS ? p.G : pd::ROWS;
     return cuda_err(launch(reinterpret_cast<const void *>(&paged_join_kernel<D>),
-                           dim3(ctas, (unsigned)((join_rows + pd::JOIN_ROWS - 1) / pd::JOIN_ROWS)), dim3(pd::JOIN_THREADS), 0, st,
+                           dim3((unsigned)ctas, (unsigned)((join_rows + pd::JOIN_ROWS - 1) / pd::JOIN_ROWS)), dim3(pd::JOIN_THREADS), 0, st,
                            jargs, false, 1, true),
                     "paged join launch");
 }

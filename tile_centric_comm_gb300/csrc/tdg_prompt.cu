@@ -191,19 +191,6 @@ __device__ __forceinline__ int64_t steal_answer(const uint4 *answer)
     return ok ? (int64_t)x : -1;
 }
 
-__device__ __forceinline__ float2 ld_cluster_f2(uint32_t a)
-{
-    float2 v;
-    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
-    return v;
-}
-__device__ __forceinline__ float4 ld_cluster_f4(uint32_t a)
-{
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
-    return v;
-}
-
 __device__ __forceinline__ uint32_t elect_one()
 {
     uint32_t r;
