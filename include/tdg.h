@@ -597,7 +597,8 @@ TDG_API int tdg_prompt_attention(tdg_symm *h, const tdg_prompt_attention_args *a
  * are split and short ones grouped.  Partial results (row maximum, row sum,
  * unnormalised output, float32) go to region(root) + part_off
  * (tdg_paged_decode_part_bytes), and a second, stream-ordered launch joins the
- * split ones in a fixed order.
+ * split ones in a fixed order.  For few sequences in a narrow table a cluster
+ * of CTAs takes each (sequence, key head) and joins by itself, in one launch.
  * What the pages hold behind a sequence's length never reaches a result.
  * A negative length, one that does not fit the table row, or a page id
  * outside the pools is reported as TDG_ERR_DEVICE (TDG_WHERE_PAGE, index b);
