@@ -27,7 +27,7 @@ const at::Tensor *plain(PyObject *o, at::ScalarType type, PyObject *device)
 
 long long address(const at::Tensor &t) { return reinterpret_cast<long long>(t.data_ptr()); }
 
-// No exception of torch's leaves a function below: what throws is Python's to judge.
+// No exception of torch's leaves a function below: what throws goes to Python.
 template <class F> PyObject *run(F native, PyObject *checked, PyObject *const *args, Py_ssize_t n)
 {
     PyObject *r = nullptr;
