@@ -239,3 +239,27 @@ def test_bad_indices_in_a_wide_table(what):
     assert st["code"] == tdg.TDG_ERR_DEVICE and st["where"] == "page" and st["index"] == 0
     k, v = c.sequence(1)
     check_attention(to_bits(out)[1:], oracle.attention(np.zeros((1, 8, 128)), k, v), 128)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("D", [64, 128])
+def test_queries_of_many_short_pairs(e4m3, D):
+    # a dozen pairs a CTA, each of one tile: the queries' two buffers are refilled all the time, and every
+    # pair's queries have a size of their own, so that another pair's would show
+    B, Hq, Hkv = 900, 32, 4
+    lens = [1 + 5 * i % 7 for i in range(B)]
+    c = Cache(2, lens, Hkv, D, 16, e4m3, seed=D)
+    g = np.random.default_rng(D + 1)
+    q = bits(g.standard_normal((B, Hq, D)) * np.exp2(g.integers(-3, 3, (B, Hkv, 1, 1)).repeat(Hq // Hkv, 2).reshape(B, Hq, 1)))
+    _, (qd, out) = strided_rows([q, np.full_like(q, 0x7FC1)])
+    first = None
+    for _ in range(5):
+        lse = torch.full((B, Hq), float("nan"), device="cuda")
+        tdg.paged_decode(c.symm, c.cache, qd, out, c.table_d, c.lens_d, c.part_off, lse=lse)
+        torch.cuda.synchronize()
+        got = q, to_bits(out), lse.cpu().numpy()
+        if first is None:
+            first = got
+            check_case(c, Hq, got, some=range(0, B, 9))
+        assert np.array_equal(got[1], first[1]) and np.array_equal(got[2], first[2])
+    assert c.symm.status()["code"] == 0

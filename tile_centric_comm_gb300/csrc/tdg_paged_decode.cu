@@ -736,9 +736,10 @@ template <int D, bool E4M3, bool PAIRS> __global__ void __launch_bounds__(pd::TH
                     phase ^= 1u;
                 }
             }
-            // The queries' buffer is free once the products have read the
-            // fragments: released any earlier, right behind their ldmatrix, the next
-            // pair's queries were seen in them.
+            // The queries' buffer is free.  Lane 0's arrival orders only what the
+            // warp barrier has put before it: without one, the other lanes' reads of
+            // the queries may still be under way when the next pair's land.
+            __syncwarp();
             if (lane == 0)
                 mbar_arrive(&bar->qempty[qb]);
             // Join the four warps.  Each leaves its output where its own keys and
