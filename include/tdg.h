@@ -150,6 +150,7 @@ typedef struct {
 #define TDG_WHERE_PAGE 7       /* a page id outside the pools, or a length outside the page table */
 #define TDG_WHERE_POS 8        /* a rotary position outside the table          */
 #define TDG_WHERE_CU 9         /* row offsets of packed sequences out of order or range */
+#define TDG_WHERE_PART 10      /* partial results that another call has overwritten */
 
 /*
  * Copy the status block to *out (may be NULL) after synchronising `stream`,
@@ -603,6 +604,10 @@ TDG_API int tdg_prompt_attention(tdg_symm *h, const tdg_prompt_attention_args *a
  * A negative length, one that does not fit the table row, or a page id
  * outside the pools is reported as TDG_ERR_DEVICE (TDG_WHERE_PAGE, index b);
  * that sequence's output is then undefined.
+ * Calls that may overlap on the GPU (on different streams) need partial results
+ * of their own, at different part_off or root: with shared ones their outputs
+ * are undefined, and where a call finds another one's description in place of
+ * its own it reports TDG_ERR_DEVICE (TDG_WHERE_PART) and leaves the sequence out.
  * q, out: B rows of Hq heads of D, head h at h*D, rows *_stride elements apart.
  * Requirements: those of the cache; Hq % Hkv == 0, Hq/Hkv <= 128; 0 <= B <=
  * 65535; 0 <= table_entries <= table_stride, table_entries * page_size < 2^31; 0 <= root <

@@ -263,3 +263,33 @@ def test_queries_of_many_short_pairs(e4m3, D):
             check_case(c, Hq, got, some=range(0, B, 9))
         assert np.array_equal(got[1], first[1]) and np.array_equal(got[2], first[2])
     assert c.symm.status()["code"] == 0
+
+
+def test_overlapping_calls_on_two_streams():
+    # each with partial results of its own: two places of one region, then two regions
+    lens = [5000, 0, 1, 300, 77, 9000]
+    c = Cache(2, lens, 2, 128, 16, seed=21, extra_entries=2048)      # a wide table: both launches, with partial results
+    part = tdg.paged_decode_part_bytes(16, 2, 128)
+    symm = tdg.Symm(2, c.part_off + 2 * part, 64)
+    for r in range(2):
+        for to, of in zip(c.cache.pools(symm, r), c.cache.pools(c.symm, r)):
+            to.copy_(of)
+    g = np.random.default_rng(22)
+    q = [bits(g.standard_normal((B, 16, 128))) for B in (6, 4)]
+    qd = [torch.from_numpy(x.view(np.int16)).view(torch.bfloat16).cuda() for x in q]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for offs, roots in (((c.part_off, c.part_off + part), (0, 0)), ((c.part_off, c.part_off), (0, 1))):
+        outs = [[torch.empty_like(x) for _ in range(20)] for x in qd]
+        torch.cuda.synchronize()
+        for i in range(20):
+            for j, n in enumerate((6, 4)):
+                tdg.paged_decode(symm, c.cache, qd[j], outs[j][i], c.table_d[:n], c.lens_d[:n], offs[j], root=roots[j],
+                                 stream=streams[j])
+        torch.cuda.synchronize()
+        assert symm.status()["code"] == 0
+        for j, n in enumerate((6, 4)):
+            for b in range(n):
+                k, v = c.sequence(b)
+                want = oracle.attention(oracle.bf16_to_f64(q[j][b:b + 1]), k, v)
+                check_attention(to_bits(outs[j][0])[b:b + 1], want, 128, f"call {j}, sequence {b}")
+            assert all(torch.equal(o.view(torch.int16), outs[j][0].view(torch.int16)) for o in outs[j])

@@ -94,7 +94,7 @@ struct PagedDecodeParams {
     __nv_bfloat16 *out;
     float *lse;
     const int32_t *table, *lens;
-    int4 *desc;     // [MAX_CTAS]: the split pair that ends in a CTA
+    int4 *desc;     // [MAX_CTAS]: the split pair that ends in a CTA (sequence or -1, line, first CTA, pd_tag)
     float *part_ml; // [MAX_CTAS][2][ROWS][2]
     float *part_o;  // [MAX_CTAS][2][ROWS][D]
 };
@@ -194,6 +194,12 @@ template <int TILE> __device__ __forceinline__ int64_t pd_units(const PagedDecod
     const int tiles = pd_tiles<TILE>(p, b);
     return tiles ? tiles + pd::PAIR_UNITS : 0;
 }
+
+// What a description ends with: in which of its first CTA's two places the pair
+// lies, behind the call's epoch (below 2^31).  The join takes only its own call's
+// descriptions: another call that has the same room at the same time may be of
+// other sizes, and what it describes may lie outside this one's output.
+__device__ __forceinline__ int pd_tag(const PagedDecodeParams &p, int place) { return (int)(p.epoch << 1 | (uint32_t)place); }
 
 // the first CTA whose run holds unit u, given total = base * ctas + rem
 __device__ __forceinline__ int pd_owner(int64_t u, int64_t base, int64_t rem)
@@ -512,7 +518,7 @@ template <int D, bool E4M3, bool PAIRS> __global__ void __launch_bounds__(pd::TH
         __syncthreads();
         if (u0 >= u1) {
             if (threadIdx.x == 0)
-                p.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+                p.desc[blockIdx.x] = make_int4(-1, 0, 0, pd_tag(p, 0));
             return;
         }
         w = bar->begin;
@@ -655,7 +661,7 @@ template <int D, bool E4M3, bool PAIRS> __global__ void __launch_bounds__(pd::TH
             }
             __syncwarp(); // what follows (ldmatrix, mma, named barriers) wants the whole warp
         };
-        int4 desc = make_int4(-1, 0, 0, 0);
+        int4 desc = make_int4(-1, 0, 0, pd_tag(p, 0));
         while (u < u1) {
             const int64_t len = p.lens[w.b];
             const int g = w.hg / p.groups, mg = w.hg % p.groups;
@@ -843,7 +849,7 @@ template <int D, bool E4M3, bool PAIRS> __global__ void __launch_bounds__(pd::TH
             if (!PAIRS && pair_u0 < u0 && end == w.tiles) { // a pair from earlier CTAs ends here
                 const int c0 = pd_owner(pair_u0, base, rem);
                 const int64_t c0_u0 = c0 * base + min((int64_t)c0, rem);
-                desc = make_int4((int)w.b, w.hg, c0, pair_u0 > c0_u0 ? 1 : 0);
+                desc = make_int4((int)w.b, w.hg, c0, pd_tag(p, pair_u0 > c0_u0 ? 1 : 0));
             }
             u += end - w.tile;
             w.tile = end;
@@ -873,6 +879,12 @@ template <int D> __global__ void __launch_bounds__(pd::JOIN_THREADS) paged_join_
     griddep_launch_dependents();
     griddep_wait();
     const int4 desc = p.desc[blockIdx.x];
+    const int place = desc.w & 1;
+    if (desc.w - place != pd_tag(p, 0)) {
+        if (threadIdx.x == 0)
+            report_fault(p.status, TDG_ERR_DEVICE, TDG_WHERE_PART, blockIdx.x, p.epoch);
+        return;
+    }
     if (desc.x < 0)
         return;
     const int g = desc.y / p.groups, mg = desc.y % p.groups;
@@ -889,7 +901,7 @@ template <int D> __global__ void __launch_bounds__(pd::JOIN_THREADS) paged_join_
                 ml[i] = make_float2(-INFINITY, 0.f);
                 x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (c0 + i <= c1) {
-                    const size_t at = (size_t)((c0 + i) * 2 + (i == 0 ? desc.w : 0)) * pd::ROWS + row;
+                    const size_t at = (size_t)((c0 + i) * 2 + (i == 0 ? place : 0)) * pd::ROWS + row;
                     ml[i] = __ldcg(reinterpret_cast<const float2 *>(p.part_ml + at * 2));
                     x[i] = __ldcg(reinterpret_cast<const float4 *>(p.part_o + at * D + col));
                 }
@@ -923,7 +935,7 @@ template <int D> __global__ void __launch_bounds__(pd::JOIN_THREADS) paged_join_
     const int row = blockIdx.y * pd::JOIN_ROWS + group / per, part = group % per;
     const bool used = group / per < rows;
     // slot of CTA c: the first one's may be its second
-    auto at = [&](int c) -> size_t { return (size_t)(c * 2 + (c == c0 ? desc.w : 0)) * pd::ROWS + row; };
+    auto at = [&](int c) -> size_t { return (size_t)(c * 2 + (c == c0 ? place : 0)) * pd::ROWS + row; };
     float M = -INFINITY, L = 0.f;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
     auto add = [&](const float2 &ml, const float4 &x, float ms) {

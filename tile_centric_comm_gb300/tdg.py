@@ -33,7 +33,7 @@ B_KN, B_NK = 0, 1
 MOE_ROUTE, MOE_DISPATCH, MOE_COMBINE, MOE_ALL = 1, 2, 4, 7
 KV_BF16, KV_E4M3 = 0, 1
 WHERE = {1: "ag_flag", 2: "pipe", 3: "ll", 4: "moe_expert", 5: "ring", 6: "rs_signal",
-         7: "page", 8: "pos", 9: "cu"}
+         7: "page", 8: "pos", 9: "cu", 10: "part"}
 
 # every symbol include/tdg.h declares
 EXPORTS = [
@@ -649,7 +649,9 @@ def paged_decode(symm: Symm, cache: PagedCache, q, out, table, lens, part_off: i
     """Attention of one new token per sequence over the paged cache: q and out
     (B, Hq, D), rows possibly strided; table (B, entries) int32 page ids; lens
     (B,) int32 lengths with the new token; lse (B, Hq) float32 or None.  The
-    partial results (paged_decode_part_bytes) go to region(root) + part_off."""
+    partial results (paged_decode_part_bytes) go to region(root) + part_off;
+    calls that may overlap, on different streams, need a part_off or root of
+    their own."""
     if _torch is None:
         _attn()
     dev = symm.device
