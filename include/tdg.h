@@ -613,8 +613,8 @@ TDG_API int tdg_prompt_attention(tdg_symm *h, const tdg_prompt_attention_args *a
  * 65535; 0 <= table_entries <= table_stride, table_entries * page_size < 2^31; 0 <= root <
  * world; strides multiples of 8 elements and at least the row's extent; q,
  * out and part_off 16-byte aligned; scale finite and >= 0 (0 = 1/sqrt(D));
- * the partials overlapping neither pool, out not overlapping q.  B == 0 is a
- * no-op.
+ * the partials, out and lse overlapping neither each other, nor a pool of any
+ * rank, nor anything that the call reads.  B == 0 is a no-op.
  */
 typedef struct {
     int world, root;

@@ -293,3 +293,48 @@ def test_overlapping_calls_on_two_streams():
                 want = oracle.attention(oracle.bf16_to_f64(q[j][b:b + 1]), k, v)
                 check_attention(to_bits(outs[j][0])[b:b + 1], want, 128, f"call {j}, sequence {b}")
             assert all(torch.equal(o.view(torch.int16), outs[j][0].view(torch.int16)) for o in outs[j])
+
+
+@pytest.mark.parametrize("extra", [0, 1024])
+def test_refuses_what_would_overwrite_its_inputs(extra):
+    # both paths; nothing is launched: the heap, tables and outputs keep their bytes
+    c = Cache(2, [90, 300], 2, 128, 16, True, seed=8, extra_entries=extra)
+    n = c.table.shape[1]
+    row = 8 * 128 * 2                                           # bytes of an output row
+    q = torch.zeros((2, 8, 128), dtype=torch.bfloat16, device="cuda")
+    out, lse = torch.full_like(q, 7.0), torch.full((2, 8), 7.0, device="cuda")
+    scale = torch.full((4096,), 0.5, device="cuda")             # the key scales lie in a buffer with room behind them
+    region, base, part = c.symm.region_bytes, c.symm.base, c.part_off
+
+    def rc(desc=(), **kw):
+        a = tdg.PagedDecodeArgs(world=2, root=0, cache=c.cache.desc, B=2, Hq=8, q=q.data_ptr(), q_stride=1024,
+                                out=out.data_ptr(), out_stride=1024, lse=lse.data_ptr(), table=c.table_d.data_ptr(),
+                                table_entries=n, table_stride=n, lens=c.lens_d.data_ptr(), part_off=part)
+        a.cache.k_scale = scale.data_ptr()
+        for key, v in kw.items():
+            setattr(a, key, v)
+        return tdg.lib().tdg_paged_decode(c.symm.h, ctypes.byref(a), None)
+
+    bad = tdg.TDG_ERR_INVALID
+    free = c.symm.base_off + region + part                      # rank 1's room for partial results is not used
+    c.symm.buf[free:free + 16 * row] = 0xFF
+    before = c.symm.buf.clone()
+    part_bytes = tdg.paged_decode_part_bytes(8, 2, 128)
+    for r in range(2):                                          # over the pools of any rank
+        for off in (0, c.v_off):
+            assert rc(out=base + r * region + off) == bad and rc(lse=base + r * region + off + 4) == bad
+    assert rc(out=base + part) == bad and rc(out=base + part + part_bytes - 16) == bad   # over the partial results
+    assert rc(lse=base + part) == bad and rc(q=base + part) == bad
+    assert rc(q=base + part + part_bytes - 16) == bad
+    assert rc(lse=out.data_ptr() + row) == bad and rc(lse=q.data_ptr() + 2 * row - 4) == bad
+    assert rc(lse=c.lens_d.data_ptr()) == bad and rc(lse=c.table_d.data_ptr() + 4) == bad
+    assert rc(lse=scale.data_ptr() + 4) == bad and rc(out=scale.data_ptr()) == bad
+    assert rc(lens=base + part) == bad and rc(table=base + part + 64) == bad
+    assert rc(lens=out.data_ptr()) == bad and rc(table=out.data_ptr() + 16) == bad
+    torch.cuda.synchronize()
+    assert torch.equal(c.symm.buf, before) and (out == 7).all() and (lse == 7).all()
+    # next to one another is no overlap
+    assert rc(out=base + region + part, lse=base + region + part + 2 * row, q=base + region + part + 2 * row + 64) == 0
+    assert rc(lse=scale.data_ptr() + 8) == 0 and rc() == 0
+    torch.cuda.synchronize()
+    assert c.symm.status()["code"] == 0 and not torch.equal(c.symm.buf[free:free + 2 * row], before[free:free + 2 * row])

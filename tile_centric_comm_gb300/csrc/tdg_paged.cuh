@@ -113,4 +113,40 @@ inline bool rows_clash(int64_t an, const void *a, int64_t as, int64_t aw, int64_
     return d < aw || d + bw > as;
 }
 
+// Bytes that a call writes or reads.
+struct Range {
+    const void *at;
+    uint64_t bytes;
+};
+
+template <int A, int B> bool ranges_overlap(const Range (&a)[A], const Range (&b)[B])
+{
+    for (const Range &x : a)
+        for (const Range &y : b)
+            if (rows_overlap(x.at, x.bytes, y.at, y.bytes))
+                return true;
+    return false;
+}
+
+// whether a range reaches into a pool of any rank
+template <int A> bool pools_overlap(const tdg_symm *h, const tdg_paged_cache &c, const Range (&a)[A])
+{
+    const uint64_t pool = tdg_paged_pool_bytes(c.pages, c.page_size, c.Hkv, c.D, c.kv_type);
+    for (int r = 0; r < h->world; ++r) {
+        const uint8_t *region = h->base + (uint64_t)r * h->region_bytes;
+        const Range pools[] = {{region + c.k_off, pool}, {region + c.v_off, pool}};
+        if (ranges_overlap(a, pools))
+            return true;
+    }
+    return false;
+}
+
+inline Range table_range(const int32_t *table, int64_t rows, int64_t entries, int64_t stride)
+{
+    return {table, rows <= 0 ? 0 : ((uint64_t)(rows - 1) * stride + entries) * 4};
+}
+
+// the scales of an 8-bit cache (none otherwise)
+inline uint64_t scale_bytes(const tdg_paged_cache &c) { return c.kv_type == TDG_KV_E4M3 ? (uint64_t)c.Hkv * 4 : 0; }
+
 } // namespace tdg_host

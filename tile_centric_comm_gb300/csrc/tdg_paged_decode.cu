@@ -1098,6 +1098,15 @@ extern "C" int tdg_paged_decode(tdg_symm *h, const tdg_paged_decode_args *a, voi
         return TDG_ERR_INVALID;
     if (rows_clash(a->B, a->out, a->out_stride, Hq * D, a->B, a->q, a->q_stride, Hq * D))
         return TDG_ERR_INVALID;
+    // nothing that is written lies over anything else
+    uint8_t *part_at = h->base + (uint64_t)a->root * h->region_bytes + a->part_off;
+    const Range q{a->q, rows_extent(a->B, a->q_stride, Hq * D)}, out{a->out, rows_extent(a->B, a->out_stride, Hq * D)};
+    const Range lse{a->lse, (uint64_t)a->B * Hq * 4}, partials{part_at, part};
+    const Range k_scale{a->cache.k_scale, scale_bytes(a->cache)}, v_scale{a->cache.v_scale, scale_bytes(a->cache)};
+    const Range lens{a->lens, (uint64_t)a->B * 4}, table = table_range(a->table, a->B, a->table_entries, a->table_stride);
+    if (ranges_overlap({out, lse, partials}, {k_scale, v_scale, lens, table}) || ranges_overlap({lse, partials}, {q, out}) ||
+        ranges_overlap({lse}, {partials}) || pools_overlap(h, a->cache, {out, lse}))
+        return TDG_ERR_INVALID;
     p.status = h->status;
     p.epoch = next_epoch(h);
     p.B = a->B;
@@ -1115,7 +1124,6 @@ extern "C" int tdg_paged_decode(tdg_symm *h, const tdg_paged_decode_args *a, voi
     p.lse = a->lse;
     p.table = a->table;
     p.lens = a->lens;
-    uint8_t *part_at = h->base + (uint64_t)a->root * h->region_bytes + a->part_off;
     p.desc = reinterpret_cast<int4 *>(part_at);
     p.part_ml = reinterpret_cast<float *>(p.desc + pd::MAX_CTAS);
     p.part_o = p.part_ml + (size_t)pd::MAX_CTAS * 2 * pd::ROWS * 2;
