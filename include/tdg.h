@@ -516,7 +516,8 @@ TDG_API size_t tdg_paged_pool_bytes(int64_t pages, int page_size, int64_t Hkv, i
  *   What is not wanted is left out: q and q_out NULL (no queries, Hq = 0),
  * k_out NULL, table NULL (no cache write; v, cu, lens and the pools are then
  * not read), rot_dim = 0 (no rotation).  q_out may be q, and k_out may be k
- * (same stride); other overlaps are not allowed.
+ * (same stride); what is written (q_out, k_out, the pools of every rank) must
+ * not overlap anything else of the call.
  * Requirements: world the heap's; 0 <= T < 2^31; B >= 0; Hq, Hkv <= 65536;
  * rot_dim a multiple of 16, at most D; sections non-negative with the sum
  * rot_dim/2; strides multiples of 8 elements and at least the row's extent;

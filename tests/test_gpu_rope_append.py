@@ -219,3 +219,51 @@ def test_refusals():
         tdg.PagedCache(1, 16, 1, 64, 0, 1024, e4m3=True)
     torch.cuda.synchronize()
     assert c.c.symm.status()["code"] == 0
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_refuses_what_would_overwrite_its_inputs(e4m3):
+    # nothing is launched: heap and outputs keep their bytes
+    c = Case(2, [30, 5], [30, 2], 4, 2, 128, 16, e4m3, axes=2, seed=13)
+    m = c.c.table.shape[1]
+    q, k, v = to_dev_bf16(c.q), to_dev_bf16(c.k), to_dev_bf16(c.v)
+    q_out, k_out = torch.full_like(q, 7.0), torch.full_like(k, 7.0)
+    cs, pos, cu = (torch.from_numpy(x).cuda() for x in (c.cos_sin, c.pos, c.cu))
+    base, region = c.c.symm.base, c.c.symm.region_bytes
+
+    def rc(desc=(), **kw):
+        a = tdg.RopeAppendArgs(world=2, cache=c.c.cache.desc, T=c.T, B=2, Hq=4, q=q.data_ptr(), k=k.data_ptr(),
+                               v=v.data_ptr(), q_stride=512, k_stride=256, v_stride=256, q_out=q_out.data_ptr(),
+                               k_out=k_out.data_ptr(), q_out_stride=512, k_out_stride=256, cos_sin=cs.data_ptr(),
+                               max_pos=37, rot_dim=128, axes=2, sections=(ctypes.c_int * 3)(30, 34, 0),
+                               pos=pos.data_ptr(), pos_stride=c.T, cu=cu.data_ptr(), table=c.c.table_d.data_ptr(),
+                               table_entries=m, table_stride=m, lens=c.c.lens_d.data_ptr())
+        for key, x in kw.items():
+            setattr(a, key, x)
+        for key, x in desc:
+            setattr(a.cache, key, x)
+        return tdg.lib().tdg_rope_append(c.c.symm.h, ctypes.byref(a), None)
+
+    bad = tdg.TDG_ERR_INVALID
+    before = c.c.symm.buf.clone()
+    for out in (q_out, k_out):                                   # indices and tables under an output
+        at = out.data_ptr()
+        for name in ("cos_sin", "pos", "cu", "table", "lens"):
+            assert rc(**{name: at}) == bad and rc(**{name: at + 4096}) == bad, name
+        assert rc(pos=at - 4 * c.T - 4, pos_stride=c.T) == bad   # the second axis' positions
+        if e4m3:
+            assert rc(desc=[("k_scale", at)]) == bad and rc(desc=[("v_scale", at + 64)]) == bad
+    for r in range(2):                                           # and in a pool of any rank
+        for off in (0, c.c.v_off):
+            at = base + r * region + off
+            for name in ("cos_sin", "pos", "cu", "table", "lens", "q", "k", "v", "q_out", "k_out"):
+                assert rc(**{name: at}) == bad, name
+            if e4m3:
+                assert rc(desc=[("v_scale", at)]) == bad
+    torch.cuda.synchronize()
+    assert torch.equal(c.c.symm.buf, before) and (q_out == 7).all() and (k_out == 7).all()
+    # what is not read may lie anywhere
+    assert rc(table=None, lens=k_out.data_ptr(), cu=q_out.data_ptr()) == 0
+    assert rc(rot_dim=0, pos=q_out.data_ptr(), cos_sin=k_out.data_ptr()) == 0
+    torch.cuda.synchronize()
+    assert c.c.symm.status()["code"] == 0

@@ -328,23 +328,27 @@ extern "C" int tdg_rope_append(tdg_symm *h, const tdg_rope_append_args *a, void 
         return TDG_ERR_INVALID;
     RopeParams p;
     memset(&p, 0, sizeof p);
-    const uint64_t qx = rows_extent(T, a->q_stride, Hq * D), qox = rows_extent(T, a->q_out_stride, Hq * D);
-    const uint64_t kx = rows_extent(T, a->k_stride, Hkv * D), kox = rows_extent(T, a->k_out_stride, Hkv * D);
+    const Range q_out{a->q_out, rows_extent(T, a->q_out_stride, Hq * D)}, k_out{a->k_out, rows_extent(T, a->k_out_stride, Hkv * D)};
+    const uint64_t turn = a->rot_dim ? (uint64_t)a->max_pos * a->rot_dim * 4 : 0;
+    const Range cos_sin{a->cos_sin, turn}, pos{a->pos, turn ? ((uint64_t)(a->axes - 1) * a->pos_stride + T) * 4 : 0};
+    if (ranges_overlap({q_out, k_out}, {cos_sin, pos}))
+        return TDG_ERR_INVALID;
     if (a->table) {
         if (const int rc = paged_view(h, a->cache, p.c))
             return rc;
         if (!rows_ok(a->v, a->v_stride, Hkv * D) || !a->lens || !aligned4(a->lens) || !aligned4(a->cu) ||
             !table_ok(a->table, a->table_entries, a->table_stride, a->cache.page_size) || (!a->cu && a->B != T))
             return TDG_ERR_INVALID;
-        // the pools (written) hold none of the rows
-        const uint64_t vx = rows_extent(T, a->v_stride, Hkv * D);
-        const uint64_t pool = tdg_paged_pool_bytes(a->cache.pages, a->cache.page_size, Hkv, D, a->cache.kv_type);
-        const struct { const void *at; uint64_t n; } rows[] = {{a->q, qx}, {a->k, kx}, {a->v, vx}, {a->q_out, qox}, {a->k_out, kox}};
-        for (int r = 0; r < h->world; ++r)
-            for (const auto &x : rows)
-                if (rows_overlap(x.at, x.n, h->base + (uint64_t)r * h->region_bytes + a->cache.k_off, pool) ||
-                    rows_overlap(x.at, x.n, h->base + (uint64_t)r * h->region_bytes + a->cache.v_off, pool))
-                    return TDG_ERR_INVALID;
+        // the pools (written) hold nothing else of the call, and the rows written
+        // none of the indices
+        const Range q{a->q, rows_extent(T, a->q_stride, Hq * D)}, k{a->k, rows_extent(T, a->k_stride, Hkv * D)};
+        const Range v{a->v, rows_extent(T, a->v_stride, Hkv * D)};
+        const Range k_scale{a->cache.k_scale, scale_bytes(a->cache)}, v_scale{a->cache.v_scale, scale_bytes(a->cache)};
+        const Range cu{a->cu, (uint64_t)(a->B + 1) * 4}, lens{a->lens, (uint64_t)a->B * 4};
+        const Range table = table_range(a->table, a->B, a->table_entries, a->table_stride);
+        if (ranges_overlap({q_out, k_out}, {k_scale, v_scale, cu, lens, table}) ||
+            pools_overlap(h, a->cache, {q, k, v, q_out, k_out, cos_sin, pos, k_scale, v_scale, cu, lens, table}))
+            return TDG_ERR_INVALID;
     } else {
         p.c.Hkv = (int)Hkv;
         p.c.D = (int)D;
