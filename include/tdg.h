@@ -570,8 +570,9 @@ TDG_API int tdg_rope_append(tdg_symm *h, const tdg_rope_append_args *args, void 
  * Requirements: D 64 or 128; Hq % Hkv == 0, Hq/Hkv <= 128; 0 <= Tq, Tk < 2^31;
  * 0 <= B <= 65535; strides multiples of 8 elements and at least the row's
  * extent; pointers 16-byte aligned (cu_q, cu_k, lse 4-byte); scale finite and
- * >= 0 (0 = 1/sqrt(D)); causal 0 or 1; out overlapping no input.  Tq == 0 or
- * B == 0 is a no-op; Tk == 0 gives rows that see nothing.
+ * >= 0 (0 = 1/sqrt(D)); causal 0 or 1; out and lse overlapping no input and
+ * not each other.  Tq == 0 or B == 0 is a no-op; Tk == 0 gives rows that see
+ * nothing.
  */
 typedef struct {
     int64_t Tq, Tk, B, Hq, Hkv, D;

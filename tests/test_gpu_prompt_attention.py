@@ -251,3 +251,34 @@ def test_many_items(symm, D, causal, Hq, Hkv, nq, nk):
     c.check(got, causal, some=[b for b in range(len(nq)) if b != bad])
     again = c.run(symm, causal)
     assert np.array_equal(got[0], again[0]) and np.array_equal(got[1], again[1], equal_nan=True)
+
+
+def test_refuses_what_would_overwrite_its_inputs(symm):
+    # nothing is launched: every buffer keeps its bytes
+    c = Case([30, 20], [30, 20], 4, 2, 128)
+    q, k, v = (to_dev_bf16(x) for x in (c.q, c.k, c.v))
+    out = torch.full_like(q, 7.0)
+    lse = torch.full((50, 4), 7.0, device="cuda")
+    cu_q, cu_k = torch.from_numpy(c.cu_q).cuda(), torch.from_numpy(c.cu_k).cuda()
+
+    def rc(**kw):
+        a = tdg.PromptAttentionArgs(Tq=50, Tk=50, B=2, Hq=4, Hkv=2, D=128, q=q.data_ptr(), k=k.data_ptr(),
+                                    v=v.data_ptr(), q_stride=512, k_stride=256, v_stride=256, out=out.data_ptr(),
+                                    out_stride=512, lse=lse.data_ptr(), cu_q=cu_q.data_ptr(), cu_k=cu_k.data_ptr(), causal=1)
+        for key, x in kw.items():
+            setattr(a, key, x)
+        return tdg.lib().tdg_prompt_attention(symm.h, ctypes.byref(a), None)
+
+    bad = tdg.TDG_ERR_INVALID
+    kept = [(x, x.clone()) for x in (q, k, v, out, lse, cu_q, cu_k)]
+    for x in (q, k, v, out):                                             # lse over rows: their first, their last bytes
+        assert rc(lse=x.data_ptr()) == bad and rc(lse=x.data_ptr() + x.numel() * 2 - 4) == bad
+    for x in (cu_q, cu_k):                                               # outputs over offsets
+        assert rc(lse=x.data_ptr() + 8) == bad and rc(lse=x.data_ptr() - 50 * 4 * 4 + 4) == bad
+    for name in ("cu_q", "cu_k"):
+        assert rc(**{name: out.data_ptr() + 64}) == bad and rc(**{name: lse.data_ptr() + 50 * 4 * 4 - 4}) == bad
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in kept)
+    assert rc(cu_k=cu_q.data_ptr()) == 0 and rc(lse=None) == 0           # inputs may be one another
+    torch.cuda.synchronize()
+    assert symm.status()["code"] == 0

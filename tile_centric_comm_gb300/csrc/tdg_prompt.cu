@@ -1020,6 +1020,11 @@ extern "C" int tdg_prompt_attention(tdg_symm *h, const tdg_prompt_attention_args
         rows_clash(a->Tq, a->out, a->out_stride, Hq * D, a->Tk, a->k, a->k_stride, Hkv * D) ||
         rows_clash(a->Tq, a->out, a->out_stride, Hq * D, a->Tk, a->v, a->v_stride, Hkv * D))
         return TDG_ERR_INVALID;
+    const Range q{a->q, rows_extent(a->Tq, a->q_stride, Hq * D)}, out{a->out, rows_extent(a->Tq, a->out_stride, Hq * D)};
+    const Range k{a->k, rows_extent(a->Tk, a->k_stride, Hkv * D)}, v{a->v, rows_extent(a->Tk, a->v_stride, Hkv * D)};
+    const Range lse{a->lse, (uint64_t)a->Tq * Hq * 4}, cu_q{a->cu_q, (uint64_t)(a->B + 1) * 4}, cu_k{a->cu_k, (uint64_t)(a->B + 1) * 4};
+    if (ranges_overlap({lse}, {q, k, v, out}) || ranges_overlap({out, lse}, {cu_q, cu_k}))
+        return TDG_ERR_INVALID;
     PromptParams p;
     memset(&p, 0, sizeof p);
     p.status = h->status;
