@@ -471,8 +471,8 @@ TDG_API int tdg_flash_decode(tdg_symm *h, const tdg_flash_decode_args *args, voi
  * Requirements: D 64 or 128; page_size 16, 32, 64, 128 or 256; Hkv >= 1;
  * world * pages and pages * Hkv < 2^31; k_off and v_off multiples of 1024; the pools
  * (tdg_paged_pool_bytes each) inside the region (TDG_ERR_NOMEM otherwise) and
- * not overlapping; k_scale and v_scale given exactly for TDG_KV_E4M3
- * (positive finite values).
+ * not overlapping; k_scale and v_scale given exactly for TDG_KV_E4M3 (positive
+ * finite values, 4-byte aligned).
  */
 #define TDG_KV_BF16 0
 #define TDG_KV_E4M3 1

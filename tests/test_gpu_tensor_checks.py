@@ -43,3 +43,28 @@ def test_same_outcomes():
         assert isinstance(_both(tdg._flat, tdg._checked_flat, t, "t", kind, n, dev), int)
     for t, kind, n in [(m, i32, 46), (m, f32, 1), (m[:, :4], i32, 1), (m.cpu(), i32, 1), (None, i32, 0), ("m", i32, 0)]:
         assert isinstance(_both(tdg._flat, tdg._checked_flat, t, "t", kind, n, dev), tuple)
+
+
+def test_scales_off_the_4_byte_grid_are_refused():
+    import ctypes
+    from attn_util import Cache
+    c = Cache(1, [20], 2, 128, 16, True, seed=1)
+    x = torch.zeros(1, 4, 128, dtype=torch.bfloat16, device="cuda")
+    out, n = torch.empty_like(x), c.table.shape[1]
+    scale = torch.full((8,), 0.5, device="cuda")
+
+    def both(k_scale, v_scale):
+        cache = tdg.PagedCacheDesc.from_buffer_copy(c.cache.desc)
+        cache.k_scale, cache.v_scale = k_scale, v_scale
+        where = dict(table=c.table_d.data_ptr(), table_entries=n, table_stride=n, lens=c.lens_d.data_ptr())
+        rope = tdg.RopeAppendArgs(world=1, cache=cache, T=1, B=1, Hq=0, k=x.data_ptr(), v=x.data_ptr(), k_stride=512, v_stride=512, **where)
+        decode = tdg.PagedDecodeArgs(world=1, cache=cache, B=1, Hq=4, q=x.data_ptr(), q_stride=512, out=out.data_ptr(), out_stride=512,
+                                     part_off=c.part_off, **where)
+        return (tdg.lib().tdg_rope_append(c.symm.h, ctypes.byref(rope), None), tdg.lib().tdg_paged_decode(c.symm.h, ctypes.byref(decode), None))
+
+    p = scale.data_ptr()
+    assert both(p + 4, p + 8) == (0, 0)
+    for off in (1, 2, 3):
+        assert both(p + off, p) == both(p, p + off) == (tdg.TDG_ERR_INVALID, tdg.TDG_ERR_INVALID)
+    torch.cuda.synchronize()
+    assert c.symm.status()["code"] == 0

@@ -38,6 +38,8 @@ __device__ __forceinline__ float exp2_approx(float x)
 
 namespace tdg_host {
 
+inline bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
 inline bool page_size_ok(int ps) { return ps == 16 || ps == 32 || ps == 64 || ps == 128 || ps == 256; }
 
 inline bool overlap(uint64_t a, uint64_t an, uint64_t b, uint64_t bn) { return a < b + bn && b < a + an; }
@@ -53,7 +55,7 @@ inline int paged_view(const tdg_symm *h, const tdg_paged_cache &c, tdg::PagedVie
     if (!pool)
         return TDG_ERR_INVALID;
     const bool e4m3 = c.kv_type == TDG_KV_E4M3;
-    if ((c.k_scale != nullptr) != e4m3 || (c.v_scale != nullptr) != e4m3)
+    if ((c.k_scale != nullptr) != e4m3 || (c.v_scale != nullptr) != e4m3 || !aligned4(c.k_scale) || !aligned4(c.v_scale))
         return TDG_ERR_INVALID;
     const uint64_t R = h->region_bytes;
     if (pool > R || c.k_off > R - pool || c.v_off > R - pool)
@@ -73,8 +75,6 @@ inline int paged_view(const tdg_symm *h, const tdg_paged_cache &c, tdg::PagedVie
     v.ps_log2 = __builtin_ctz((unsigned)c.page_size);
     return TDG_OK;
 }
-
-inline bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 inline bool table_ok(const int32_t *table, int64_t entries, int64_t stride, int page_size)
 {
