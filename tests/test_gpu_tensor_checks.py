@@ -68,3 +68,24 @@ def test_scales_off_the_4_byte_grid_are_refused():
         assert both(p + off, p) == both(p, p + off) == (tdg.TDG_ERR_INVALID, tdg.TDG_ERR_INVALID)
     torch.cuda.synchronize()
     assert c.symm.status()["code"] == 0
+
+
+def test_scales_on_another_device_are_refused():
+    # the heap's handle says that it is on a second GPU; nothing is launched there
+    from types import SimpleNamespace
+    scale = torch.full((2,), 0.5, device="cuda")
+    cache = tdg.PagedCache(4, 16, 2, 128, 0, 1 << 16, e4m3=True, k_scale=scale, v_scale=scale)
+    heap = SimpleNamespace(device=torch.device("cuda", 1), world=1, h=None)
+    x = torch.zeros(1, 2, 128, dtype=torch.bfloat16, device="cuda")
+    table, lens = torch.zeros(1, 1, dtype=torch.int32, device="cuda"), torch.ones(1, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError, match="v_scale: on cuda:0, the heap is on cuda:1"):
+        tdg.rope_append(heap, cache, None, x, x, None, None, None, table, lens)
+    with pytest.raises(ValueError, match="v_scale: on cuda:0, the heap is on cuda:1"):
+        tdg.paged_decode(heap, cache, x, x.clone(), table, lens, 0)
+    with pytest.raises(ValueError, match="v_scale"):
+        tdg.PagedCache(4, 16, 2, 128, 0, 1 << 16, e4m3=True, k_scale=scale, v_scale=scale.cpu())
+    with pytest.raises(TypeError, match="torch.Tensor"):
+        tdg.PagedCache(4, 16, 2, 128, 0, 1 << 16, e4m3=True, k_scale=[0.5, 0.5], v_scale=scale)
+    # a cache without scales is of no device
+    with pytest.raises(ValueError, match="k: on cuda:0, the heap is on cuda:1"):
+        tdg.rope_append(heap, tdg.PagedCache(4, 16, 2, 128, 0, 1 << 16), None, x, x, None, None, None, table, lens)

@@ -453,6 +453,9 @@ class PagedCache:
             k_off=k_off, v_off=v_off,
             k_scale=_tensor(k_scale, "k_scale", torch.float32, Hkv) if e4m3 else None,
             v_scale=_tensor(v_scale, "v_scale", torch.float32, Hkv) if e4m3 else None)
+        self.device = k_scale.device if e4m3 else None      # that of the scales; the calls compare it with the heap's
+        if e4m3 and v_scale.device != self.device:
+            raise ValueError(f"v_scale: on {v_scale.device}, k_scale is on {self.device}")
         # the description's fields as the packed calls take them
         self.packed = (pages, page_size, self.desc.kv_type, Hkv, D, k_off, v_off,
                        self.desc.k_scale or 0, self.desc.v_scale or 0)
@@ -463,6 +466,10 @@ class PagedCache:
         shape = (self.pages, self.Hkv, self.page_size, self.D)
         kind = torch.float8_e4m3fn if self.e4m3 else torch.bfloat16
         return symm.view(rank, self.k_off, shape, kind), symm.view(rank, self.v_off, shape, kind)
+
+
+def _other_device(cache, device):
+    raise ValueError(f"k_scale and v_scale: on {cache.device}, the heap is on {device}")
 
 
 _torch = _current_raw_stream = _rows = _table = _flat = None
@@ -571,6 +578,8 @@ def rope_append(symm: Symm, cache: PagedCache, q, k, v, q_out, cos_sin, pos, tab
     if _torch is None:
         _attn()
     dev, i32 = symm.device, _t_i32
+    if cache.device is not None and cache.device != dev:
+        _other_device(cache, dev)
     kp, ks, T, Hkv, D = _rows(k, "k", dev)
     if Hkv != cache.Hkv or D != cache.D:
         raise ValueError(f"k: expected heads ({cache.Hkv}, {cache.D}), got ({Hkv}, {D})")
@@ -655,6 +664,8 @@ def paged_decode(symm: Symm, cache: PagedCache, q, out, table, lens, part_off: i
     if _torch is None:
         _attn()
     dev = symm.device
+    if cache.device is not None and cache.device != dev:
+        _other_device(cache, dev)
     qp, qs, B, Hq, D = _rows(q, "q", dev)
     op, os_, *like = _rows(out, "out", dev)
     tp, te, ts, n = _table(table, "table", dev)
