@@ -466,8 +466,8 @@ TDG_API int tdg_flash_decode(tdg_symm *h, const tdg_flash_decode_args *args, voi
  * entries and rows are table_stride entries apart; entries past the sequence's
  * last page are not read.
  * TDG_KV_E4M3 stores 8 bits (sign, 4 exponent, 3 mantissa bits; largest 448):
- * the value that stands for x of head h is x / scale[h], clamped to +-448 and
- * rounded to nearest even.
+ * the value that stands for x of head h is the float32 quotient x / scale[h],
+ * clamped to +-448 and rounded to nearest even (NaN stays NaN).
  * Requirements: D 64 or 128; page_size 16, 32, 64, 128 or 256; Hkv >= 1;
  * world * pages and pages * Hkv < 2^31; k_off and v_off multiples of 1024; the pools
  * (tdg_paged_pool_bytes each) inside the region (TDG_ERR_NOMEM otherwise) and

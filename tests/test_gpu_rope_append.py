@@ -267,3 +267,29 @@ def test_refuses_what_would_overwrite_its_inputs(e4m3):
     assert rc(rot_dim=0, pos=q_out.data_ptr(), cos_sin=k_out.data_ptr()) == 0
     torch.cuda.synchronize()
     assert c.c.symm.status()["code"] == 0
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_8_bit_codes_are_those_of_the_quotient(D):
+    # every bf16 value over scales with ties, ordinary ones, and one whose reciprocal passes float32; values, and
+    # keys that are not turned, are exact inputs, so the codes are determined
+    scales = np.array([7 / 256, 0.03, 0.017, 1.0, 3.0, 2.0 ** -7, 2.5e-39, 1e30], np.float32)
+    T, Hkv = 65536 // D, len(scales)
+    c = Cache(1, [T], Hkv, D, 64, True, seed=1, fill=False)
+    for s in c.scales:
+        s.copy_(torch.from_numpy(scales))
+    x = np.repeat(np.arange(65536, dtype=np.uint16).reshape(T, 1, D), Hkv, 1)
+    xd = to_dev_bf16(x)
+    tdg.rope_append(c.symm, c.cache, None, xd, xd.clone(), None, None, None, c.table_d, c.lens_d,
+                    cu=torch.tensor([0, T], dtype=torch.int32, device="cuda"))
+    torch.cuda.synchronize()
+    assert c.symm.status()["code"] == 0
+    with np.errstate(all="ignore"):
+        quotient = bf16_f64(x).astype(np.float32) / scales[None, :, None]
+    want = oracle.f64_to_e4m3(quotient)
+    nan = np.isnan(quotient)
+    for pool, what in zip(c.download(), "kv"):
+        got = oracle.gather_pages(pool, c.table[0], T)
+        assert np.all((got[nan] & 0x7F) == 0x7F), what
+        wrong = (got != want) & ~nan
+        assert not wrong.any(), f"{what}: {wrong.sum(axis=(0, 2))} codes by scale, first {quotient[wrong][0]}: {got[wrong][0]:#x} for {want[wrong][0]:#x}"
