@@ -7,7 +7,8 @@ then linked into tile_centric_comm_gb300/_build/libtdg.so with the static CUDA
 runtime, so the library has no load-time dependency on libcuda (the driver
 entry points it needs are looked up at run time).  csrc/tdg_tensors.cpp,
 the binding's tensor checks, becomes a CPython module beside it (g++, against
-torch's headers).
+torch's headers).  The library needs neither torch nor that module: without
+torch the module is left out, and when it does not compile the build warns.
 """
 from __future__ import annotations
 
@@ -19,6 +20,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -56,9 +58,12 @@ def _stale(target, inputs):
     return any(os.path.getmtime(i) > t for i in inputs)
 
 
-def build_tensors(force: bool = False) -> str:
+def build_tensors(force: bool = False) -> str | None:
     src = os.path.join(CSRC, "tdg_tensors.cpp")
-    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.submodule_search_locations:
+        return None
+    torch = spec.submodule_search_locations[0]
     headers = os.path.join(torch, "include")
     if force or _stale(TENSORS, [src, os.path.join(torch, "version.py")]):
         tmp = TENSORS + f".tmp{os.getpid()}"
@@ -72,13 +77,20 @@ def build_tensors(force: bool = False) -> str:
     return TENSORS
 
 
+def _tensors_or_warning(force):
+    try:
+        build_tensors(force)
+    except (OSError, RuntimeError) as e:
+        warnings.warn(f"the binding's tensor checks were not built: {e}")
+
+
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = _sources()
     deps = _deps()
     objs = [os.path.join(BUILD, os.path.basename(s)[:-3] + ".o") for s in srcs]
     if not force and not _stale(LIB, srcs + deps):
-        build_tensors(force)
+        _tensors_or_warning(force)
         return LIB
     cc = nvcc()
 
@@ -93,7 +105,7 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
         return obj, r.stderr
 
     with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 4))) as ex:
-        tensors = ex.submit(build_tensors, force)
+        tensors = ex.submit(_tensors_or_warning, force)
         for obj, err in ex.map(compile_one, zip(srcs, objs)):
             if verbose and err:
                 print(err, file=sys.stderr)
