@@ -24,7 +24,6 @@ def fake(monkeypatch, tmp_path):
     monkeypatch.setattr(tdg_build, "nvcc", lambda: "nvcc")
     monkeypatch.setattr(tdg_build, "BUILD", str(tmp_path))
     monkeypatch.setattr(tdg_build, "LIB", str(tmp_path / "libtdg.so"))
-    monkeypatch.setattr(tdg_build, "TENSORS", str(tmp_path / "tdg_tensors.so"))
     return state
 
 
@@ -60,3 +59,39 @@ def test_a_failing_kernel_is_an_error(fake):
     with pytest.raises(RuntimeError, match="nvcc failed"):
         tdg_build.build()
     assert not os.path.exists(tdg_build.LIB)
+
+
+def _fresh_binding():
+    """A second copy of the binding, which has not looked for the module yet."""
+    import importlib.util
+    spec = importlib.util.find_spec("tile_centric_comm_gb300.tdg")
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    return module
+
+
+def test_binding_takes_the_module_of_its_own_torch_and_python():
+    torch = pytest.importorskip("torch")
+    tdg_build.build()
+    path = tdg_build.tensors_path(torch.version.__version__)
+    assert os.path.exists(path) and path == tdg_build.build_tensors()
+    assert tdg_build.tensors_path("1.0") != path
+    b = _fresh_binding()
+    b._attn()
+    assert b._rows is not b._checked_rows and b._table is not b._checked_table and b._flat is not b._checked_flat
+
+
+def test_binding_checks_in_python_without_the_module(monkeypatch, tmp_path):
+    torch = pytest.importorskip("torch")
+    tdg_build.build()
+    other = tmp_path / "tdg_tensors.so"                 # one of unknown versions is not touched
+    other.write_text("x")
+    monkeypatch.setattr(tdg_build, "tensors_path", lambda version: str(tmp_path / ("of-" + version)))
+    b = _fresh_binding()
+    b._attn()
+    assert b._rows is b._checked_rows and b._table is b._checked_table and b._flat is b._checked_flat
+    # and the calls go through them
+    heap = SimpleNamespace(device=torch.device("cuda", 0), world=1, h=None)
+    x = torch.zeros(1, 2, 128)
+    with pytest.raises(TypeError, match="k: expected torch.bfloat16"):
+        b.rope_append(heap, b.PagedCache(4, 16, 2, 128, 0, 1 << 16), None, x, x, None, None, None, None, None)

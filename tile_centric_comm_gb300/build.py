@@ -16,6 +16,7 @@ import concurrent.futures as cf
 import glob
 import importlib.util
 import os
+import runpy
 import shutil
 import subprocess
 import sys
@@ -27,7 +28,6 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libtdg.so")
-TENSORS = os.path.join(BUILD, "tdg_tensors.so")
 INCLUDE = os.path.join(ROOT, "include")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -58,6 +58,12 @@ def _stale(target, inputs):
     return any(os.path.getmtime(i) > t for i in inputs)
 
 
+def tensors_path(torch_version: str) -> str:
+    """The tensor checks' module for a version of torch and this Python: it
+    reads their objects, so one built for others must not be loaded."""
+    return os.path.join(BUILD, f"tdg_tensors.torch-{torch_version}{sysconfig.get_config_var('EXT_SUFFIX')}")
+
+
 def build_tensors(force: bool = False) -> str | None:
     src = os.path.join(CSRC, "tdg_tensors.cpp")
     spec = importlib.util.find_spec("torch")
@@ -65,16 +71,18 @@ def build_tensors(force: bool = False) -> str | None:
         return None
     torch = spec.submodule_search_locations[0]
     headers = os.path.join(torch, "include")
-    if force or _stale(TENSORS, [src, os.path.join(torch, "version.py")]):
-        tmp = TENSORS + f".tmp{os.getpid()}"
+    version = os.path.join(torch, "version.py")
+    target = tensors_path(runpy.run_path(version)["__version__"])
+    if force or _stale(target, [src, version]):
+        tmp = target + f".tmp{os.getpid()}"
         cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-w", "-I", sysconfig.get_path("include"),
                "-I", headers, "-I", os.path.join(headers, "torch", "csrc", "api", "include"), src, "-o", tmp,
                "-L", os.path.join(torch, "lib"), "-lc10", "-ltorch_cpu", "-ltorch_python"]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"g++ failed for tdg_tensors.cpp:\n{r.stderr}")
-        os.replace(tmp, TENSORS)
-    return TENSORS
+        os.replace(tmp, target)
+    return target
 
 
 def _tensors_or_warning(force):

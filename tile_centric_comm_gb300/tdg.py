@@ -15,9 +15,10 @@ import os
 import struct
 import threading
 
+from . import build
+
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "_build", "libtdg.so")
-TENSORS_PATH = os.path.join(HERE, "_build", "tdg_tensors.so")
 
 TDG_OK = 0
 TDG_ERR_INVALID = -1
@@ -482,14 +483,16 @@ def _attn():
     global _torch, _current_raw_stream, _rows, _table, _flat, _Tensor, _t_bf16, _t_i32, _t_f32
     import torch
     L = lib()
-    if not os.path.exists(TENSORS_PATH):
-        raise RuntimeError(f"tdg_tensors.so not found at {TENSORS_PATH}: build it with "
-                           "`python -m tile_centric_comm_gb300.build`")
-    loader = importlib.machinery.ExtensionFileLoader("tdg_tensors", TENSORS_PATH)
-    checks = importlib.util.module_from_spec(importlib.util.spec_from_loader("tdg_tensors", loader))
-    loader.exec_module(checks)
-    checks.setup(torch.Tensor, _checked_rows, _checked_table, _checked_flat)
-    _rows, _table, _flat = checks.rows, checks.table, checks.flat
+    # the native checks where they were built for this torch and this Python,
+    # else the same checks in Python (5 us a call more)
+    _rows, _table, _flat = _checked_rows, _checked_table, _checked_flat
+    path = build.tensors_path(torch.version.__version__)
+    if os.path.exists(path):
+        loader = importlib.machinery.ExtensionFileLoader("tdg_tensors", path)
+        checks = importlib.util.module_from_spec(importlib.util.spec_from_loader("tdg_tensors", loader))
+        loader.exec_module(checks)
+        checks.setup(torch.Tensor, _checked_rows, _checked_table, _checked_flat)
+        _rows, _table, _flat = checks.rows, checks.table, checks.flat
     fast = ctypes.CDLL(LIB_PATH)
     for name in ("tdg_rope_append", "tdg_prompt_attention", "tdg_paged_decode"):
         f = getattr(fast, name)
