@@ -566,7 +566,9 @@ TDG_API int tdg_rope_append(tdg_symm *h, const tdg_rope_append_args *args, void 
  * q, out: Tq rows of Hq heads of D; k, v: Tk rows of Hkv heads; head h at h*D
  * of a row, rows *_stride elements apart.  Rows of q that no sequence covers
  * are left alone.  Offsets out of order, negative or past Tq / Tk are reported
- * as TDG_ERR_DEVICE (TDG_WHERE_CU, index b) and the sequence is skipped.
+ * as TDG_ERR_DEVICE (TDG_WHERE_CU, index b) and the sequence is skipped.  (Where
+ * the others then cover a row twice, that row is undefined, and where together
+ * they cover more than Tq rows, some of theirs may be left out.)
  * Requirements: D 64 or 128; Hq % Hkv == 0, Hq/Hkv <= 128; 0 <= Tq, Tk < 2^31;
  * 0 <= B <= 65535; strides multiples of 8 elements and at least the row's
  * extent; pointers 16-byte aligned (cu_q, cu_k, lse 4-byte); scale finite and

@@ -282,3 +282,55 @@ def test_refuses_what_would_overwrite_its_inputs(symm):
     assert rc(cu_k=cu_q.data_ptr()) == 0 and rc(lse=None) == 0           # inputs may be one another
     torch.cuda.synchronize()
     assert symm.status()["code"] == 0
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("cu_q,cu_k,bad", [
+    ([0, 50, 40, 90], [0, 50, 60, 90], [1]),           # backwards in the queries: rows 40 .. 49 lie in two sequences
+    ([0, 30, 60, 90], [0, 50, 40, 90], [1]),           # backwards in the keys
+    ([0, 30, 60, 91], [0, 30, 60, 90], [2]),           # past the last query
+    ([0, 30, 60, 90], [0, 30, 60, 95], [2]),           # past the last key
+    ([-1, 30, 60, 90], [0, 30, 60, 90], [0]),
+    ([0, 30, 60, 90], [0, 30, 2 ** 31 - 1, 90], [1, 2]),
+    ([0, -2 ** 31, 60, 90], [0, 30, 60, 90], [0, 1]),
+])
+def test_bad_offsets_leave_the_others_right(symm, D, cu_q, cu_k, bad):
+    c = Case([30, 30, 30], [30, 30, 30], 4, 2, D, seed=D)
+    _check_bad_offsets(symm, c, cu_q, cu_k, bad)
+
+
+@pytest.mark.parametrize("D,Hq,Hkv,n", [(128, 4, 1, 300), (64, 48, 48, 40), (128, 8, 8, 100)])
+def test_bad_offsets_among_many(symm, D, Hq, Hkv, n):
+    # more sequences than the item table has entries; items by length, with heads of 64 by two CTAs an SM
+    g = np.random.default_rng(n)
+    lens = g.integers(1, 20 if n == 300 else 300, n).tolist()
+    c = Case(lens, lens, Hq, Hkv, D, seed=n)
+    cu_q, cu_k = c.cu_q.tolist(), c.cu_k.tolist()
+    cu_k[n // 2] = len(c.k) + 7                         # the end of one sequence and the beginning of the next
+    cu_q[-1] = len(c.q) + 1
+    _check_bad_offsets(symm, c, cu_q, cu_k, [n // 2 - 1, n // 2, n - 1])
+
+
+def _check_bad_offsets(symm, c, cu_q, cu_k, bad):
+    q, k, v = (to_dev_bf16(x) for x in (c.q, c.k, c.v))
+    out = torch.empty(q.shape, dtype=torch.bfloat16, device="cuda")
+    out.view(torch.int16).fill_(0x7FC1)
+    lse = torch.full(q.shape[:2], 7.0, device="cuda")
+    tdg.prompt_attention(symm, q, k, v, out, torch.tensor(cu_q, dtype=torch.int32, device="cuda"),
+                         torch.tensor(cu_k, dtype=torch.int32, device="cuda"), lse=lse)
+    torch.cuda.synchronize()
+    st = symm.status()
+    assert st["code"] == tdg.TDG_ERR_DEVICE and st["where"] == "cu" and st["index"] in bad
+    out, lse = to_bits(out), lse.cpu().numpy()
+    times = np.zeros(len(c.q), int)
+    good = [b for b in range(len(cu_q) - 1) if b not in bad]
+    for b in good:
+        times[cu_q[b]:cu_q[b + 1]] += 1
+    for b in good:
+        rows, keys = np.arange(cu_q[b], cu_q[b + 1]), slice(cu_k[b], cu_k[b + 1])
+        want = oracle.attention(*(oracle.bf16_to_f64(x) for x in (c.q[rows], c.k[keys], c.v[keys])))
+        once = times[rows] == 1
+        want = {name: x[once] for name, x in want.items()}
+        check_attention(out[rows[once]], want, c.D, f"sequence {b}")
+        check_lse(lse[rows[once]], want, c.D, f"lse of sequence {b}")
+    assert np.all(out[times == 0] == 0x7FC1) and np.all(lse[times == 0] == 7)       # rows of no valid sequence
