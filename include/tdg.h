@@ -512,6 +512,8 @@ TDG_API size_t tdg_paged_pool_bytes(int64_t pages, int page_size, int64_t Hkv, i
  * stored.  Keys are rounded once, from float32.  A length that does not fit
  * the table row, that is below the sequence's new rows, or a page id outside
  * the pools is reported (TDG_WHERE_PAGE, index t) and the row is not stored.
+ * Offsets out of order are not reported: the rows are stored in slots of the
+ * sequence that they fall to, below its length, or not at all.
  * Two rows must not share a slot of the cache.
  *   What is not wanted is left out: q and q_out NULL (no queries, Hq = 0),
  * k_out NULL, table NULL (no cache write; v, cu, lens and the pools are then

@@ -293,3 +293,38 @@ def test_8_bit_codes_are_those_of_the_quotient(D):
         assert np.all((got[nan] & 0x7F) == 0x7F), what
         wrong = (got != want) & ~nan
         assert not wrong.any(), f"{what}: {wrong.sum(axis=(0, 2))} codes by scale, first {quotient[wrong][0]}: {got[wrong][0]:#x} for {want[wrong][0]:#x}"
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("cu", [[0, 5, 4], [0, -3, 6], [0, 100, 6], [6, 0, 6], [0, 2 ** 31 - 1, 6], [-2 ** 31, 2, 6], [3, 3, 2], [9, 9, 9]])
+def test_offsets_out_of_order_write_into_listed_sequences_only(cu, e4m3):
+    c = Case(2, [20, 9], [4, 2], 4, 2, 64, 16, e4m3, seed=12)
+    q, k = to_dev_bf16(c.q), to_dev_bf16(c.k)
+    q_out, k_out = torch.full_like(q, float("nan")), torch.full_like(k, float("nan"))
+    tdg.rope_append(c.c.symm, c.c.cache, q, k, to_dev_bf16(c.v), q_out, torch.from_numpy(c.cos_sin).cuda(),
+                    torch.from_numpy(c.pos).cuda(), c.c.table_d, c.c.lens_d, cu=torch.tensor(cu, dtype=torch.int32, device="cuda"), k_out=k_out)
+    torch.cuda.synchronize()
+    st = c.c.symm.status()
+    assert st["code"] == 0 or (st["code"] == tdg.TDG_ERR_DEVICE and st["where"] == "page")     # a length below the new rows
+    for got, x, what in ((q_out, c.q, "q"), (k_out, c.k, "k")):                                # the rows are turned all the same
+        want, mag = oracle.rope(x, c.cos_sin, c.pos)
+        _near(bf16_f64(to_bits(got)), want, mag, what)
+    # where row t goes: the first sequence that ends behind it, counted back from that one's length
+    stored = {}
+    for t in range(c.T):
+        b = sum(int(e) <= t for e in cu[1:])
+        if b < 2 and cu[b] <= t < cu[b + 1] and c.c.lens[b] >= cu[b + 1] - cu[b]:
+            j = c.c.lens[b] - (cu[b + 1] - t)
+            assert 0 <= j < c.c.lens[b]
+            stored[int(c.c.table[b, j // 16]), j % 16] = t
+    for codes, before, x, scale in zip(c.c.download(), (c.c.k, c.c.v), (c.k, c.v), (c.c.k_scale, c.c.v_scale)):
+        rest = codes.copy()
+        for (page, slot), t in stored.items():
+            want, mag = oracle.rope(x, c.cos_sin, c.pos) if x is c.k else (bf16_f64(x), 0 * bf16_f64(x))
+            if e4m3:
+                s = scale.astype(np.float64)[:, None]
+                _near8(oracle.e4m3_to_f64(codes[page, :, slot]), want[t] / s, mag[t] / s, f"row {t}")
+            else:
+                _near(bf16_f64(codes[page, :, slot]), want[t], mag[t], f"row {t}")
+            rest[page, :, slot] = before[page, :, slot]
+        assert np.array_equal(rest, before)                                                    # and nowhere else
