@@ -607,6 +607,11 @@ TDG_API int tdg_prompt_attention(tdg_symm *h, const tdg_prompt_attention_args *a
  * split ones in a fixed order.  For few sequences in a narrow table a cluster
  * of CTAs takes each (sequence, key head) and joins by itself, in one launch.
  * What the pages hold behind a sequence's length never reaches a result.
+ * Scores, softmax statistics and sums are float32; the weights are rounded to
+ * bf16 for the product with v.  Over an 8-bit cache a head's query is held in
+ * f16, scaled by a power of two that brings its largest element to [1, 2):
+ * elements down to 2^-17 of the largest are kept exactly, smaller ones to
+ * 2^-25 of it.
  * A negative length, one that does not fit the table row, or a page id
  * outside the pools is reported as TDG_ERR_DEVICE (TDG_WHERE_PAGE, index b);
  * that sequence's output is then undefined.

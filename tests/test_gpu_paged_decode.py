@@ -338,3 +338,36 @@ def test_refuses_what_would_overwrite_its_inputs(extra):
     assert rc(lse=scale.data_ptr() + 8) == 0 and rc() == 0
     torch.cuda.synchronize()
     assert c.symm.status()["code"] == 0 and not torch.equal(c.symm.buf[free:free + 2 * row], before[free:free + 2 * row])
+
+
+@pytest.mark.parametrize("extra", [0, 1024])
+@pytest.mark.parametrize("unseen", [False, True])
+@pytest.mark.parametrize("size", [2.0 ** 8, 2.0 ** 14, 2.0 ** 18])
+def test_outlier_channel_over_an_8_bit_cache(size, unseen, extra):
+    # one channel of every query far above the others; the keys use it, or hold 0 there, so that the small elements,
+    # of which f16 drops the end below 2^-25 of the largest, decide
+    c = Cache(2, [700, 33, 129], 2, 128, 32, True, seed=31, extra_entries=extra)
+    if unseen:
+        c.k[..., 5] = 0
+        c.upload()
+    g = np.random.default_rng(32)
+    x = g.standard_normal((3, 16, 128))
+    x[..., 5] = size * (1 + g.random((3, 16)))
+    q = bits(x)
+    qd = torch.from_numpy(q.view(np.int16)).view(torch.bfloat16).cuda()
+    out, lse = torch.empty_like(qd), torch.empty((3, 16), device="cuda")
+    tdg.paged_decode(c.symm, c.cache, qd, out, c.table_d, c.lens_d, c.part_off, lse=lse)
+    torch.cuda.synchronize()
+    assert c.symm.status()["code"] == 0
+    out, lse, qv = to_bits(out), lse.cpu().numpy().astype(np.float64), oracle.bf16_to_f64(q)
+    for b in range(3):
+        k, v = c.sequence(b)
+        want = oracle.attention(qv[b:b + 1], k, v)
+        # a query element is off by 2^-25 of the largest, a score by that times the key's, which moves a weight by as
+        # much and the sum of weights too; beside what any attention's scores are off by
+        top = np.abs(qv[b:b + 1]).max(-1)
+        off = 2.0 ** -25 * top * np.abs(k).sum(-1).max(0).repeat(8) / np.sqrt(128)
+        tol = ((2 * 2.0 ** -8 + 128 * 2.0 ** -23 * want["smag"] + 2 * np.expm1(2 * off))[..., None]) * want["mag"] + 1e-30
+        assert np.all(np.abs(oracle.bf16_to_f64(out[b:b + 1]) - want["out"]) <= tol), f"sequence {b}"
+        tol = 128 * 2.0 ** -23 * want["smag"] + 2.0 ** -20 * (np.abs(want["lse"]) + 1) + off
+        assert np.all(np.abs(lse[b] - want["lse"]) <= tol), f"lse of sequence {b}"

@@ -6,7 +6,7 @@
 // sum 2^(s - m'),  o' = o 2^(m - m') + P V;  partial results (m, l, o) join the
 // same way.  All of m, l, o are float32; P is rounded to bf16 for the
 // product, the only rounding besides the output's (keys and queries of an
-// 8-bit cache meet in f16, exactly but for elements 2^-14 below a query's
+// 8-bit cache meet in f16, exactly but for elements below 2^-17 of a query's
 // largest).
 //
 // Bound by HBM: K and V are read once, about 2 G flops per byte.  The G =
@@ -170,9 +170,10 @@ __device__ __forceinline__ uint32_t f16x2_bf16x2(uint32_t r)
     return pack_bf16x2(f.x, f.y);
 }
 
-// 2^-e for a row whose largest magnitude is `top`, so that the row scaled by it
-// lies within +-4: f16 then holds every bf16 value down to 2^-14 of the largest
-// exactly and the smaller ones to 2^-25 of it.
+// e for a row whose largest magnitude is `top`, so that the row times 2^-e lies
+// within +-2 (+-4 from 2^127 on): f16 (whose smallest step is 2^-24) then holds every bf16 value, of
+// 8 significant bits, down to 2^-17 of the largest exactly and the smaller ones
+// to 2^-25 of it.
 __device__ __forceinline__ int pd_exponent(float top)
 {
     const int e = (int)(__float_as_uint(top) >> 23) - 127;
