@@ -132,11 +132,14 @@ template <int A, int B> bool ranges_overlap(const Range (&a)[A], const Range (&b
 template <int A> bool pools_overlap(const tdg_symm *h, const tdg_paged_cache &c, const Range (&a)[A])
 {
     const uint64_t pool = tdg_paged_pool_bytes(c.pages, c.page_size, c.Hkv, c.D, c.kv_type);
-    for (int r = 0; r < h->world; ++r) {
-        const uint8_t *region = h->base + (uint64_t)r * h->region_bytes;
-        const Range pools[] = {{region + c.k_off, pool}, {region + c.v_off, pool}};
-        if (ranges_overlap(a, pools))
-            return true;
+    for (const Range &x : a) {
+        if (!rows_overlap(x.at, x.bytes, h->base, h->world * h->region_bytes)) // outside the heap, as most are
+            continue;
+        for (int r = 0; r < h->world; ++r) {
+            const uint8_t *region = h->base + (uint64_t)r * h->region_bytes;
+            if (rows_overlap(x.at, x.bytes, region + c.k_off, pool) || rows_overlap(x.at, x.bytes, region + c.v_off, pool))
+                return true;
+        }
     }
     return false;
 }
