@@ -9,9 +9,11 @@
 // 8-bit cache meet in f16, exactly but for elements below 2^-17 of a query's
 // largest).
 //
-// Bound by HBM: K and V are read once, about 2 G flops per byte.  The G =
-// Hq/Hkv query heads of a key head are the 16 rows of mma.sync (m16n8k16), so
-// a page is read once for all of them.
+// Bound by HBM: K and V are read once, about 2 G flops per byte, for up to 16
+// query heads a key head (G = Hq/Hkv): they are the 16 rows of mma.sync
+// (m16n8k16).  More heads are taken in groups of 16, each of which fetches the
+// pages for itself: 64 sequences of 1..16384 on one key head 52 us with 16 query
+// heads, 77 with 20 or 32, 230 with 128 (8-bit 191).
 //
 // Split: the (sequence, key head) pairs' tiles (64 tokens; 128 of an 8-bit
 // cache) form one long line, in which a pair also counts for the tiles that its
@@ -31,11 +33,15 @@
 // Measured on one GB300 (copy rate 6.79 TB/s), 64 / 8 heads of 128, both launches:
 //   2 sequences of 200,000..262,144          288 us, 7.0 TB/s
 //   64 of 1..8192, pages of 16               174 us, 6.6 TB/s
-//   128 of 2048..4096, 8-bit                 144 us, 5.5 TB/s: the conversions
+//   128 of 2048..4096, 8-bit                 145 us, 5.5 TB/s: the conversions
 //                                            e4m3 -> f16 -> bf16 and what waits
-//                                            for them; three CTAs an SM spill
+//                                            for them (44 bytes a thread spilled, 68
+//                                            with clusters; three CTAs an SM spill more)
 //   64 of 1..512                             19 us, 4.3 TB/s: pairs of a few tiles
-//   one sequence of 1000 (a cluster a pair)  7.3 us: launch, lookups, two tiles
+//   one sequence of 1000                     7.3 to 7.7 us in a table as wide as it
+//                                            (a cluster a pair: launch, lookups, two
+//                                            tiles), 9.0 in one of 131,072 tokens
+//   64 of 1..8192, 64 / 8 heads of 64        94 us, 5.9 TB/s; 8-bit 63 us, 4.4 TB/s
 #include <cuda_fp16.h>
 
 #include "tdg_paged.cuh"

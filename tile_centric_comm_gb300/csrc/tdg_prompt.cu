@@ -30,15 +30,19 @@
 //
 // Bound: 4 D flops per query, key and head on the tensor cores.  Measured on
 // one GB300 (dense peak measured there: 1876 TFLOP/s):
-//   8192 tokens, 64 / 8 heads of 128           635 us, 1730 TFLOP/s, 92 %
+// (a call alone; back to back the power cap lowers the clock: 8192 tokens 670 to 690)
+//   8192 tokens, 64 / 8 heads of 128           632 us, 1740 TFLOP/s, 93 %; not
+//                                              causal 1236 us, 1780 TFLOP/s
 //   1000 behind 7000, 2 x, same heads          333 us, 1505 TFLOP/s; 3.4 items
 //                                              an SM: 85 % of what 4 would take
-//   12 of 17..2311, 40 / 8 heads of 128        214 us, 1200 TFLOP/s: short items,
-//                                              the first and the last block of each
-//   4 of 2048..4096, 32 heads of 64            240 us, 830 TFLOP/s: with weights
-//                                              left as they are 167 us, that is what
-//                                              products of 64 columns reach here
-//   119 tokens, 64 / 8 heads of 128            8.1 us: launch, table, one block
+//   12 of 17..2311, 40 / 8 heads of 128        214 us, 1200 TFLOP/s: short items; at
+//                                              each one's end the softmax's warps also
+//                                              divide and store, and its next scores wait
+//   4 of 2048..4096, 32 heads of 64            230 us, 870 TFLOP/s (60 bytes a thread
+//                                              spilled): with weights left as they are
+//                                              167 us, that is what products of 64
+//                                              columns reach here
+//   119 tokens, 64 / 8 heads of 128            8.8 us: launch, table, one block
 #include <type_traits>
 
 #include "tdg_paged.cuh"

@@ -11,10 +11,13 @@
 // into shared memory; then they walk over all (row, head) pairs of the group,
 // 16 elements a thread, four pairs' loads in flight at a time.
 //
-// Measured on one GB300, 64 / 8 heads of 128: 9 prompts of 301..4093 tokens (927 MB)
-// 159 us, 5.8 TB/s (a copy makes 6.8 here, a stream that is half writes 6.0);
-// 256 tokens into an 8-bit cache 4.9 us and one token 3.8 us: launch and lookups
-// (a call of either takes the host 6.4 us).
+// Measured on one GB300 (copy rate 6.79 TB/s), 64 / 8 heads of 128: 9 prompts of
+// 301..4093 tokens (927 MB) 160 us, 5.8 TB/s; 8 prompts of 2500 153 us, 5.7 TB/s,
+// and 157 us, 5.3 TB/s, into an 8-bit cache (the divisions by the scale; 152 with
+// a reciprocal, whose codes differ); heads of 64 80 and 88 us.  256 tokens into an
+// 8-bit cache 5.6 us and one token 4.1 us: the launch, and lookups that this code
+// does one after the other, of which only the page id waits for the length and
+// the cosines for the position (a call of either takes the host 6 us).
 #include "tdg_paged.cuh"
 
 namespace tdg {
@@ -76,8 +79,9 @@ __device__ __forceinline__ uint4 ld_once(const __nv_bfloat16 *p)
     return v;
 }
 
-// (four CTAs per SM rather than three are worth 5 % of a long bf16 write; the
-// 8-bit kernel does not fit the registers that this leaves)
+// (four CTAs per SM rather than three are worth 5 % of a long bf16 write, with 4 to
+// 12 bytes a thread spilled; the 8-bit kernel does not fit the registers that this
+// leaves)
 template <int D, bool INTER, bool E4M3>
 __global__ void __launch_bounds__(rp::THREADS, E4M3 ? 3 : 4) rope_append_kernel(const __grid_constant__ RopeParams p)
 {
