@@ -334,8 +334,10 @@ def run(state):
     if op == "dispatch":
         tdg.moe_dispatch_e4m3(s["symm"], case["T"], case["H"], case["k"], s["x_off"], s["slot"], s["codes"], s["scale"])
         return [s["codes"], s["scale"]]
-    tdg.moe_grad(s["symm"], case["T"], case["H"], case["k"], s["slot"], gate_off=s["gate_off"], dout_off=s["dout_off"],
-                 dx_off=s["dx_off"], dgate_off=s["dgate_off"], y=s["y"], dy=s["dy"], drecv=s["drecv"])
+    # the experts' own backward pass stands between the two and gives drecv
+    T, H, k = case["T"], case["H"], case["k"]
+    tdg.moe_combine_grad(s["symm"], T, H, k, s["gate_off"], s["dout_off"], s["dgate_off"], s["slot"], s["y"], s["dy"])
+    tdg.moe_dispatch_grad(s["symm"], T, H, k, s["dx_off"], s["slot"], s["drecv"])
     return [s["dy"], s["dgate"], s["dx"]]
 
 
