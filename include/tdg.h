@@ -1,8 +1,8 @@
 /*
  * tdg.h -- C ABI of libtdg: tile-centric overlapped AllGather+GEMM,
- * GEMM+ReduceScatter and MoE dispatch/combine, and the attention of a serving
- * step (rotary positions, packed prompts, a paged cache) on one GB300
- * (sm_103a).
+ * GEMM+ReduceScatter and MoE dispatch/combine (with its gradient and an 8-bit
+ * form), products of 8-bit matrices, and the attention of a serving step
+ * (rotary positions, packed prompts, a paged cache) on one GB300 (sm_103a).
  *
  * Model.  W logical ranks live in ONE device allocation that the caller owns:
  * W equal "regions" (rank r's symmetric heap) followed by W signal areas and
@@ -149,8 +149,9 @@ typedef struct {
 #define TDG_WHERE_RS_SIGNAL 6  /* GEMM-RS arrival counter update did not settle */
 #define TDG_WHERE_PAGE 7       /* a page id outside the pools, or a length outside the page table */
 #define TDG_WHERE_POS 8        /* a rotary position outside the table          */
-#define TDG_WHERE_CU 9         /* row offsets of packed sequences out of order or range */
+#define TDG_WHERE_CU 9         /* row offsets of packed sequences or of experts out of order or range */
 #define TDG_WHERE_PART 10      /* partial results that another call has overwritten */
+#define TDG_WHERE_SLOT 11      /* a receive row outside the receive buffer      */
 
 /*
  * Copy the status block to *out (may be NULL) after synchronising `stream`,
@@ -735,6 +736,163 @@ TDG_API int tdg_moe_dispatch_combine(tdg_symm *h, const tdg_moe_args *args, void
  */
 #define TDG_MOE_STATIC_WORKSPACE_BYTES (2u * 1024u * 1024u)
 TDG_API int tdg_moe_dispatch_combine_noalloc(tdg_symm *h, const tdg_moe_args *args, void *stream);
+
+/* ---- 8 bits with a scale for each block ---------------------------------------- */
+/*
+ * A matrix "in 8 bits" is e4m3 codes (sign, 4 exponent, 3 mantissa bits;
+ * largest 448) with a float32 scale for each block of 128 elements along the
+ * contraction: rows of activations have one for each row and block (1 x 128),
+ * weights one for each 128 x 128 block.  The last block of a row (and of a
+ * matrix's rows) may be short.
+ *
+ * tdg_quantise writes codes and scales of bf16 values:
+ *   scale = max(a / 448, 2^-100), a the largest |x| of the block (float32
+ *           quotient);
+ *   code  = the float32 quotient x / scale, clamped to +-448 and rounded to
+ *           nearest even.
+ * A NaN takes no part in the maximum and its code is NaN; an infinity makes
+ * the block's scale infinite, its own code NaN and the block's others 0.
+ *   TDG_QUANT_ROWS:   x has `rows` rows of K; scale: rows of ceil(K/128).
+ *   TDG_QUANT_GATED:  x has `rows` rows of 2K, columns [0, K) the gate g and
+ *                     [K, 2K) the up projection u; what is quantised is
+ *                     g / (1 + exp(-g)) * u in float32 (not rounded to
+ *                     bf16; finite g and u).
+ *   TDG_QUANT_BLOCKS: x is E matrices of `rows` x K, one behind the other
+ *                     (matrix e from row e * rows on); scale: E matrices of
+ *                     ceil(rows/128) x ceil(K/128).
+ * count (ROWS and GATED; NULL: all): device int64, the rows in use; rows from
+ * *count on are left alone.  A count outside [0, rows] is reported as
+ * TDG_ERR_DEVICE (TDG_WHERE_CU) and cut to it.
+ * Requirements: rows, E >= 0, rows * E < 2^31 (E 1 unless BLOCKS); K a multiple of 16, 16 <= K
+ * < 2^30; strides in elements, at least the row's extent, x's a multiple of 8
+ * and the codes' of 16; scale_stride >= ceil(K/128) (BLOCKS: equal); x and
+ * codes 16-byte aligned, scale 4-byte, count 8-byte; outputs overlapping no
+ * input and not each other.  rows == 0 or E == 0 is a no-op.
+ */
+#define TDG_QUANT_ROWS 0
+#define TDG_QUANT_GATED 1
+#define TDG_QUANT_BLOCKS 2
+
+typedef struct {
+    int kind;
+    int64_t rows, K, E;
+    const void *x;        /* bf16                                               */
+    int64_t x_stride;
+    void *codes;          /* e4m3                                               */
+    int64_t codes_stride;
+    float *scale;
+    int64_t scale_stride;
+    const int64_t *count; /* device, or NULL                                    */
+} tdg_quantise_args;
+
+TDG_API int tdg_quantise(tdg_symm *h, const tdg_quantise_args *args, void *stream);
+
+/*
+ * The product of 8-bit matrices, rows of activations a (M x K) with weights b
+ * (N x K):
+ *   out[m][n] = sum_j a_scale[m][j] b_scale[n/128][j] sum_{k in block j} a[m][k] b[n][k].
+ * With base (device, E + 1 int64 row offsets, as the MoE routing writes them)
+ * b is E such matrices with their scales, one behind the other, and rows
+ * [base[e], base[e+1]) of a are multiplied with matrix e; rows that no expert
+ * has are left alone.  Without it E is 1 and all M rows count.
+ * A block's product of codes is summed in float32 by the tensor cores, then
+ * multiplied with the product of its two scales (one float32 rounding) and
+ * added in float32 to the blocks before; out is bf16 (rounded once, to
+ * nearest even) or, with out_f32 = 1, those sums.  With few rows K may be cut
+ * into parts whose sums are added in a fixed order: results depend on sizes
+ * only, not on when a call runs.
+ * Scales may be any float32 values whose products stay within its range.  A
+ * row's codes and scales reach only that row of out (a NaN in one row gives
+ * NaN there alone).
+ * Offsets out of order, negative or past M are reported as TDG_ERR_DEVICE
+ * (TDG_WHERE_CU, index e) and the expert is left out (where others then cover
+ * a row twice, that row is undefined).
+ * Requirements: 0 <= M < 2^31; N a multiple of 8, 8 <= N < 2^24; K a multiple of 16, 16 <= K
+ * < 2^24; 1 <= E <= 4096, E * N < 2^31, and E = 1 without base; a_stride (a multiple of 16) and
+ * out_stride (of 8; of 4 with out_f32) at least the row's extent, all strides below 2^31; a, b and out
+ * 16-byte aligned, scales 4-byte, base 8-byte; a_scale_stride >= ceil(K/128);
+ * out overlapping no input.  M == 0 is a no-op.
+ */
+typedef struct {
+    int64_t M, N, K, E;
+    const void *a;         /* e4m3, M rows, a_stride elements apart             */
+    int64_t a_stride;
+    const float *a_scale;  /* M rows of ceil(K/128), a_scale_stride apart       */
+    int64_t a_scale_stride;
+    const void *b;         /* e4m3, E x N x K                                   */
+    const float *b_scale;  /* E x ceil(N/128) x ceil(K/128)                     */
+    void *out;             /* bf16 or float32, M rows, out_stride elements apart */
+    int64_t out_stride;
+    int out_f32;
+    const int64_t *base;   /* device, E + 1 row offsets, or NULL                */
+} tdg_scaled_gemm_args;
+
+TDG_API int tdg_scaled_gemm(tdg_symm *h, const tdg_scaled_gemm_args *args, void *stream);
+
+/* ---- MoE dispatch in 8 bits, gradients of dispatch and combine ------------------ */
+/*
+ * tdg_moe_dispatch_e4m3: the dispatch of tdg_moe_dispatch_combine with rows
+ * quantised on the way (as TDG_QUANT_ROWS): codes[slot(src,t,kk)] and
+ * scale[slot(src,t,kk)] are those of x_src[t] (T x H bf16 at region(src) +
+ * x_off).  slot as the routing phase writes it; codes: W*T*k rows of H e4m3,
+ * scale: W*T*k rows of ceil(H/128) float32.
+ * Requirements: H a multiple of 16, 16 <= H < 2^30; otherwise as for the
+ * gradients below.
+ *
+ * The gradients, for a loss whose gradient of out_src is dout_src (T x H bf16
+ * at region(src) + dout_off).  Combine: out = sum_kk gate[kk] y[slot(kk)], so
+ *   dy[slot(src,t,kk)]  = bf16(gate_src[t][kk] * dout_src[t]),
+ *   dgate_src[t][kk]    = sum_h dout_src[t][h] y[slot(src,t,kk)][h]
+ * (T x k float32 at region(src) + dgate_off; summed in float32 in an order
+ * fixed by H).  Dispatch: recv[slot(kk)] = x, so
+ *   dx_src[t] = bf16(sum_kk drecv[slot(src,t,kk)])
+ * (float32 sum in kk order; T x H bf16 at region(src) + dx_off).  y, dy and
+ * drecv have the receive layout, W*T*k rows of H bf16; dy may be y itself.
+ * A slot of -1 (an expert id that the routing has refused) has no row: its
+ * dgate is 0 and it adds nothing.  Any other slot outside [0, W*T*k) is
+ * reported as TDG_ERR_DEVICE (TDG_WHERE_SLOT, index (src*T + t)*k + kk) and
+ * treated like it.  Two choices must not share a slot.  Receive rows that no
+ * slot names are left alone.
+ * Requirements: world the heap's; T >= 0; H % 8 == 0, 8 <= H < 2^30; 1 <= k <= 32; W*T*k < 2^31;
+ * x_off, dout_off, dx_off, y, dy, drecv, codes 16-byte aligned, gate_off,
+ * dgate_off and scale 4-byte, slot 8-byte; per-rank data inside its region
+ * (TDG_ERR_NOMEM otherwise); what is written overlapping nothing else of the
+ * call (but dy being y).  T == 0 is a no-op.
+ */
+typedef struct {
+    int world;
+    int k;
+    int64_t T, H;
+    size_t x_off;
+    const int64_t *slot;
+    void *codes;
+    float *scale;
+} tdg_moe_dispatch_e4m3_args;
+
+TDG_API int tdg_moe_dispatch_e4m3(tdg_symm *h, const tdg_moe_dispatch_e4m3_args *args, void *stream);
+
+typedef struct {
+    int world;
+    int k;
+    int64_t T, H;
+    size_t gate_off, dout_off, dgate_off;
+    const int64_t *slot;
+    const void *y;
+    void *dy;
+} tdg_moe_combine_grad_args;
+
+TDG_API int tdg_moe_combine_grad(tdg_symm *h, const tdg_moe_combine_grad_args *args, void *stream);
+
+typedef struct {
+    int world;
+    int k;
+    int64_t T, H;
+    size_t dx_off;
+    const int64_t *slot;
+    const void *drecv;
+} tdg_moe_dispatch_grad_args;
+
+TDG_API int tdg_moe_dispatch_grad(tdg_symm *h, const tdg_moe_dispatch_grad_args *args, void *stream);
 
 #ifdef __cplusplus
 }

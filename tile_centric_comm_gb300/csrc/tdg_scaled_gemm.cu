@@ -1,0 +1,692 @@
+// tdg_scaled_gemm.cu -- products of e4m3 matrices with a float32 scale for each
+// block of 128 along the contraction, of one matrix of weights or of many
+// experts' (rows sorted by expert, offsets on the device).
+//
+//   out[m][n] = sum_j sa[m][j] sw[n/128][j] (sum_{k in block j} a[m][k] w[n][k])
+//
+// The weights are the tensor cores' first operand (128 rows a CTA) and the
+// rows of a the second, whose count an instruction takes in steps of 16 (32
+// for a pair of CTAs): an expert with few or an odd number of rows then costs
+// what it has, not a tile of 128.  A block's product of codes is one
+// accumulator in TMEM; the epilogue warps take it from there and add it, times
+// its scales, to sums in registers while the next block is multiplied, so every
+// block passes through TMEM once: with 256 columns and 512 cycles of tensor work
+// a block, the loads take 256 and the packed multiply-adds 128.
+//
+// Warps of a CTA:
+//   warp 0      TMA loader: 128 x 128 codes of the weights and the tile's rows
+//               into a ring of shared memory
+//   warp 1      MMA issuer: four tcgen05.mma.kind::f8f6f4 (K = 32) a block
+//   warps 2, 3  scales: sa * sw of the tile's rows, four blocks at a time
+//   warps 4..   epilogue: TMEM -> registers, multiply-add, at the end of the
+//               tile bf16 (or float32) rows
+// A thread of the epilogue holds, of each 8 x 8 square, two neighbouring rows
+// of a (their scales are a float pair, so the multiply-adds are packed) for one
+// row of the weights; for the store a transposing stmatrix turns the squares.
+#include "tdg_scaled.cuh"
+
+namespace tdg {
+
+namespace sg {
+constexpr int BK = 128;                 // codes of a block: one scale, one swizzled row
+constexpr int WROWS = 128;              // weight rows of a CTA
+constexpr int W_BYTES = WROWS * BK;
+constexpr int SK = 4;                   // blocks whose scales are loaded together
+constexpr int SCH = 2;                  // such chunks in the ring
+constexpr int STG_ROW = 80;             // bytes of a staged row: 32 bf16 and a pad
+constexpr int STG = 8 * STG_ROW;        // of an epilogue warp
+constexpr int RED = 132;                // floats of a row of partial sums: 128 and a pad
+constexpr int NGROUP = 8;               // weight tiles that are visited together
+constexpr int MAX_E = 4096;
+} // namespace sg
+
+template <int PAIR_, int BT_, int EPIW_, int STAGES_, int TBUF_, int BOX_> struct ScaledShape {
+    static constexpr int PAIR = PAIR_;               // 1: a pair of CTAs shares the tile's rows of a
+    static constexpr int BT = BT_;                   // rows of a in a tile, at most
+    static constexpr int EPIW = EPIW_;               // epilogue warps
+    static constexpr int STAGES = STAGES_;
+    static constexpr int TBUF = TBUF_;               // accumulators in TMEM
+    static constexpr int BOX = BOX_;                 // rows of a TMA box
+    static constexpr int TROWS = PAIR ? BT / 2 : BT; // rows of a that a CTA holds
+    static constexpr int STAGE_BYTES = sg::W_BYTES + TROWS * sg::BK;
+    static constexpr int CW = BT / (EPIW / 4);       // columns of an epilogue warp
+    static constexpr int STEP = PAIR ? 32 : 16;      // of an instruction's columns
+    static constexpr int WTILE = PAIR ? 2 * sg::WROWS : sg::WROWS;
+    static constexpr int THREADS = 128 + 32 * EPIW;
+    static constexpr int SROW = BT + 8;              // floats of a block's scales
+    static constexpr int OFF_SCALE = STAGES * STAGE_BYTES;
+    static constexpr int OFF_STG = OFF_SCALE + sg::SCH * sg::SK * SROW * 4;
+    static constexpr int OFF_BAR = OFF_STG + EPIW * sg::STG;
+    static constexpr int OFF_PRE = OFF_BAR + 512;    // tiles before each expert
+    static constexpr int SMEM = OFF_PRE + 1024;      // + 4 (E + 1), + alignment slack
+    static_assert(TBUF * BT <= 512 && SMEM + 4 * (sg::MAX_E + 1) <= 232448, "TMEM or shared memory");
+    static_assert(BT * sg::RED * 4 <= OFF_SCALE, "partial sums fit the ring");
+};
+
+using ScaledWide = ScaledShape<1, 256, 8, 6, 2, 32>;
+using ScaledNarrow = ScaledShape<0, 64, 4, 8, 8, 16>;
+
+struct ScaledParams {
+    DevStatus *status;
+    uint32_t epoch;
+    uint64_t timeout_ns;
+    int64_t M, a_scale_stride, out_stride;
+    int N, E, k_blocks, n_tiles, n_blocks, out_f32;
+    int split;                   // CTAs of a cluster that share K (1: none)
+    const float *a_scale, *b_scale;
+    void *out;
+    const int64_t *base;
+};
+
+struct ScaledSmem {
+    uint64_t full[8], empty[8], tfull[8], tempty[8];
+    uint64_t sfull[sg::SCH], sempty[sg::SCH], drain;
+    uint32_t tmem_base;
+    volatile int abort;
+    uint32_t issued, consumed; // ring fills issued by the loader, consumed by the issuer
+    uint32_t scan[16];
+};
+static_assert(sizeof(ScaledSmem) <= 512, "barrier block");
+
+// e4m3 A and B (K-major), float32 D
+__device__ __forceinline__ constexpr uint32_t idesc_e4m3(int M, int N)
+{
+    return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+template <int PAIR> __device__ __forceinline__ void umma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+{
+    if (PAIR)
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                     "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+                     : "memory");
+    else
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                     "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+                     : "memory");
+}
+
+// 16 lanes x 32 columns: r[4i], r[4i+1] are columns 8i + 2(t%4) and the next of
+// lane t/4, r[4i+2], r[4i+3] those of lane t/4 + 8
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+                   "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(taddr));
+}
+
+// the loads before it have arrived; what reads r stays behind it
+__device__ __forceinline__ void tmem_ld_arrived(uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]),
+                   "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
+}
+
+__device__ __forceinline__ void fma_pair(uint64_t &acc, uint32_t lo, uint32_t hi, uint64_t scale)
+{
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(lo), "r"(hi));
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(v), "l"(scale));
+}
+
+__device__ __forceinline__ float2 halves(uint64_t v)
+{
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+    return f;
+}
+
+__device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+{
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
+                 : "memory");
+}
+
+struct ScaledTile {
+    int e;            // expert
+    int n0;           // first weight row of the cluster's tile
+    int width;        // columns of the instruction
+    int64_t tok0, end; // rows of a: [tok0, end)
+};
+
+// The item's tile.  pre: the tiles before each expert.  An expert's rows are
+// divided evenly over as few tiles as hold them; its tiles are visited in
+// groups of NGROUP weight tiles, so that those in flight together share both
+// operands in L2.
+template <class S> __device__ __forceinline__ ScaledTile scaled_tile(const ScaledParams &p, const uint32_t *pre, uint32_t item)
+{
+    ScaledTile t;
+    int lo = 0, hi = p.E; // pre[lo] <= item < pre[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (pre[mid] <= item)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    t.e = lo;
+    const int64_t first = p.base ? p.base[lo] : 0, rows = (p.base ? p.base[lo + 1] : p.M) - first;
+    const uint32_t tiles = (uint32_t)((rows + S::BT - 1) / S::BT), width = (uint32_t)((rows + tiles - 1) / tiles);
+    t.width = (int)((width + S::STEP - 1) / S::STEP * S::STEP);
+    const uint32_t local = item - pre[lo], per = sg::NGROUP * tiles, g = local / per, r = local - g * per;
+    const uint32_t in_group = min((uint32_t)sg::NGROUP, (uint32_t)p.n_tiles - g * sg::NGROUP);
+    const uint32_t row = r / in_group;
+    t.n0 = (int)(g * sg::NGROUP + (r - row * in_group)) * S::WTILE;
+    t.tok0 = first + (int64_t)row * t.width;
+    t.end = min(first + rows, t.tok0 + t.width);
+    return t;
+}
+
+template <class S>
+__global__ void __launch_bounds__(S::THREADS, 1)
+    scaled_gemm_kernel(const __grid_constant__ ScaledParams p, const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a)
+{
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    ScaledSmem *ps = reinterpret_cast<ScaledSmem *>(smem + S::OFF_BAR);
+    uint32_t *pre = reinterpret_cast<uint32_t *>(smem + S::OFF_PRE);
+    float *scales = reinterpret_cast<float *>(smem + S::OFF_SCALE);
+    constexpr bool PAIR = S::PAIR != 0;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int cl = PAIR ? 2 : p.split; // CTAs of the cluster
+    const int crank = cl > 1 ? (int)cluster_ctarank() : 0;
+    const int half = PAIR ? crank : 0;
+    const bool leader = half == 0;
+    const uint32_t unit = blockIdx.x / cl, units = gridDim.x / cl;
+    const uint64_t tmo = p.timeout_ns;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S::STAGES; ++i) {
+            mbar_init(&ps->full[i], 1);
+            mbar_init(&ps->empty[i], 1);
+        }
+        for (int i = 0; i < S::TBUF; ++i) {
+            mbar_init(&ps->tfull[i], 1);
+            mbar_init(&ps->tempty[i], S::EPIW * (PAIR ? 2 : 1));
+        }
+        for (int i = 0; i < sg::SCH; ++i) {
+            mbar_init(&ps->sfull[i], 2);
+            mbar_init(&ps->sempty[i], S::EPIW);
+        }
+        mbar_init(&ps->drain, 1);
+        ps->abort = 0;
+        ps->issued = 0;
+        ps->consumed = 0;
+        fence_mbar_init();
+        prefetch_tensormap(&map_w);
+        prefetch_tensormap(&map_a);
+    }
+    if (warp == 1) {
+        if (PAIR) {
+            tmem_alloc_pair(&ps->tmem_base, 512);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(&ps->tmem_base, 512);
+            tmem_relinquish();
+        }
+        tc_fence_before();
+    }
+    griddep_launch_dependents();
+    griddep_wait();
+    // the tiles before each expert: a segment of experts a thread, then a scan
+    {
+        const int per = (p.E + S::THREADS - 1) / S::THREADS;
+        const int lo = min(p.E, (int)threadIdx.x * per), hi = min(p.E, lo + per);
+        const uint64_t most = 0x7fffffffu;
+        auto tiles_of = [&](int e) -> uint64_t {
+            const int64_t b0 = p.base ? p.base[e] : 0, b1 = p.base ? p.base[e + 1] : p.M;
+            if (b0 < 0 || b1 < b0 || b1 > p.M) {
+                if (blockIdx.x == 0)
+                    report_fault(p.status, TDG_ERR_DEVICE, TDG_WHERE_CU, (uint32_t)e, p.epoch);
+                return 0;
+            }
+            return (uint64_t)((b1 - b0 + S::BT - 1) / S::BT) * p.n_tiles;
+        };
+        uint64_t own = 0;
+        for (int e = lo; e < hi; ++e)
+            own = min(most, own + tiles_of(e));
+        uint64_t upto = own; // of the warp's lanes up to this one
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const uint64_t v = __shfl_up_sync(0xffffffffu, upto, d);
+            if (lane >= d)
+                upto = min(most, upto + v);
+        }
+        if (lane == 31)
+            ps->scan[warp] = (uint32_t)upto;
+        __syncthreads();
+        uint64_t run = 0;
+        for (int w = 0; w < warp; ++w)
+            run = min(most, run + ps->scan[w]);
+        const uint64_t before = __shfl_up_sync(0xffffffffu, upto, 1);
+        run = lane ? min(most, run + before) : run;
+        for (int e = lo; e < hi; ++e) {
+            pre[e] = (uint32_t)run;
+            run = min(most, run + tiles_of(e));
+            if (e == p.E - 1)
+                pre[p.E] = (uint32_t)run;
+        }
+    }
+    __syncthreads();
+    if (cl > 1)
+        cluster_sync(); // the peers' barriers are initialised before any remote use
+    tc_fence_after();
+    const uint32_t tmem = ps->tmem_base;
+    const uint32_t items = p.split > 1 ? min(pre[p.E], units) : pre[p.E]; // with K cut a cluster has one tile
+    // this CTA's blocks of K
+    const int kb0 = p.split > 1 ? (int)((int64_t)p.k_blocks * crank / p.split) : 0;
+    const int kb1 = p.split > 1 ? (int)((int64_t)p.k_blocks * (crank + 1) / p.split) : p.k_blocks;
+    const uint32_t full0 = PAIR ? mapa_shared(smem_u32(&ps->full[0]), 0) : smem_u32(&ps->full[0]);
+    const uint32_t tempty0 = PAIR ? mapa_shared(smem_u32(&ps->tempty[0]), 0) : smem_u32(&ps->tempty[0]);
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0, issued = 0;
+            for (uint32_t it = unit; it < items && !ps->abort; it += units) {
+                const ScaledTile t = scaled_tile<S>(p, pre, it);
+                const int rows = PAIR ? t.width / 2 : t.width, boxes = (rows + S::BOX - 1) / S::BOX;
+                const uint32_t bytes = (uint32_t)(sg::W_BYTES + boxes * S::BOX * sg::BK);
+                const uint32_t row = (uint32_t)t.tok0 + half * rows;
+                const int wrow = t.n0 + half * sg::WROWS;
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    if (!mbar_wait(&ps->empty[stage], phase ^ 1u, tmo)) {
+                        report_fault(p.status, TDG_ERR_TIMEOUT, TDG_WHERE_PIPE, 0, p.epoch);
+                        ps->abort = 1;
+                        break;
+                    }
+                    uint8_t *dst = smem + stage * S::STAGE_BYTES;
+                    if (leader) // for both CTAs' bytes
+                        mbar_arrive_expect_tx(&ps->full[stage], PAIR ? 2 * bytes : bytes);
+                    const uint32_t bar = full0 + stage * 8;
+                    if (PAIR) {
+                        tma_load_3d_pair(dst, &map_w, bar, kb * sg::BK, wrow, t.e);
+                        for (int i = 0; i < boxes; ++i)
+                            tma_load_2d_pair(dst + sg::W_BYTES + i * S::BOX * sg::BK, &map_a, bar, kb * sg::BK, (int)(row + i * S::BOX));
+                    } else {
+                        tma_load_3d_addr(dst, &map_w, bar, kb * sg::BK, wrow, t.e);
+                        for (int i = 0; i < boxes; ++i)
+                            tma_load_2d_addr(dst + sg::W_BYTES + i * S::BOX * sg::BK, &map_a, bar, kb * sg::BK, (int)(row + i * S::BOX));
+                    }
+                    ++issued;
+                    if (++stage == S::STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            ps->issued = issued;
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0 && leader) {
+            int stage = 0, buf = 0;
+            uint32_t phase = 0, bphase = 0, consumed = 0;
+            const uint32_t sbase = smem_u32(smem);
+            for (uint32_t it = unit; it < items && !ps->abort; it += units) {
+                const ScaledTile t = scaled_tile<S>(p, pre, it);
+                const uint32_t idesc = idesc_e4m3(S::WTILE, t.width);
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    if (!mbar_wait(&ps->tempty[buf], bphase ^ 1u, tmo) || !mbar_wait(&ps->full[stage], phase, tmo)) {
+                        report_fault(p.status, TDG_ERR_TIMEOUT, TDG_WHERE_PIPE, 1, p.epoch);
+                        ps->abort = 1;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t wd = sdesc_sw128(sbase + stage * S::STAGE_BYTES, 16, 1024);
+                    const uint64_t ad = sdesc_sw128(sbase + stage * S::STAGE_BYTES + sg::W_BYTES, 16, 1024);
+                    const uint32_t d = tmem + (uint32_t)(buf * S::BT);
+#pragma unroll
+                    for (int k = 0; k < sg::BK / 32; ++k)
+                        umma_e4m3<S::PAIR>(d, wd + 2 * k, ad + 2 * k, idesc, k ? 1u : 0u);
+                    if (PAIR) {
+                        umma_commit_pair_mask(&ps->empty[stage], 3);
+                        umma_commit_pair_mask(&ps->tfull[buf], 3);
+                    } else {
+                        umma_commit(&ps->empty[stage]);
+                        umma_commit(&ps->tfull[buf]);
+                    }
+                    ++consumed;
+                    if (++stage == S::STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                    if (++buf == S::TBUF) {
+                        buf = 0;
+                        bphase ^= 1u;
+                    }
+                }
+            }
+            ps->consumed = consumed;
+            if (ps->abort) { // every MMA issued has finished before TMEM is freed
+                if (PAIR)
+                    umma_commit_pair_mask(&ps->drain, 3);
+                else
+                    umma_commit(&ps->drain);
+                (void)mbar_wait(&ps->drain, 0, tmo);
+            }
+        }
+        __syncwarp();
+    } else if (warp < 4) {
+        // scales: 8 rows of a x SK blocks a step, each warp every other step
+        int chunk = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        const int j = lane % sg::SK, r0 = lane / sg::SK + (warp - 2) * 8;
+        for (uint32_t it = unit; it < items && ok; it += units) {
+            const ScaledTile t = scaled_tile<S>(p, pre, it);
+            const int nb = min((t.n0 + half * sg::WROWS) / sg::WROWS, p.n_blocks - 1);
+            const float *sw = p.b_scale + ((int64_t)t.e * p.n_blocks + nb) * p.k_blocks;
+            const int rows = (int)(t.end - t.tok0);
+            const float *sa = p.a_scale + t.tok0 * p.a_scale_stride;
+            for (int kb = kb0; kb < kb1; kb += sg::SK) {
+                const bool in = kb + j < kb1;
+                const float w = in ? sw[kb + j] : 0.f;
+                float v[S::BT / 16];
+#pragma unroll
+                for (int i = 0; i < S::BT / 16; ++i) {
+                    const int r = r0 + 16 * i;
+                    v[i] = in && r < rows ? sa[(int64_t)r * p.a_scale_stride + kb + j] : 0.f;
+                }
+                ok = mbar_wait(&ps->sempty[chunk], phase ^ 1u, tmo);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) {
+                    if (lane == 0)
+                        report_fault(p.status, TDG_ERR_TIMEOUT, TDG_WHERE_PIPE, 2, p.epoch);
+                    ps->abort = 1;
+                    break;
+                }
+                float *dst = scales + (chunk * sg::SK + j) * S::SROW + r0;
+#pragma unroll
+                for (int i = 0; i < S::BT / 16; ++i)
+                    dst[16 * i] = v[i] * w;
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&ps->sfull[chunk]);
+                if (++chunk == sg::SCH) {
+                    chunk = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+    } else {
+        const int q = warp & 3, cg = (warp - 4) >> 2; // lanes of TMEM, group of CW columns
+        uint8_t *stg = smem + S::OFF_STG + (warp - 4) * sg::STG;
+        constexpr int CH = S::CW / 32; // chunks of 32 columns
+        int buf = 0, chunk = 0;
+        uint32_t bphase = 0, sphase = 0;
+        for (uint32_t it = unit; it < items; it += units) {
+            const ScaledTile t = scaled_tile<S>(p, pre, it);
+            const int cols = t.width - cg * S::CW; // of this warp, the first CW of them
+            uint64_t acc[CH][2][8];
+#pragma unroll
+            for (int c = 0; c < CH; ++c)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    acc[c][0][i] = acc[c][1][i] = 0;
+            bool ok = true;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                const int in_chunk = (kb - kb0) % sg::SK;
+                if (in_chunk == 0)
+                    ok = mbar_wait(&ps->sfull[chunk], sphase, tmo);
+                ok = ok && mbar_wait(&ps->tfull[buf], bphase, tmo);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) {
+                    if (lane == 0)
+                        report_fault(p.status, TDG_ERR_TIMEOUT, TDG_WHERE_PIPE, 3, p.epoch);
+                    ps->abort = 1;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t at = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * S::BT + cg * S::CW);
+                const float *sc = scales + (chunk * sg::SK + in_chunk) * S::SROW + cg * S::CW + 2 * (lane & 3);
+#pragma unroll
+                for (int c = 0; c < CH; ++c) {
+                    if (c * 32 < cols) {
+                        uint32_t lo[16], hi[16];
+                        tmem_ld_16x256b_x4(at + c * 32, lo);
+                        tmem_ld_16x256b_x4(at + (16u << 16) + c * 32, hi);
+                        uint64_t s[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            s[i] = *reinterpret_cast<const uint64_t *>(sc + c * 32 + 8 * i);
+                        tmem_ld_arrived(lo);
+                        tmem_ld_arrived(hi);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            fma_pair(acc[c][0][2 * i], lo[4 * i], lo[4 * i + 1], s[i]);
+                            fma_pair(acc[c][0][2 * i + 1], lo[4 * i + 2], lo[4 * i + 3], s[i]);
+                            fma_pair(acc[c][1][2 * i], hi[4 * i], hi[4 * i + 1], s[i]);
+                            fma_pair(acc[c][1][2 * i + 1], hi[4 * i + 2], hi[4 * i + 3], s[i]);
+                        }
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (PAIR)
+                        mbar_arrive_remote(tempty0 + buf * 8);
+                    else
+                        mbar_arrive(&ps->tempty[buf]);
+                }
+                if (++buf == S::TBUF) {
+                    buf = 0;
+                    bphase ^= 1u;
+                }
+                if (in_chunk == sg::SK - 1 || kb == kb1 - 1) {
+                    if (lane == 0)
+                        mbar_arrive(&ps->sempty[chunk]);
+                    if (++chunk == sg::SCH) {
+                        chunk = 0;
+                        sphase ^= 1u;
+                    }
+                }
+            }
+            if (!ok)
+                break;
+            if (p.split > 1) { // partial sums, for the cluster to add
+                float *red = reinterpret_cast<float *>(smem);
+#pragma unroll
+                for (int c = 0; c < CH; ++c)
+                    if (c * 32 < cols)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+#pragma unroll
+                            for (int m = 0; m < 4; ++m) {
+                                const float2 f = halves(acc[c][m >> 1][2 * i + (m & 1)]);
+                                float *d = red + (cg * S::CW + c * 32 + 8 * i + 2 * (lane & 3)) * sg::RED + q * 32 + 8 * m + (lane >> 2);
+                                d[0] = f.x;
+                                d[sg::RED] = f.y;
+                            }
+                continue;
+            }
+            const int n = t.n0 + half * sg::WROWS + q * 32;
+            const int64_t row0 = t.tok0 + cg * S::CW;
+            if (p.out_f32) {
+                float *out = static_cast<float *>(p.out);
+#pragma unroll
+                for (int c = 0; c < CH; ++c)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int m = 0; m < 4; ++m) {
+                            const float2 f = halves(acc[c][m >> 1][2 * i + (m & 1)]);
+                            const int64_t row = row0 + c * 32 + 8 * i + 2 * (lane & 3);
+                            const int col = n + 8 * m + (lane >> 2);
+                            if (col < p.N && row < t.end)
+                                out[row * p.out_stride + col] = f.x;
+                            if (col < p.N && row + 1 < t.end)
+                                out[(row + 1) * p.out_stride + col] = f.y;
+                        }
+            } else {
+                const uint32_t put = smem_u32(stg) + (lane & 7) * sg::STG_ROW + (lane >> 3) * 16;
+                const uint8_t *get = stg + (lane >> 2) * sg::STG_ROW + (lane & 3) * 16;
+                const int col = n + (lane & 3) * 8;
+#pragma unroll
+                for (int c = 0; c < CH; ++c)
+                    if (c * 32 < cols)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int m = 0; m < 4; ++m) {
+                                const float2 f = halves(acc[c][m >> 1][2 * i + (m & 1)]);
+                                w[m] = pack_bf16x2(f.x, f.y);
+                            }
+                            __syncwarp();
+                            stmatrix_x4_trans(put, w[0], w[1], w[2], w[3]);
+                            __syncwarp();
+                            const uint4 v = *reinterpret_cast<const uint4 *>(get);
+                            const int64_t row = row0 + c * 32 + 8 * i + (lane >> 2);
+                            if (col < p.N && row < t.end)
+                                *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + row * p.out_stride + col) = v;
+                        }
+            }
+        }
+    }
+    __syncthreads();
+    if (ps->abort && threadIdx.x == 0) {
+        // wait (bounded) until no TMA write of this CTA is still in flight
+        if (!PAIR || leader) {
+            for (uint32_t f = ps->consumed; f < ps->issued; ++f)
+                (void)mbar_wait(&ps->full[f % S::STAGES], (f / S::STAGES) & 1u, tmo);
+        } else { // a peer's fill is known done once the leader has freed its slot
+            for (uint32_t f = ps->issued > (uint32_t)S::STAGES ? ps->issued - S::STAGES : 0u; f < ps->issued; ++f)
+                (void)mbar_wait(&ps->empty[f % S::STAGES], (f / S::STAGES) & 1u, tmo);
+        }
+    }
+    __syncthreads();
+    if (cl > 1)
+        cluster_sync(); // the partial sums are there; no CTA leaves while another may still touch it
+    if (!PAIR && p.split > 1) {
+        if (unit < items && !ps->abort) {
+            // this CTA's share of the rows, summed over the cluster in rank order
+            const ScaledTile t = scaled_tile<S>(p, pre, unit);
+            const int rows = (int)(t.end - t.tok0), mine = (rows - crank + p.split - 1) / p.split;
+            const uint32_t red = smem_u32(smem);
+            for (int i = threadIdx.x; i < mine * 32; i += S::THREADS) {
+                const int r = crank + (i >> 5) * p.split, c = (i & 31) * 4;
+                if (t.n0 + c >= p.N)
+                    continue;
+                float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int k = 0; k < p.split; ++k) {
+                    const float4 v = ld_cluster_f4(mapa_shared(red + (uint32_t)(r * sg::RED + c) * 4, (uint32_t)k));
+                    sum.x += v.x;
+                    sum.y += v.y;
+                    sum.z += v.z;
+                    sum.w += v.w;
+                }
+                const int64_t at = (t.tok0 + r) * p.out_stride + t.n0 + c;
+                if (p.out_f32)
+                    *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at) = sum;
+                else
+                    *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + at) =
+                        make_uint2(pack_bf16x2(sum.x, sum.y), pack_bf16x2(sum.z, sum.w));
+            }
+        }
+        cluster_sync();
+    }
+    if (warp == 1) {
+        tc_fence_after();
+        if (PAIR)
+            tmem_dealloc_pair(tmem, 512);
+        else
+            tmem_dealloc(tmem, 512);
+    }
+}
+
+} // namespace tdg
+
+using namespace tdg;
+using namespace tdg_host;
+
+namespace {
+
+bool map_codes(CUtensorMap *m, const void *base, int64_t inner, int64_t rows, int64_t row_bytes, int64_t matrices, int box_rows, bool flat)
+{
+    const uint64_t dims[3] = {(uint64_t)inner, (uint64_t)rows, (uint64_t)matrices};
+    const uint64_t strides[2] = {(uint64_t)row_bytes, (uint64_t)(rows * row_bytes)};
+    const uint32_t box[3] = {sg::BK, (uint32_t)box_rows, 1};
+    return encode_tiled(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, flat ? 2 : 3, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+template <class S> int run(tdg_symm *h, const tdg_scaled_gemm_args *a, ScaledParams &p, int split, int64_t units, cudaStream_t s)
+{
+    CUtensorMap map_w, map_a;
+    if (!map_codes(&map_w, a->b, a->K, a->N, a->K, a->E, sg::WROWS, false) || !map_codes(&map_a, a->a, a->K, a->M, a->a_stride, 1, S::BOX, true))
+        return TDG_ERR_CUDA;
+    const void *fn = reinterpret_cast<const void *>(&scaled_gemm_kernel<S>);
+    const int smem = S::SMEM + 4 * (sg::MAX_E + 1);
+    cudaError_t e = set_smem(fn, smem);
+    if (e != cudaSuccess)
+        return cuda_err(e, "scaled gemm smem");
+    p.split = split;
+    p.n_tiles = (int)((a->N + S::WTILE - 1) / S::WTILE);
+    const int cl = S::PAIR ? 2 : split;
+    void *args[] = {&p, &map_w, &map_a};
+    return cuda_err(launch(fn, dim3((unsigned)(units * cl)), dim3(S::THREADS), S::SMEM + 4 * ((size_t)a->E + 1), s, args, false, cl, true),
+                    "scaled gemm launch");
+}
+
+} // namespace
+
+extern "C" int tdg_scaled_gemm(tdg_symm *h, const tdg_scaled_gemm_args *a, void *stream)
+{
+    if (!h || !a)
+        return TDG_ERR_INVALID;
+    if (const int drc = check_device(h))
+        return drc;
+    if (a->M < 0 || a->M > INT32_MAX || a->N < 8 || a->N % 8 || a->N >= (1 << 24) || a->K < 16 || a->K % 16 || a->K >= (1 << 24) || a->E < 1 ||
+        a->E > sg::MAX_E || a->E * a->N > INT32_MAX || (!a->base && a->E != 1) || (a->out_f32 & ~1))
+        return TDG_ERR_INVALID;
+    const int64_t kb = (a->K + 127) / 128, nb = (a->N + 127) / 128;
+    if (a->M == 0)
+        return TDG_OK;
+    const int esz = a->out_f32 ? 4 : 2;
+    if (!a->a || !aligned16(a->a) || !a->b || !aligned16(a->b) || !a->out || !aligned16(a->out) || !a->a_scale || !aligned4(a->a_scale) ||
+        !a->b_scale || !aligned4(a->b_scale) || !aligned8(a->base) || !stride_ok(a->a_stride, a->K, 16) ||
+        !stride_ok(a->a_scale_stride, kb, 1) || !stride_ok(a->out_stride, a->N, 16 / esz))
+        return TDG_ERR_INVALID;
+    const Range out{a->out, extent(a->M, a->out_stride, a->N, esz)}, ra{a->a, extent(a->M, a->a_stride, a->K, 1)};
+    const Range rs{a->a_scale, extent(a->M, a->a_scale_stride, kb, 4)}, rb{a->b, (uint64_t)a->E * a->N * a->K};
+    const Range rbs{a->b_scale, (uint64_t)a->E * nb * kb * 4}, base{a->base, (uint64_t)(a->E + 1) * 8};
+    if (ranges_overlap({out}, {ra, rs, rb, rbs, base}))
+        return TDG_ERR_INVALID;
+    // the tiles, at most, of each kernel's shape: one more for every expert than its rows fill
+    const int64_t used = a->E < a->M ? a->E : a->M;
+    const int64_t wide = (used + a->M / ScaledWide::BT) * ((a->N + ScaledWide::WTILE - 1) / ScaledWide::WTILE);
+    const int64_t narrow = (used + a->M / ScaledNarrow::BT) * ((a->N + ScaledNarrow::WTILE - 1) / ScaledNarrow::WTILE);
+    if (narrow > INT32_MAX)
+        return TDG_ERR_INVALID;
+    ScaledParams p;
+    memset(&p, 0, sizeof p);
+    p.status = h->status;
+    p.epoch = next_epoch(h);
+    p.timeout_ns = pipe_timeout(timeout_or_default(0));
+    p.M = a->M;
+    p.a_scale_stride = a->a_scale_stride;
+    p.out_stride = a->out_stride;
+    p.N = (int)a->N;
+    p.E = (int)a->E;
+    p.k_blocks = (int)kb;
+    p.n_blocks = (int)nb;
+    p.out_f32 = a->out_f32;
+    p.a_scale = a->a_scale;
+    p.b_scale = a->b_scale;
+    p.out = a->out;
+    p.base = a->base;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (a->M / a->E > 64) {
+        const int64_t pairs = h->sm_count / 2;
+        return run<ScaledWide>(h, a, p, 1, wide < pairs ? wide : pairs, s);
+    }
+    // few tiles: K cut over the CTAs of a cluster, two blocks of it each at least
+    int split = 1;
+    while (split < 8 && narrow * split * 2 <= h->sm_count && kb >= 4 * split)
+        split *= 2;
+    const int64_t units = h->sm_count / split;
+    return run<ScaledNarrow>(h, a, p, split, narrow < units ? narrow : units, s);
+}

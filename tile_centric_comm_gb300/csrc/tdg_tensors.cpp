@@ -1,5 +1,5 @@
-// tdg_tensors.cpp -- the tensor checks of the attention calls' binding, as a
-// CPython module that reads torch's tensors directly.
+// tdg_tensors.cpp -- the tensor checks of the attention and 8-bit calls'
+// binding, as a CPython module that reads torch's tensors directly.
 //
 // A call of one token takes the GPU 4 us, and checking its up to ten tensors
 // took Python 6: a frame and five or six attribute calls for each.  Here a
@@ -12,7 +12,7 @@
 
 namespace {
 
-PyObject *tensor_type, *checked_rows, *checked_table, *checked_flat;
+PyObject *tensor_type, *checked_rows, *checked_table, *checked_flat, *checked_matrix;
 
 // the plain tensor behind `o`, of the type and on the device; NULL for any other
 const at::Tensor *plain(PyObject *o, at::ScalarType type, PyObject *device)
@@ -92,14 +92,32 @@ PyObject *flat(PyObject *, PyObject *const *args, Py_ssize_t n)
         checked_flat, args, n);
 }
 
-// setup(Tensor, rows, table, flat): torch's class and the Python functions
+// matrix(tensor, name, dtype, device) -> (address, row stride, rows, columns)
+PyObject *matrix(PyObject *, PyObject *const *args, Py_ssize_t n)
+{
+    return run(
+        [&]() -> PyObject * {
+            if (n != 4 || !THPDtype_Check(args[2]))
+                return nullptr;
+            const at::Tensor *t = plain(args[0], reinterpret_cast<THPDtype *>(args[2])->scalar_type, args[3]);
+            if (!t || t->dim() != 2)
+                return nullptr;
+            const long long rows = t->size(0), columns = t->size(1);
+            if (columns > 1 && t->stride(1) != 1)
+                return nullptr;
+            return Py_BuildValue("(LLLL)", address(*t), rows <= 1 ? columns : static_cast<long long>(t->stride(0)), rows, columns);
+        },
+        checked_matrix, args, n);
+}
+
+// setup(Tensor, rows, table, flat, matrix): torch's class and the Python functions
 PyObject *setup(PyObject *, PyObject *args)
 {
-    PyObject *o[4];
-    if (!PyArg_ParseTuple(args, "OOOO", &o[0], &o[1], &o[2], &o[3]))
+    PyObject *o[5];
+    if (!PyArg_ParseTuple(args, "OOOOO", &o[0], &o[1], &o[2], &o[3], &o[4]))
         return nullptr;
-    PyObject **const to[4] = {&tensor_type, &checked_rows, &checked_table, &checked_flat};
-    for (int i = 0; i < 4; ++i) {
+    PyObject **const to[5] = {&tensor_type, &checked_rows, &checked_table, &checked_flat, &checked_matrix};
+    for (int i = 0; i < 5; ++i) {
         Py_INCREF(o[i]);
         Py_XDECREF(*to[i]);
         *to[i] = o[i];
@@ -113,7 +131,8 @@ template <PyObject *(*F)(PyObject *, PyObject *const *, Py_ssize_t)> PyMethodDef
 }
 
 PyMethodDef methods[] = {
-    {"setup", setup, METH_VARARGS, nullptr}, fast<rows>("rows"), fast<table>("table"), fast<flat>("flat"), {nullptr, nullptr, 0, nullptr},
+    {"setup", setup, METH_VARARGS, nullptr}, fast<rows>("rows"), fast<table>("table"), fast<flat>("flat"), fast<matrix>("matrix"),
+    {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "tdg_tensors", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -34,7 +34,8 @@ B_KN, B_NK = 0, 1
 MOE_ROUTE, MOE_DISPATCH, MOE_COMBINE, MOE_ALL = 1, 2, 4, 7
 KV_BF16, KV_E4M3 = 0, 1
 WHERE = {1: "ag_flag", 2: "pipe", 3: "ll", 4: "moe_expert", 5: "ring", 6: "rs_signal",
-         7: "page", 8: "pos", 9: "cu", 10: "part"}
+         7: "page", 8: "pos", 9: "cu", 10: "part", 11: "slot"}
+QUANT_ROWS, QUANT_GATED, QUANT_BLOCKS = 0, 1, 2
 
 # every symbol include/tdg.h declares
 EXPORTS = [
@@ -45,6 +46,7 @@ EXPORTS = [
     "tdg_allreduce_recv_bytes", "tdg_allreduce", "tdg_flash_decode_part_bytes", "tdg_flash_decode",
     "tdg_paged_pool_bytes", "tdg_rope_append", "tdg_prompt_attention",
     "tdg_paged_decode_part_bytes", "tdg_paged_decode",
+    "tdg_quantise", "tdg_scaled_gemm", "tdg_moe_dispatch_e4m3", "tdg_moe_combine_grad", "tdg_moe_dispatch_grad",
 ]
 MOE_STATIC_WORKSPACE_BYTES = 2 * 1024 * 1024
 
@@ -136,6 +138,32 @@ class PagedDecodeArgs(ctypes.Structure):
                 ("lens", _vp), ("part_off", _sz), ("scale", ctypes.c_float)]
 
 
+class QuantiseArgs(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int), ("rows", _i64), ("K", _i64), ("E", _i64), ("x", _vp), ("x_stride", _i64),
+                ("codes", _vp), ("codes_stride", _i64), ("scale", _vp), ("scale_stride", _i64), ("count", _vp)]
+
+
+class ScaledGemmArgs(ctypes.Structure):
+    _fields_ = [("M", _i64), ("N", _i64), ("K", _i64), ("E", _i64), ("a", _vp), ("a_stride", _i64), ("a_scale", _vp),
+                ("a_scale_stride", _i64), ("b", _vp), ("b_scale", _vp), ("out", _vp), ("out_stride", _i64),
+                ("out_f32", ctypes.c_int), ("base", _vp)]
+
+
+class MoeDispatchE4m3Args(ctypes.Structure):
+    _fields_ = [("world", ctypes.c_int), ("k", ctypes.c_int), ("T", _i64), ("H", _i64), ("x_off", _sz), ("slot", _vp),
+                ("codes", _vp), ("scale", _vp)]
+
+
+class MoeCombineGradArgs(ctypes.Structure):
+    _fields_ = [("world", ctypes.c_int), ("k", ctypes.c_int), ("T", _i64), ("H", _i64), ("gate_off", _sz),
+                ("dout_off", _sz), ("dgate_off", _sz), ("slot", _vp), ("y", _vp), ("dy", _vp)]
+
+
+class MoeDispatchGradArgs(ctypes.Structure):
+    _fields_ = [("world", ctypes.c_int), ("k", ctypes.c_int), ("T", _i64), ("H", _i64), ("dx_off", _sz), ("slot", _vp),
+                ("drecv", _vp)]
+
+
 class TdgError(RuntimeError):
     def __init__(self, code, what):
         self.code = code
@@ -205,6 +233,11 @@ def lib():
             L.tdg_paged_decode_part_bytes.argtypes = [_i64, _i64, _i64]
             L.tdg_paged_decode.restype = ctypes.c_int
             L.tdg_paged_decode.argtypes = [_vp, ctypes.POINTER(PagedDecodeArgs), _vp]
+            for n, args in (("tdg_quantise", QuantiseArgs), ("tdg_scaled_gemm", ScaledGemmArgs),
+                            ("tdg_moe_dispatch_e4m3", MoeDispatchE4m3Args), ("tdg_moe_combine_grad", MoeCombineGradArgs),
+                            ("tdg_moe_dispatch_grad", MoeDispatchGradArgs)):
+                getattr(L, n).restype = ctypes.c_int
+                getattr(L, n).argtypes = [_vp, ctypes.POINTER(args), _vp]
             L.tdg_moe_dispatch_combine_noalloc.restype = ctypes.c_int
             L.tdg_moe_dispatch_combine_noalloc.argtypes = [_vp, ctypes.POINTER(MoeArgs), _vp]
             _lib = L
@@ -473,33 +506,35 @@ def _other_device(cache, device):
     raise ValueError(f"k_scale and v_scale: on {cache.device}, the heap is on {device}")
 
 
-_torch = _current_raw_stream = _rows = _table = _flat = None
+_torch = _current_raw_stream = _rows = _table = _flat = _matrix = None
 
 
 def _attn():
-    """torch, and the library's attention entry points taking packed arguments
-    (one struct.pack call costs a fraction of filling a ctypes structure field
-    by field, and these calls are short)."""
-    global _torch, _current_raw_stream, _rows, _table, _flat, _Tensor, _t_bf16, _t_i32, _t_f32
+    """torch, and the attention and 8-bit entry points of the library taking
+    packed arguments (one struct.pack call costs a fraction of filling a ctypes
+    structure field by field, and these calls are short)."""
+    global _torch, _current_raw_stream, _rows, _table, _flat, _matrix, _Tensor, _t_bf16, _t_i32, _t_f32, _t_i64, _t_e4m3
     import torch
     L = lib()
     # the native checks where they were built for this torch and this Python,
     # else the same checks in Python (5 us a call more)
-    _rows, _table, _flat = _checked_rows, _checked_table, _checked_flat
+    _rows, _table, _flat, _matrix = _checked_rows, _checked_table, _checked_flat, _checked_matrix
     path = build.tensors_path(torch.version.__version__)
     if os.path.exists(path):
         loader = importlib.machinery.ExtensionFileLoader("tdg_tensors", path)
         checks = importlib.util.module_from_spec(importlib.util.spec_from_loader("tdg_tensors", loader))
         loader.exec_module(checks)
-        checks.setup(torch.Tensor, _checked_rows, _checked_table, _checked_flat)
-        _rows, _table, _flat = checks.rows, checks.table, checks.flat
+        checks.setup(torch.Tensor, _checked_rows, _checked_table, _checked_flat, _checked_matrix)
+        _rows, _table, _flat, _matrix = checks.rows, checks.table, checks.flat, checks.matrix
     fast = ctypes.CDLL(LIB_PATH)
-    for name in ("tdg_rope_append", "tdg_prompt_attention", "tdg_paged_decode"):
+    for name in ("tdg_rope_append", "tdg_prompt_attention", "tdg_paged_decode", "tdg_quantise", "tdg_scaled_gemm",
+                 "tdg_moe_dispatch_e4m3", "tdg_moe_combine_grad", "tdg_moe_dispatch_grad"):
         f = getattr(fast, name)
         f.restype, f.argtypes = ctypes.c_int, [_vp, ctypes.c_char_p, _vp]
         globals()["_" + name] = f
     _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     _Tensor, _t_bf16, _t_i32, _t_f32 = torch.Tensor, torch.bfloat16, torch.int32, torch.float32
+    _t_i64, _t_e4m3 = torch.int64, torch.float8_e4m3fn
     _torch = torch
     return L
 
@@ -508,6 +543,11 @@ _DESC = "qiiqqNNPP"                                          # tdg_paged_cache
 _pack_rope = struct.Struct("@i4x" + _DESC + "qqqPPPqqqPPqqPqiiiiiiPqPPqqP").pack
 _pack_prompt = struct.Struct("@qqqqqqPPPqqqPqPPPif").pack
 _pack_decode = struct.Struct("@ii" + _DESC + "qqPqPqPPqqPNf0q").pack
+_pack_quantise = struct.Struct("@i4xqqqPqPqPqP").pack
+_pack_scaled = struct.Struct("@qqqqPqPqPPPqi4xP").pack
+_pack_dispatch_e4m3 = struct.Struct("@iiqqNPPP").pack
+_pack_combine_grad = struct.Struct("@iiqqNNNPPP").pack
+_pack_dispatch_grad = struct.Struct("@iiqqNPP").pack
 
 
 def _raw_stream(stream, device):
@@ -567,6 +607,24 @@ def _checked_flat(t, name, dtype, numel, device):
             and t.numel() >= numel:
         return t.data_ptr()
     return _tensor(t, name, dtype, numel, device)
+
+
+def _checked_matrix(t, name, dtype, device):
+    """Check a matrix whose rows may be strided; returns (pointer, row stride in
+    elements, rows, columns)."""
+    if not isinstance(t, _Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    stride = t.stride()
+    if len(stride) != 2:
+        raise ValueError(f"{name}: expected (rows, columns), got {tuple(t.shape)}")
+    rows, columns = t.shape
+    if columns > 1 and stride[1] != 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous, strides {stride}")
+    if t.get_device() != device.index:
+        raise ValueError(f"{name}: on {t.device}, the heap is on {device}")
+    return t.data_ptr(), columns if rows <= 1 else stride[0], rows, columns
 
 
 def rope_append(symm: Symm, cache: PagedCache, q, k, v, q_out, cos_sin, pos, table, lens, cu=None,
@@ -734,3 +792,124 @@ def moe_dispatch_combine_noalloc(symm: Symm, T: int, H: int, E: int, k: int, x_o
                   y, row_src, row_tok, row_k, phases)
     _check(lib().tdg_moe_dispatch_combine_noalloc(symm.h, ctypes.byref(a), _stream(stream)),
            "tdg_moe_dispatch_combine_noalloc")
+
+
+def _blocks(n):
+    return -(-n // 128)
+
+
+def quantise_rows(symm: Symm, x, codes, scale, gated=False, count=None, stream=None):
+    """Rows x (n, K) bfloat16 into e4m3 codes (n, K) with a float32 scale for
+    each row and block of 128, scale (n, ceil(K / 128)); rows of all three may
+    be strided.  gated: x is (n, 2K), gate columns before up columns, and what
+    is quantised is silu(gate) * up.  count: int64 tensor whose first element is
+    the number of rows in use (base[E:] of the MoE routing); the others are
+    left alone."""
+    if _torch is None:
+        _attn()
+    dev = symm.device
+    xp, xs, n, width = _matrix(x, "x", _t_bf16, dev)
+    cp, cs, *like = _matrix(codes, "codes", _t_e4m3, dev)
+    sp, ss, *slike = _matrix(scale, "scale", _t_f32, dev)
+    K = like[1]
+    if like[0] != n or width != (2 * K if gated else K) or slike != [n, _blocks(K)]:
+        raise ValueError(f"x {tuple(x.shape)}, codes {tuple(codes.shape)} and scale {tuple(scale.shape)} do not fit together")
+    np_ = 0 if count is None else _flat(count, "count", _t_i64, 1, dev)
+    a = _pack_quantise(QUANT_GATED if gated else QUANT_ROWS, n, K, 1, xp, xs, cp, cs, sp, ss, np_)
+    rc = _tdg_quantise(symm.h, a, _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "tdg_quantise")
+
+
+def quantise_blocks(symm: Symm, x, codes, scale, stream=None):
+    """Weights x (N, K) or (E, N, K) bfloat16 into e4m3 codes of the same shape
+    with a float32 scale for each 128 x 128 block, scale (..., ceil(N / 128),
+    ceil(K / 128)); all contiguous."""
+    if _torch is None:
+        _attn()
+    dev = symm.device
+    if x.dim() not in (2, 3):
+        raise ValueError(f"x: expected (N, K) or (E, N, K), got {tuple(x.shape)}")
+    *E, N, K = x.shape
+    if tuple(codes.shape) != tuple(x.shape) or tuple(scale.shape) != (*E, _blocks(N), _blocks(K)):
+        raise ValueError(f"x {tuple(x.shape)}, codes {tuple(codes.shape)} and scale {tuple(scale.shape)} do not fit together")
+    xp, cp = _flat(x, "x", _t_bf16, 0, dev), _flat(codes, "codes", _t_e4m3, 0, dev)
+    sp = _flat(scale, "scale", _t_f32, 0, dev)
+    a = _pack_quantise(QUANT_BLOCKS, N, K, E[0] if E else 1, xp, K, cp, K, sp, _blocks(K), 0)
+    rc = _tdg_quantise(symm.h, a, _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "tdg_quantise")
+
+
+def scaled_gemm(symm: Symm, a, a_scale, b, b_scale, out, base=None, stream=None):
+    """out = a @ b.T of 8-bit matrices with a scale for each block of 128 along
+    K: a (M, K) e4m3 with a_scale (M, ceil(K / 128)), b (N, K) e4m3 with b_scale
+    (ceil(N / 128), ceil(K / 128)), out (M, N) bfloat16 or float32; rows of a,
+    a_scale and out may be strided.  base (E + 1,) int64: rows [base[e],
+    base[e + 1]) of a go by matrix e of b (E, N, K) and b_scale (E, ...)."""
+    if _torch is None:
+        _attn()
+    dev = symm.device
+    ap, as_, M, K = _matrix(a, "a", _t_e4m3, dev)
+    sp, ss, *slike = _matrix(a_scale, "a_scale", _t_f32, dev)
+    f32 = out.dtype is _t_f32
+    op, os_, *olike = _matrix(out, "out", _t_f32 if f32 else _t_bf16, dev)
+    bshape = tuple(b.shape)
+    E = 1
+    if base is not None:
+        E = bshape[0] if len(bshape) == 3 else -1
+    N = olike[1]
+    lead = () if base is None else (E,)
+    if olike[0] != M or slike != [M, _blocks(K)] or bshape != (*lead, N, K) or \
+            tuple(b_scale.shape) != (*lead, _blocks(N), _blocks(K)):
+        raise ValueError(f"a {tuple(a.shape)}, a_scale {tuple(a_scale.shape)}, b {bshape}, b_scale "
+                         f"{tuple(b_scale.shape)} and out {tuple(out.shape)} do not fit together")
+    bp, bsp = _flat(b, "b", _t_e4m3, 0, dev), _flat(b_scale, "b_scale", _t_f32, 0, dev)
+    np_ = 0 if base is None else _flat(base, "base", _t_i64, E + 1, dev)
+    args = _pack_scaled(M, N, K, E, ap, as_, sp, ss, bp, bsp, op, os_, 1 if f32 else 0, np_)
+    rc = _tdg_scaled_gemm(symm.h, args, _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "tdg_scaled_gemm")
+
+
+def moe_dispatch_e4m3(symm: Symm, T: int, H: int, k: int, x_off: int, slot, codes, scale, stream=None):
+    """The dispatch of moe_dispatch_combine with rows quantised on the way:
+    codes (W*T*k, H) e4m3 and scale (W*T*k, ceil(H / 128)) float32 of every
+    choice's row, slot (W*T*k) int64 as the routing phase writes it."""
+    if _torch is None:
+        _attn()
+    dev, rows = symm.device, symm.world * T * k
+    a = _pack_dispatch_e4m3(symm.world, k, T, H, x_off, _flat(slot, "slot", _t_i64, rows, dev),
+                            _flat(codes, "codes", _t_e4m3, rows * H, dev),
+                            _flat(scale, "scale", _t_f32, rows * _blocks(H), dev))
+    rc = _tdg_moe_dispatch_e4m3(symm.h, a, _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "tdg_moe_dispatch_e4m3")
+
+
+def moe_combine_grad(symm: Symm, T: int, H: int, k: int, gate_off: int, dout_off: int, dgate_off: int, slot, y, dy,
+                     stream=None):
+    """Gradient of the combine: from dout (T, H) bfloat16 at dout_off of every
+    region, the gates at gate_off and the experts' outputs y (W*T*k, H), writes
+    dy (W*T*k, H) bfloat16 (may be y) and dgate (T, k) float32 at dgate_off."""
+    if _torch is None:
+        _attn()
+    dev, rows = symm.device, symm.world * T * k
+    a = _pack_combine_grad(symm.world, k, T, H, gate_off, dout_off, dgate_off, _flat(slot, "slot", _t_i64, rows, dev),
+                           _flat(y, "y", _t_bf16, rows * H, dev), _flat(dy, "dy", _t_bf16, rows * H, dev))
+    rc = _tdg_moe_combine_grad(symm.h, a, _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "tdg_moe_combine_grad")
+
+
+def moe_dispatch_grad(symm: Symm, T: int, H: int, k: int, dx_off: int, slot, drecv, stream=None):
+    """Gradient of the dispatch: dx (T, H) bfloat16 at dx_off of every region,
+    the sum of the gradients drecv (W*T*k, H) of a token's rows."""
+    if _torch is None:
+        _attn()
+    dev, rows = symm.device, symm.world * T * k
+    a = _pack_dispatch_grad(symm.world, k, T, H, dx_off, _flat(slot, "slot", _t_i64, rows, dev),
+                            _flat(drecv, "drecv", _t_bf16, rows * H, dev))
+    rc = _tdg_moe_dispatch_grad(symm.h, a, _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "tdg_moe_dispatch_grad")
