@@ -4,67 +4,75 @@
 //
 //   out[m][n] = sum_j sa[m][j] sw[n/128][j] (sum_{k in block j} a[m][k] w[n][k])
 //
-// The weights are the tensor cores' first operand (128 rows a CTA) and the
-// rows of a the second, whose count an instruction takes in steps of 16 (32
-// for a pair of CTAs): an expert with few or an odd number of rows then costs
-// what it has, not a tile of 128.  A block's product of codes is one
-// accumulator in TMEM; the epilogue warps take it from there and add it, times
-// its scales, to sums in registers while the next block is multiplied, so every
-// block passes through TMEM once: with 256 columns and 512 cycles of tensor work
-// a block, the loads take 256 and the packed multiply-adds 128.
+// A block's product of codes is one accumulator in TMEM.  The epilogue warps
+// take it from there and add it, times its two scales, to sums in registers
+// while the next block is multiplied; at the end of the tile the sums are
+// rounded and stored.  Two kernels, by the number of rows:
 //
-// Warps of a CTA:
-//   warp 0      TMA loader: 128 x 128 codes of the weights and the tile's rows
-//               into a ring of shared memory
+//   wide    256 rows of a x 256 weight rows by a pair of CTAs.  Rows of a are
+//           TMEM's lanes, so a thread of the epilogue needs one scale a block.
+//   narrow  128 weight rows x up to 64 rows of a.  The weights are the lanes and
+//           the rows of a the columns, which an instruction takes in steps of 16:
+//           an expert with few rows costs what it has, and streaming the weights
+//           is what bounds the call.  With few tiles the blocks of K are divided
+//           over the CTAs of a cluster, whose sums are added in rank order.
+//
+// Warps of a CTA (either kernel):
+//   warp 0      TMA loader: the codes of a block into a ring of shared memory
 //   warp 1      MMA issuer: four tcgen05.mma.kind::f8f6f4 (K = 32) a block
 //   warps 2, 3  scales: sa * sw of the tile's rows, four blocks at a time
-//   warps 4..   epilogue: TMEM -> registers, multiply-add, at the end of the
-//               tile bf16 (or float32) rows
-// A thread of the epilogue holds, of each 8 x 8 square, two neighbouring rows
-// of a (their scales are a float pair, so the multiply-adds are packed) for one
-// row of the weights; for the store a transposing stmatrix turns the squares.
+//   warps 4..   epilogue
 #include "tdg_scaled.cuh"
 
 namespace tdg {
 
 namespace sg {
 constexpr int BK = 128;                 // codes of a block: one scale, one swizzled row
-constexpr int WROWS = 128;              // weight rows of a CTA
-constexpr int W_BYTES = WROWS * BK;
+constexpr int ROWS = 128;               // lanes of TMEM: rows of a CTA's first operand
+constexpr int A_BYTES = ROWS * BK;
 constexpr int SK = 4;                   // blocks whose scales are loaded together
-constexpr int SCH = 2;                  // such chunks in the ring
-constexpr int STG_ROW = 80;             // bytes of a staged row: 32 bf16 and a pad
-constexpr int STG = 8 * STG_ROW;        // of an epilogue warp
-constexpr int RED = 132;                // floats of a row of partial sums: 128 and a pad
+constexpr int SCH = 3;                  // such chunks in the ring
 constexpr int NGROUP = 8;               // weight tiles that are visited together
 constexpr int MAX_E = 4096;
+constexpr int BAR_BYTES = 512;
 } // namespace sg
 
-template <int PAIR_, int BT_, int EPIW_, int STAGES_, int TBUF_, int BOX_> struct ScaledShape {
-    static constexpr int PAIR = PAIR_;               // 1: a pair of CTAs shares the tile's rows of a
-    static constexpr int BT = BT_;                   // rows of a in a tile, at most
-    static constexpr int EPIW = EPIW_;               // epilogue warps
-    static constexpr int STAGES = STAGES_;
-    static constexpr int TBUF = TBUF_;               // accumulators in TMEM
-    static constexpr int BOX = BOX_;                 // rows of a TMA box
-    static constexpr int TROWS = PAIR ? BT / 2 : BT; // rows of a that a CTA holds
-    static constexpr int STAGE_BYTES = sg::W_BYTES + TROWS * sg::BK;
-    static constexpr int CW = BT / (EPIW / 4);       // columns of an epilogue warp
-    static constexpr int STEP = PAIR ? 32 : 16;      // of an instruction's columns
-    static constexpr int WTILE = PAIR ? 2 * sg::WROWS : sg::WROWS;
-    static constexpr int THREADS = 128 + 32 * EPIW;
-    static constexpr int SROW = BT + 8;              // floats of a block's scales
+struct WideShape {
+    static constexpr bool PAIR = true;
+    static constexpr int BT = 256;                   // rows of a in a tile, over the pair
+    static constexpr int WTILE = 256;                // weight rows of a tile
+    static constexpr int STAGES = 6, STAGE_BYTES = 2 * sg::A_BYTES;
+    static constexpr int TBUF = 2, TCOLS = 256;      // accumulators in TMEM
+    static constexpr int EPIW = 8, THREADS = 128 + 32 * EPIW;
+    static constexpr int REGS_OTHER = 72, REGS_EPI = 216; // registers of a thread
+    static_assert(128 * REGS_OTHER + 32 * EPIW * REGS_EPI <= THREADS * (65536 / THREADS / 8 * 8), "registers of the launch");
+    static constexpr int SROW = 2 * sg::ROWS + 8;    // floats of a block's scales: for each half of the columns, and a pad
     static constexpr int OFF_SCALE = STAGES * STAGE_BYTES;
-    static constexpr int OFF_STG = OFF_SCALE + sg::SCH * sg::SK * SROW * 4;
-    static constexpr int OFF_BAR = OFF_STG + EPIW * sg::STG;
-    static constexpr int OFF_PRE = OFF_BAR + 512;    // tiles before each expert
-    static constexpr int SMEM = OFF_PRE + 1024;      // + 4 (E + 1), + alignment slack
-    static_assert(TBUF * BT <= 512 && SMEM + 4 * (sg::MAX_E + 1) <= 232448, "TMEM or shared memory");
-    static_assert(BT * sg::RED * 4 <= OFF_SCALE, "partial sums fit the ring");
+    static constexpr int OFF_BAR = OFF_SCALE + sg::SCH * sg::SK * SROW * 4;
+    static constexpr int OFF_PRE = OFF_BAR + sg::BAR_BYTES; // tiles before each expert
+    static constexpr int SMEM = OFF_PRE + 1024;      // + 4 (E + 1); + alignment slack
 };
 
-using ScaledWide = ScaledShape<1, 256, 8, 6, 2, 32>;
-using ScaledNarrow = ScaledShape<0, 64, 4, 8, 8, 16>;
+struct NarrowShape {
+    static constexpr bool PAIR = false;
+    static constexpr int BT = 64;                    // rows of a in a tile, at most
+    static constexpr int WTILE = sg::ROWS;
+    static constexpr int STEP = 16;                  // of an instruction's columns, and rows of a TMA box
+    static constexpr int STAGES = 8, STAGE_BYTES = sg::A_BYTES + BT * sg::BK;
+    static constexpr int TBUF = 8, TCOLS = BT;
+    static constexpr int EPIW = 4, THREADS = 128 + 32 * EPIW;
+    static constexpr int SROW = BT + 8;
+    static constexpr int STG_ROW = 80;               // bytes of a staged row: 32 bf16 and a pad
+    static constexpr int STG = 8 * STG_ROW;          // of an epilogue warp
+    static constexpr int RED = 132;                  // floats of a row of partial sums: 128 and a pad
+    static constexpr int OFF_SCALE = STAGES * STAGE_BYTES;
+    static constexpr int OFF_STG = OFF_SCALE + sg::SCH * sg::SK * SROW * 4;
+    static constexpr int OFF_BAR = OFF_STG + EPIW * STG;
+    static constexpr int OFF_PRE = OFF_BAR + sg::BAR_BYTES;
+    static constexpr int SMEM = OFF_PRE + 1024;
+    static_assert(BT * RED * 4 <= OFF_SCALE, "partial sums fit the ring");
+};
+static_assert(WideShape::SMEM + 4 * (sg::MAX_E + 1) <= 232448 && NarrowShape::SMEM + 4 * (sg::MAX_E + 1) <= 232448, "shared memory");
 
 struct ScaledParams {
     DevStatus *status;
@@ -72,7 +80,8 @@ struct ScaledParams {
     uint64_t timeout_ns;
     int64_t M, a_scale_stride, out_stride;
     int N, E, k_blocks, n_tiles, n_blocks, out_f32;
-    int split;                   // CTAs of a cluster that share K (1: none)
+    int out32;                   // rows of out are 32-byte aligned
+    int split;                   // narrow: CTAs of a cluster that share K (1: none)
     const float *a_scale, *b_scale;
     void *out;
     const int64_t *base;
@@ -86,7 +95,7 @@ struct ScaledSmem {
     uint32_t issued, consumed; // ring fills issued by the loader, consumed by the issuer
     uint32_t scan[16];
 };
-static_assert(sizeof(ScaledSmem) <= 512, "barrier block");
+static_assert(sizeof(ScaledSmem) <= sg::BAR_BYTES, "barrier block");
 
 // e4m3 A and B (K-major), float32 D
 __device__ __forceinline__ constexpr uint32_t idesc_e4m3(int M, int N)
@@ -94,7 +103,7 @@ __device__ __forceinline__ constexpr uint32_t idesc_e4m3(int M, int N)
     return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-template <int PAIR> __device__ __forceinline__ void umma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+template <bool PAIR> __device__ __forceinline__ void umma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
 {
     if (PAIR)
         asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
@@ -117,19 +126,17 @@ __device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)
                  : "r"(taddr));
 }
 
-// the loads before it have arrived; what reads r stays behind it
-__device__ __forceinline__ void tmem_ld_arrived(uint32_t (&r)[16])
-{
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]),
-                   "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
-}
-
+// acc += (lo, hi) * scale.  volatile: it stays behind the wait for its values.
 __device__ __forceinline__ void fma_pair(uint64_t &acc, uint32_t lo, uint32_t hi, uint64_t scale)
 {
-    uint64_t v;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(lo), "r"(hi));
-    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(v), "l"(scale));
+    asm volatile("{\n\t.reg .b64 v;\n\tmov.b64 v, {%1, %2};\n\tfma.rn.f32x2 %0, v, %3, %0;\n\t}" : "+l"(acc) : "r"(lo), "r"(hi), "l"(scale));
+}
+
+__device__ __forceinline__ uint64_t twice(float v)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(v));
+    return r;
 }
 
 __device__ __forceinline__ float2 halves(uint64_t v)
@@ -139,23 +146,51 @@ __device__ __forceinline__ float2 halves(uint64_t v)
     return f;
 }
 
+__device__ __forceinline__ uint32_t narrowed(uint64_t v)
+{
+    const float2 f = halves(v);
+    return pack_bf16x2(f.x, f.y);
+}
+
 __device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
 {
     asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
                  : "memory");
 }
 
+// Arrive on a barrier of the pair's leader.  What it tells is that this warp's
+// loads from TMEM are in registers (tcgen05.wait::ld), so no memory is released:
+// with .release the arrival waits for all of the thread's memory operations
+// (measured: 1300 cycles a block, twice the block's tensor work).
+__device__ __forceinline__ void mbar_arrive_remote_relaxed(uint32_t cluster_addr)
+{
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+// 8 words of one row, 32-byte aligned or in two halves of 16 bytes
+__device__ __forceinline__ void store_words(void *p, const uint32_t (&w)[8], bool aligned32)
+{
+    if (aligned32) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]),
+                     "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4 *>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        reinterpret_cast<uint4 *>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
+
 struct ScaledTile {
-    int e;            // expert
-    int n0;           // first weight row of the cluster's tile
-    int width;        // columns of the instruction
+    int e;             // expert
+    int n0;            // first weight row
+    int width;         // narrow: columns of the instruction
     int64_t tok0, end; // rows of a: [tok0, end)
 };
 
-// The item's tile.  pre: the tiles before each expert.  An expert's rows are
-// divided evenly over as few tiles as hold them; its tiles are visited in
-// groups of NGROUP weight tiles, so that those in flight together share both
-// operands in L2.
+// The item's tile.  pre: the tiles before each expert.  The tiles of an expert
+// are visited in groups of NGROUP weight tiles, so that those in flight
+// together share both operands in L2.  Narrow: an expert's rows are divided
+// evenly over as few tiles as hold them.
 template <class S> __device__ __forceinline__ ScaledTile scaled_tile(const ScaledParams &p, const uint32_t *pre, uint32_t item)
 {
     ScaledTile t;
@@ -169,8 +204,11 @@ template <class S> __device__ __forceinline__ ScaledTile scaled_tile(const Scale
     }
     t.e = lo;
     const int64_t first = p.base ? p.base[lo] : 0, rows = (p.base ? p.base[lo + 1] : p.M) - first;
-    const uint32_t tiles = (uint32_t)((rows + S::BT - 1) / S::BT), width = (uint32_t)((rows + tiles - 1) / tiles);
-    t.width = (int)((width + S::STEP - 1) / S::STEP * S::STEP);
+    const uint32_t tiles = (uint32_t)((rows + S::BT - 1) / S::BT);
+    if constexpr (S::PAIR)
+        t.width = S::BT;
+    else
+        t.width = (int)(((uint32_t)((rows + tiles - 1) / tiles) + S::STEP - 1) / S::STEP * S::STEP);
     const uint32_t local = item - pre[lo], per = sg::NGROUP * tiles, g = local / per, r = local - g * per;
     const uint32_t in_group = min((uint32_t)sg::NGROUP, (uint32_t)p.n_tiles - g * sg::NGROUP);
     const uint32_t row = r / in_group;
@@ -180,24 +218,12 @@ template <class S> __device__ __forceinline__ ScaledTile scaled_tile(const Scale
     return t;
 }
 
-template <class S>
-__global__ void __launch_bounds__(S::THREADS, 1)
-    scaled_gemm_kernel(const __grid_constant__ ScaledParams p, const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a)
+// Barriers and TMEM, then (behind the launch before) the tiles before each
+// expert: a segment of experts a thread, then a scan.  Sums are cut at 2^31 - 1:
+// offsets that are in order never reach that.
+template <class S> __device__ __forceinline__ void scaled_begin(const ScaledParams &p, ScaledSmem *ps, uint32_t *pre, int cl)
 {
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    ScaledSmem *ps = reinterpret_cast<ScaledSmem *>(smem + S::OFF_BAR);
-    uint32_t *pre = reinterpret_cast<uint32_t *>(smem + S::OFF_PRE);
-    float *scales = reinterpret_cast<float *>(smem + S::OFF_SCALE);
-    constexpr bool PAIR = S::PAIR != 0;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int cl = PAIR ? 2 : p.split; // CTAs of the cluster
-    const int crank = cl > 1 ? (int)cluster_ctarank() : 0;
-    const int half = PAIR ? crank : 0;
-    const bool leader = half == 0;
-    const uint32_t unit = blockIdx.x / cl, units = gridDim.x / cl;
-    const uint64_t tmo = p.timeout_ns;
-
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::STAGES; ++i) {
             mbar_init(&ps->full[i], 1);
@@ -205,7 +231,7 @@ __global__ void __launch_bounds__(S::THREADS, 1)
         }
         for (int i = 0; i < S::TBUF; ++i) {
             mbar_init(&ps->tfull[i], 1);
-            mbar_init(&ps->tempty[i], S::EPIW * (PAIR ? 2 : 1));
+            mbar_init(&ps->tempty[i], S::EPIW * (S::PAIR ? 2 : 1));
         }
         for (int i = 0; i < sg::SCH; ++i) {
             mbar_init(&ps->sfull[i], 2);
@@ -216,11 +242,9 @@ __global__ void __launch_bounds__(S::THREADS, 1)
         ps->issued = 0;
         ps->consumed = 0;
         fence_mbar_init();
-        prefetch_tensormap(&map_w);
-        prefetch_tensormap(&map_a);
     }
     if (warp == 1) {
-        if (PAIR) {
+        if (S::PAIR) {
             tmem_alloc_pair(&ps->tmem_base, 512);
             tmem_relinquish_pair();
         } else {
@@ -231,86 +255,154 @@ __global__ void __launch_bounds__(S::THREADS, 1)
     }
     griddep_launch_dependents();
     griddep_wait();
-    // the tiles before each expert: a segment of experts a thread, then a scan
-    {
-        const int per = (p.E + S::THREADS - 1) / S::THREADS;
-        const int lo = min(p.E, (int)threadIdx.x * per), hi = min(p.E, lo + per);
-        const uint64_t most = 0x7fffffffu;
-        auto tiles_of = [&](int e) -> uint64_t {
-            const int64_t b0 = p.base ? p.base[e] : 0, b1 = p.base ? p.base[e + 1] : p.M;
-            if (b0 < 0 || b1 < b0 || b1 > p.M) {
-                if (blockIdx.x == 0)
-                    report_fault(p.status, TDG_ERR_DEVICE, TDG_WHERE_CU, (uint32_t)e, p.epoch);
-                return 0;
-            }
-            return (uint64_t)((b1 - b0 + S::BT - 1) / S::BT) * p.n_tiles;
-        };
-        uint64_t own = 0;
-        for (int e = lo; e < hi; ++e)
-            own = min(most, own + tiles_of(e));
-        uint64_t upto = own; // of the warp's lanes up to this one
+    const int per = (p.E + S::THREADS - 1) / S::THREADS;
+    const int lo = min(p.E, (int)threadIdx.x * per), hi = min(p.E, lo + per);
+    const uint64_t most = 0x7fffffffu;
+    auto tiles_of = [&](int e) -> uint64_t {
+        const int64_t b0 = p.base ? p.base[e] : 0, b1 = p.base ? p.base[e + 1] : p.M;
+        if (b0 < 0 || b1 < b0 || b1 > p.M) {
+            if (blockIdx.x == 0)
+                report_fault(p.status, TDG_ERR_DEVICE, TDG_WHERE_CU, (uint32_t)e, p.epoch);
+            return 0;
+        }
+        return (uint64_t)((b1 - b0 + S::BT - 1) / S::BT) * p.n_tiles;
+    };
+    uint64_t upto = 0; // of the warp's lanes up to this one
+    for (int e = lo; e < hi; ++e)
+        upto = min(most, upto + tiles_of(e));
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const uint64_t v = __shfl_up_sync(0xffffffffu, upto, d);
-            if (lane >= d)
-                upto = min(most, upto + v);
-        }
-        if (lane == 31)
-            ps->scan[warp] = (uint32_t)upto;
-        __syncthreads();
-        uint64_t run = 0;
-        for (int w = 0; w < warp; ++w)
-            run = min(most, run + ps->scan[w]);
-        const uint64_t before = __shfl_up_sync(0xffffffffu, upto, 1);
-        run = lane ? min(most, run + before) : run;
-        for (int e = lo; e < hi; ++e) {
-            pre[e] = (uint32_t)run;
-            run = min(most, run + tiles_of(e));
-            if (e == p.E - 1)
-                pre[p.E] = (uint32_t)run;
-        }
+    for (int d = 1; d < 32; d <<= 1) {
+        const uint64_t v = __shfl_up_sync(0xffffffffu, upto, d);
+        if (lane >= d)
+            upto = min(most, upto + v);
+    }
+    if (lane == 31)
+        ps->scan[warp] = (uint32_t)upto;
+    __syncthreads();
+    uint64_t run = 0;
+    for (int w = 0; w < warp; ++w)
+        run = min(most, run + ps->scan[w]);
+    const uint64_t before = __shfl_up_sync(0xffffffffu, upto, 1);
+    run = lane ? min(most, run + before) : run;
+    for (int e = lo; e < hi; ++e) {
+        pre[e] = (uint32_t)run;
+        run = min(most, run + tiles_of(e));
+        if (e == p.E - 1)
+            pre[p.E] = (uint32_t)run;
     }
     __syncthreads();
     if (cl > 1)
         cluster_sync(); // the peers' barriers are initialised before any remote use
     tc_fence_after();
-    const uint32_t tmem = ps->tmem_base;
-    const uint32_t items = p.split > 1 ? min(pre[p.E], units) : pre[p.E]; // with K cut a cluster has one tile
-    // this CTA's blocks of K
-    const int kb0 = p.split > 1 ? (int)((int64_t)p.k_blocks * crank / p.split) : 0;
-    const int kb1 = p.split > 1 ? (int)((int64_t)p.k_blocks * (crank + 1) / p.split) : p.k_blocks;
-    const uint32_t full0 = PAIR ? mapa_shared(smem_u32(&ps->full[0]), 0) : smem_u32(&ps->full[0]);
-    const uint32_t tempty0 = PAIR ? mapa_shared(smem_u32(&ps->tempty[0]), 0) : smem_u32(&ps->tempty[0]);
+}
+
+// The MMA issuer's loop (one thread of the CTA, or of the pair's leader).
+// columns(tile): those of the instruction.
+template <class S, class F>
+__device__ __forceinline__ void scaled_issue(const ScaledParams &p, ScaledSmem *ps, uint32_t sbase, uint32_t tmem, const uint32_t *pre, uint32_t items,
+                                             uint32_t unit, uint32_t units, int kb0, int kb1, F columns)
+{
+    const uint64_t tmo = p.timeout_ns;
+    int stage = 0, buf = 0;
+    uint32_t phase = 0, bphase = 0, consumed = 0;
+    for (uint32_t it = unit; it < items && !ps->abort; it += units) {
+        const uint32_t idesc = idesc_e4m3(S::PAIR ? 2 * sg::ROWS : sg::ROWS, columns(scaled_tile<S>(p, pre, it)));
+        for (int kb = kb0; kb < kb1; ++kb) {
+            if (!mbar_wait(&ps->tempty[buf], bphase ^ 1u, tmo) || !mbar_wait(&ps->full[stage], phase, tmo)) {
+                report_fault(p.status, TDG_ERR_TIMEOUT, TDG_WHERE_PIPE, 1, p.epoch);
+                ps->abort = 1;
+                break;
+            }
+            tc_fence_after();
+            const uint64_t ad = sdesc_sw128(sbase + stage * S::STAGE_BYTES, 16, 1024);
+            const uint64_t bd = sdesc_sw128(sbase + stage * S::STAGE_BYTES + sg::A_BYTES, 16, 1024);
+            const uint32_t d = tmem + (uint32_t)(buf * S::TCOLS);
+#pragma unroll
+            for (int k = 0; k < sg::BK / 32; ++k)
+                umma_e4m3<S::PAIR>(d, ad + 2 * k, bd + 2 * k, idesc, k ? 1u : 0u);
+            if (S::PAIR) {
+                umma_commit_pair_mask(&ps->empty[stage], 3);
+                umma_commit_pair_mask(&ps->tfull[buf], 3);
+            } else {
+                umma_commit(&ps->empty[stage]);
+                umma_commit(&ps->tfull[buf]);
+            }
+            ++consumed;
+            if (++stage == S::STAGES) {
+                stage = 0;
+                phase ^= 1u;
+            }
+            if (++buf == S::TBUF) {
+                buf = 0;
+                bphase ^= 1u;
+            }
+        }
+    }
+    ps->consumed = consumed;
+    if (ps->abort) { // every MMA issued has finished before TMEM is freed
+        if (S::PAIR)
+            umma_commit_pair_mask(&ps->drain, 3);
+        else
+            umma_commit(&ps->drain);
+        (void)mbar_wait(&ps->drain, 0, tmo);
+    }
+}
+
+// After the roles: where a wait ran out, wait (bounded) until no TMA write of
+// this CTA is still in flight.
+template <class S> __device__ __forceinline__ void scaled_drain(const ScaledParams &p, ScaledSmem *ps, bool leader)
+{
+    __syncthreads();
+    if (ps->abort && threadIdx.x == 0) {
+        if (leader) {
+            for (uint32_t f = ps->consumed; f < ps->issued; ++f)
+                (void)mbar_wait(&ps->full[f % S::STAGES], (f / S::STAGES) & 1u, p.timeout_ns);
+        } else { // a peer's fill is known done once the leader has freed its slot
+            for (uint32_t f = ps->issued > (uint32_t)S::STAGES ? ps->issued - S::STAGES : 0u; f < ps->issued; ++f)
+                (void)mbar_wait(&ps->empty[f % S::STAGES], (f / S::STAGES) & 1u, p.timeout_ns);
+        }
+    }
+    __syncthreads();
+}
+
+__global__ void __launch_bounds__(WideShape::THREADS, 1)
+    scaled_wide_kernel(const __grid_constant__ ScaledParams p, const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a)
+{
+    using S = WideShape;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    ScaledSmem *ps = reinterpret_cast<ScaledSmem *>(smem + S::OFF_BAR);
+    uint32_t *pre = reinterpret_cast<uint32_t *>(smem + S::OFF_PRE);
+    float *scales = reinterpret_cast<float *>(smem + S::OFF_SCALE);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int half = (int)cluster_ctarank();
+    const uint32_t unit = blockIdx.x / 2, units = gridDim.x / 2;
+    const uint64_t tmo = p.timeout_ns;
+    scaled_begin<S>(p, ps, pre, 2);
+    const uint32_t tmem = ps->tmem_base, items = pre[p.E];
+    // an instruction's columns: the weight rows of the tile in steps of 32, each CTA holding half of them
+    auto columns = [&](const ScaledTile &t) { return min(S::WTILE, (p.N - t.n0 + 31) / 32 * 32); };
 
     if (warp == 0) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::REGS_OTHER));
         if (lane == 0) {
+            const uint32_t full0 = mapa_shared(smem_u32(&ps->full[0]), 0);
             int stage = 0;
             uint32_t phase = 0, issued = 0;
             for (uint32_t it = unit; it < items && !ps->abort; it += units) {
                 const ScaledTile t = scaled_tile<S>(p, pre, it);
-                const int rows = PAIR ? t.width / 2 : t.width, boxes = (rows + S::BOX - 1) / S::BOX;
-                const uint32_t bytes = (uint32_t)(sg::W_BYTES + boxes * S::BOX * sg::BK);
-                const uint32_t row = (uint32_t)t.tok0 + half * rows;
-                const int wrow = t.n0 + half * sg::WROWS;
-                for (int kb = kb0; kb < kb1; ++kb) {
-                    if (!mbar_wait(&ps->empty[stage], phase ^ 1u, tmo)) {
+                const int row = (int)((uint32_t)t.tok0 + half * sg::ROWS), wrow = t.n0 + half * (columns(t) / 2);
+                for (int kb = 0; kb < p.k_blocks; ++kb) {
+                    if (!mbar_wait_sleep(&ps->empty[stage], phase ^ 1u, tmo, 64)) {
                         report_fault(p.status, TDG_ERR_TIMEOUT, TDG_WHERE_PIPE, 0, p.epoch);
                         ps->abort = 1;
                         break;
                     }
                     uint8_t *dst = smem + stage * S::STAGE_BYTES;
-                    if (leader) // for both CTAs' bytes
-                        mbar_arrive_expect_tx(&ps->full[stage], PAIR ? 2 * bytes : bytes);
-                    const uint32_t bar = full0 + stage * 8;
-                    if (PAIR) {
-                        tma_load_3d_pair(dst, &map_w, bar, kb * sg::BK, wrow, t.e);
-                        for (int i = 0; i < boxes; ++i)
-                            tma_load_2d_pair(dst + sg::W_BYTES + i * S::BOX * sg::BK, &map_a, bar, kb * sg::BK, (int)(row + i * S::BOX));
-                    } else {
-                        tma_load_3d_addr(dst, &map_w, bar, kb * sg::BK, wrow, t.e);
-                        for (int i = 0; i < boxes; ++i)
-                            tma_load_2d_addr(dst + sg::W_BYTES + i * S::BOX * sg::BK, &map_a, bar, kb * sg::BK, (int)(row + i * S::BOX));
-                    }
+                    if (half == 0) // for both CTAs' bytes
+                        mbar_arrive_expect_tx(&ps->full[stage], 2 * S::STAGE_BYTES);
+                    tma_load_2d_pair(dst, &map_a, full0 + stage * 8, kb * sg::BK, row);
+                    tma_load_3d_pair(dst + sg::A_BYTES, &map_w, full0 + stage * 8, kb * sg::BK, wrow, t.e);
                     ++issued;
                     if (++stage == S::STAGES) {
                         stage = 0;
@@ -322,64 +414,228 @@ __global__ void __launch_bounds__(S::THREADS, 1)
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0 && leader) {
-            int stage = 0, buf = 0;
-            uint32_t phase = 0, bphase = 0, consumed = 0;
-            const uint32_t sbase = smem_u32(smem);
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::REGS_OTHER));
+        if (lane == 0 && half == 0)
+            scaled_issue<S>(p, ps, smem_u32(smem), tmem, pre, items, unit, units, 0, p.k_blocks, columns);
+        __syncwarp();
+    } else if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::REGS_OTHER));
+        // scales: each warp half of the CTA's rows, 8 rows x SK blocks a step, for both column halves
+        const int j = lane % sg::SK, r0 = lane / sg::SK + (warp - 2) * 64;
+        int chunk = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (uint32_t it = unit; it < items && ok; it += units) {
+            const ScaledTile t = scaled_tile<S>(p, pre, it);
+            const float *sw = p.b_scale + ((int64_t)t.e * p.n_blocks + t.n0 / 128) * p.k_blocks;
+            const int64_t next = t.n0 / 128 + 1 < p.n_blocks ? p.k_blocks : 0;
+            const int64_t first = t.tok0 + half * sg::ROWS;
+            const int rows = (int)max((int64_t)0, min((int64_t)sg::ROWS, t.end - first));
+            const float *sa = p.a_scale + first * p.a_scale_stride;
+            for (int kb = 0; kb < p.k_blocks; kb += sg::SK) {
+                const bool in = kb + j < p.k_blocks;
+                const float w0 = in ? sw[kb + j] : 0.f, w1 = in ? sw[next + kb + j] : 0.f;
+                float v[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    v[i] = in && r0 + 8 * i < rows ? sa[(int64_t)(r0 + 8 * i) * p.a_scale_stride + kb + j] : 0.f;
+                ok = mbar_wait_sleep(&ps->sempty[chunk], phase ^ 1u, tmo, 64);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) {
+                    if (lane == 0)
+                        report_fault(p.status, TDG_ERR_TIMEOUT, TDG_WHERE_PIPE, 2, p.epoch);
+                    ps->abort = 1;
+                    break;
+                }
+                float *dst = scales + (chunk * sg::SK + j) * S::SROW + r0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    dst[8 * i] = v[i] * w0;
+                    dst[8 * i + sg::ROWS] = v[i] * w1;
+                }
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&ps->sfull[chunk]);
+                if (++chunk == sg::SCH) {
+                    chunk = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::REGS_EPI));
+        const int q = warp & 3, cg = (warp - 4) >> 2; // lanes of TMEM, half of the columns
+        const uint32_t tempty0 = mapa_shared(smem_u32(&ps->tempty[0]), 0);
+        int buf = 0, chunk = 0;
+        uint32_t bphase = 0, sphase = 0;
+        bool ok = true;
+        for (uint32_t it = unit; it < items && ok; it += units) {
+            const ScaledTile t = scaled_tile<S>(p, pre, it);
+            const int left = p.N - t.n0 - cg * 128; // columns of this warp that exist, if below 128
+            uint64_t acc[4][16];
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    acc[c][i] = 0;
+            for (int kb = 0; kb < p.k_blocks; ++kb) {
+                const int in_chunk = kb % sg::SK;
+                if (in_chunk == 0)
+                    ok = mbar_wait(&ps->sfull[chunk], sphase, tmo);
+                ok = ok && mbar_wait(&ps->tfull[buf], bphase, tmo);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) {
+                    if (lane == 0)
+                        report_fault(p.status, TDG_ERR_TIMEOUT, TDG_WHERE_PIPE, 3, p.epoch);
+                    ps->abort = 1;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t at = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * S::TCOLS + cg * 128);
+                // a chunk of 32 columns is on its way while the one before is added
+                uint32_t r[2][32];
+                tmem_ld_32x32b_x32(at, r[0]);
+                const uint64_t s = twice(scales[(chunk * sg::SK + in_chunk) * S::SROW + cg * sg::ROWS + q * 32 + lane]);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    tmem_ld_wait();
+                    if (c < 3) {
+                        tmem_ld_32x32b_x32(at + 32 * c + 32, r[(c + 1) & 1]);
+                    } else {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive_remote_relaxed(tempty0 + buf * 8);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        fma_pair(acc[c][i], r[c & 1][2 * i], r[c & 1][2 * i + 1], s);
+                }
+                if (++buf == S::TBUF) {
+                    buf = 0;
+                    bphase ^= 1u;
+                }
+                if (in_chunk == sg::SK - 1 || kb == p.k_blocks - 1) {
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&ps->sempty[chunk]);
+                    if (++chunk == sg::SCH) {
+                        chunk = 0;
+                        sphase ^= 1u;
+                    }
+                }
+            }
+            const int64_t row = t.tok0 + half * sg::ROWS + q * 32 + lane;
+            if (!ok || row >= t.end)
+                continue;
+            const int64_t first = row * p.out_stride + t.n0 + cg * 128;
+            if (p.out_f32) {
+                float *out = static_cast<float *>(p.out) + first;
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (c * 32 + i * 8 < left) {
+                            uint32_t w[8];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const float2 f = halves(acc[c][4 * i + k]);
+                                w[2 * k] = __float_as_uint(f.x);
+                                w[2 * k + 1] = __float_as_uint(f.y);
+                            }
+                            store_words(out + c * 32 + i * 8, w, p.out32);
+                        }
+            } else {
+                __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out) + first;
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        uint32_t w[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            w[k] = narrowed(acc[c][8 * i + k]);
+                        if (c * 32 + i * 16 + 16 <= left)
+                            store_words(out + c * 32 + i * 16, w, p.out32);
+                        else if (c * 32 + i * 16 < left)
+                            *reinterpret_cast<uint4 *>(out + c * 32 + i * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+            }
+        }
+    }
+    scaled_drain<S>(p, ps, half == 0);
+    cluster_sync(); // no CTA leaves while the other may still touch it
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, 512);
+    }
+}
+
+// A thread of the epilogue holds, of each 8 x 8 square, two neighbouring rows
+// of a (their scales are a float pair, so the multiply-adds are packed) for one
+// row of the weights; for the store a transposing stmatrix turns the squares.
+__global__ void __launch_bounds__(NarrowShape::THREADS, 1)
+    scaled_narrow_kernel(const __grid_constant__ ScaledParams p, const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a)
+{
+    using S = NarrowShape;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    ScaledSmem *ps = reinterpret_cast<ScaledSmem *>(smem + S::OFF_BAR);
+    uint32_t *pre = reinterpret_cast<uint32_t *>(smem + S::OFF_PRE);
+    float *scales = reinterpret_cast<float *>(smem + S::OFF_SCALE);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int crank = p.split > 1 ? (int)cluster_ctarank() : 0;
+    const uint32_t unit = blockIdx.x / p.split, units = gridDim.x / p.split;
+    const uint64_t tmo = p.timeout_ns;
+    scaled_begin<S>(p, ps, pre, p.split);
+    const uint32_t tmem = ps->tmem_base;
+    const uint32_t items = p.split > 1 ? min(pre[p.E], units) : pre[p.E]; // with K divided a cluster has one tile
+    // this CTA's blocks of K
+    const int kb0 = (int)((int64_t)p.k_blocks * crank / p.split), kb1 = (int)((int64_t)p.k_blocks * (crank + 1) / p.split);
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0, issued = 0;
             for (uint32_t it = unit; it < items && !ps->abort; it += units) {
                 const ScaledTile t = scaled_tile<S>(p, pre, it);
-                const uint32_t idesc = idesc_e4m3(S::WTILE, t.width);
+                const int boxes = t.width / S::STEP;
                 for (int kb = kb0; kb < kb1; ++kb) {
-                    if (!mbar_wait(&ps->tempty[buf], bphase ^ 1u, tmo) || !mbar_wait(&ps->full[stage], phase, tmo)) {
-                        report_fault(p.status, TDG_ERR_TIMEOUT, TDG_WHERE_PIPE, 1, p.epoch);
+                    if (!mbar_wait(&ps->empty[stage], phase ^ 1u, tmo)) {
+                        report_fault(p.status, TDG_ERR_TIMEOUT, TDG_WHERE_PIPE, 0, p.epoch);
                         ps->abort = 1;
                         break;
                     }
-                    tc_fence_after();
-                    const uint64_t wd = sdesc_sw128(sbase + stage * S::STAGE_BYTES, 16, 1024);
-                    const uint64_t ad = sdesc_sw128(sbase + stage * S::STAGE_BYTES + sg::W_BYTES, 16, 1024);
-                    const uint32_t d = tmem + (uint32_t)(buf * S::BT);
-#pragma unroll
-                    for (int k = 0; k < sg::BK / 32; ++k)
-                        umma_e4m3<S::PAIR>(d, wd + 2 * k, ad + 2 * k, idesc, k ? 1u : 0u);
-                    if (PAIR) {
-                        umma_commit_pair_mask(&ps->empty[stage], 3);
-                        umma_commit_pair_mask(&ps->tfull[buf], 3);
-                    } else {
-                        umma_commit(&ps->empty[stage]);
-                        umma_commit(&ps->tfull[buf]);
-                    }
-                    ++consumed;
+                    uint8_t *dst = smem + stage * S::STAGE_BYTES;
+                    mbar_arrive_expect_tx(&ps->full[stage], (uint32_t)(sg::A_BYTES + t.width * sg::BK));
+                    const uint32_t bar = smem_u32(&ps->full[stage]);
+                    tma_load_3d_addr(dst, &map_w, bar, kb * sg::BK, t.n0, t.e);
+                    for (int i = 0; i < boxes; ++i)
+                        tma_load_2d_addr(dst + sg::A_BYTES + i * S::STEP * sg::BK, &map_a, bar, kb * sg::BK,
+                                         (int)((uint32_t)t.tok0 + i * S::STEP));
+                    ++issued;
                     if (++stage == S::STAGES) {
                         stage = 0;
                         phase ^= 1u;
                     }
-                    if (++buf == S::TBUF) {
-                        buf = 0;
-                        bphase ^= 1u;
-                    }
                 }
             }
-            ps->consumed = consumed;
-            if (ps->abort) { // every MMA issued has finished before TMEM is freed
-                if (PAIR)
-                    umma_commit_pair_mask(&ps->drain, 3);
-                else
-                    umma_commit(&ps->drain);
-                (void)mbar_wait(&ps->drain, 0, tmo);
-            }
+            ps->issued = issued;
         }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0)
+            scaled_issue<S>(p, ps, smem_u32(smem), tmem, pre, items, unit, units, kb0, kb1, [](const ScaledTile &t) { return t.width; });
         __syncwarp();
     } else if (warp < 4) {
         // scales: 8 rows of a x SK blocks a step, each warp every other step
+        const int j = lane % sg::SK, r0 = lane / sg::SK + (warp - 2) * 8;
         int chunk = 0;
         uint32_t phase = 0;
         bool ok = true;
-        const int j = lane % sg::SK, r0 = lane / sg::SK + (warp - 2) * 8;
         for (uint32_t it = unit; it < items && ok; it += units) {
             const ScaledTile t = scaled_tile<S>(p, pre, it);
-            const int nb = min((t.n0 + half * sg::WROWS) / sg::WROWS, p.n_blocks - 1);
-            const float *sw = p.b_scale + ((int64_t)t.e * p.n_blocks + nb) * p.k_blocks;
+            const float *sw = p.b_scale + ((int64_t)t.e * p.n_blocks + t.n0 / 128) * p.k_blocks;
             const int rows = (int)(t.end - t.tok0);
             const float *sa = p.a_scale + t.tok0 * p.a_scale_stride;
             for (int kb = kb0; kb < kb1; kb += sg::SK) {
@@ -413,21 +669,20 @@ __global__ void __launch_bounds__(S::THREADS, 1)
             }
         }
     } else {
-        const int q = warp & 3, cg = (warp - 4) >> 2; // lanes of TMEM, group of CW columns
-        uint8_t *stg = smem + S::OFF_STG + (warp - 4) * sg::STG;
-        constexpr int CH = S::CW / 32; // chunks of 32 columns
+        const int q = warp & 3; // lanes of TMEM
+        uint8_t *stg = smem + S::OFF_STG + (warp - 4) * S::STG;
+        constexpr int CH = S::BT / 32; // chunks of 32 columns
         int buf = 0, chunk = 0;
         uint32_t bphase = 0, sphase = 0;
-        for (uint32_t it = unit; it < items; it += units) {
+        bool ok = true;
+        for (uint32_t it = unit; it < items && ok; it += units) {
             const ScaledTile t = scaled_tile<S>(p, pre, it);
-            const int cols = t.width - cg * S::CW; // of this warp, the first CW of them
             uint64_t acc[CH][2][8];
 #pragma unroll
             for (int c = 0; c < CH; ++c)
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     acc[c][0][i] = acc[c][1][i] = 0;
-            bool ok = true;
             for (int kb = kb0; kb < kb1; ++kb) {
                 const int in_chunk = (kb - kb0) % sg::SK;
                 if (in_chunk == 0)
@@ -441,11 +696,11 @@ __global__ void __launch_bounds__(S::THREADS, 1)
                     break;
                 }
                 tc_fence_after();
-                const uint32_t at = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * S::BT + cg * S::CW);
-                const float *sc = scales + (chunk * sg::SK + in_chunk) * S::SROW + cg * S::CW + 2 * (lane & 3);
+                const uint32_t at = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * S::TCOLS);
+                const float *sc = scales + (chunk * sg::SK + in_chunk) * S::SROW + 2 * (lane & 3);
 #pragma unroll
                 for (int c = 0; c < CH; ++c) {
-                    if (c * 32 < cols) {
+                    if (c * 32 < t.width) {
                         uint32_t lo[16], hi[16];
                         tmem_ld_16x256b_x4(at + c * 32, lo);
                         tmem_ld_16x256b_x4(at + (16u << 16) + c * 32, hi);
@@ -453,8 +708,7 @@ __global__ void __launch_bounds__(S::THREADS, 1)
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
                             s[i] = *reinterpret_cast<const uint64_t *>(sc + c * 32 + 8 * i);
-                        tmem_ld_arrived(lo);
-                        tmem_ld_arrived(hi);
+                        tmem_ld_wait();
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             fma_pair(acc[c][0][2 * i], lo[4 * i], lo[4 * i + 1], s[i]);
@@ -466,12 +720,8 @@ __global__ void __launch_bounds__(S::THREADS, 1)
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) {
-                    if (PAIR)
-                        mbar_arrive_remote(tempty0 + buf * 8);
-                    else
-                        mbar_arrive(&ps->tempty[buf]);
-                }
+                if (lane == 0)
+                    mbar_arrive(&ps->tempty[buf]);
                 if (++buf == S::TBUF) {
                     buf = 0;
                     bphase ^= 1u;
@@ -491,20 +741,19 @@ __global__ void __launch_bounds__(S::THREADS, 1)
                 float *red = reinterpret_cast<float *>(smem);
 #pragma unroll
                 for (int c = 0; c < CH; ++c)
-                    if (c * 32 < cols)
+                    if (c * 32 < t.width)
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
 #pragma unroll
                             for (int m = 0; m < 4; ++m) {
                                 const float2 f = halves(acc[c][m >> 1][2 * i + (m & 1)]);
-                                float *d = red + (cg * S::CW + c * 32 + 8 * i + 2 * (lane & 3)) * sg::RED + q * 32 + 8 * m + (lane >> 2);
+                                float *d = red + (c * 32 + 8 * i + 2 * (lane & 3)) * S::RED + q * 32 + 8 * m + (lane >> 2);
                                 d[0] = f.x;
-                                d[sg::RED] = f.y;
+                                d[S::RED] = f.y;
                             }
                 continue;
             }
-            const int n = t.n0 + half * sg::WROWS + q * 32;
-            const int64_t row0 = t.tok0 + cg * S::CW;
+            const int n = t.n0 + q * 32;
             if (p.out_f32) {
                 float *out = static_cast<float *>(p.out);
 #pragma unroll
@@ -514,7 +763,7 @@ __global__ void __launch_bounds__(S::THREADS, 1)
 #pragma unroll
                         for (int m = 0; m < 4; ++m) {
                             const float2 f = halves(acc[c][m >> 1][2 * i + (m & 1)]);
-                            const int64_t row = row0 + c * 32 + 8 * i + 2 * (lane & 3);
+                            const int64_t row = t.tok0 + c * 32 + 8 * i + 2 * (lane & 3);
                             const int col = n + 8 * m + (lane >> 2);
                             if (col < p.N && row < t.end)
                                 out[row * p.out_stride + col] = f.x;
@@ -522,46 +771,29 @@ __global__ void __launch_bounds__(S::THREADS, 1)
                                 out[(row + 1) * p.out_stride + col] = f.y;
                         }
             } else {
-                const uint32_t put = smem_u32(stg) + (lane & 7) * sg::STG_ROW + (lane >> 3) * 16;
-                const uint8_t *get = stg + (lane >> 2) * sg::STG_ROW + (lane & 3) * 16;
+                const uint32_t put = smem_u32(stg) + (lane & 7) * S::STG_ROW + (lane >> 3) * 16;
+                const uint8_t *get = stg + (lane >> 2) * S::STG_ROW + (lane & 3) * 16;
                 const int col = n + (lane & 3) * 8;
 #pragma unroll
                 for (int c = 0; c < CH; ++c)
-                    if (c * 32 < cols)
+                    if (c * 32 < t.width)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            uint32_t w[4];
-#pragma unroll
-                            for (int m = 0; m < 4; ++m) {
-                                const float2 f = halves(acc[c][m >> 1][2 * i + (m & 1)]);
-                                w[m] = pack_bf16x2(f.x, f.y);
-                            }
                             __syncwarp();
-                            stmatrix_x4_trans(put, w[0], w[1], w[2], w[3]);
+                            stmatrix_x4_trans(put, narrowed(acc[c][0][2 * i]), narrowed(acc[c][0][2 * i + 1]), narrowed(acc[c][1][2 * i]),
+                                              narrowed(acc[c][1][2 * i + 1]));
                             __syncwarp();
                             const uint4 v = *reinterpret_cast<const uint4 *>(get);
-                            const int64_t row = row0 + c * 32 + 8 * i + (lane >> 2);
+                            const int64_t row = t.tok0 + c * 32 + 8 * i + (lane >> 2);
                             if (col < p.N && row < t.end)
                                 *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + row * p.out_stride + col) = v;
                         }
             }
         }
     }
-    __syncthreads();
-    if (ps->abort && threadIdx.x == 0) {
-        // wait (bounded) until no TMA write of this CTA is still in flight
-        if (!PAIR || leader) {
-            for (uint32_t f = ps->consumed; f < ps->issued; ++f)
-                (void)mbar_wait(&ps->full[f % S::STAGES], (f / S::STAGES) & 1u, tmo);
-        } else { // a peer's fill is known done once the leader has freed its slot
-            for (uint32_t f = ps->issued > (uint32_t)S::STAGES ? ps->issued - S::STAGES : 0u; f < ps->issued; ++f)
-                (void)mbar_wait(&ps->empty[f % S::STAGES], (f / S::STAGES) & 1u, tmo);
-        }
-    }
-    __syncthreads();
-    if (cl > 1)
-        cluster_sync(); // the partial sums are there; no CTA leaves while another may still touch it
-    if (!PAIR && p.split > 1) {
+    scaled_drain<S>(p, ps, true);
+    if (p.split > 1) {
+        cluster_sync(); // the partial sums are there
         if (unit < items && !ps->abort) {
             // this CTA's share of the rows, summed over the cluster in rank order
             const ScaledTile t = scaled_tile<S>(p, pre, unit);
@@ -573,7 +805,7 @@ __global__ void __launch_bounds__(S::THREADS, 1)
                     continue;
                 float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
                 for (int k = 0; k < p.split; ++k) {
-                    const float4 v = ld_cluster_f4(mapa_shared(red + (uint32_t)(r * sg::RED + c) * 4, (uint32_t)k));
+                    const float4 v = ld_cluster_f4(mapa_shared(red + (uint32_t)(r * S::RED + c) * 4, (uint32_t)k));
                     sum.x += v.x;
                     sum.y += v.y;
                     sum.z += v.z;
@@ -587,14 +819,11 @@ __global__ void __launch_bounds__(S::THREADS, 1)
                         make_uint2(pack_bf16x2(sum.x, sum.y), pack_bf16x2(sum.z, sum.w));
             }
         }
-        cluster_sync();
+        cluster_sync(); // no CTA leaves while another may still read its sums
     }
     if (warp == 1) {
         tc_fence_after();
-        if (PAIR)
-            tmem_dealloc_pair(tmem, 512);
-        else
-            tmem_dealloc(tmem, 512);
+        tmem_dealloc(tmem, 512);
     }
 }
 
@@ -616,9 +845,10 @@ bool map_codes(CUtensorMap *m, const void *base, int64_t inner, int64_t rows, in
 template <class S> int run(tdg_symm *h, const tdg_scaled_gemm_args *a, ScaledParams &p, int split, int64_t units, cudaStream_t s)
 {
     CUtensorMap map_w, map_a;
-    if (!map_codes(&map_w, a->b, a->K, a->N, a->K, a->E, sg::WROWS, false) || !map_codes(&map_a, a->a, a->K, a->M, a->a_stride, 1, S::BOX, true))
+    const int box = S::PAIR ? sg::ROWS : NarrowShape::STEP;
+    if (!map_codes(&map_w, a->b, a->K, a->N, a->K, a->E, sg::ROWS, false) || !map_codes(&map_a, a->a, a->K, a->M, a->a_stride, 1, box, true))
         return TDG_ERR_CUDA;
-    const void *fn = reinterpret_cast<const void *>(&scaled_gemm_kernel<S>);
+    const void *fn = S::PAIR ? reinterpret_cast<const void *>(&scaled_wide_kernel) : reinterpret_cast<const void *>(&scaled_narrow_kernel);
     const int smem = S::SMEM + 4 * (sg::MAX_E + 1);
     cudaError_t e = set_smem(fn, smem);
     if (e != cudaSuccess)
@@ -657,8 +887,8 @@ extern "C" int tdg_scaled_gemm(tdg_symm *h, const tdg_scaled_gemm_args *a, void 
         return TDG_ERR_INVALID;
     // the tiles, at most, of each kernel's shape: one more for every expert than its rows fill
     const int64_t used = a->E < a->M ? a->E : a->M;
-    const int64_t wide = (used + a->M / ScaledWide::BT) * ((a->N + ScaledWide::WTILE - 1) / ScaledWide::WTILE);
-    const int64_t narrow = (used + a->M / ScaledNarrow::BT) * ((a->N + ScaledNarrow::WTILE - 1) / ScaledNarrow::WTILE);
+    const int64_t wide = (used + a->M / WideShape::BT) * ((a->N + WideShape::WTILE - 1) / WideShape::WTILE);
+    const int64_t narrow = (used + a->M / NarrowShape::BT) * ((a->N + NarrowShape::WTILE - 1) / NarrowShape::WTILE);
     if (narrow > INT32_MAX)
         return TDG_ERR_INVALID;
     ScaledParams p;
@@ -674,6 +904,7 @@ extern "C" int tdg_scaled_gemm(tdg_symm *h, const tdg_scaled_gemm_args *a, void 
     p.k_blocks = (int)kb;
     p.n_blocks = (int)nb;
     p.out_f32 = a->out_f32;
+    p.out32 = reinterpret_cast<uintptr_t>(a->out) % 32 == 0 && a->out_stride * esz % 32 == 0;
     p.a_scale = a->a_scale;
     p.b_scale = a->b_scale;
     p.out = a->out;
@@ -681,12 +912,12 @@ extern "C" int tdg_scaled_gemm(tdg_symm *h, const tdg_scaled_gemm_args *a, void 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (a->M / a->E > 64) {
         const int64_t pairs = h->sm_count / 2;
-        return run<ScaledWide>(h, a, p, 1, wide < pairs ? wide : pairs, s);
+        return run<WideShape>(h, a, p, 1, wide < pairs ? wide : pairs, s);
     }
     // few tiles: K cut over the CTAs of a cluster, two blocks of it each at least
     int split = 1;
     while (split < 8 && narrow * split * 2 <= h->sm_count && kb >= 4 * split)
         split *= 2;
     const int64_t units = h->sm_count / split;
-    return run<ScaledNarrow>(h, a, p, split, narrow < units ? narrow : units, s);
+    return run<NarrowShape>(h, a, p, split, narrow < units ? narrow : units, s);
 }
