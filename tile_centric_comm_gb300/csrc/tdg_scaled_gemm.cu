@@ -20,7 +20,7 @@
 // Warps of a CTA (either kernel):
 //   warp 0      TMA loader: the codes of a block into a ring of shared memory
 //   warp 1      MMA issuer: four tcgen05.mma.kind::f8f6f4 (K = 32) a block
-//   warps 2, 3  scales: sa * sw of the tile's rows, four blocks at a time
+//   warps 2, 3  scales: sa * sw of the tile's rows, some blocks at a time
 //   warps 4..   epilogue
 #include "tdg_scaled.cuh"
 
@@ -30,8 +30,6 @@ namespace sg {
 constexpr int BK = 128;                 // codes of a block: one scale, one swizzled row
 constexpr int ROWS = 128;               // lanes of TMEM: rows of a CTA's first operand
 constexpr int A_BYTES = ROWS * BK;
-constexpr int SK = 4;                   // blocks whose scales are loaded together
-constexpr int SCH = 3;                  // such chunks in the ring
 constexpr int NGROUP = 8;               // weight tiles that are visited together
 constexpr int MAX_E = 4096;
 constexpr int BAR_BYTES = 512;
@@ -46,9 +44,10 @@ struct WideShape {
     static constexpr int EPIW = 8, THREADS = 128 + 32 * EPIW;
     static constexpr int REGS_OTHER = 72, REGS_EPI = 216; // registers of a thread
     static_assert(128 * REGS_OTHER + 32 * EPIW * REGS_EPI <= THREADS * (65536 / THREADS / 8 * 8), "registers of the launch");
+    static constexpr int SK = 4, SCH = 3;            // blocks whose scales are loaded together, such chunks in the ring
     static constexpr int SROW = 2 * sg::ROWS + 8;    // floats of a block's scales: for each half of the columns, and a pad
     static constexpr int OFF_SCALE = STAGES * STAGE_BYTES;
-    static constexpr int OFF_BAR = OFF_SCALE + sg::SCH * sg::SK * SROW * 4;
+    static constexpr int OFF_BAR = OFF_SCALE + SCH * SK * SROW * 4;
     static constexpr int OFF_PRE = OFF_BAR + sg::BAR_BYTES; // tiles before each expert
     static constexpr int SMEM = OFF_PRE + 1024;      // + 4 (E + 1); + alignment slack
 };
@@ -61,12 +60,13 @@ struct NarrowShape {
     static constexpr int STAGES = 8, STAGE_BYTES = sg::A_BYTES + BT * sg::BK;
     static constexpr int TBUF = 8, TCOLS = BT;
     static constexpr int EPIW = 4, THREADS = 128 + 32 * EPIW;
+    static constexpr int SK = 4, SCH = 3;
     static constexpr int SROW = BT + 8;
     static constexpr int STG_ROW = 80;               // bytes of a staged row: 32 bf16 and a pad
     static constexpr int STG = 8 * STG_ROW;          // of an epilogue warp
     static constexpr int RED = 132;                  // floats of a row of partial sums: 128 and a pad
     static constexpr int OFF_SCALE = STAGES * STAGE_BYTES;
-    static constexpr int OFF_STG = OFF_SCALE + sg::SCH * sg::SK * SROW * 4;
+    static constexpr int OFF_STG = OFF_SCALE + SCH * SK * SROW * 4;
     static constexpr int OFF_BAR = OFF_STG + EPIW * STG;
     static constexpr int OFF_PRE = OFF_BAR + sg::BAR_BYTES;
     static constexpr int SMEM = OFF_PRE + 1024;
@@ -89,7 +89,7 @@ struct ScaledParams {
 
 struct ScaledSmem {
     uint64_t full[8], empty[8], tfull[8], tempty[8];
-    uint64_t sfull[sg::SCH], sempty[sg::SCH], drain;
+    uint64_t sfull[4], sempty[4], drain;
     uint32_t tmem_base;
     volatile int abort;
     uint32_t issued, consumed; // ring fills issued by the loader, consumed by the issuer
@@ -126,17 +126,27 @@ __device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)
                  : "r"(taddr));
 }
 
+// 32 lanes x 16 columns: thread i has lane i's
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+                   "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(taddr));
+}
+
 // acc += (lo, hi) * scale.  volatile: it stays behind the wait for its values.
 __device__ __forceinline__ void fma_pair(uint64_t &acc, uint32_t lo, uint32_t hi, uint64_t scale)
 {
     asm volatile("{\n\t.reg .b64 v;\n\tmov.b64 v, {%1, %2};\n\tfma.rn.f32x2 %0, v, %3, %0;\n\t}" : "+l"(acc) : "r"(lo), "r"(hi), "l"(scale));
 }
 
-__device__ __forceinline__ uint64_t twice(float v)
+// acc += v * scale, one at a time: a packed multiply-add takes two cycles for two,
+// and to have its pairs in place the compiler moved three registers for each
+__device__ __forceinline__ void fma_one(float &acc, uint32_t v, float scale)
 {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(v));
-    return r;
+    asm volatile("fma.rn.f32 %0, %1, %2, %0;" : "+f"(acc) : "f"(__uint_as_float(v)), "f"(scale));
 }
 
 __device__ __forceinline__ float2 halves(uint64_t v)
@@ -158,13 +168,54 @@ __device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uin
                  : "memory");
 }
 
-// Arrive on a barrier of the pair's leader.  What it tells is that this warp's
-// loads from TMEM are in registers (tcgen05.wait::ld), so no memory is released:
-// with .release the arrival waits for all of the thread's memory operations
-// (measured: 1300 cycles a block, twice the block's tensor work).
-__device__ __forceinline__ void mbar_arrive_remote_relaxed(uint32_t cluster_addr)
+// A wait whose thread is suspended until the phase completes, for up to 10 us at
+// a time: 12 warps that poll without a time hint take issue slots and barrier
+// accesses from the ones at work (481 us instead of 437 at 8192 x 7168 x 8192).
+// One piece of PTX, since the epilogue waits once a block and a phase that is
+// complete must cost it one instruction and one branch.  Sets `failed` when the
+// time is up (the clock is read only between the suspensions).
+__device__ __forceinline__ void mbar_wait_suspended(uint32_t bar, uint32_t parity, uint64_t timeout_ns, uint32_t &failed)
 {
-    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .u64 t, end;\n\t"
+                 "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %4;\n\t"
+                 "@p bra DONE_%=;\n\t"
+                 "mov.u64 end, %%globaltimer;\n\t"
+                 "add.u64 end, end, %3;\n\t"
+                 "AGAIN_%=:\n\t"
+                 "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %4;\n\t"
+                 "@p bra DONE_%=;\n\t"
+                 "mov.u64 t, %%globaltimer;\n\t"
+                 "setp.lt.u64 p, t, end;\n\t"
+                 "@p bra AGAIN_%=;\n\t"
+                 "mov.u32 %0, 1;\n\t"
+                 "DONE_%=:\n\t}"
+                 : "+r"(failed)
+                 : "r"(bar), "r"(parity), "l"(timeout_ns), "r"(10000u)
+                 : "memory");
+}
+__device__ __forceinline__ bool mbar_wait_suspended(uint64_t *bar, uint32_t parity, uint64_t timeout_ns)
+{
+    uint32_t failed = 0;
+    mbar_wait_suspended(smem_u32(bar), parity, timeout_ns, failed);
+    return !failed;
+}
+
+// Arrivals that tell of loads which are in registers (tcgen05.wait::ld, or
+// values already used), so that no memory is released: with .release an arrival
+// waits for all of the thread's memory operations (1300 cycles a block on the
+// pair leader's barrier, twice the block's tensor work; 350 on an own one that
+// follows an arrival there).  By the lanes with `by`, without a branch.
+__device__ __forceinline__ void mbar_arrive_remote_relaxed(uint32_t cluster_addr, bool by)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+                 "@p mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n\t}" ::"r"(cluster_addr), "r"(by ? 1u : 0u)
+                 : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_relaxed(uint64_t *bar, bool by)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+                 "@p mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];\n\t}" ::"r"(smem_u32(bar)), "r"(by ? 1u : 0u)
+                 : "memory");
 }
 
 // 8 words of one row, 32-byte aligned or in two halves of 16 bytes
@@ -233,7 +284,7 @@ template <class S> __device__ __forceinline__ void scaled_begin(const ScaledPara
             mbar_init(&ps->tfull[i], 1);
             mbar_init(&ps->tempty[i], S::EPIW * (S::PAIR ? 2 : 1));
         }
-        for (int i = 0; i < sg::SCH; ++i) {
+        for (int i = 0; i < S::SCH; ++i) {
             mbar_init(&ps->sfull[i], 2);
             mbar_init(&ps->sempty[i], S::EPIW);
         }
@@ -296,37 +347,54 @@ template <class S> __device__ __forceinline__ void scaled_begin(const ScaledPara
     tc_fence_after();
 }
 
-// The MMA issuer's loop (one thread of the CTA, or of the pair's leader).
+// one lane of a converged warp
+__device__ __forceinline__ bool elected()
+{
+    uint32_t is;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(is));
+    return is != 0;
+}
+
+// The MMA issuer's loop, of one warp (of the pair's leader).  The whole warp
+// walks it and one elected lane issues: what the loop computes is then the same
+// in all lanes and stays in uniform registers, where the instruction takes its
+// operands from (issued by a loop of one lane, four MMAs and two commits took
+// 440 cycles of the 512 that the tensor cores need for them).
 // columns(tile): those of the instruction.
 template <class S, class F>
 __device__ __forceinline__ void scaled_issue(const ScaledParams &p, ScaledSmem *ps, uint32_t sbase, uint32_t tmem, const uint32_t *pre, uint32_t items,
                                              uint32_t unit, uint32_t units, int kb0, int kb1, F columns)
 {
     const uint64_t tmo = p.timeout_ns;
+    // a ring slot's offset never carries out of the descriptor's address field
+    const uint64_t ad0 = sdesc_sw128(sbase, 16, 1024);
     int stage = 0, buf = 0;
     uint32_t phase = 0, bphase = 0, consumed = 0;
-    for (uint32_t it = unit; it < items && !ps->abort; it += units) {
+    bool ok = true;
+    for (uint32_t it = unit; it < items && ok; it += units) {
         const uint32_t idesc = idesc_e4m3(S::PAIR ? 2 * sg::ROWS : sg::ROWS, columns(scaled_tile<S>(p, pre, it)));
         for (int kb = kb0; kb < kb1; ++kb) {
-            if (!mbar_wait(&ps->tempty[buf], bphase ^ 1u, tmo) || !mbar_wait(&ps->full[stage], phase, tmo)) {
-                report_fault(p.status, TDG_ERR_TIMEOUT, TDG_WHERE_PIPE, 1, p.epoch);
-                ps->abort = 1;
-                break;
-            }
-            tc_fence_after();
-            const uint64_t ad = sdesc_sw128(sbase + stage * S::STAGE_BYTES, 16, 1024);
-            const uint64_t bd = sdesc_sw128(sbase + stage * S::STAGE_BYTES + sg::A_BYTES, 16, 1024);
+            const uint64_t ad = ad0 + (uint64_t)(stage * (S::STAGE_BYTES >> 4)), bd = ad + (sg::A_BYTES >> 4);
             const uint32_t d = tmem + (uint32_t)(buf * S::TCOLS);
+            // the accumulator last: it is what is waited for
+            ok = mbar_wait_suspended(&ps->full[stage], phase, tmo) && mbar_wait_suspended(&ps->tempty[buf], bphase ^ 1u, tmo);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok)
+                break;
+            tc_fence_after();
+            if (elected()) {
 #pragma unroll
-            for (int k = 0; k < sg::BK / 32; ++k)
-                umma_e4m3<S::PAIR>(d, ad + 2 * k, bd + 2 * k, idesc, k ? 1u : 0u);
-            if (S::PAIR) {
-                umma_commit_pair_mask(&ps->empty[stage], 3);
-                umma_commit_pair_mask(&ps->tfull[buf], 3);
-            } else {
-                umma_commit(&ps->empty[stage]);
-                umma_commit(&ps->tfull[buf]);
+                for (int k = 0; k < sg::BK / 32; ++k)
+                    umma_e4m3<S::PAIR>(d, ad + 2 * k, bd + 2 * k, idesc, k ? 1u : 0u);
+                if (S::PAIR) {
+                    umma_commit_pair_mask(&ps->tfull[buf], 3);
+                    umma_commit_pair_mask(&ps->empty[stage], 3);
+                } else {
+                    umma_commit(&ps->tfull[buf]);
+                    umma_commit(&ps->empty[stage]);
+                }
             }
+            __syncwarp();
             ++consumed;
             if (++stage == S::STAGES) {
                 stage = 0;
@@ -338,14 +406,21 @@ __device__ __forceinline__ void scaled_issue(const ScaledParams &p, ScaledSmem *
             }
         }
     }
-    ps->consumed = consumed;
-    if (ps->abort) { // every MMA issued has finished before TMEM is freed
-        if (S::PAIR)
-            umma_commit_pair_mask(&ps->drain, 3);
-        else
-            umma_commit(&ps->drain);
-        (void)mbar_wait(&ps->drain, 0, tmo);
+    if (elected()) {
+        ps->consumed = consumed;
+        if (!ok) {
+            report_fault(p.status, TDG_ERR_TIMEOUT, TDG_WHERE_PIPE, 1, p.epoch);
+            ps->abort = 1;
+            // every MMA issued has finished before TMEM is freed (commits tell of
+            // the executing thread's own: the lane elected here is the one above)
+            if (S::PAIR)
+                umma_commit_pair_mask(&ps->drain, 3);
+            else
+                umma_commit(&ps->drain);
+            (void)mbar_wait(&ps->drain, 0, tmo);
+        }
     }
+    __syncwarp();
 }
 
 // After the roles: where a wait ran out, wait (bounded) until no TMA write of
@@ -393,7 +468,7 @@ __global__ void __launch_bounds__(WideShape::THREADS, 1)
                 const ScaledTile t = scaled_tile<S>(p, pre, it);
                 const int row = (int)((uint32_t)t.tok0 + half * sg::ROWS), wrow = t.n0 + half * (columns(t) / 2);
                 for (int kb = 0; kb < p.k_blocks; ++kb) {
-                    if (!mbar_wait_sleep(&ps->empty[stage], phase ^ 1u, tmo, 64)) {
+                    if (!mbar_wait_suspended(&ps->empty[stage], phase ^ 1u, tmo)) {
                         report_fault(p.status, TDG_ERR_TIMEOUT, TDG_WHERE_PIPE, 0, p.epoch);
                         ps->abort = 1;
                         break;
@@ -415,13 +490,13 @@ __global__ void __launch_bounds__(WideShape::THREADS, 1)
         __syncwarp();
     } else if (warp == 1) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::REGS_OTHER));
-        if (lane == 0 && half == 0)
+        if (half == 0)
             scaled_issue<S>(p, ps, smem_u32(smem), tmem, pre, items, unit, units, 0, p.k_blocks, columns);
-        __syncwarp();
     } else if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::REGS_OTHER));
-        // scales: each warp half of the CTA's rows, 8 rows x SK blocks a step, for both column halves
-        const int j = lane % sg::SK, r0 = lane / sg::SK + (warp - 2) * 64;
+        // scales: each warp half of the CTA's rows, 32 / SK rows x SK blocks a step, for both column halves
+        constexpr int RS = 32 / S::SK;
+        const int j = lane % S::SK, r0 = lane / S::SK + (warp - 2) * 64;
         int chunk = 0;
         uint32_t phase = 0;
         bool ok = true;
@@ -432,14 +507,14 @@ __global__ void __launch_bounds__(WideShape::THREADS, 1)
             const int64_t first = t.tok0 + half * sg::ROWS;
             const int rows = (int)max((int64_t)0, min((int64_t)sg::ROWS, t.end - first));
             const float *sa = p.a_scale + first * p.a_scale_stride;
-            for (int kb = 0; kb < p.k_blocks; kb += sg::SK) {
+            for (int kb = 0; kb < p.k_blocks; kb += S::SK) {
                 const bool in = kb + j < p.k_blocks;
                 const float w0 = in ? sw[kb + j] : 0.f, w1 = in ? sw[next + kb + j] : 0.f;
-                float v[8];
+                float v[64 / RS];
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    v[i] = in && r0 + 8 * i < rows ? sa[(int64_t)(r0 + 8 * i) * p.a_scale_stride + kb + j] : 0.f;
-                ok = mbar_wait_sleep(&ps->sempty[chunk], phase ^ 1u, tmo, 64);
+                for (int i = 0; i < 64 / RS; ++i)
+                    v[i] = in && r0 + RS * i < rows ? sa[(int64_t)(r0 + RS * i) * p.a_scale_stride + kb + j] : 0.f;
+                ok = mbar_wait_suspended(&ps->sempty[chunk], phase ^ 1u, tmo);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) {
                     if (lane == 0)
@@ -447,16 +522,16 @@ __global__ void __launch_bounds__(WideShape::THREADS, 1)
                     ps->abort = 1;
                     break;
                 }
-                float *dst = scales + (chunk * sg::SK + j) * S::SROW + r0;
+                float *dst = scales + (chunk * S::SK + j) * S::SROW + r0;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    dst[8 * i] = v[i] * w0;
-                    dst[8 * i + sg::ROWS] = v[i] * w1;
+                for (int i = 0; i < 64 / RS; ++i) {
+                    dst[RS * i] = v[i] * w0;
+                    dst[RS * i + sg::ROWS] = v[i] * w1;
                 }
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(&ps->sfull[chunk]);
-                if (++chunk == sg::SCH) {
+                if (++chunk == S::SCH) {
                     chunk = 0;
                     phase ^= 1u;
                 }
@@ -466,100 +541,103 @@ __global__ void __launch_bounds__(WideShape::THREADS, 1)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::REGS_EPI));
         const int q = warp & 3, cg = (warp - 4) >> 2; // lanes of TMEM, half of the columns
         const uint32_t tempty0 = mapa_shared(smem_u32(&ps->tempty[0]), 0);
-        int buf = 0, chunk = 0;
-        uint32_t bphase = 0, sphase = 0;
+        const uint32_t at = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(cg * 128);
+        const uint32_t tfull0 = smem_u32(&ps->tfull[0]), sfull0 = smem_u32(&ps->sfull[0]);
+        const float *scale_at = scales + cg * sg::ROWS + q * 32 + lane;
+        int chunk = 0;
+        uint32_t buf = 0, bphase = 0, sphase = 0, failed = 0;
         bool ok = true;
         for (uint32_t it = unit; it < items && ok; it += units) {
             const ScaledTile t = scaled_tile<S>(p, pre, it);
-            const int left = p.N - t.n0 - cg * 128; // columns of this warp that exist, if below 128
-            uint64_t acc[4][16];
+            float acc[8][16];
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
+            for (int c = 0; c < 8; ++c)
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
-                    acc[c][i] = 0;
-            for (int kb = 0; kb < p.k_blocks; ++kb) {
-                const int in_chunk = kb % sg::SK;
-                if (in_chunk == 0)
-                    ok = mbar_wait(&ps->sfull[chunk], sphase, tmo);
-                ok = ok && mbar_wait(&ps->tfull[buf], bphase, tmo);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) {
-                    if (lane == 0)
-                        report_fault(p.status, TDG_ERR_TIMEOUT, TDG_WHERE_PIPE, 3, p.epoch);
-                    ps->abort = 1;
-                    break;
-                }
-                tc_fence_after();
-                const uint32_t at = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * S::TCOLS + cg * 128);
-                // a chunk of 32 columns is on its way while the one before is added
-                uint32_t r[2][32];
-                tmem_ld_32x32b_x32(at, r[0]);
-                const uint64_t s = twice(scales[(chunk * sg::SK + in_chunk) * S::SROW + cg * sg::ROWS + q * 32 + lane]);
+                    acc[c][i] = 0.f;
+            // a chunk of 16 columns is on its way while the one before is added,
+            // from one block to the next too (chunks of 32 do not fit the registers)
+            uint32_t r[2][16];
+            mbar_wait_suspended(tfull0 + buf * 8, bphase, tmo, failed);
+            mbar_wait_suspended(sfull0 + chunk * 8, sphase, tmo, failed);
+            tc_fence_after();
+            tmem_ld_32x32b_x16(at + buf * S::TCOLS, r[0]);
+            float s = scale_at[chunk * S::SK * S::SROW];
+            for (int kb = 0, in_chunk = 0; kb < p.k_blocks && !failed; ++kb) {
+                const bool more = kb + 1 < p.k_blocks;
+                float next = 0.f;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
+                for (int c = 0; c < 8; ++c) {
                     tmem_ld_wait();
-                    if (c < 3) {
-                        tmem_ld_32x32b_x32(at + 32 * c + 32, r[(c + 1) & 1]);
-                    } else {
+                    if (c < 7) {
+                        tmem_ld_32x32b_x16(at + buf * S::TCOLS + 16 * c + 16, r[(c + 1) & 1]);
+                    } else { // the accumulator is read: the tensor cores may write it again
                         tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0)
-                            mbar_arrive_remote_relaxed(tempty0 + buf * 8);
+                        mbar_arrive_remote_relaxed(tempty0 + buf * 8, lane == 0);
+                        buf ^= 1;
+                        bphase ^= buf ^ 1;
+                        if (more) {
+                            mbar_wait_suspended(tfull0 + buf * 8, bphase, tmo, failed);
+                            tc_fence_after();
+                            tmem_ld_32x32b_x16(at + buf * S::TCOLS, r[0]);
+                        }
+                    }
+                    if (c == 1) { // the next block's scale
+                        if (++in_chunk == S::SK || !more) {
+                            in_chunk = 0;
+                            __syncwarp();
+                            mbar_arrive_relaxed(&ps->sempty[chunk], lane == 0);
+                            if (++chunk == S::SCH) {
+                                chunk = 0;
+                                sphase ^= 1u;
+                            }
+                            if (more)
+                                mbar_wait_suspended(sfull0 + chunk * 8, sphase, tmo, failed);
+                        }
+                        if (more)
+                            next = scale_at[(chunk * S::SK + in_chunk) * S::SROW];
                     }
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
-                        fma_pair(acc[c][i], r[c & 1][2 * i], r[c & 1][2 * i + 1], s);
+                        fma_one(acc[c][i], r[c & 1][i], s);
                 }
-                if (++buf == S::TBUF) {
-                    buf = 0;
-                    bphase ^= 1u;
-                }
-                if (in_chunk == sg::SK - 1 || kb == p.k_blocks - 1) {
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(&ps->sempty[chunk]);
-                    if (++chunk == sg::SCH) {
-                        chunk = 0;
-                        sphase ^= 1u;
-                    }
-                }
+                s = next;
+            }
+            tmem_ld_wait();
+            ok = __all_sync(0xffffffffu, !failed);
+            if (!ok) {
+                if (lane == 0)
+                    report_fault(p.status, TDG_ERR_TIMEOUT, TDG_WHERE_PIPE, 3, p.epoch);
+                ps->abort = 1;
+                break;
             }
             const int64_t row = t.tok0 + half * sg::ROWS + q * 32 + lane;
-            if (!ok || row >= t.end)
+            if (row >= t.end)
                 continue;
-            const int64_t first = row * p.out_stride + t.n0 + cg * 128;
-            if (p.out_f32) {
-                float *out = static_cast<float *>(p.out) + first;
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
+            for (int c = 0; c < 8; ++c) {
+                const int n = t.n0 + cg * 128 + c * 16, left = p.N - n;
+                uint32_t w[8];
+                if (p.out_f32) {
+                    float *out = static_cast<float *>(p.out) + row * p.out_stride + n;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (c * 32 + i * 8 < left) {
-                            uint32_t w[8];
+                    for (int i = 0; i < 2; ++i)
+                        if (i * 8 < left) {
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const float2 f = halves(acc[c][4 * i + k]);
-                                w[2 * k] = __float_as_uint(f.x);
-                                w[2 * k + 1] = __float_as_uint(f.y);
-                            }
-                            store_words(out + c * 32 + i * 8, w, p.out32);
+                            for (int k = 0; k < 8; ++k)
+                                w[k] = __float_as_uint(acc[c][8 * i + k]);
+                            store_words(out + i * 8, w, p.out32);
                         }
-            } else {
-                __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out) + first;
+                } else {
+                    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out) + row * p.out_stride + n;
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        uint32_t w[8];
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            w[k] = narrowed(acc[c][8 * i + k]);
-                        if (c * 32 + i * 16 + 16 <= left)
-                            store_words(out + c * 32 + i * 16, w, p.out32);
-                        else if (c * 32 + i * 16 < left)
-                            *reinterpret_cast<uint4 *>(out + c * 32 + i * 16) = make_uint4(w[0], w[1], w[2], w[3]);
-                    }
+                    for (int k = 0; k < 8; ++k)
+                        w[k] = pack_bf16x2(acc[c][2 * k], acc[c][2 * k + 1]);
+                    if (left >= 16)
+                        store_words(out, w, p.out32);
+                    else if (left > 0)
+                        *reinterpret_cast<uint4 *>(out) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
             }
         }
     }
@@ -601,7 +679,7 @@ __global__ void __launch_bounds__(NarrowShape::THREADS, 1)
                 const ScaledTile t = scaled_tile<S>(p, pre, it);
                 const int boxes = t.width / S::STEP;
                 for (int kb = kb0; kb < kb1; ++kb) {
-                    if (!mbar_wait(&ps->empty[stage], phase ^ 1u, tmo)) {
+                    if (!mbar_wait_suspended(&ps->empty[stage], phase ^ 1u, tmo)) {
                         report_fault(p.status, TDG_ERR_TIMEOUT, TDG_WHERE_PIPE, 0, p.epoch);
                         ps->abort = 1;
                         break;
@@ -624,12 +702,10 @@ __global__ void __launch_bounds__(NarrowShape::THREADS, 1)
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0)
-            scaled_issue<S>(p, ps, smem_u32(smem), tmem, pre, items, unit, units, kb0, kb1, [](const ScaledTile &t) { return t.width; });
-        __syncwarp();
+        scaled_issue<S>(p, ps, smem_u32(smem), tmem, pre, items, unit, units, kb0, kb1, [](const ScaledTile &t) { return t.width; });
     } else if (warp < 4) {
         // scales: 8 rows of a x SK blocks a step, each warp every other step
-        const int j = lane % sg::SK, r0 = lane / sg::SK + (warp - 2) * 8;
+        const int j = lane % S::SK, r0 = lane / S::SK + (warp - 2) * 8;
         int chunk = 0;
         uint32_t phase = 0;
         bool ok = true;
@@ -638,7 +714,7 @@ __global__ void __launch_bounds__(NarrowShape::THREADS, 1)
             const float *sw = p.b_scale + ((int64_t)t.e * p.n_blocks + t.n0 / 128) * p.k_blocks;
             const int rows = (int)(t.end - t.tok0);
             const float *sa = p.a_scale + t.tok0 * p.a_scale_stride;
-            for (int kb = kb0; kb < kb1; kb += sg::SK) {
+            for (int kb = kb0; kb < kb1; kb += S::SK) {
                 const bool in = kb + j < kb1;
                 const float w = in ? sw[kb + j] : 0.f;
                 float v[S::BT / 16];
@@ -647,7 +723,7 @@ __global__ void __launch_bounds__(NarrowShape::THREADS, 1)
                     const int r = r0 + 16 * i;
                     v[i] = in && r < rows ? sa[(int64_t)r * p.a_scale_stride + kb + j] : 0.f;
                 }
-                ok = mbar_wait(&ps->sempty[chunk], phase ^ 1u, tmo);
+                ok = mbar_wait_suspended(&ps->sempty[chunk], phase ^ 1u, tmo);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) {
                     if (lane == 0)
@@ -655,14 +731,14 @@ __global__ void __launch_bounds__(NarrowShape::THREADS, 1)
                     ps->abort = 1;
                     break;
                 }
-                float *dst = scales + (chunk * sg::SK + j) * S::SROW + r0;
+                float *dst = scales + (chunk * S::SK + j) * S::SROW + r0;
 #pragma unroll
                 for (int i = 0; i < S::BT / 16; ++i)
                     dst[16 * i] = v[i] * w;
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(&ps->sfull[chunk]);
-                if (++chunk == sg::SCH) {
+                if (++chunk == S::SCH) {
                     chunk = 0;
                     phase ^= 1u;
                 }
@@ -684,10 +760,10 @@ __global__ void __launch_bounds__(NarrowShape::THREADS, 1)
                 for (int i = 0; i < 8; ++i)
                     acc[c][0][i] = acc[c][1][i] = 0;
             for (int kb = kb0; kb < kb1; ++kb) {
-                const int in_chunk = (kb - kb0) % sg::SK;
+                const int in_chunk = (kb - kb0) % S::SK;
                 if (in_chunk == 0)
-                    ok = mbar_wait(&ps->sfull[chunk], sphase, tmo);
-                ok = ok && mbar_wait(&ps->tfull[buf], bphase, tmo);
+                    ok = mbar_wait_suspended(&ps->sfull[chunk], sphase, tmo);
+                ok = ok && mbar_wait_suspended(&ps->tfull[buf], bphase, tmo);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) {
                     if (lane == 0)
@@ -697,7 +773,7 @@ __global__ void __launch_bounds__(NarrowShape::THREADS, 1)
                 }
                 tc_fence_after();
                 const uint32_t at = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * S::TCOLS);
-                const float *sc = scales + (chunk * sg::SK + in_chunk) * S::SROW + 2 * (lane & 3);
+                const float *sc = scales + (chunk * S::SK + in_chunk) * S::SROW + 2 * (lane & 3);
 #pragma unroll
                 for (int c = 0; c < CH; ++c) {
                     if (c * 32 < t.width) {
@@ -726,10 +802,10 @@ __global__ void __launch_bounds__(NarrowShape::THREADS, 1)
                     buf = 0;
                     bphase ^= 1u;
                 }
-                if (in_chunk == sg::SK - 1 || kb == kb1 - 1) {
+                if (in_chunk == S::SK - 1 || kb == kb1 - 1) {
                     if (lane == 0)
                         mbar_arrive(&ps->sempty[chunk]);
-                    if (++chunk == sg::SCH) {
+                    if (++chunk == S::SCH) {
                         chunk = 0;
                         sphase ^= 1u;
                     }
@@ -845,8 +921,8 @@ bool map_codes(CUtensorMap *m, const void *base, int64_t inner, int64_t rows, in
 template <class S> int run(tdg_symm *h, const tdg_scaled_gemm_args *a, ScaledParams &p, int split, int64_t units, cudaStream_t s)
 {
     CUtensorMap map_w, map_a;
-    const int box = S::PAIR ? sg::ROWS : NarrowShape::STEP;
-    if (!map_codes(&map_w, a->b, a->K, a->N, a->K, a->E, sg::ROWS, false) || !map_codes(&map_a, a->a, a->K, a->M, a->a_stride, 1, box, true))
+    const int box = S::PAIR ? sg::ROWS : NarrowShape::STEP, wbox = sg::ROWS;
+    if (!map_codes(&map_w, a->b, a->K, a->N, a->K, a->E, wbox, false) || !map_codes(&map_a, a->a, a->K, a->M, a->a_stride, 1, box, true))
         return TDG_ERR_CUDA;
     const void *fn = S::PAIR ? reinterpret_cast<const void *>(&scaled_wide_kernel) : reinterpret_cast<const void *>(&scaled_narrow_kernel);
     const int smem = S::SMEM + 4 * (sg::MAX_E + 1);
