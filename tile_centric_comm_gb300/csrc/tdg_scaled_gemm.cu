@@ -22,6 +22,8 @@
 //   warp 1      MMA issuer: four tcgen05.mma.kind::f8f6f4 (K = 32) a block
 //   warps 2, 3  scales: sa * sw of the tile's rows, some blocks at a time
 //   warps 4..   epilogue
+#include <type_traits>
+
 #include "tdg_scaled.cuh"
 
 namespace tdg {
@@ -39,7 +41,8 @@ struct WideShape {
     static constexpr bool PAIR = true;
     static constexpr int BT = 256;                   // rows of a in a tile, over the pair
     static constexpr int WTILE = 256;                // weight rows of a tile
-    static constexpr int STAGES = 6, STAGE_BYTES = 2 * sg::A_BYTES;
+    static constexpr int BPS = 1;                    // blocks of a ring stage
+    static constexpr int BLOCK_BYTES = 2 * sg::A_BYTES, STAGES = 6, STAGE_BYTES = BLOCK_BYTES;
     static constexpr int TBUF = 2, TCOLS = 256;      // accumulators in TMEM
     static constexpr int EPIW = 8, THREADS = 128 + 32 * EPIW;
     static constexpr int REGS_OTHER = 72, REGS_EPI = 216; // registers of a thread
@@ -57,8 +60,9 @@ struct NarrowShape {
     static constexpr int BT = 64;                    // rows of a in a tile, at most
     static constexpr int WTILE = sg::ROWS;
     static constexpr int STEP = 16;                  // of an instruction's columns, and rows of a TMA box
-    static constexpr int STAGES = 8, STAGE_BYTES = sg::A_BYTES + BT * sg::BK;
-    static constexpr int TBUF = 8, TCOLS = BT;
+    static constexpr int BPS = 2;                    // two blocks a wait: every role's time is its waits'
+    static constexpr int BLOCK_BYTES = sg::A_BYTES + BT * sg::BK, STAGES = 4, STAGE_BYTES = BPS * BLOCK_BYTES;
+    static constexpr int TBUF = 4, TCOLS = BT;
     static constexpr int EPIW = 4, THREADS = 128 + 32 * EPIW;
     static constexpr int SK = 4, SCH = 3;
     static constexpr int SROW = BT + 8;
@@ -373,9 +377,9 @@ __device__ __forceinline__ void scaled_issue(const ScaledParams &p, ScaledSmem *
     bool ok = true;
     for (uint32_t it = unit; it < items && ok; it += units) {
         const uint32_t idesc = idesc_e4m3(S::PAIR ? 2 * sg::ROWS : sg::ROWS, columns(scaled_tile<S>(p, pre, it)));
-        for (int kb = kb0; kb < kb1; ++kb) {
-            const uint64_t ad = ad0 + (uint64_t)(stage * (S::STAGE_BYTES >> 4)), bd = ad + (sg::A_BYTES >> 4);
-            const uint32_t d = tmem + (uint32_t)(buf * S::TCOLS);
+        for (int kb = kb0; kb < kb1; kb += S::BPS) {
+            const uint64_t ad = ad0 + (uint64_t)(stage * (S::STAGE_BYTES >> 4));
+            const uint32_t d = tmem + (uint32_t)(buf * S::BPS * S::TCOLS);
             // the accumulator last: it is what is waited for
             ok = mbar_wait_suspended(&ps->full[stage], phase, tmo) && mbar_wait_suspended(&ps->tempty[buf], bphase ^ 1u, tmo);
             ok = __all_sync(0xffffffffu, ok);
@@ -384,11 +388,16 @@ __device__ __forceinline__ void scaled_issue(const ScaledParams &p, ScaledSmem *
             tc_fence_after();
             if (elected()) {
 #pragma unroll
-                for (int k = 0; k < sg::BK / 32; ++k)
-                    umma_e4m3<S::PAIR>(d, ad + 2 * k, bd + 2 * k, idesc, k ? 1u : 0u);
+                for (int j = 0; j < S::BPS; ++j)
+                    if (j == 0 || kb + j < kb1) {
+                        const uint64_t aj = ad + (uint64_t)(j * (S::BLOCK_BYTES >> 4)), bj = aj + (sg::A_BYTES >> 4);
+#pragma unroll
+                        for (int k = 0; k < sg::BK / 32; ++k)
+                            umma_e4m3<S::PAIR>(d + j * S::TCOLS, aj + 2 * k, bj + 2 * k, idesc, k ? 1u : 0u);
+                    }
                 if (S::PAIR) {
-                    umma_commit_pair_mask(&ps->tfull[buf], 3);
                     umma_commit_pair_mask(&ps->empty[stage], 3);
+                    umma_commit_pair_mask(&ps->tfull[buf], 3);
                 } else {
                     umma_commit(&ps->tfull[buf]);
                     umma_commit(&ps->empty[stage]);
@@ -678,19 +687,22 @@ __global__ void __launch_bounds__(NarrowShape::THREADS, 1)
             for (uint32_t it = unit; it < items && !ps->abort; it += units) {
                 const ScaledTile t = scaled_tile<S>(p, pre, it);
                 const int boxes = t.width / S::STEP;
-                for (int kb = kb0; kb < kb1; ++kb) {
+                for (int kb = kb0; kb < kb1; kb += S::BPS) {
                     if (!mbar_wait_suspended(&ps->empty[stage], phase ^ 1u, tmo)) {
                         report_fault(p.status, TDG_ERR_TIMEOUT, TDG_WHERE_PIPE, 0, p.epoch);
                         ps->abort = 1;
                         break;
                     }
-                    uint8_t *dst = smem + stage * S::STAGE_BYTES;
-                    mbar_arrive_expect_tx(&ps->full[stage], (uint32_t)(sg::A_BYTES + t.width * sg::BK));
+                    const int blocks = min(S::BPS, kb1 - kb);
                     const uint32_t bar = smem_u32(&ps->full[stage]);
-                    tma_load_3d_addr(dst, &map_w, bar, kb * sg::BK, t.n0, t.e);
-                    for (int i = 0; i < boxes; ++i)
-                        tma_load_2d_addr(dst + sg::A_BYTES + i * S::STEP * sg::BK, &map_a, bar, kb * sg::BK,
-                                         (int)((uint32_t)t.tok0 + i * S::STEP));
+                    mbar_arrive_expect_tx(&ps->full[stage], (uint32_t)(blocks * (sg::A_BYTES + t.width * sg::BK)));
+                    for (int j = 0; j < blocks; ++j) {
+                        uint8_t *dst = smem + stage * S::STAGE_BYTES + j * S::BLOCK_BYTES;
+                        tma_load_3d_addr(dst, &map_w, bar, (kb + j) * sg::BK, t.n0, t.e);
+                        for (int i = 0; i < boxes; ++i)
+                            tma_load_2d_addr(dst + sg::A_BYTES + i * S::STEP * sg::BK, &map_a, bar, (kb + j) * sg::BK,
+                                             (int)((uint32_t)t.tok0 + i * S::STEP));
+                    }
                     ++issued;
                     if (++stage == S::STAGES) {
                         stage = 0;
@@ -748,8 +760,10 @@ __global__ void __launch_bounds__(NarrowShape::THREADS, 1)
         const int q = warp & 3; // lanes of TMEM
         uint8_t *stg = smem + S::OFF_STG + (warp - 4) * S::STG;
         constexpr int CH = S::BT / 32; // chunks of 32 columns
+        const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
+        const uint32_t tfull0 = smem_u32(&ps->tfull[0]), sfull0 = smem_u32(&ps->sfull[0]);
         int buf = 0, chunk = 0;
-        uint32_t bphase = 0, sphase = 0;
+        uint32_t bphase = 0, sphase = 0, failed = 0;
         bool ok = true;
         for (uint32_t it = unit; it < items && ok; it += units) {
             const ScaledTile t = scaled_tile<S>(p, pre, it);
@@ -759,57 +773,85 @@ __global__ void __launch_bounds__(NarrowShape::THREADS, 1)
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     acc[c][0][i] = acc[c][1][i] = 0;
-            for (int kb = kb0; kb < kb1; ++kb) {
-                const int in_chunk = (kb - kb0) % S::SK;
-                if (in_chunk == 0)
-                    ok = mbar_wait_suspended(&ps->sfull[chunk], sphase, tmo);
-                ok = ok && mbar_wait_suspended(&ps->tfull[buf], bphase, tmo);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) {
-                    if (lane == 0)
-                        report_fault(p.status, TDG_ERR_TIMEOUT, TDG_WHERE_PIPE, 3, p.epoch);
-                    ps->abort = 1;
-                    break;
-                }
-                tc_fence_after();
-                const uint32_t at = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * S::TCOLS);
-                const float *sc = scales + (chunk * S::SK + in_chunk) * S::SROW + 2 * (lane & 3);
+            // The blocks of a tile whose rows fill N chunks: code without a branch for each
+            // chunk (with one, a block of 16 rows took 750 cycles).  One block's
+            // accumulator is on its way while the one before is added.
+            auto add_blocks = [&](auto chunks) {
+                constexpr int N = decltype(chunks)::value;
+                for (int kb = kb0, in_chunk = 0; kb < kb1 && !failed; kb += S::BPS) {
+                    const bool two = kb + 1 < kb1;
+                    if (in_chunk == 0)
+                        mbar_wait_suspended(sfull0 + chunk * 8, sphase, tmo, failed);
+                    uint64_t s[S::BPS][N][4];
+                    const float *sc = scales + (chunk * S::SK + in_chunk) * S::SROW + 2 * (lane & 3);
 #pragma unroll
-                for (int c = 0; c < CH; ++c) {
-                    if (c * 32 < t.width) {
-                        uint32_t lo[16], hi[16];
-                        tmem_ld_16x256b_x4(at + c * 32, lo);
-                        tmem_ld_16x256b_x4(at + (16u << 16) + c * 32, hi);
-                        uint64_t s[4];
+                    for (int j = 0; j < S::BPS; ++j) // (a chunk holds whole pairs; zeros behind the last block)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            s[i] = *reinterpret_cast<const uint64_t *>(sc + c * 32 + 8 * i);
+                        for (int c = 0; c < N; ++c)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                s[j][c][i] = *reinterpret_cast<const uint64_t *>(sc + j * S::SROW + c * 32 + 8 * i);
+                    uint32_t lo[S::BPS][N][16], hi[S::BPS][N][16];
+                    auto load = [&](int j) {
+                        const uint32_t at = lanes + (uint32_t)((buf * S::BPS + j) * S::TCOLS);
+#pragma unroll
+                        for (int c = 0; c < N; ++c) {
+                            tmem_ld_16x256b_x4(at + c * 32, lo[j][c]);
+                            tmem_ld_16x256b_x4(at + (16u << 16) + c * 32, hi[j][c]);
+                        }
+                    };
+                    auto add = [&](int j) {
+#pragma unroll
+                        for (int c = 0; c < N; ++c)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                fma_pair(acc[c][0][2 * i], lo[j][c][4 * i], lo[j][c][4 * i + 1], s[j][c][i]);
+                                fma_pair(acc[c][0][2 * i + 1], lo[j][c][4 * i + 2], lo[j][c][4 * i + 3], s[j][c][i]);
+                                fma_pair(acc[c][1][2 * i], hi[j][c][4 * i], hi[j][c][4 * i + 1], s[j][c][i]);
+                                fma_pair(acc[c][1][2 * i + 1], hi[j][c][4 * i + 2], hi[j][c][4 * i + 3], s[j][c][i]);
+                            }
+                    };
+                    mbar_wait_suspended(tfull0 + buf * 8, bphase, tmo, failed);
+                    tc_fence_after();
+                    load(0);
+                    tmem_ld_wait();
+                    if (two) {
+                        load(1);
+                        add(0);
                         tmem_ld_wait();
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            fma_pair(acc[c][0][2 * i], lo[4 * i], lo[4 * i + 1], s[i]);
-                            fma_pair(acc[c][0][2 * i + 1], lo[4 * i + 2], lo[4 * i + 3], s[i]);
-                            fma_pair(acc[c][1][2 * i], hi[4 * i], hi[4 * i + 1], s[i]);
-                            fma_pair(acc[c][1][2 * i + 1], hi[4 * i + 2], hi[4 * i + 3], s[i]);
+                        tc_fence_before();
+                        mbar_arrive_relaxed(&ps->tempty[buf], lane == 0);
+                        add(1);
+                    } else {
+                        tc_fence_before();
+                        mbar_arrive_relaxed(&ps->tempty[buf], lane == 0);
+                        add(0);
+                    }
+                    if (++buf == S::TBUF) {
+                        buf = 0;
+                        bphase ^= 1u;
+                    }
+                    in_chunk += S::BPS;
+                    if (in_chunk == S::SK || kb + S::BPS >= kb1) {
+                        in_chunk = 0;
+                        __syncwarp();
+                        mbar_arrive_relaxed(&ps->sempty[chunk], lane == 0);
+                        if (++chunk == S::SCH) {
+                            chunk = 0;
+                            sphase ^= 1u;
                         }
                     }
                 }
-                tc_fence_before();
-                __syncwarp();
+            };
+            if (t.width <= 32)
+                add_blocks(std::integral_constant<int, 1>{});
+            else
+                add_blocks(std::integral_constant<int, 2>{});
+            ok = __all_sync(0xffffffffu, !failed);
+            if (!ok) {
                 if (lane == 0)
-                    mbar_arrive(&ps->tempty[buf]);
-                if (++buf == S::TBUF) {
-                    buf = 0;
-                    bphase ^= 1u;
-                }
-                if (in_chunk == S::SK - 1 || kb == kb1 - 1) {
-                    if (lane == 0)
-                        mbar_arrive(&ps->sempty[chunk]);
-                    if (++chunk == S::SCH) {
-                        chunk = 0;
-                        sphase ^= 1u;
-                    }
-                }
+                    report_fault(p.status, TDG_ERR_TIMEOUT, TDG_WHERE_PIPE, 3, p.epoch);
+                ps->abort = 1;
             }
             if (!ok)
                 break;
@@ -961,10 +1003,12 @@ extern "C" int tdg_scaled_gemm(tdg_symm *h, const tdg_scaled_gemm_args *a, void 
     const Range rbs{a->b_scale, (uint64_t)a->E * nb * kb * 4}, base{a->base, (uint64_t)(a->E + 1) * 8};
     if (ranges_overlap({out}, {ra, rs, rb, rbs, base}))
         return TDG_ERR_INVALID;
-    // the tiles, at most, of each kernel's shape: one more for every expert than its rows fill
-    const int64_t used = a->E < a->M ? a->E : a->M;
-    const int64_t wide = (used + a->M / WideShape::BT) * ((a->N + WideShape::WTILE - 1) / WideShape::WTILE);
-    const int64_t narrow = (used + a->M / NarrowShape::BT) * ((a->N + NarrowShape::WTILE - 1) / NarrowShape::WTILE);
+    // the tiles, at most, of each kernel's shape: with experts, one more for each than its rows fill
+    auto most_tiles = [&](int64_t bt, int64_t wtile) {
+        const int64_t rows = a->base ? (a->E < a->M ? a->E : a->M) + a->M / bt : (a->M + bt - 1) / bt;
+        return rows * ((a->N + wtile - 1) / wtile);
+    };
+    const int64_t wide = most_tiles(WideShape::BT, WideShape::WTILE), narrow = most_tiles(NarrowShape::BT, NarrowShape::WTILE);
     if (narrow > INT32_MAX)
         return TDG_ERR_INVALID;
     ScaledParams p;
@@ -990,9 +1034,11 @@ extern "C" int tdg_scaled_gemm(tdg_symm *h, const tdg_scaled_gemm_args *a, void 
         const int64_t pairs = h->sm_count / 2;
         return run<WideShape>(h, a, p, 1, wide < pairs ? wide : pairs, s);
     }
-    // few tiles: K cut over the CTAs of a cluster, two blocks of it each at least
+    // few tiles: K divided over the CTAs of a cluster, two blocks of it each at
+    // least (clusters of 8 start 5 us later: 2048 x 2048, one row, 6.6 us by 4
+    // CTAs and 11.8 by 8)
     int split = 1;
-    while (split < 8 && narrow * split * 2 <= h->sm_count && kb >= 4 * split)
+    while (split < 4 && narrow * split * 2 <= h->sm_count && kb >= 4 * split)
         split *= 2;
     const int64_t units = h->sm_count / split;
     return run<NarrowShape>(h, a, p, split, narrow < units ? narrow : units, s);
