@@ -1030,16 +1030,24 @@ extern "C" int tdg_scaled_gemm(tdg_symm *h, const tdg_scaled_gemm_args *a, void 
     p.out = a->out;
     p.base = a->base;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (a->M / a->E > 64) {
-        const int64_t pairs = h->sm_count / 2;
-        return run<WideShape>(h, a, p, 1, wide < pairs ? wide : pairs, s);
-    }
     // few tiles: K divided over the CTAs of a cluster, two blocks of it each at
     // least (clusters of 8 start 5 us later: 2048 x 2048, one row, 6.6 us by 4
     // CTAs and 11.8 by 8)
     int split = 1;
     while (split < 4 && narrow * split * 2 <= h->sm_count && kb >= 4 * split)
         split *= 2;
+    // The kernel whose tiles take less time, with an expert's share the average one:
+    // rounds of the grid, each of a time for the tile and one for every block of K
+    // (us; 7168 x 8192: 27 narrow and 35 wide for 128 rows, 50 and 35 for 192;
+    // 32 experts of 4096 x 2048: 49 and 71 for 64 rows each, 100 and 73 for 80)
+    const int64_t used = a->E < a->M ? a->E : a->M, share = (a->M + used - 1) / used, pairs = h->sm_count / 2;
+    auto time_of = [&](int64_t bt, int64_t wtile, int64_t at_once, double tile, double block) {
+        const int64_t tiles = used * ((share + bt - 1) / bt) * ((a->N + wtile - 1) / wtile);
+        return (double)((tiles + at_once - 1) / at_once) * (tile + block * (double)kb);
+    };
+    if (time_of(WideShape::BT, WideShape::WTILE, pairs, 2.0, 0.47) <
+        time_of(NarrowShape::BT, NarrowShape::WTILE, h->sm_count / split, 0.7, 0.3 / split))
+        return run<WideShape>(h, a, p, 1, wide < pairs ? wide : pairs, s);
     const int64_t units = h->sm_count / split;
     return run<NarrowShape>(h, a, p, split, narrow < units ? narrow : units, s);
 }
