@@ -10,10 +10,13 @@ Bounds (u = 2^-24, the unit roundoff of float32):
     where the output has that type;
   - codes of bf16 values are those of the correctly rounded float32 quotient:
     bit for bit;
-  - a gated value: exp within 2 ulp (4u), its product with the gate, 1 + exp
-    and the product with up rounded (u each), the exp in numerator and
-    denominator, 2 ulp (4u) of the division: 16u relative at most, 2^-20; its scale as much, and its code half a step off the quotient
-    (2^-4 relative, 2^-10 below the smallest normal) plus 2^-19 relative.
+  - a gated value g r u, r the reciprocal (1 ulp: 2u) of 1 + e (u), e = 2^t
+    (2 ulp: 4u), t = -g log2(e): the constant and the product rounded, u |t|
+    each, which moves e by 2u |t| ln 2 = 2u |g| relative, and two products (u
+    each).  e counts in full for negative g and by e / (1 + e) for positive,
+    where |g| e / (1 + e) < 0.28: 9u + 2u max(-g, 0.28), taken as 2^-20 +
+    2^-23 max(-g, 0); its scale as much, and its code half a step off the
+    quotient (2^-4 relative, 2^-10 below the smallest normal) plus twice that.
 """
 from __future__ import annotations
 
