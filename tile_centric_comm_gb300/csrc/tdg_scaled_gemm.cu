@@ -42,14 +42,16 @@ struct WideShape {
     static constexpr int BT = 256;                   // rows of a in a tile, over the pair
     static constexpr int WTILE = 256;                // weight rows of a tile
     static constexpr int BPS = 1;                    // blocks of a ring stage
-    static constexpr int BLOCK_BYTES = 2 * sg::A_BYTES, STAGES = 6, STAGE_BYTES = BLOCK_BYTES;
+    static constexpr int BLOCK_BYTES = 2 * sg::A_BYTES, STAGES = 5, STAGE_BYTES = BLOCK_BYTES;
     static constexpr int TBUF = 2, TCOLS = 256;      // accumulators in TMEM
     static constexpr int EPIW = 8, THREADS = 128 + 32 * EPIW;
     static constexpr int REGS_OTHER = 72, REGS_EPI = 216; // registers of a thread
     static_assert(128 * REGS_OTHER + 32 * EPIW * REGS_EPI <= THREADS * (65536 / THREADS / 8 * 8), "registers of the launch");
     static constexpr int SK = 4, SCH = 3;            // blocks whose scales are loaded together, such chunks in the ring
     static constexpr int SROW = 2 * sg::ROWS + 8;    // floats of a block's scales: for each half of the columns, and a pad
-    static constexpr int OFF_SCALE = STAGES * STAGE_BYTES;
+    static constexpr int STG = 32 * 128;             // staged rows of an epilogue warp: 128 bytes of each
+    static constexpr int OFF_STG = STAGES * STAGE_BYTES; // (swizzled by address: 1024-byte aligned)
+    static constexpr int OFF_SCALE = OFF_STG + EPIW * STG;
     static constexpr int OFF_BAR = OFF_SCALE + SCH * SK * SROW * 4;
     static constexpr int OFF_PRE = OFF_BAR + sg::BAR_BYTES; // tiles before each expert
     static constexpr int SMEM = OFF_PRE + 1024;      // + 4 (E + 1); + alignment slack
@@ -84,13 +86,15 @@ struct ScaledParams {
     uint64_t timeout_ns;
     int64_t M, a_scale_stride, out_stride;
     int N, E, k_blocks, n_tiles, n_blocks, out_f32;
-    int out32;                   // rows of out are 32-byte aligned
     int split;                   // narrow: CTAs of a cluster that share K (1: none)
     const float *a_scale, *b_scale;
     void *out;
     const int64_t *base;
 };
 
+// tile: wide, the tiles whose scales the ring holds.  The scale warps are at most
+// SCH chunks ahead of the epilogue, so a tile's entry is written again only when
+// the epilogue has stored that tile.
 struct ScaledSmem {
     uint64_t full[8], empty[8], tfull[8], tempty[8];
     uint64_t sfull[4], sempty[4], drain;
@@ -98,6 +102,10 @@ struct ScaledSmem {
     volatile int abort;
     uint32_t issued, consumed; // ring fills issued by the loader, consumed by the issuer
     uint32_t scan[16];
+    struct {
+        int64_t row, end; // of this CTA's first row, and of the tile
+        int n0;
+    } tile[4];
 };
 static_assert(sizeof(ScaledSmem) <= sg::BAR_BYTES, "barrier block");
 
@@ -220,19 +228,6 @@ __device__ __forceinline__ void mbar_arrive_relaxed(uint64_t *bar, bool by)
     asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\t"
                  "@p mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];\n\t}" ::"r"(smem_u32(bar)), "r"(by ? 1u : 0u)
                  : "memory");
-}
-
-// 8 words of one row, 32-byte aligned or in two halves of 16 bytes
-__device__ __forceinline__ void store_words(void *p, const uint32_t (&w)[8], bool aligned32)
-{
-    if (aligned32) {
-        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]),
-                     "r"(w[5]), "r"(w[6]), "r"(w[7])
-                     : "memory");
-    } else {
-        reinterpret_cast<uint4 *>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        reinterpret_cast<uint4 *>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-    }
 }
 
 struct ScaledTile {
@@ -509,7 +504,8 @@ __global__ void __launch_bounds__(WideShape::THREADS, 1)
         int chunk = 0;
         uint32_t phase = 0;
         bool ok = true;
-        for (uint32_t it = unit; it < items && ok; it += units) {
+        uint32_t nth = 0;
+        for (uint32_t it = unit; it < items && ok; it += units, ++nth) {
             const ScaledTile t = scaled_tile<S>(p, pre, it);
             const float *sw = p.b_scale + ((int64_t)t.e * p.n_blocks + t.n0 / 128) * p.k_blocks;
             const int64_t next = t.n0 / 128 + 1 < p.n_blocks ? p.k_blocks : 0;
@@ -530,6 +526,11 @@ __global__ void __launch_bounds__(WideShape::THREADS, 1)
                         report_fault(p.status, TDG_ERR_TIMEOUT, TDG_WHERE_PIPE, 2, p.epoch);
                     ps->abort = 1;
                     break;
+                }
+                if (kb == 0 && warp == 2 && lane == 0) {
+                    ps->tile[nth & 3].row = first;
+                    ps->tile[nth & 3].end = t.end;
+                    ps->tile[nth & 3].n0 = t.n0;
                 }
                 float *dst = scales + (chunk * S::SK + j) * S::SROW + r0;
 #pragma unroll
@@ -556,8 +557,9 @@ __global__ void __launch_bounds__(WideShape::THREADS, 1)
         int chunk = 0;
         uint32_t buf = 0, bphase = 0, sphase = 0, failed = 0;
         bool ok = true;
-        for (uint32_t it = unit; it < items && ok; it += units) {
-            const ScaledTile t = scaled_tile<S>(p, pre, it);
+        uint8_t *stg = smem + S::OFF_STG + (warp - 4) * S::STG;
+        uint32_t nth = 0;
+        for (uint32_t it = unit; it < items && ok; it += units, ++nth) {
             float acc[8][16];
 #pragma unroll
             for (int c = 0; c < 8; ++c)
@@ -620,33 +622,41 @@ __global__ void __launch_bounds__(WideShape::THREADS, 1)
                 ps->abort = 1;
                 break;
             }
-            const int64_t row = t.tok0 + half * sg::ROWS + q * 32 + lane;
-            if (row >= t.end)
-                continue;
+            // 128 bytes of each of the warp's 32 rows at a time through shared memory, so
+            // that a store covers 4 whole lines (one of 32 rows takes 32 cycles)
+            const int64_t row = ps->tile[nth & 3].row + q * 32, rows_left = ps->tile[nth & 3].end - row;
+            const int n = ps->tile[nth & 3].n0 + cg * 128, piece = lane & 7;
+            auto pass = [&](int col, int per16, auto words) { // columns from col on, per16 of them in 16 bytes
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                const int n = t.n0 + cg * 128 + c * 16, left = p.N - n;
-                uint32_t w[8];
-                if (p.out_f32) {
-                    float *out = static_cast<float *>(p.out) + row * p.out_stride + n;
+                for (int j = 0; j < 8; ++j)
+                    *reinterpret_cast<uint4 *>(stg + lane * 128 + ((j ^ (lane & 7)) << 4)) = words(j);
+                __syncwarp();
+                const int left = p.N - n - col - piece * per16;
+                uint8_t *out = static_cast<uint8_t *>(p.out) + ((row + (lane >> 3)) * p.out_stride + n + col) * (16 / per16) + piece * 16;
+                const int64_t step = 4 * p.out_stride * (16 / per16);
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        if (i * 8 < left) {
-#pragma unroll
-                            for (int k = 0; k < 8; ++k)
-                                w[k] = __float_as_uint(acc[c][8 * i + k]);
-                            store_words(out + i * 8, w, p.out32);
-                        }
-                } else {
-                    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out) + row * p.out_stride + n;
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        w[k] = pack_bf16x2(acc[c][2 * k], acc[c][2 * k + 1]);
-                    if (left >= 16)
-                        store_words(out, w, p.out32);
-                    else if (left > 0)
-                        *reinterpret_cast<uint4 *>(out) = make_uint4(w[0], w[1], w[2], w[3]);
+                for (int i = 0; i < 8; ++i) {
+                    const int r = 4 * i + (lane >> 3);
+                    const uint4 v = *reinterpret_cast<const uint4 *>(stg + r * 128 + ((piece ^ (r & 7)) << 4));
+                    if (r < rows_left && left > 0)
+                        *reinterpret_cast<uint4 *>(out + i * step) = v;
                 }
+                __syncwarp();
+            };
+            if (p.out_f32) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    pass(c * 32, 4, [&](int j) {
+                        const float *a = &acc[2 * c + (j >> 2)][(j & 3) * 4];
+                        return make_uint4(__float_as_uint(a[0]), __float_as_uint(a[1]), __float_as_uint(a[2]), __float_as_uint(a[3]));
+                    });
+            } else {
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    pass(c * 64, 8, [&](int j) {
+                        const float *a = &acc[4 * c + (j >> 1)][(j & 1) * 8];
+                        return make_uint4(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(a[4], a[5]), pack_bf16x2(a[6], a[7]));
+                    });
             }
         }
     }
@@ -1024,7 +1034,6 @@ extern "C" int tdg_scaled_gemm(tdg_symm *h, const tdg_scaled_gemm_args *a, void 
     p.k_blocks = (int)kb;
     p.n_blocks = (int)nb;
     p.out_f32 = a->out_f32;
-    p.out32 = reinterpret_cast<uintptr_t>(a->out) % 32 == 0 && a->out_stride * esz % 32 == 0;
     p.a_scale = a->a_scale;
     p.b_scale = a->b_scale;
     p.out = a->out;
