@@ -445,7 +445,8 @@ template <class S> __device__ __forceinline__ void scaled_drain(const ScaledPara
 }
 
 __global__ void __launch_bounds__(WideShape::THREADS, 1)
-    scaled_wide_kernel(const __grid_constant__ ScaledParams p, const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a)
+    scaled_wide_kernel(const __grid_constant__ ScaledParams p, const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a,
+                       const __grid_constant__ CUtensorMap map_out)
 {
     using S = WideShape;
     extern __shared__ uint8_t smem_raw[];
@@ -622,15 +623,30 @@ __global__ void __launch_bounds__(WideShape::THREADS, 1)
                 ps->abort = 1;
                 break;
             }
-            // 128 bytes of each of the warp's 32 rows at a time through shared memory, so
-            // that a store covers 4 whole lines (one of 32 rows takes 32 cycles)
-            const int64_t row = ps->tile[nth & 3].row + q * 32, rows_left = ps->tile[nth & 3].end - row;
+            // 128 bytes of each of the warp's 32 rows at a time through shared memory, from
+            // where one TMA store takes them while the next tile is multiplied (an SM writes
+            // about 22 bytes a cycle, 3000 cycles for a tile).  Rows that end inside the
+            // tile are stored by the lanes.
+            const int64_t row = ps->tile[nth & 3].row + q * 32, end = ps->tile[nth & 3].end;
             const int n = ps->tile[nth & 3].n0 + cg * 128, piece = lane & 7;
+            const bool whole = row + 32 <= end || end == p.M; // (the map ends at row M)
             auto pass = [&](int col, int per16, auto words) { // columns from col on, per16 of them in 16 bytes
+                if (lane == 0)
+                    bulk_wait_read<0>();
+                __syncwarp();
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
                     *reinterpret_cast<uint4 *>(stg + lane * 128 + ((j ^ (lane & 7)) << 4)) = words(j);
+                if (whole)
+                    fence_proxy_async_smem();
                 __syncwarp();
+                if (whole) {
+                    if (lane == 0 && row < end && n + col < p.N) {
+                        tma_store_2d(&map_out, stg, n + col, (int)row);
+                        bulk_commit();
+                    }
+                    return;
+                }
                 const int left = p.N - n - col - piece * per16;
                 uint8_t *out = static_cast<uint8_t *>(p.out) + ((row + (lane >> 3)) * p.out_stride + n + col) * (16 / per16) + piece * 16;
                 const int64_t step = 4 * p.out_stride * (16 / per16);
@@ -638,10 +654,9 @@ __global__ void __launch_bounds__(WideShape::THREADS, 1)
                 for (int i = 0; i < 8; ++i) {
                     const int r = 4 * i + (lane >> 3);
                     const uint4 v = *reinterpret_cast<const uint4 *>(stg + r * 128 + ((piece ^ (r & 7)) << 4));
-                    if (r < rows_left && left > 0)
+                    if (row + r < end && left > 0)
                         *reinterpret_cast<uint4 *>(out + i * step) = v;
                 }
-                __syncwarp();
             };
             if (p.out_f32) {
 #pragma unroll
@@ -659,6 +674,8 @@ __global__ void __launch_bounds__(WideShape::THREADS, 1)
                     });
             }
         }
+        if (lane == 0)
+            bulk_wait<0>();
     }
     scaled_drain<S>(p, ps, half == 0);
     cluster_sync(); // no CTA leaves while the other may still touch it
@@ -972,9 +989,12 @@ bool map_codes(CUtensorMap *m, const void *base, int64_t inner, int64_t rows, in
 
 template <class S> int run(tdg_symm *h, const tdg_scaled_gemm_args *a, ScaledParams &p, int split, int64_t units, cudaStream_t s)
 {
-    CUtensorMap map_w, map_a;
+    CUtensorMap map_w, map_a, map_out;
     const int box = S::PAIR ? sg::ROWS : NarrowShape::STEP, wbox = sg::ROWS;
     if (!map_codes(&map_w, a->b, a->K, a->N, a->K, a->E, wbox, false) || !map_codes(&map_a, a->a, a->K, a->M, a->a_stride, 1, box, true))
+        return TDG_ERR_CUDA;
+    if (S::PAIR && !(a->out_f32 ? map_f32_2d(&map_out, a->out, a->N, a->M, a->out_stride * 4, 32, 32)
+                                : map_bf16_2d(&map_out, a->out, a->N, a->M, a->out_stride * 2, 64, 32)))
         return TDG_ERR_CUDA;
     const void *fn = S::PAIR ? reinterpret_cast<const void *>(&scaled_wide_kernel) : reinterpret_cast<const void *>(&scaled_narrow_kernel);
     const int smem = S::SMEM + 4 * (sg::MAX_E + 1);
@@ -984,7 +1004,7 @@ template <class S> int run(tdg_symm *h, const tdg_scaled_gemm_args *a, ScaledPar
     p.split = split;
     p.n_tiles = (int)((a->N + S::WTILE - 1) / S::WTILE);
     const int cl = S::PAIR ? 2 : split;
-    void *args[] = {&p, &map_w, &map_a};
+    void *args[] = {&p, &map_w, &map_a, &map_out}; // (the narrow kernel takes three)
     return cuda_err(launch(fn, dim3((unsigned)(units * cl)), dim3(S::THREADS), S::SMEM + 4 * ((size_t)a->E + 1), s, args, false, cl, true),
                     "scaled gemm launch");
 }
