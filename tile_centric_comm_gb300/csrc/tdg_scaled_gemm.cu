@@ -271,7 +271,7 @@ template <class S> __device__ __forceinline__ ScaledTile scaled_tile(const Scale
 // Barriers and TMEM, then (behind the launch before) the tiles before each
 // expert: a segment of experts a thread, then a scan.  Sums are cut at 2^31 - 1:
 // offsets that are in order never reach that.
-template <class S> __device__ __forceinline__ void scaled_begin(const ScaledParams &p, ScaledSmem *ps, uint32_t *pre, int cl)
+template <class S> __device__ __forceinline__ void scaled_begin(const ScaledParams &p, ScaledSmem *ps, uint32_t *pre)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -305,11 +305,22 @@ template <class S> __device__ __forceinline__ void scaled_begin(const ScaledPara
     }
     griddep_launch_dependents();
     griddep_wait();
+    if (!p.base) {
+        if (threadIdx.x == 0) {
+            pre[0] = 0;
+            pre[1] = (uint32_t)((p.M + S::BT - 1) / S::BT) * p.n_tiles;
+        }
+        __syncthreads();
+        if (S::PAIR)
+            cluster_sync(); // the peer's barriers are initialised before any remote use
+        tc_fence_after();
+        return;
+    }
     const int per = (p.E + S::THREADS - 1) / S::THREADS;
     const int lo = min(p.E, (int)threadIdx.x * per), hi = min(p.E, lo + per);
     const uint64_t most = 0x7fffffffu;
     auto tiles_of = [&](int e) -> uint64_t {
-        const int64_t b0 = p.base ? p.base[e] : 0, b1 = p.base ? p.base[e + 1] : p.M;
+        const int64_t b0 = p.base[e], b1 = p.base[e + 1];
         if (b0 < 0 || b1 < b0 || b1 > p.M) {
             if (blockIdx.x == 0)
                 report_fault(p.status, TDG_ERR_DEVICE, TDG_WHERE_CU, (uint32_t)e, p.epoch);
@@ -341,8 +352,8 @@ template <class S> __device__ __forceinline__ void scaled_begin(const ScaledPara
             pre[p.E] = (uint32_t)run;
     }
     __syncthreads();
-    if (cl > 1)
-        cluster_sync(); // the peers' barriers are initialised before any remote use
+    if (S::PAIR)
+        cluster_sync();
     tc_fence_after();
 }
 
@@ -458,7 +469,7 @@ __global__ void __launch_bounds__(WideShape::THREADS, 1)
     const int half = (int)cluster_ctarank();
     const uint32_t unit = blockIdx.x / 2, units = gridDim.x / 2;
     const uint64_t tmo = p.timeout_ns;
-    scaled_begin<S>(p, ps, pre, 2);
+    scaled_begin<S>(p, ps, pre);
     const uint32_t tmem = ps->tmem_base, items = pre[p.E];
     // an instruction's columns: the weight rows of the tile in steps of 32, each CTA holding half of them
     auto columns = [&](const ScaledTile &t) { return min(S::WTILE, (p.N - t.n0 + 31) / 32 * 32); };
@@ -701,7 +712,11 @@ __global__ void __launch_bounds__(NarrowShape::THREADS, 1)
     const int crank = p.split > 1 ? (int)cluster_ctarank() : 0;
     const uint32_t unit = blockIdx.x / p.split, units = gridDim.x / p.split;
     const uint64_t tmo = p.timeout_ns;
-    scaled_begin<S>(p, ps, pre, p.split);
+    if (threadIdx.x == 64) {
+        prefetch_tensormap(&map_w);
+        prefetch_tensormap(&map_a);
+    }
+    scaled_begin<S>(p, ps, pre);
     const uint32_t tmem = ps->tmem_base;
     const uint32_t items = p.split > 1 ? min(pre[p.E], units) : pre[p.E]; // with K divided a cluster has one tile
     // this CTA's blocks of K
@@ -1067,15 +1082,15 @@ extern "C" int tdg_scaled_gemm(tdg_symm *h, const tdg_scaled_gemm_args *a, void 
         split *= 2;
     // The kernel whose tiles take less time, with an expert's share the average one:
     // rounds of the grid, each of a time for the tile and one for every block of K
-    // (us; 7168 x 8192: 27 narrow and 35 wide for 128 rows, 50 and 35 for 192;
-    // 32 experts of 4096 x 2048: 49 and 71 for 64 rows each, 100 and 73 for 80)
+    // (us; 7168 x 8192: 25 narrow and 34 wide for 128 rows, 50 and 34 for 192;
+    // 32 experts of 4096 x 2048: 48 and 66 for 64 rows each, 100 and 68 for 80)
     const int64_t used = a->E < a->M ? a->E : a->M, share = (a->M + used - 1) / used, pairs = h->sm_count / 2;
     auto time_of = [&](int64_t bt, int64_t wtile, int64_t at_once, double tile, double block) {
         const int64_t tiles = used * ((share + bt - 1) / bt) * ((a->N + wtile - 1) / wtile);
         return (double)((tiles + at_once - 1) / at_once) * (tile + block * (double)kb);
     };
-    if (time_of(WideShape::BT, WideShape::WTILE, pairs, 2.0, 0.47) <
-        time_of(NarrowShape::BT, NarrowShape::WTILE, h->sm_count / split, 0.7, 0.3 / split))
+    if (time_of(WideShape::BT, WideShape::WTILE, pairs, 1.6, 0.455) <
+        time_of(NarrowShape::BT, NarrowShape::WTILE, h->sm_count / split, 0.5, 0.33 / split))
         return run<WideShape>(h, a, p, 1, wide < pairs ? wide : pairs, s);
     const int64_t units = h->sm_count / split;
     return run<NarrowShape>(h, a, p, split, narrow < units ? narrow : units, s);
