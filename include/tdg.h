@@ -763,8 +763,8 @@ TDG_API int tdg_moe_dispatch_combine_noalloc(tdg_symm *h, const tdg_moe_args *ar
  * count (ROWS and GATED; NULL: all): device int64, the rows in use; rows from
  * *count on are left alone.  A count outside [0, rows] is reported as
  * TDG_ERR_DEVICE (TDG_WHERE_CU) and cut to it.
- * Requirements: rows, E >= 0, rows * E < 2^31 (E 1 unless BLOCKS); K a multiple of 16, 16 <= K
- * < 2^30; strides in elements, at least the row's extent, x's a multiple of 8
+ * Requirements: rows, E >= 0, rows * E < 2^31 (E 1 unless BLOCKS), K a multiple of 16, 16 <= K
+ * < 2^30, fewer than 2^32 - 128 blocks of 1 x 128 (2^31 of 128 x 128); strides in elements, at least the row's extent, x's a multiple of 8
  * and the codes' of 16; scale_stride >= ceil(K/128) (BLOCKS: equal); x and
  * codes 16-byte aligned, scale 4-byte, count 8-byte; outputs overlapping no
  * input and not each other.  rows == 0 or E == 0 is a no-op.

@@ -47,7 +47,8 @@ __global__ void __launch_bounds__(mg::THREADS) moe_combine_grad_kernel(const __g
     __shared__ float gate[32], part[mg::THREADS / 32][32];
     griddep_launch_dependents();
     griddep_wait();
-    const int64_t tok = blockIdx.x, src = tok / m.T, t = tok - src * m.T;
+    const uint32_t src = blockIdx.x / (uint32_t)m.T;
+    const int64_t tok = blockIdx.x, t = blockIdx.x - src * (uint32_t)m.T;
     uint8_t *region = m.regions + (uint64_t)src * m.region_bytes;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if ((int)threadIdx.x < m.k) {
@@ -108,7 +109,8 @@ __global__ void __launch_bounds__(mg::THREADS) moe_dispatch_grad_kernel(const __
     __shared__ int64_t row[32];
     griddep_launch_dependents();
     griddep_wait();
-    const int64_t tok = blockIdx.x, src = tok / m.T, t = tok - src * m.T;
+    const uint32_t src = blockIdx.x / (uint32_t)m.T;
+    const int64_t tok = blockIdx.x, t = blockIdx.x - src * (uint32_t)m.T;
     if ((int)threadIdx.x < m.k)
         row[threadIdx.x] = moe_row(m, tok, threadIdx.x, true);
     __syncthreads();
