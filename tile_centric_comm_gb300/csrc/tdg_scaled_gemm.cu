@@ -138,16 +138,6 @@ __device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)
                  : "r"(taddr));
 }
 
-// 32 lanes x 16 columns: thread i has lane i's
-__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16])
-{
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
-                   "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-                 : "r"(taddr));
-}
-
 // acc += (lo, hi) * scale.  volatile: it stays behind the wait for its values.
 __device__ __forceinline__ void fma_pair(uint64_t &acc, uint32_t lo, uint32_t hi, uint64_t scale)
 {
@@ -578,51 +568,55 @@ __global__ void __launch_bounds__(WideShape::THREADS, 1)
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                     acc[c][i] = 0.f;
-            // a chunk of 16 columns is on its way while the one before is added,
-            // from one block to the next too (chunks of 32 do not fit the registers)
-            uint32_t r[2][16];
+            // Half of the warp's columns at a time, as many as the registers take: what the
+            // tensor cores wait for is the accumulator's release, so its loads come first
+            // and what can wait stands behind the release (chunks of 16 columns, each on
+            // its way while the one before is added, released it 160 cycles later: 374 us
+            // for 8192 x 7168 x 8192, 348 like this).
+            uint32_t r[2][32];
+            auto load = [&](int col) {
+                tmem_ld_32x32b_x32(at + buf * S::TCOLS + col, r[0]);
+                tmem_ld_32x32b_x32(at + buf * S::TCOLS + col + 32, r[1]);
+            };
             mbar_wait_suspended(tfull0 + buf * 8, bphase, tmo, failed);
             mbar_wait_suspended(sfull0 + chunk * 8, sphase, tmo, failed);
             tc_fence_after();
-            tmem_ld_32x32b_x16(at + buf * S::TCOLS, r[0]);
+            load(0);
             float s = scale_at[chunk * S::SK * S::SROW];
             for (int kb = 0, in_chunk = 0; kb < p.k_blocks && !failed; ++kb) {
                 const bool more = kb + 1 < p.k_blocks;
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 64; ++i)
+                    fma_one(acc[i >> 4][i & 15], r[i >> 5][i & 31], s);
+                load(64);
+                tmem_ld_wait();
+                tc_fence_before();
+                mbar_arrive_remote_relaxed(tempty0 + buf * 8, lane == 0);
+                buf ^= 1;
+                bphase ^= buf ^ 1;
+                // the next block's scale
+                if (++in_chunk == S::SK || !more) {
+                    in_chunk = 0;
+                    __syncwarp();
+                    mbar_arrive_relaxed(&ps->sempty[chunk], lane == 0);
+                    if (++chunk == S::SCH) {
+                        chunk = 0;
+                        sphase ^= 1u;
+                    }
+                    if (more)
+                        mbar_wait_suspended(sfull0 + chunk * 8, sphase, tmo, failed);
+                }
                 float next = 0.f;
+                if (more)
+                    next = scale_at[(chunk * S::SK + in_chunk) * S::SROW];
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    tmem_ld_wait();
-                    if (c < 7) {
-                        tmem_ld_32x32b_x16(at + buf * S::TCOLS + 16 * c + 16, r[(c + 1) & 1]);
-                    } else { // the accumulator is read: the tensor cores may write it again
-                        tc_fence_before();
-                        mbar_arrive_remote_relaxed(tempty0 + buf * 8, lane == 0);
-                        buf ^= 1;
-                        bphase ^= buf ^ 1;
-                        if (more) {
-                            mbar_wait_suspended(tfull0 + buf * 8, bphase, tmo, failed);
-                            tc_fence_after();
-                            tmem_ld_32x32b_x16(at + buf * S::TCOLS, r[0]);
-                        }
-                    }
-                    if (c == 1) { // the next block's scale
-                        if (++in_chunk == S::SK || !more) {
-                            in_chunk = 0;
-                            __syncwarp();
-                            mbar_arrive_relaxed(&ps->sempty[chunk], lane == 0);
-                            if (++chunk == S::SCH) {
-                                chunk = 0;
-                                sphase ^= 1u;
-                            }
-                            if (more)
-                                mbar_wait_suspended(sfull0 + chunk * 8, sphase, tmo, failed);
-                        }
-                        if (more)
-                            next = scale_at[(chunk * S::SK + in_chunk) * S::SROW];
-                    }
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        fma_one(acc[c][i], r[c & 1][i], s);
+                for (int i = 0; i < 64; ++i)
+                    fma_one(acc[4 + (i >> 4)][i & 15], r[i >> 5][i & 31], s);
+                if (more) {
+                    mbar_wait_suspended(tfull0 + buf * 8, bphase, tmo, failed);
+                    tc_fence_after();
+                    load(0);
                 }
                 s = next;
             }
@@ -1082,14 +1076,14 @@ extern "C" int tdg_scaled_gemm(tdg_symm *h, const tdg_scaled_gemm_args *a, void 
         split *= 2;
     // The kernel whose tiles take less time, with an expert's share the average one:
     // rounds of the grid, each of a time for the tile and one for every block of K
-    // (us; 7168 x 8192: 25 narrow and 34 wide for 128 rows, 50 and 34 for 192;
-    // 32 experts of 4096 x 2048: 48 and 66 for 64 rows each, 100 and 68 for 80)
+    // (us; 7168 x 8192: 25 narrow and 32 wide for 128 rows, 50 and 32 for 192;
+    // 32 experts of 4096 x 2048: 48 and 62 for 64 rows each, 100 and 64 for 80)
     const int64_t used = a->E < a->M ? a->E : a->M, share = (a->M + used - 1) / used, pairs = h->sm_count / 2;
     auto time_of = [&](int64_t bt, int64_t wtile, int64_t at_once, double tile, double block) {
         const int64_t tiles = used * ((share + bt - 1) / bt) * ((a->N + wtile - 1) / wtile);
         return (double)((tiles + at_once - 1) / at_once) * (tile + block * (double)kb);
     };
-    if (time_of(WideShape::BT, WideShape::WTILE, pairs, 1.6, 0.455) <
+    if (time_of(WideShape::BT, WideShape::WTILE, pairs, 1.6, 0.415) <
         time_of(NarrowShape::BT, NarrowShape::WTILE, h->sm_count / split, 0.5, 0.33 / split))
         return run<WideShape>(h, a, p, 1, wide < pairs ? wide : pairs, s);
     const int64_t units = h->sm_count / split;
