@@ -806,7 +806,8 @@ TDG_API int tdg_quantise(tdg_symm *h, const tdg_quantise_args *args, void *strea
  * NaN there alone).
  * Offsets out of order, negative or past M are reported as TDG_ERR_DEVICE
  * (TDG_WHERE_CU, index e) and the expert is left out (where others then cover
- * a row twice, that row is undefined).
+ * a row twice, that row is undefined, and where together they cover more than
+ * M rows, some of theirs may be left out).
  * Requirements: 0 <= M < 2^31; N a multiple of 8, 8 <= N < 2^24; K a multiple of 16, 16 <= K
  * < 2^24; 1 <= E <= 4096, E * N < 2^31, and E = 1 without base; a_stride (a multiple of 16) and
  * out_stride (of 8; of 4 with out_f32) at least the row's extent, all strides below 2^31; a, b and out

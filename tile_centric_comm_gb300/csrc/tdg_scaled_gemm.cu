@@ -62,7 +62,7 @@ struct NarrowShape {
     static constexpr int BT = 64;                    // rows of a in a tile, at most
     static constexpr int WTILE = sg::ROWS;
     static constexpr int STEP = 16;                  // of an instruction's columns, and rows of a TMA box
-    static constexpr int BPS = 2;                    // two blocks a wait: every role's time is its waits'
+    static constexpr int BPS = 2;                    // two blocks a wait, which costs every role 100 cycles
     static constexpr int BLOCK_BYTES = sg::A_BYTES + BT * sg::BK, STAGES = 4, STAGE_BYTES = BPS * BLOCK_BYTES;
     static constexpr int TBUF = 4, TCOLS = BT;
     static constexpr int EPIW = 4, THREADS = 128 + 32 * EPIW;
@@ -395,8 +395,8 @@ __device__ __forceinline__ void scaled_issue(const ScaledParams &p, ScaledSmem *
                     umma_commit_pair_mask(&ps->empty[stage], 3);
                     umma_commit_pair_mask(&ps->tfull[buf], 3);
                 } else {
-                    umma_commit(&ps->tfull[buf]);
                     umma_commit(&ps->empty[stage]);
+                    umma_commit(&ps->tfull[buf]); // the last arrival of a CTA is one that is waited for
                 }
             }
             __syncwarp();

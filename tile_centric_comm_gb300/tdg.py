@@ -828,13 +828,13 @@ def quantise_blocks(symm: Symm, x, codes, scale, stream=None):
     if _torch is None:
         _attn()
     dev = symm.device
+    xp, cp = _flat(x, "x", _t_bf16, 0, dev), _flat(codes, "codes", _t_e4m3, 0, dev)
+    sp = _flat(scale, "scale", _t_f32, 0, dev)
     if x.dim() not in (2, 3):
         raise ValueError(f"x: expected (N, K) or (E, N, K), got {tuple(x.shape)}")
     *E, N, K = x.shape
-    if tuple(codes.shape) != tuple(x.shape) or tuple(scale.shape) != (*E, _blocks(N), _blocks(K)):
+    if codes.shape != x.shape or tuple(scale.shape) != (*E, _blocks(N), _blocks(K)):
         raise ValueError(f"x {tuple(x.shape)}, codes {tuple(codes.shape)} and scale {tuple(scale.shape)} do not fit together")
-    xp, cp = _flat(x, "x", _t_bf16, 0, dev), _flat(codes, "codes", _t_e4m3, 0, dev)
-    sp = _flat(scale, "scale", _t_f32, 0, dev)
     a = _pack_quantise(QUANT_BLOCKS, N, K, E[0] if E else 1, xp, K, cp, K, sp, _blocks(K), 0)
     rc = _tdg_quantise(symm.h, a, _raw_stream(stream, dev))
     if rc:
@@ -852,8 +852,9 @@ def scaled_gemm(symm: Symm, a, a_scale, b, b_scale, out, base=None, stream=None)
     dev = symm.device
     ap, as_, M, K = _matrix(a, "a", _t_e4m3, dev)
     sp, ss, *slike = _matrix(a_scale, "a_scale", _t_f32, dev)
-    f32 = out.dtype is _t_f32
+    f32 = getattr(out, "dtype", None) is _t_f32
     op, os_, *olike = _matrix(out, "out", _t_f32 if f32 else _t_bf16, dev)
+    bp, bsp = _flat(b, "b", _t_e4m3, 0, dev), _flat(b_scale, "b_scale", _t_f32, 0, dev)
     bshape = tuple(b.shape)
     E = 1
     if base is not None:
@@ -864,7 +865,6 @@ def scaled_gemm(symm: Symm, a, a_scale, b, b_scale, out, base=None, stream=None)
             tuple(b_scale.shape) != (*lead, _blocks(N), _blocks(K)):
         raise ValueError(f"a {tuple(a.shape)}, a_scale {tuple(a_scale.shape)}, b {bshape}, b_scale "
                          f"{tuple(b_scale.shape)} and out {tuple(out.shape)} do not fit together")
-    bp, bsp = _flat(b, "b", _t_e4m3, 0, dev), _flat(b_scale, "b_scale", _t_f32, 0, dev)
     np_ = 0 if base is None else _flat(base, "base", _t_i64, E + 1, dev)
     args = _pack_scaled(M, N, K, E, ap, as_, sp, ss, bp, bsp, op, os_, 1 if f32 else 0, np_)
     rc = _tdg_scaled_gemm(symm.h, args, _raw_stream(stream, dev))
