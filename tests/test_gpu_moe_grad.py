@@ -173,6 +173,23 @@ def test_a_layer_against_autograd():
         assert float((got - want).norm() / want.norm()) <= 4 * 2.0 ** -8
 
 
+def test_far_rows():
+    """Receive rows whose offsets pass 32 bits."""
+    W, T, H, k = 2, 16000, 8192, 10
+    c = Case(W, T, H, 16, k, seed=3)
+    c.run()
+    assert c.symm.status()["code"] == 0
+    at = c.slot.view(W, T, k)
+    for r, t in ((0, 0), (0, T - 1), (1, 777), (1, T - 1)):
+        dout, gate, rows = c.dout(r)[t].double(), c.gate(r)[t].double(), at[r, t]
+        assert torch.equal(c.dy[rows], (gate[:, None] * dout).float().to(torch.bfloat16))
+        parts = c.y[rows].double() * dout
+        assert bool(((c.dgate(r)[t].double() - parts.sum(-1)).abs() <= 2.0 ** -23 * (H + 8) * parts.abs().sum(-1)).all())
+        parts = c.drecv[rows].double()
+        tol = 2.0 ** -8 * parts.sum(0).abs() + 2.0 ** -23 * k * parts.abs().sum(0)
+        assert bool(((c.dx(r)[t].double() - parts.sum(0)).abs() <= tol).all())
+
+
 def test_replayed_with_other_data():
     c = Case(2, 31, 520, 8, 2, seed=7)
     side = torch.cuda.Stream()

@@ -160,6 +160,20 @@ def test_a_count_out_of_range_is_reported(symm, n, used):
     assert bool((scale[used:] == -1).all()) and bool((scale[:used] > 0).all())
 
 
+def test_far_rows(symm):
+    """Offsets past 32 bits: rows of 5 GB."""
+    n, K = 300001, 8192
+    x = torch.empty(n, K, dtype=torch.bfloat16, device="cuda").normal_(generator=generator(4))
+    codes, scale = torch.empty(n, K, dtype=E4M3, device="cuda"), torch.empty(n, blocks(K), device="cuda")
+    tdg.quantise_rows(symm, x, codes, scale)
+    for lo in (0, 131071, 262143, n - 50):
+        want, s = quantised(x[lo:lo + 50])
+        assert torch.equal(scale[lo:lo + 50], s) and torch.equal(codes[lo:lo + 50].view(torch.uint8), want)
+    tdg.quantise_blocks(symm, x[None], codes[None], scale[None, :blocks(n)].contiguous())
+    want, _ = quantised(x[262144:262272], rows=128)
+    assert torch.equal(codes[262144:262272].view(torch.uint8), want)
+
+
 def test_captured_and_replayed_on_another_stream(symm):
     x = _rows(generator(6), 64, 256)
     codes, scale = _outputs(64, 256)

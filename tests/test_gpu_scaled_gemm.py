@@ -219,6 +219,23 @@ def test_far_offsets(symm):
             check_product(c.out[lo:hi, n:n + 16], want, mag, K)
 
 
+@pytest.mark.parametrize("M,N,K", [(600000, 4096, 256), (3, 1 << 20, 48)])
+def test_far_rows_and_columns(symm, M, N, K):
+    """Outputs (and rows of a) whose offsets pass 32 bits; very many columns."""
+    g = generator(2)
+    a = torch.empty(M, K, dtype=E4M3, device="cuda")
+    a.view(torch.uint8).random_(0, 0x70, generator=g)
+    b, sa, sb = random_codes(g, N, K), random_scales(g, M, blocks(K)), random_scales(g, blocks(N), blocks(K))
+    out = torch.full((M, N), float("nan"), dtype=torch.bfloat16, device="cuda")     # (of 2 G finite outputs some are MARK)
+    tdg.scaled_gemm(symm, a, sa, b, sb, out)
+    assert symm.status()["code"] == 0
+    for lo in (0, M // 2, max(0, M - 40)):
+        for n in (0, N // 2 // 128 * 128, N - 128):
+            want, mag = product(a[lo:lo + 40], sa[lo:lo + 40], b[n:n + 128], sb[n // 128:n // 128 + 1])
+            check_product(out[lo:lo + 40, n:n + 128], want, mag, K)
+    assert not bool(out[:, ::1031].isnan().any())
+
+
 def test_refusals(symm):
     c = Case(24, 136, 256, f32=False)
     a, sa, b, sb, out = c.a, c.a_scale, c.b, c.b_scale, c.out.contiguous()
