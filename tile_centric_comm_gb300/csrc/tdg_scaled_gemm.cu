@@ -1069,11 +1069,11 @@ extern "C" int tdg_scaled_gemm(tdg_symm *h, const tdg_scaled_gemm_args *a, void 
     p.base = a->base;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     // few tiles: K divided over the CTAs of a cluster, two blocks of it each at
-    // least (clusters of 8 start 5 us later: 2048 x 2048, one row, 6.6 us by 4
-    // CTAs and 11.8 by 8)
-    int split = 1;
-    while (split < 4 && narrow * split * 2 <= h->sm_count && kb >= 4 * split)
-        split *= 2;
+    // least, as long as all run at once (clusters of 6 and 8 start 5 us later: 2048 x
+    // 2048, one row, 5.4 us by 4 CTAs and 11.8 by 8; 3200 x 5120 6.8 by 4 and 12.2 by 6)
+    int64_t most = h->sm_count / narrow < kb / 2 ? h->sm_count / narrow : kb / 2;
+    most = most < 4 ? most : 4;
+    const int split = most < 1 ? 1 : (int)most;
     // The kernel whose tiles take less time, with an expert's share the average one:
     // rounds of the grid, each of a time for the tile and one for every block of K
     // (us; 7168 x 8192: 25 narrow and 32 wide for 128 rows, 50 and 32 for 192;
