@@ -42,16 +42,16 @@ struct WideShape {
     static constexpr int BT = 256;                   // rows of a in a tile, over the pair
     static constexpr int WTILE = 256;                // weight rows of a tile
     static constexpr int BPS = 1;                    // blocks of a ring stage
-    static constexpr int BLOCK_BYTES = 2 * sg::A_BYTES, STAGES = 5, STAGE_BYTES = BLOCK_BYTES;
+    static constexpr int BLOCK_BYTES = 2 * sg::A_BYTES, STAGES = 4, STAGE_BYTES = BLOCK_BYTES;
     static constexpr int TBUF = 2, TCOLS = 256;      // accumulators in TMEM
     static constexpr int EPIW = 8, THREADS = 128 + 32 * EPIW;
     static constexpr int REGS_OTHER = 72, REGS_EPI = 216; // registers of a thread
     static_assert(128 * REGS_OTHER + 32 * EPIW * REGS_EPI <= THREADS * (65536 / THREADS / 8 * 8), "registers of the launch");
     static constexpr int SK = 4, SCH = 3;            // blocks whose scales are loaded together, such chunks in the ring
     static constexpr int SROW = 2 * sg::ROWS + 8;    // floats of a block's scales: for each half of the columns, and a pad
-    static constexpr int STG = 32 * 128;             // staged rows of an epilogue warp: 128 bytes of each
+    static constexpr int STG = 32 * 128;             // staged rows of an epilogue warp: 128 bytes of each, twice
     static constexpr int OFF_STG = STAGES * STAGE_BYTES; // (swizzled by address: 1024-byte aligned)
-    static constexpr int OFF_SCALE = OFF_STG + EPIW * STG;
+    static constexpr int OFF_SCALE = OFF_STG + 2 * EPIW * STG;
     static constexpr int OFF_BAR = OFF_SCALE + SCH * SK * SROW * 4;
     static constexpr int OFF_PRE = OFF_BAR + sg::BAR_BYTES; // tiles before each expert
     static constexpr int SMEM = OFF_PRE + 1024;      // + 4 (E + 1); + alignment slack
@@ -559,7 +559,8 @@ __global__ void __launch_bounds__(WideShape::THREADS, 1)
         int chunk = 0;
         uint32_t buf = 0, bphase = 0, sphase = 0, failed = 0;
         bool ok = true;
-        uint8_t *stg = smem + S::OFF_STG + (warp - 4) * S::STG;
+        uint8_t *const stg0 = smem + S::OFF_STG + 2 * (warp - 4) * S::STG;
+        int side = 0; // of the two staging buffers
         uint32_t nth = 0;
         for (uint32_t it = unit; it < items && ok; it += units, ++nth) {
             float acc[8][16];
@@ -636,8 +637,10 @@ __global__ void __launch_bounds__(WideShape::THREADS, 1)
             const int n = ps->tile[nth & 3].n0 + cg * 128, piece = lane & 7;
             const bool whole = row + 32 <= end || end == p.M; // (the map ends at row M)
             auto pass = [&](int col, int per16, auto words) { // columns from col on, per16 of them in 16 bytes
+                uint8_t *stg = stg0 + side * S::STG;
+                side ^= 1;
                 if (lane == 0)
-                    bulk_wait_read<0>();
+                    bulk_wait_read<1>(); // the copy from this buffer, two passes ago
                 __syncwarp();
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
@@ -645,13 +648,13 @@ __global__ void __launch_bounds__(WideShape::THREADS, 1)
                 if (whole)
                     fence_proxy_async_smem();
                 __syncwarp();
-                if (whole) {
-                    if (lane == 0 && row < end && n + col < p.N) {
+                if (lane == 0) {
+                    if (whole && row < end && n + col < p.N)
                         tma_store_2d(&map_out, stg, n + col, (int)row);
-                        bulk_commit();
-                    }
-                    return;
+                    bulk_commit(); // one group a pass, if an empty one: the wait above counts them
                 }
+                if (whole)
+                    return;
                 const int left = p.N - n - col - piece * per16;
                 uint8_t *out = static_cast<uint8_t *>(p.out) + ((row + (lane >> 3)) * p.out_stride + n + col) * (16 / per16) + piece * 16;
                 const int64_t step = 4 * p.out_stride * (16 / per16);
