@@ -61,6 +61,14 @@ def test_one_matrix(symm, M, N, K, f32):
     c.check(symm)
 
 
+@pytest.mark.parametrize("tiles", [36, 37, 46, 47, 76, 77])
+@pytest.mark.parametrize("K", [512, 1040])
+def test_weight_tiles_around_the_clusters_that_run_at_once(symm, tiles, K):
+    c = Case(19, 128 * tiles - 8, K)
+    c.run(symm)
+    c.check(symm)
+
+
 @pytest.mark.parametrize("M,N,K", [(5, 72, 144), (40, 256, 2048), (300, 264, 272)])
 @pytest.mark.parametrize("f32", [False, True])
 def test_strided_rows(symm, M, N, K, f32):

@@ -22,6 +22,7 @@
 //   warp 1      MMA issuer: four tcgen05.mma.kind::f8f6f4 (K = 32) a block
 //   warps 2, 3  scales: sa * sw of the tile's rows, some blocks at a time
 //   warps 4..   epilogue
+#include <atomic>
 #include <type_traits>
 
 #include "tdg_scaled.cuh"
@@ -1021,6 +1022,24 @@ template <class S> int run(tdg_symm *h, const tdg_scaled_gemm_args *a, ScaledPar
                     "scaled gemm launch");
 }
 
+// The clusters of cl CTAs of the narrow kernel that run at once; a property of the
+// device, asked once for each (the query takes microseconds).
+int narrow_clusters(int device, int cl)
+{
+    static std::atomic<int> known[64][5];
+    const bool keep = device >= 0 && device < 64;
+    int n = keep ? known[device][cl].load(std::memory_order_relaxed) : 0;
+    if (n == 0) {
+        const void *fn = reinterpret_cast<const void *>(&scaled_narrow_kernel);
+        const int smem = NarrowShape::SMEM + 4 * (sg::MAX_E + 1);
+        if (set_smem(fn, smem) == cudaSuccess)
+            n = max_clusters(fn, NarrowShape::THREADS, smem, cl);
+        if (keep)
+            known[device][cl].store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
+
 } // namespace
 
 extern "C" int tdg_scaled_gemm(tdg_symm *h, const tdg_scaled_gemm_args *a, void *stream)
@@ -1071,12 +1090,17 @@ extern "C" int tdg_scaled_gemm(tdg_symm *h, const tdg_scaled_gemm_args *a, void 
     p.out = a->out;
     p.base = a->base;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    // few tiles: K divided over the CTAs of a cluster, two blocks of it each at
-    // least, as long as all run at once (clusters of 6 and 8 start 5 us later: 2048 x
-    // 2048, one row, 5.4 us by 4 CTAs and 11.8 by 8; 3200 x 5120 6.8 by 4 and 12.2 by 6)
-    int64_t most = h->sm_count / narrow < kb / 2 ? h->sm_count / narrow : kb / 2;
-    most = most < 4 ? most : 4;
-    const int split = most < 1 ? 1 : (int)most;
+    // Few tiles: K divided over the CTAs of a cluster, two blocks of it each at least,
+    // as long as all clusters run at once.  How many do is less than the SMs hold (46 of
+    // 3, 36 of 4), since a cluster stays in its part of the chip: 38 weight tiles of 2048,
+    // one row, 6.1 us by clusters of 3 and 10.4 by clusters of 4.  (Clusters of 6 and 8
+    // start 5 us later: 2048 x 2048, one row, 5.4 by 4 CTAs and 11.8 by 8.)
+    int split = 4, at_once = 0;
+    for (; split > 1; --split)
+        if (kb / 2 >= split && narrow <= (at_once = narrow_clusters(h->device, split)))
+            break;
+    if (split == 1)
+        at_once = h->sm_count;
     // The kernel whose tiles take less time, with an expert's share the average one:
     // rounds of the grid, each of a time for the tile and one for every block of K
     // (us; 7168 x 8192: 25 narrow and 32 wide for 128 rows, 50 and 32 for 192;
@@ -1087,8 +1111,7 @@ extern "C" int tdg_scaled_gemm(tdg_symm *h, const tdg_scaled_gemm_args *a, void 
         return (double)((tiles + at_once - 1) / at_once) * (tile + block * (double)kb);
     };
     if (time_of(WideShape::BT, WideShape::WTILE, pairs, 1.6, 0.415) <
-        time_of(NarrowShape::BT, NarrowShape::WTILE, h->sm_count / split, 0.5, 0.33 / split))
+        time_of(NarrowShape::BT, NarrowShape::WTILE, at_once, 0.5, 0.33 / split))
         return run<WideShape>(h, a, p, 1, wide < pairs ? wide : pairs, s);
-    const int64_t units = h->sm_count / split;
-    return run<NarrowShape>(h, a, p, split, narrow < units ? narrow : units, s);
+    return run<NarrowShape>(h, a, p, split, narrow < at_once ? narrow : at_once, s);
 }
