@@ -95,6 +95,40 @@ def test_experts(symm, name, N, K, first, spare, f32):
     c.check(symm, ends)
 
 
+# shapes that two pairs of CTAs share a tile of: 21 blocks of K, rows and columns that end inside a tile
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("M,N,lead", [(250, 5112, 0), (100, 8072, 1), (500, 4392, 1), (129, 9216, 0)])
+def test_tiles_with_halves_of_k(symm, M, N, lead, f32):
+    c = Case(M, N, 2576, f32=f32, lead=lead)
+    c.run(symm)
+    c.check(symm)
+    before = c.out.clone()
+    c.run(symm)
+    assert torch.equal(c.out, before)
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("rows", [[200, 0, 256], [0, 456, 0], [455, 0, 1], [70, 130, 256], [0, 0, 7]])
+def test_experts_with_halves_of_k(symm, rows, f32):
+    ends = [0]
+    for n in rows:
+        ends.append(ends[-1] + n)
+    c = Case(456, 2304, 2576, E=3, f32=f32)
+    c.run(symm, base=torch.tensor(ends, dtype=torch.int64, device="cuda"))
+    c.check(symm, ends)
+
+
+def test_offsets_that_go_back_with_halves_of_k(symm):
+    """More tiles than the rows can have: reported, the call ends, and the next one is right."""
+    c = Case(1000, 768, 5136, E=8)
+    c.run(symm, base=torch.tensor([0, 1000] * 4 + [0], dtype=torch.int64, device="cuda"))
+    torch.cuda.synchronize()
+    assert symm.status()["code"] != 0
+    ends = [0, 100, 300, 400, 500, 600, 800, 801, 1000]
+    c.run(symm, base=torch.tensor(ends, dtype=torch.int64, device="cuda"))
+    c.check(symm, ends)
+
+
 def test_most_experts(symm):
     ends = [0]
     for e in range(4096):

@@ -11,6 +11,8 @@
 //
 //   wide    256 rows of a x 256 weight rows by a pair of CTAs.  Rows of a are
 //           TMEM's lanes, so a thread of the epilogue needs one scale a block.
+//           For few tiles two pairs, a cluster of four, halve K and exchange halves
+//           of their sums.
 //   narrow  128 weight rows x up to 64 rows of a.  The weights are the lanes and
 //           the rows of a the columns, which an instruction takes in steps of 16:
 //           an expert with few rows costs what it has, and streaming the weights
@@ -361,10 +363,10 @@ __device__ __forceinline__ bool elected()
 // in all lanes and stays in uniform registers, where the instruction takes its
 // operands from (issued by a loop of one lane, four MMAs and two commits took
 // 440 cycles of the 512 that the tensor cores need for them).
-// columns(tile): those of the instruction.
+// columns(tile): those of the instruction; pair: its CTAs in the cluster, as a mask.
 template <class S, class F>
 __device__ __forceinline__ void scaled_issue(const ScaledParams &p, ScaledSmem *ps, uint32_t sbase, uint32_t tmem, const uint32_t *pre, uint32_t items,
-                                             uint32_t unit, uint32_t units, int kb0, int kb1, F columns)
+                                             uint32_t unit, uint32_t units, int kb0, int kb1, uint16_t pair, F columns)
 {
     const uint64_t tmo = p.timeout_ns;
     // a ring slot's offset never carries out of the descriptor's address field
@@ -393,8 +395,8 @@ __device__ __forceinline__ void scaled_issue(const ScaledParams &p, ScaledSmem *
                             umma_e4m3<S::PAIR>(d + j * S::TCOLS, aj + 2 * k, bj + 2 * k, idesc, k ? 1u : 0u);
                     }
                 if (S::PAIR) {
-                    umma_commit_pair_mask(&ps->empty[stage], 3);
-                    umma_commit_pair_mask(&ps->tfull[buf], 3);
+                    umma_commit_pair_mask(&ps->empty[stage], pair);
+                    umma_commit_pair_mask(&ps->tfull[buf], pair);
                 } else {
                     umma_commit(&ps->empty[stage]);
                     umma_commit(&ps->tfull[buf]); // the last arrival of a CTA is one that is waited for
@@ -420,7 +422,7 @@ __device__ __forceinline__ void scaled_issue(const ScaledParams &p, ScaledSmem *
             // every MMA issued has finished before TMEM is freed (commits tell of
             // the executing thread's own: the lane elected here is the one above)
             if (S::PAIR)
-                umma_commit_pair_mask(&ps->drain, 3);
+                umma_commit_pair_mask(&ps->drain, pair);
             else
                 umma_commit(&ps->drain);
             (void)mbar_wait(&ps->drain, 0, tmo);
@@ -457,24 +459,27 @@ __global__ void __launch_bounds__(WideShape::THREADS, 1)
     uint32_t *pre = reinterpret_cast<uint32_t *>(smem + S::OFF_PRE);
     float *scales = reinterpret_cast<float *>(smem + S::OFF_SCALE);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int half = (int)cluster_ctarank();
-    const uint32_t unit = blockIdx.x / 2, units = gridDim.x / 2;
+    // the pair's place in the cluster is its part of K, the CTA's place in the pair its half of the tile
+    const int rank = (int)cluster_ctarank(), half = rank & 1, part = rank >> 1, leader = rank & ~1;
+    const uint32_t unit = blockIdx.x / 2 / p.split, units = gridDim.x / 2 / p.split;
+    const int kb0 = part * p.k_blocks / p.split, kb1 = (part + 1) * p.k_blocks / p.split;
     const uint64_t tmo = p.timeout_ns;
     scaled_begin<S>(p, ps, pre);
-    const uint32_t tmem = ps->tmem_base, items = pre[p.E];
+    const uint32_t tmem = ps->tmem_base;
+    const uint32_t items = p.split > 1 ? min(pre[p.E], units) : pre[p.E]; // with K divided a cluster has one tile
     // an instruction's columns: the weight rows of the tile in steps of 32, each CTA holding half of them
     auto columns = [&](const ScaledTile &t) { return min(S::WTILE, (p.N - t.n0 + 31) / 32 * 32); };
 
     if (warp == 0) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::REGS_OTHER));
         if (lane == 0) {
-            const uint32_t full0 = mapa_shared(smem_u32(&ps->full[0]), 0);
+            const uint32_t full0 = mapa_shared(smem_u32(&ps->full[0]), leader);
             int stage = 0;
             uint32_t phase = 0, issued = 0;
             for (uint32_t it = unit; it < items && !ps->abort; it += units) {
                 const ScaledTile t = scaled_tile<S>(p, pre, it);
                 const int row = (int)((uint32_t)t.tok0 + half * sg::ROWS), wrow = t.n0 + half * (columns(t) / 2);
-                for (int kb = 0; kb < p.k_blocks; ++kb) {
+                for (int kb = kb0; kb < kb1; ++kb) {
                     if (!mbar_wait_suspended(&ps->empty[stage], phase ^ 1u, tmo)) {
                         report_fault(p.status, TDG_ERR_TIMEOUT, TDG_WHERE_PIPE, 0, p.epoch);
                         ps->abort = 1;
@@ -498,7 +503,7 @@ __global__ void __launch_bounds__(WideShape::THREADS, 1)
     } else if (warp == 1) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::REGS_OTHER));
         if (half == 0)
-            scaled_issue<S>(p, ps, smem_u32(smem), tmem, pre, items, unit, units, 0, p.k_blocks, columns);
+            scaled_issue<S>(p, ps, smem_u32(smem), tmem, pre, items, unit, units, kb0, kb1, (uint16_t)(3 << leader), columns);
     } else if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::REGS_OTHER));
         // scales: each warp half of the CTA's rows, 32 / SK rows x SK blocks a step, for both column halves
@@ -515,8 +520,8 @@ __global__ void __launch_bounds__(WideShape::THREADS, 1)
             const int64_t first = t.tok0 + half * sg::ROWS;
             const int rows = (int)max((int64_t)0, min((int64_t)sg::ROWS, t.end - first));
             const float *sa = p.a_scale + first * p.a_scale_stride;
-            for (int kb = 0; kb < p.k_blocks; kb += S::SK) {
-                const bool in = kb + j < p.k_blocks;
+            for (int kb = kb0; kb < kb1; kb += S::SK) {
+                const bool in = kb + j < kb1;
                 const float w0 = in ? sw[kb + j] : 0.f, w1 = in ? sw[next + kb + j] : 0.f;
                 float v[64 / RS];
 #pragma unroll
@@ -530,7 +535,7 @@ __global__ void __launch_bounds__(WideShape::THREADS, 1)
                     ps->abort = 1;
                     break;
                 }
-                if (kb == 0 && warp == 2 && lane == 0) {
+                if (kb == kb0 && warp == 2 && lane == 0) {
                     ps->tile[nth & 3].row = first;
                     ps->tile[nth & 3].end = t.end;
                     ps->tile[nth & 3].n0 = t.n0;
@@ -553,7 +558,7 @@ __global__ void __launch_bounds__(WideShape::THREADS, 1)
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::REGS_EPI));
         const int q = warp & 3, cg = (warp - 4) >> 2; // lanes of TMEM, half of the columns
-        const uint32_t tempty0 = mapa_shared(smem_u32(&ps->tempty[0]), 0);
+        const uint32_t tempty0 = mapa_shared(smem_u32(&ps->tempty[0]), leader);
         const uint32_t at = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(cg * 128);
         const uint32_t tfull0 = smem_u32(&ps->tfull[0]), sfull0 = smem_u32(&ps->sfull[0]);
         const float *scale_at = scales + cg * sg::ROWS + q * 32 + lane;
@@ -585,8 +590,8 @@ __global__ void __launch_bounds__(WideShape::THREADS, 1)
             tc_fence_after();
             load(0);
             float s = scale_at[chunk * S::SK * S::SROW];
-            for (int kb = 0, in_chunk = 0; kb < p.k_blocks && !failed; ++kb) {
-                const bool more = kb + 1 < p.k_blocks;
+            for (int kb = kb0, in_chunk = 0; kb < kb1 && !failed; ++kb) {
+                const bool more = kb + 1 < kb1;
                 tmem_ld_wait();
 #pragma unroll
                 for (int i = 0; i < 64; ++i)
@@ -628,14 +633,38 @@ __global__ void __launch_bounds__(WideShape::THREADS, 1)
                 if (lane == 0)
                     report_fault(p.status, TDG_ERR_TIMEOUT, TDG_WHERE_PIPE, 3, p.epoch);
                 ps->abort = 1;
+                if (p.split > 1)
+                    cluster_sync();
                 break;
+            }
+            // Where two pairs share the tile's K: each leaves the half of its columns that
+            // the other stores in its ring, whose loads the last products have used up.
+            // (a + b is b + a: the sums do not depend on who adds.)
+            if (p.split > 1) {
+                float4 *give = reinterpret_cast<float4 *>(smem) + (threadIdx.x - 128);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float *lo = &acc[i >> 2][(i & 3) * 4], *hi = &acc[4 + (i >> 2)][(i & 3) * 4];
+                    give[i * 32 * S::EPIW] = part ? make_float4(lo[0], lo[1], lo[2], lo[3]) : make_float4(hi[0], hi[1], hi[2], hi[3]);
+                }
+                cluster_sync();
+                const uint32_t take = mapa_shared(smem_u32(give), (uint32_t)(rank ^ 2));
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float4 v = ld_cluster_f4(take + i * 32 * S::EPIW * 16);
+                    float *lo = &acc[i >> 2][(i & 3) * 4], *hi = &acc[4 + (i >> 2)][(i & 3) * 4];
+                    lo[0] = (part ? hi[0] : lo[0]) + v.x;
+                    lo[1] = (part ? hi[1] : lo[1]) + v.y;
+                    lo[2] = (part ? hi[2] : lo[2]) + v.z;
+                    lo[3] = (part ? hi[3] : lo[3]) + v.w;
+                }
             }
             // 128 bytes of each of the warp's 32 rows at a time through shared memory, from
             // where one TMA store takes them while the next tile is multiplied (an SM writes
             // about 22 bytes a cycle, 3000 cycles for a tile).  Rows that end inside the
             // tile are stored by the lanes.
             const int64_t row = ps->tile[nth & 3].row + q * 32, end = ps->tile[nth & 3].end;
-            const int n = ps->tile[nth & 3].n0 + cg * 128, piece = lane & 7;
+            const int n = ps->tile[nth & 3].n0 + cg * 128 + part * 64, piece = lane & 7;
             const bool whole = row + 32 <= end || end == p.M; // (the map ends at row M)
             auto pass = [&](int col, int per16, auto words) { // columns from col on, per16 of them in 16 bytes
                 uint8_t *stg = stg0 + side * S::STG;
@@ -669,23 +698,31 @@ __global__ void __launch_bounds__(WideShape::THREADS, 1)
             };
             if (p.out_f32) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
+                for (int c = 0; c < 4; ++c) {
+                    if (c == 2 && p.split > 1)
+                        break;
                     pass(c * 32, 4, [&](int j) {
                         const float *a = &acc[2 * c + (j >> 2)][(j & 3) * 4];
                         return make_uint4(__float_as_uint(a[0]), __float_as_uint(a[1]), __float_as_uint(a[2]), __float_as_uint(a[3]));
                     });
+                }
             } else {
 #pragma unroll
-                for (int c = 0; c < 2; ++c)
+                for (int c = 0; c < 2; ++c) {
+                    if (c == 1 && p.split > 1)
+                        break;
                     pass(c * 64, 8, [&](int j) {
                         const float *a = &acc[4 * c + (j >> 1)][(j & 1) * 8];
                         return make_uint4(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(a[4], a[5]), pack_bf16x2(a[6], a[7]));
                     });
+                }
             }
         }
         if (lane == 0)
             bulk_wait<0>();
     }
+    if (p.split > 1 && (warp < 4 || unit >= items))
+        cluster_sync(); // the one of the epilogue's exchange
     scaled_drain<S>(p, ps, half == 0);
     cluster_sync(); // no CTA leaves while the other may still touch it
     if (warp == 1) {
@@ -754,7 +791,7 @@ __global__ void __launch_bounds__(NarrowShape::THREADS, 1)
         }
         __syncwarp();
     } else if (warp == 1) {
-        scaled_issue<S>(p, ps, smem_u32(smem), tmem, pre, items, unit, units, kb0, kb1, [](const ScaledTile &t) { return t.width; });
+        scaled_issue<S>(p, ps, smem_u32(smem), tmem, pre, items, unit, units, kb0, kb1, 0, [](const ScaledTile &t) { return t.width; });
     } else if (warp < 4) {
         // scales: 8 rows of a x SK blocks a step, each warp every other step
         const int j = lane % S::SK, r0 = lane / S::SK + (warp - 2) * 8;
@@ -1000,6 +1037,28 @@ bool map_codes(CUtensorMap *m, const void *base, int64_t inner, int64_t rows, in
     return encode_tiled(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, flat ? 2 : 3, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+template <class S> const void *kernel_of()
+{
+    return S::PAIR ? reinterpret_cast<const void *>(&scaled_wide_kernel) : reinterpret_cast<const void *>(&scaled_narrow_kernel);
+}
+
+// The clusters of cl CTAs of a kernel that run at once; a property of the device,
+// asked once for each (the query takes microseconds).
+template <class S> int clusters_at_once(int device, int cl)
+{
+    static std::atomic<int> known[64][5];
+    const bool keep = device >= 0 && device < 64;
+    int n = keep ? known[device][cl].load(std::memory_order_relaxed) : 0;
+    if (n == 0) {
+        const int smem = S::SMEM + 4 * (sg::MAX_E + 1);
+        if (set_smem(kernel_of<S>(), smem) == cudaSuccess)
+            n = max_clusters(kernel_of<S>(), S::THREADS, smem, cl);
+        if (keep)
+            known[device][cl].store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
+
 template <class S> int run(tdg_symm *h, const tdg_scaled_gemm_args *a, ScaledParams &p, int split, int64_t units, cudaStream_t s)
 {
     CUtensorMap map_w, map_a, map_out;
@@ -1009,35 +1068,17 @@ template <class S> int run(tdg_symm *h, const tdg_scaled_gemm_args *a, ScaledPar
     if (S::PAIR && !(a->out_f32 ? map_f32_2d(&map_out, a->out, a->N, a->M, a->out_stride * 4, 32, 32)
                                 : map_bf16_2d(&map_out, a->out, a->N, a->M, a->out_stride * 2, 64, 32)))
         return TDG_ERR_CUDA;
-    const void *fn = S::PAIR ? reinterpret_cast<const void *>(&scaled_wide_kernel) : reinterpret_cast<const void *>(&scaled_narrow_kernel);
+    const void *fn = kernel_of<S>();
     const int smem = S::SMEM + 4 * (sg::MAX_E + 1);
     cudaError_t e = set_smem(fn, smem);
     if (e != cudaSuccess)
         return cuda_err(e, "scaled gemm smem");
     p.split = split;
     p.n_tiles = (int)((a->N + S::WTILE - 1) / S::WTILE);
-    const int cl = S::PAIR ? 2 : split;
+    const int cl = S::PAIR ? 2 * split : split;
     void *args[] = {&p, &map_w, &map_a, &map_out}; // (the narrow kernel takes three)
     return cuda_err(launch(fn, dim3((unsigned)(units * cl)), dim3(S::THREADS), S::SMEM + 4 * ((size_t)a->E + 1), s, args, false, cl, true),
                     "scaled gemm launch");
-}
-
-// The clusters of cl CTAs of the narrow kernel that run at once; a property of the
-// device, asked once for each (the query takes microseconds).
-int narrow_clusters(int device, int cl)
-{
-    static std::atomic<int> known[64][5];
-    const bool keep = device >= 0 && device < 64;
-    int n = keep ? known[device][cl].load(std::memory_order_relaxed) : 0;
-    if (n == 0) {
-        const void *fn = reinterpret_cast<const void *>(&scaled_narrow_kernel);
-        const int smem = NarrowShape::SMEM + 4 * (sg::MAX_E + 1);
-        if (set_smem(fn, smem) == cudaSuccess)
-            n = max_clusters(fn, NarrowShape::THREADS, smem, cl);
-        if (keep)
-            known[device][cl].store(n, std::memory_order_relaxed);
-    }
-    return n;
 }
 
 } // namespace
@@ -1097,21 +1138,29 @@ extern "C" int tdg_scaled_gemm(tdg_symm *h, const tdg_scaled_gemm_args *a, void 
     // start 5 us later: 2048 x 2048, one row, 5.4 by 4 CTAs and 11.8 by 8.)
     int split = 4, at_once = 0;
     for (; split > 1; --split)
-        if (kb / 2 >= split && narrow <= (at_once = narrow_clusters(h->device, split)))
+        if (kb / 2 >= split && narrow <= (at_once = clusters_at_once<NarrowShape>(h->device, split)))
             break;
     if (split == 1)
         at_once = h->sm_count;
     // The kernel whose tiles take less time, with an expert's share the average one:
     // rounds of the grid, each of a time for the tile and one for every block of K
-    // (us; 7168 x 8192: 25 narrow and 32 wide for 128 rows, 50 and 32 for 192;
-    // 32 experts of 4096 x 2048: 48 and 62 for 64 rows each, 100 and 64 for 80)
+    // (us; 7168 x 8192, 128 rows: 25 narrow, 32 wide, 21 wide by two pairs a tile;
+    // 5120 x 3200, 96 rows: 10.7, 15.5 and 12.7, and 256 rows: 15.5 wide, 13.0 by two;
+    // 32 experts of 4096 x 2048: 48 narrow and 62 wide for 64 rows each, 100 and 64 for 80)
     const int64_t used = a->E < a->M ? a->E : a->M, share = (a->M + used - 1) / used, pairs = h->sm_count / 2;
     auto time_of = [&](int64_t bt, int64_t wtile, int64_t at_once, double tile, double block) {
         const int64_t tiles = used * ((share + bt - 1) / bt) * ((a->N + wtile - 1) / wtile);
         return (double)((tiles + at_once - 1) / at_once) * (tile + block * (double)kb);
     };
-    if (time_of(WideShape::BT, WideShape::WTILE, pairs, 1.6, 0.415) <
-        time_of(NarrowShape::BT, NarrowShape::WTILE, at_once, 0.5, 0.33 / split))
+    const double by_narrow = time_of(NarrowShape::BT, NarrowShape::WTILE, at_once, 0.5, 0.33 / split);
+    const double by_wide = time_of(WideShape::BT, WideShape::WTILE, pairs, 1.6, 0.415);
+    // by two pairs a tile, all tiles at once (never less time for fewer than 10 blocks: both have some)
+    if (wide <= clusters_at_once<WideShape>(h->device, 4)) {
+        const double by_two = time_of(WideShape::BT, WideShape::WTILE, pairs, 3.6, 0.415 / 2);
+        if (by_two < by_wide && by_two < by_narrow)
+            return run<WideShape>(h, a, p, 2, wide, s);
+    }
+    if (by_wide < by_narrow)
         return run<WideShape>(h, a, p, 1, wide < pairs ? wide : pairs, s);
     return run<NarrowShape>(h, a, p, split, narrow < at_once ? narrow : at_once, s);
 }
