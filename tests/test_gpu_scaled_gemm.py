@@ -108,6 +108,14 @@ def test_tiles_with_halves_of_k(symm, M, N, lead, f32):
 
 
 @pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("M,N", [(600, 7160), (300, 10008)])
+def test_whole_rounds_and_halves_of_k(symm, M, N, f32):
+    c = Case(M, N, 4112, f32=f32, lead=1)
+    c.run(symm)
+    c.check(symm)
+
+
+@pytest.mark.parametrize("f32", [False, True])
 @pytest.mark.parametrize("rows", [[200, 0, 256], [0, 456, 0], [455, 0, 1], [70, 130, 256], [0, 0, 7]])
 def test_experts_with_halves_of_k(symm, rows, f32):
     ends = [0]

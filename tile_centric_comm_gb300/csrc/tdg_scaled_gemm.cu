@@ -89,7 +89,8 @@ struct ScaledParams {
     uint64_t timeout_ns;
     int64_t M, a_scale_stride, out_stride;
     int N, E, k_blocks, n_tiles, n_blocks, out_f32;
-    int split;                   // narrow: CTAs of a cluster that share K (1: none)
+    int split;                   // CTAs (wide: pairs) of a cluster that share K (1: none)
+    uint32_t item0, item1;       // wide: the tiles of this launch, [item0, item1)
     const float *a_scale, *b_scale;
     void *out;
     const int64_t *base;
@@ -461,12 +462,12 @@ __global__ void __launch_bounds__(WideShape::THREADS, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // the pair's place in the cluster is its part of K, the CTA's place in the pair its half of the tile
     const int rank = (int)cluster_ctarank(), half = rank & 1, part = rank >> 1, leader = rank & ~1;
-    const uint32_t unit = blockIdx.x / 2 / p.split, units = gridDim.x / 2 / p.split;
+    const uint32_t unit = p.item0 + blockIdx.x / 2 / p.split, units = gridDim.x / 2 / p.split;
     const int kb0 = part * p.k_blocks / p.split, kb1 = (part + 1) * p.k_blocks / p.split;
     const uint64_t tmo = p.timeout_ns;
     scaled_begin<S>(p, ps, pre);
     const uint32_t tmem = ps->tmem_base;
-    const uint32_t items = p.split > 1 ? min(pre[p.E], units) : pre[p.E]; // with K divided a cluster has one tile
+    const uint32_t items = min(pre[p.E], p.split > 1 ? p.item0 + units : p.item1); // with K divided a cluster has one tile
     // an instruction's columns: the weight rows of the tile in steps of 32, each CTA holding half of them
     auto columns = [&](const ScaledTile &t) { return min(S::WTILE, (p.N - t.n0 + 31) / 32 * 32); };
 
@@ -1130,6 +1131,7 @@ extern "C" int tdg_scaled_gemm(tdg_symm *h, const tdg_scaled_gemm_args *a, void 
     p.b_scale = a->b_scale;
     p.out = a->out;
     p.base = a->base;
+    p.item1 = INT32_MAX;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     // Few tiles: K divided over the CTAs of a cluster, two blocks of it each at least,
     // as long as all clusters run at once.  How many do is less than the SMs hold (46 of
@@ -1154,11 +1156,23 @@ extern "C" int tdg_scaled_gemm(tdg_symm *h, const tdg_scaled_gemm_args *a, void 
     };
     const double by_narrow = time_of(NarrowShape::BT, NarrowShape::WTILE, at_once, 0.5, 0.33 / split);
     const double by_wide = time_of(WideShape::BT, WideShape::WTILE, pairs, 1.6, 0.415);
-    // by two pairs a tile, all tiles at once (never less time for fewer than 10 blocks: both have some)
-    if (wide <= clusters_at_once<WideShape>(h->device, 4)) {
-        const double by_two = time_of(WideShape::BT, WideShape::WTILE, pairs, 3.6, 0.415 / 2);
-        if (by_two < by_wide && by_two < by_narrow)
-            return run<WideShape>(h, a, p, 2, wide, s);
+    // By two pairs a tile, as many tiles as run at once: all, or, where their number is
+    // known, those behind whole rounds, by a launch of their own, 4.5 us (1024 rows by
+    // 7168 x 8192, 112 tiles: 59 us in two whole rounds, 54 like this; 5120 x 3200, 80
+    // tiles: 26.6 and 27.8).  Halves of K always have a block: two pairs take less time
+    // from 10 blocks on.
+    const int64_t rest = wide % pairs, whole = wide - rest;
+    if (rest && (!whole || !a->base) && rest <= clusters_at_once<WideShape>(h->device, 4)) {
+        const double by_two = 3.6 + 0.415 / 2 * (double)kb + (whole ? (double)(whole / pairs) * (1.6 + 0.415 * (double)kb) + 4.5 : 0.);
+        if (by_two < by_wide && by_two < by_narrow) {
+            if (whole) {
+                p.item1 = (uint32_t)whole;
+                if (const int rc = run<WideShape>(h, a, p, 1, pairs, s))
+                    return rc;
+                p.item0 = (uint32_t)whole;
+            }
+            return run<WideShape>(h, a, p, 2, rest, s);
+        }
     }
     if (by_wide < by_narrow)
         return run<WideShape>(h, a, p, 1, wide < pairs ? wide : pairs, s);
