@@ -798,7 +798,7 @@ TDG_API int tdg_quantise(tdg_symm *h, const tdg_quantise_args *args, void *strea
  * A block's product of codes is summed in float32 by the tensor cores, then
  * multiplied with the product of its two scales (one float32 rounding) and
  * added in float32 to the blocks before; out is bf16 (rounded once, to
- * nearest even) or, with out_f32 = 1, those sums.  With few rows K may be cut
+ * nearest even) or, with out_f32 = 1, those sums.  For few tiles K may be cut
  * into parts whose sums are added in a fixed order: results depend on sizes
  * only, not on when a call runs.
  * Scales may be any float32 values whose products stay within its range.  A

@@ -236,6 +236,28 @@ def test_same_bits_again_and_in_a_graph(symm):
             c.check(symm)
 
 
+def test_halves_of_k_in_a_graph_and_on_streams_at_once(symm):
+    cases = [Case(m, n, 4112, seed=i) for i, (m, n) in enumerate(((250, 5112), (600, 7160), (1, 4096), (500, 4096)))]
+    streams = [torch.cuda.Stream() for _ in cases]
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=streams[0]):
+        for c in cases:
+            c.run(symm)
+    for _ in range(3):
+        for c, s in zip(cases, streams):
+            c.run(symm, stream=s)
+    torch.cuda.synchronize()
+    first = [c.out.clone() for c in cases]
+    for c in cases:
+        c.check(symm)
+        c.out.fill_(MARK)
+    graph.replay()
+    torch.cuda.synchronize()
+    for c, f in zip(cases, first):
+        assert torch.equal(c.out, f)
+
+
 def test_two_streams_at_once(symm):
     cases = [Case(m, 520, 1024, seed=s) for s, m in enumerate((3, 200, 40, 600))]
     streams = [torch.cuda.Stream() for _ in cases]
