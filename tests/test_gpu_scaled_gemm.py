@@ -95,6 +95,26 @@ def test_experts(symm, name, N, K, first, spare, f32):
     c.check(symm, ends)
 
 
+# shapes of narrow tiles with more than 64 rows
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("M,N,K,lead", [(100, 7160, 8208, 0), (65, 7168, 8192, 1), (128, 7176, 8064, 0), (333, 5112, 3216, 1)])
+def test_tiles_of_more_than_64_rows(symm, M, N, K, lead, f32):
+    c = Case(M, N, K, f32=f32, lead=lead)
+    c.run(symm)
+    c.check(symm)
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("rows", [[100, 128, 65, 0, 200, 129, 64, 114], [1, 17, 33, 49, 80, 81, 112, 427], [800, 0, 0, 0, 0, 0, 0, 0], [96] * 8])
+def test_experts_with_tiles_of_more_than_64_rows(symm, rows, f32):
+    ends = [0]
+    for n in rows:
+        ends.append(ends[-1] + n)
+    c = Case(800, 2056, 4112, E=8, f32=f32)
+    c.run(symm, base=torch.tensor(ends, dtype=torch.int64, device="cuda"))
+    c.check(symm, ends)
+
+
 # shapes that two pairs of CTAs share a tile of: 21 blocks of K, rows and columns that end inside a tile
 @pytest.mark.parametrize("f32", [False, True])
 @pytest.mark.parametrize("M,N,lead", [(250, 5112, 0), (100, 8072, 1), (500, 4392, 1), (129, 9216, 0)])

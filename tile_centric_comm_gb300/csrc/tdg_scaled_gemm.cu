@@ -16,13 +16,13 @@
 //           tile for start and store.  8192 rows by 7168 x 8192: 342 us, 2810 TFLOP/s.
 //           For few tiles two pairs, a cluster of four, halve K and exchange halves
 //           of their sums (192 rows by 7168 x 8192: 32 us by one pair a tile, 21 by two).
-//   narrow  128 weight rows x up to 64 rows of a.  The weights are the lanes and
-//           the rows of a the columns, which an instruction takes in steps of 16:
+//   narrow  128 weight rows x up to 64 or 128 rows of a.  The weights are the lanes
+//           and the rows of a the columns, which an instruction takes in steps of 16:
 //           an expert with few rows costs what it has, and streaming the weights
 //           is what bounds the call.  With few tiles the blocks of K are divided
 //           over the CTAs of a cluster, whose sums are added in rank order.  64 experts
-//           of 4096 x 7168 with 16 rows each: 276 us, 6.4 TB/s; one row by 3200 x 5120
-//           7.2 us, which is latency.
+//           of 4096 x 7168 with 16 rows each: 280 us, 6.7 TB/s, with 128 rows 329; one
+//           row by 3200 x 5120 7.2 us, which is latency.
 //
 // Warps of a CTA (either kernel):
 //   warp 0      TMA loader: the codes of a block into a ring of shared memory
@@ -46,6 +46,7 @@ constexpr int BAR_BYTES = 512;
 } // namespace sg
 
 struct WideShape {
+    static constexpr int BOX = sg::ROWS;             // rows of a TMA box
     static constexpr bool PAIR = true;
     static constexpr int BT = 256;                   // rows of a in a tile, over the pair
     static constexpr int WTILE = 256;                // weight rows of a tile
@@ -65,15 +66,17 @@ struct WideShape {
     static constexpr int SMEM = OFF_PRE + 1024;      // + 4 (E + 1); + alignment slack
 };
 
-struct NarrowShape {
+template <int ROWS> struct NarrowShape {
     static constexpr bool PAIR = false;
-    static constexpr int BT = 64;                    // rows of a in a tile, at most
+    static constexpr int BT = ROWS;                  // rows of a in a tile, at most
     static constexpr int WTILE = sg::ROWS;
-    static constexpr int STEP = 16;                  // of an instruction's columns, and rows of a TMA box
+    static constexpr int STEP = 16, BOX = 64;        // of an instruction's columns; rows of a TMA box, for up to STEP rows and for more
     static constexpr int BPS = 2;                    // two blocks a wait, which costs every role 100 cycles
-    static constexpr int BLOCK_BYTES = sg::A_BYTES + BT * sg::BK, STAGES = 4, STAGE_BYTES = BPS * BLOCK_BYTES;
-    static constexpr int TBUF = 4, TCOLS = BT;
-    static constexpr int EPIW = 4, THREADS = 128 + 32 * EPIW;
+    static constexpr int BLOCK_BYTES = sg::A_BYTES + BT * sg::BK, STAGES = BT == 64 ? 4 : 3, STAGE_BYTES = BPS * BLOCK_BYTES;
+    static constexpr int TCOLS = BT, TBUF = 512 / (BPS * TCOLS);
+    static constexpr int GROUPS = BT / 64, EPIW = 4 * GROUPS, THREADS = 128 + 32 * EPIW; // groups of epilogue warps: 64 sums a thread
+    static constexpr bool REGS = GROUPS > 1;         // registers are moved to the epilogue
+    static constexpr int REGS_OTHER = 72, REGS_EPI = 216;
     static constexpr int SK = 4, SCH = 3;
     static constexpr int SROW = BT + 8;
     static constexpr int STG_ROW = 80;               // bytes of a staged row: 32 bf16 and a pad
@@ -86,7 +89,8 @@ struct NarrowShape {
     static constexpr int SMEM = OFF_PRE + 1024;
     static_assert(BT * RED * 4 <= OFF_SCALE, "partial sums fit the ring");
 };
-static_assert(WideShape::SMEM + 4 * (sg::MAX_E + 1) <= 232448 && NarrowShape::SMEM + 4 * (sg::MAX_E + 1) <= 232448, "shared memory");
+static_assert(WideShape::SMEM + 4 * (sg::MAX_E + 1) <= 232448 && NarrowShape<64>::SMEM + 4 * (sg::MAX_E + 1) <= 232448 &&
+                  NarrowShape<128>::SMEM + 4 * (sg::MAX_E + 1) <= 232448, "shared memory");
 
 struct ScaledParams {
     DevStatus *status;
@@ -740,10 +744,11 @@ __global__ void __launch_bounds__(WideShape::THREADS, 1)
 // A thread of the epilogue holds, of each 8 x 8 square, two neighbouring rows
 // of a (their scales are a float pair, so the multiply-adds are packed) for one
 // row of the weights; for the store a transposing stmatrix turns the squares.
-__global__ void __launch_bounds__(NarrowShape::THREADS, 1)
-    scaled_narrow_kernel(const __grid_constant__ ScaledParams p, const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a)
+template <class S>
+__global__ void __launch_bounds__(S::THREADS, 1)
+    scaled_narrow_kernel(const __grid_constant__ ScaledParams p, const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a,
+                         const __grid_constant__ CUtensorMap map_a16)
 {
-    using S = NarrowShape;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     ScaledSmem *ps = reinterpret_cast<ScaledSmem *>(smem + S::OFF_BAR);
@@ -756,6 +761,7 @@ __global__ void __launch_bounds__(NarrowShape::THREADS, 1)
     if (threadIdx.x == 64) {
         prefetch_tensormap(&map_w);
         prefetch_tensormap(&map_a);
+        prefetch_tensormap(&map_a16);
     }
     scaled_begin<S>(p, ps, pre);
     const uint32_t tmem = ps->tmem_base;
@@ -764,12 +770,16 @@ __global__ void __launch_bounds__(NarrowShape::THREADS, 1)
     const int kb0 = (int)((int64_t)p.k_blocks * crank / p.split), kb1 = (int)((int64_t)p.k_blocks * (crank + 1) / p.split);
 
     if (warp == 0) {
+        if constexpr (S::REGS)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::REGS_OTHER));
         if (lane == 0) {
             int stage = 0;
             uint32_t phase = 0, issued = 0;
             for (uint32_t it = unit; it < items && !ps->abort; it += units) {
                 const ScaledTile t = scaled_tile<S>(p, pre, it);
-                const int boxes = t.width / S::STEP;
+                // (boxes of 16 rows alone: 64 experts of 4096 x 7168 with 128 rows each 420 us, 331 like this)
+                const int box = t.width <= S::STEP ? S::STEP : S::BOX, boxes = (t.width + box - 1) / box;
+                const CUtensorMap *map = t.width <= S::STEP ? &map_a16 : &map_a;
                 for (int kb = kb0; kb < kb1; kb += S::BPS) {
                     if (!mbar_wait_suspended(&ps->empty[stage], phase ^ 1u, tmo)) {
                         report_fault(p.status, TDG_ERR_TIMEOUT, TDG_WHERE_PIPE, 0, p.epoch);
@@ -778,13 +788,12 @@ __global__ void __launch_bounds__(NarrowShape::THREADS, 1)
                     }
                     const int blocks = min(S::BPS, kb1 - kb);
                     const uint32_t bar = smem_u32(&ps->full[stage]);
-                    mbar_arrive_expect_tx(&ps->full[stage], (uint32_t)(blocks * (sg::A_BYTES + t.width * sg::BK)));
+                    mbar_arrive_expect_tx(&ps->full[stage], (uint32_t)(blocks * (sg::A_BYTES + boxes * box * sg::BK)));
                     for (int j = 0; j < blocks; ++j) {
                         uint8_t *dst = smem + stage * S::STAGE_BYTES + j * S::BLOCK_BYTES;
                         tma_load_3d_addr(dst, &map_w, bar, (kb + j) * sg::BK, t.n0, t.e);
                         for (int i = 0; i < boxes; ++i)
-                            tma_load_2d_addr(dst + sg::A_BYTES + i * S::STEP * sg::BK, &map_a, bar, (kb + j) * sg::BK,
-                                             (int)((uint32_t)t.tok0 + i * S::STEP));
+                            tma_load_2d_addr(dst + sg::A_BYTES + i * box * sg::BK, map, bar, (kb + j) * sg::BK, (int)((uint32_t)t.tok0 + i * box));
                     }
                     ++issued;
                     if (++stage == S::STAGES) {
@@ -797,8 +806,12 @@ __global__ void __launch_bounds__(NarrowShape::THREADS, 1)
         }
         __syncwarp();
     } else if (warp == 1) {
+        if constexpr (S::REGS)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::REGS_OTHER));
         scaled_issue<S>(p, ps, smem_u32(smem), tmem, pre, items, unit, units, kb0, kb1, 0, [](const ScaledTile &t) { return t.width; });
     } else if (warp < 4) {
+        if constexpr (S::REGS)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::REGS_OTHER));
         // scales: 8 rows of a x SK blocks a step, each warp every other step
         const int j = lane % S::SK, r0 = lane / S::SK + (warp - 2) * 8;
         int chunk = 0;
@@ -840,10 +853,13 @@ __global__ void __launch_bounds__(NarrowShape::THREADS, 1)
             }
         }
     } else {
-        const int q = warp & 3; // lanes of TMEM
+        if constexpr (S::REGS)
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::REGS_EPI));
+        // lanes of TMEM; the group's chunks of 32 columns are g, g + GROUPS, ...
+        const int q = warp & 3, g = (warp - 4) >> 2;
         uint8_t *stg = smem + S::OFF_STG + (warp - 4) * S::STG;
-        constexpr int CH = S::BT / 32; // chunks of 32 columns
-        const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
+        constexpr int CH = S::BT / 32 / S::GROUPS, CW = 32 * S::GROUPS; // chunks of a warp, columns from one to the next
+        const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + g * 32;
         const uint32_t tfull0 = smem_u32(&ps->tfull[0]), sfull0 = smem_u32(&ps->sfull[0]);
         int buf = 0, chunk = 0;
         uint32_t bphase = 0, sphase = 0, failed = 0;
@@ -866,21 +882,21 @@ __global__ void __launch_bounds__(NarrowShape::THREADS, 1)
                     if (in_chunk == 0)
                         mbar_wait_suspended(sfull0 + chunk * 8, sphase, tmo, failed);
                     uint64_t s[S::BPS][N][4];
-                    const float *sc = scales + (chunk * S::SK + in_chunk) * S::SROW + 2 * (lane & 3);
+                    const float *sc = scales + (chunk * S::SK + in_chunk) * S::SROW + g * 32 + 2 * (lane & 3);
 #pragma unroll
                     for (int j = 0; j < S::BPS; ++j) // (a chunk holds whole pairs; zeros behind the last block)
 #pragma unroll
                         for (int c = 0; c < N; ++c)
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
-                                s[j][c][i] = *reinterpret_cast<const uint64_t *>(sc + j * S::SROW + c * 32 + 8 * i);
+                                s[j][c][i] = *reinterpret_cast<const uint64_t *>(sc + j * S::SROW + c * CW + 8 * i);
                     uint32_t lo[S::BPS][N][16], hi[S::BPS][N][16];
                     auto load = [&](int j) {
                         const uint32_t at = lanes + (uint32_t)((buf * S::BPS + j) * S::TCOLS);
 #pragma unroll
                         for (int c = 0; c < N; ++c) {
-                            tmem_ld_16x256b_x4(at + c * 32, lo[j][c]);
-                            tmem_ld_16x256b_x4(at + (16u << 16) + c * 32, hi[j][c]);
+                            tmem_ld_16x256b_x4(at + c * CW, lo[j][c]);
+                            tmem_ld_16x256b_x4(at + (16u << 16) + c * CW, hi[j][c]);
                         }
                     };
                     auto add = [&](int j) {
@@ -926,7 +942,7 @@ __global__ void __launch_bounds__(NarrowShape::THREADS, 1)
                     }
                 }
             };
-            if (t.width <= 32)
+            if (t.width <= CW)
                 add_blocks(std::integral_constant<int, 1>{});
             else
                 add_blocks(std::integral_constant<int, 2>{});
@@ -942,13 +958,13 @@ __global__ void __launch_bounds__(NarrowShape::THREADS, 1)
                 float *red = reinterpret_cast<float *>(smem);
 #pragma unroll
                 for (int c = 0; c < CH; ++c)
-                    if (c * 32 < t.width)
+                    if (c * CW + g * 32 < t.width)
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
 #pragma unroll
                             for (int m = 0; m < 4; ++m) {
                                 const float2 f = halves(acc[c][m >> 1][2 * i + (m & 1)]);
-                                float *d = red + (c * 32 + 8 * i + 2 * (lane & 3)) * S::RED + q * 32 + 8 * m + (lane >> 2);
+                                float *d = red + (c * CW + g * 32 + 8 * i + 2 * (lane & 3)) * S::RED + q * 32 + 8 * m + (lane >> 2);
                                 d[0] = f.x;
                                 d[S::RED] = f.y;
                             }
@@ -964,7 +980,7 @@ __global__ void __launch_bounds__(NarrowShape::THREADS, 1)
 #pragma unroll
                         for (int m = 0; m < 4; ++m) {
                             const float2 f = halves(acc[c][m >> 1][2 * i + (m & 1)]);
-                            const int64_t row = t.tok0 + c * 32 + 8 * i + 2 * (lane & 3);
+                            const int64_t row = t.tok0 + c * CW + g * 32 + 8 * i + 2 * (lane & 3);
                             const int col = n + 8 * m + (lane >> 2);
                             if (col < p.N && row < t.end)
                                 out[row * p.out_stride + col] = f.x;
@@ -977,7 +993,7 @@ __global__ void __launch_bounds__(NarrowShape::THREADS, 1)
                 const int col = n + (lane & 3) * 8;
 #pragma unroll
                 for (int c = 0; c < CH; ++c)
-                    if (c * 32 < t.width)
+                    if (c * CW + g * 32 < t.width)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             __syncwarp();
@@ -985,7 +1001,7 @@ __global__ void __launch_bounds__(NarrowShape::THREADS, 1)
                                               narrowed(acc[c][1][2 * i + 1]));
                             __syncwarp();
                             const uint4 v = *reinterpret_cast<const uint4 *>(get);
-                            const int64_t row = t.tok0 + c * 32 + 8 * i + (lane >> 2);
+                            const int64_t row = t.tok0 + c * CW + g * 32 + 8 * i + (lane >> 2);
                             if (col < p.N && row < t.end)
                                 *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + row * p.out_stride + col) = v;
                         }
@@ -1045,7 +1061,10 @@ bool map_codes(CUtensorMap *m, const void *base, int64_t inner, int64_t rows, in
 
 template <class S> const void *kernel_of()
 {
-    return S::PAIR ? reinterpret_cast<const void *>(&scaled_wide_kernel) : reinterpret_cast<const void *>(&scaled_narrow_kernel);
+    if constexpr (S::PAIR)
+        return reinterpret_cast<const void *>(&scaled_wide_kernel);
+    else
+        return reinterpret_cast<const void *>(&scaled_narrow_kernel<S>);
 }
 
 // The clusters of cl CTAs of a kernel that run at once; a property of the device,
@@ -1067,12 +1086,14 @@ template <class S> int clusters_at_once(int device, int cl)
 
 template <class S> int run(tdg_symm *h, const tdg_scaled_gemm_args *a, ScaledParams &p, int split, int64_t units, cudaStream_t s)
 {
-    CUtensorMap map_w, map_a, map_out;
-    const int box = S::PAIR ? sg::ROWS : NarrowShape::STEP, wbox = sg::ROWS;
-    if (!map_codes(&map_w, a->b, a->K, a->N, a->K, a->E, wbox, false) || !map_codes(&map_a, a->a, a->K, a->M, a->a_stride, 1, box, true))
+    CUtensorMap map_w, map_a, third; // of the output; narrow: of a, in smaller boxes
+    if (!map_codes(&map_w, a->b, a->K, a->N, a->K, a->E, sg::ROWS, false) || !map_codes(&map_a, a->a, a->K, a->M, a->a_stride, 1, S::BOX, true))
         return TDG_ERR_CUDA;
-    if (S::PAIR && !(a->out_f32 ? map_f32_2d(&map_out, a->out, a->N, a->M, a->out_stride * 4, 32, 32)
-                                : map_bf16_2d(&map_out, a->out, a->N, a->M, a->out_stride * 2, 64, 32)))
+    if constexpr (!S::PAIR) {
+        if (!map_codes(&third, a->a, a->K, a->M, a->a_stride, 1, S::STEP, true))
+            return TDG_ERR_CUDA;
+    } else if (!(a->out_f32 ? map_f32_2d(&third, a->out, a->N, a->M, a->out_stride * 4, 32, 32)
+                            : map_bf16_2d(&third, a->out, a->N, a->M, a->out_stride * 2, 64, 32)))
         return TDG_ERR_CUDA;
     const void *fn = kernel_of<S>();
     const int smem = S::SMEM + 4 * (sg::MAX_E + 1);
@@ -1082,7 +1103,7 @@ template <class S> int run(tdg_symm *h, const tdg_scaled_gemm_args *a, ScaledPar
     p.split = split;
     p.n_tiles = (int)((a->N + S::WTILE - 1) / S::WTILE);
     const int cl = S::PAIR ? 2 * split : split;
-    void *args[] = {&p, &map_w, &map_a, &map_out}; // (the narrow kernel takes three)
+    void *args[] = {&p, &map_w, &map_a, &third};
     return cuda_err(launch(fn, dim3((unsigned)(units * cl)), dim3(S::THREADS), S::SMEM + 4 * ((size_t)a->E + 1), s, args, false, cl, true),
                     "scaled gemm launch");
 }
@@ -1116,9 +1137,9 @@ extern "C" int tdg_scaled_gemm(tdg_symm *h, const tdg_scaled_gemm_args *a, void 
         const int64_t rows = a->base ? (a->E < a->M ? a->E : a->M) + a->M / bt : (a->M + bt - 1) / bt;
         return rows * ((a->N + wtile - 1) / wtile);
     };
-    const int64_t wide = most_tiles(WideShape::BT, WideShape::WTILE), narrow = most_tiles(NarrowShape::BT, NarrowShape::WTILE);
-    if (narrow > INT32_MAX)
+    if (most_tiles(NarrowShape<64>::BT, NarrowShape<64>::WTILE) > INT32_MAX)
         return TDG_ERR_INVALID;
+    const int64_t wide = most_tiles(WideShape::BT, WideShape::WTILE);
     ScaledParams p;
     memset(&p, 0, sizeof p);
     p.status = h->status;
@@ -1138,28 +1159,44 @@ extern "C" int tdg_scaled_gemm(tdg_symm *h, const tdg_scaled_gemm_args *a, void 
     p.base = a->base;
     p.item1 = INT32_MAX;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    // Few tiles: K divided over the CTAs of a cluster, two blocks of it each at least,
-    // as long as all clusters run at once.  How many do is less than the SMs hold (46 of
-    // 3, 36 of 4), since a cluster stays in its part of the chip: 38 weight tiles of 2048,
-    // one row, 6.1 us by clusters of 3 and 10.4 by clusters of 4.  (Clusters of 6 and 8
-    // start 5 us later: 2048 x 2048, one row, 5.4 by 4 CTAs and 11.8 by 8.)
-    int split = 4, at_once = 0;
-    for (; split > 1; --split)
-        if (kb / 2 >= split && narrow <= (at_once = clusters_at_once<NarrowShape>(h->device, split)))
-            break;
-    if (split == 1)
-        at_once = h->sm_count;
-    // The kernel whose tiles take less time, with an expert's share the average one:
-    // rounds of the grid, each of a time for the tile and one for every block of K
-    // (us; 7168 x 8192, 128 rows: 25 narrow, 32 wide, 21 wide by two pairs a tile;
-    // 5120 x 3200, 96 rows: 10.7, 15.5 and 12.7, and 256 rows: 15.5 wide, 13.0 by two;
-    // 32 experts of 4096 x 2048: 48 narrow and 62 wide for 64 rows each, 100 and 64 for 80)
+    // The kernel whose tiles take less time (us), with an expert's share the average
+    // one: rounds of the grid, each of a time for the tile and one for every block of K.
     const int64_t used = a->E < a->M ? a->E : a->M, share = (a->M + used - 1) / used, pairs = h->sm_count / 2;
     auto time_of = [&](int64_t bt, int64_t wtile, int64_t at_once, double tile, double block) {
         const int64_t tiles = used * ((share + bt - 1) / bt) * ((a->N + wtile - 1) / wtile);
         return (double)((tiles + at_once - 1) / at_once) * (tile + block * (double)kb);
     };
-    const double by_narrow = time_of(NarrowShape::BT, NarrowShape::WTILE, at_once, 0.5, 0.33 / split);
+    // Narrow, few tiles: K divided over the CTAs of a cluster, two blocks of it each at
+    // least, as long as all clusters run at once.  How many do is less than the SMs hold
+    // (46 of 3, 36 of 4), since a cluster stays in its part of the chip: 38 weight tiles
+    // of 2048, one row, 6.1 us by clusters of 3 and 10.4 by clusters of 4.  (Clusters of
+    // 6 and 8 start 5 us later: 2048 x 2048, one row, 5.4 by 4 CTAs and 11.8 by 8.)
+    struct Plan {
+        int split;
+        int64_t units;
+        double time;
+    };
+    auto narrow = [&](auto shape, double tile, double block, double join) {
+        using S = decltype(shape);
+        const int64_t tiles = most_tiles(S::BT, S::WTILE);
+        int split = 4, at_once = h->sm_count;
+        for (; split > 1; --split)
+            if (kb / 2 >= split && tiles <= clusters_at_once<S>(h->device, split)) {
+                at_once = clusters_at_once<S>(h->device, split);
+                break;
+            }
+        return Plan{split, tiles < at_once ? tiles : at_once, time_of(S::BT, S::WTILE, at_once, tile + (split > 1 ? join : 0.), block / split)};
+    };
+    // us measured with tiles of 64 rows, of 128, wide, and wide by two pairs a tile:
+    //   64 experts of 4096 x 7168, 64 rows each   291  299
+    //                              80 rows        383  315  385
+    //                              128 rows            329  396
+    //   7168 x 8192, 128 rows                      25   19   32   21
+    //   5120 x 3200, 96 rows                      9.3 10.3 15.5 12.7
+    //                333 rows                      20 13.1 15.6
+    // (4 us: partial sums of 128 x 128 are joined)
+    const Plan n64 = narrow(NarrowShape<64>{}, 0.5, 0.30, 0.), n128 = narrow(NarrowShape<128>{}, 1., 0.36, 4.);
+    const double by_narrow = n64.time <= n128.time ? n64.time : n128.time;
     const double by_wide = time_of(WideShape::BT, WideShape::WTILE, pairs, 1.6, 0.415);
     // By two pairs a tile, as many tiles as run at once: all, or, where their number is
     // known, those behind whole rounds, by a launch of their own, 4.5 us (1024 rows by
@@ -1181,5 +1218,7 @@ extern "C" int tdg_scaled_gemm(tdg_symm *h, const tdg_scaled_gemm_args *a, void 
     }
     if (by_wide < by_narrow)
         return run<WideShape>(h, a, p, 1, wide < pairs ? wide : pairs, s);
-    return run<NarrowShape>(h, a, p, split, narrow < at_once ? narrow : at_once, s);
+    if (n64.time <= n128.time)
+        return run<NarrowShape<64>>(h, a, p, n64.split, n64.units, s);
+    return run<NarrowShape<128>>(h, a, p, n128.split, n128.units, s);
 }
