@@ -845,7 +845,7 @@ TDG_API int tdg_scaled_gemm(tdg_symm *h, const tdg_scaled_gemm_args *args, void 
  *   dy[slot(src,t,kk)]  = bf16(gate_src[t][kk] * dout_src[t]),
  *   dgate_src[t][kk]    = sum_h dout_src[t][h] y[slot(src,t,kk)][h]
  * (T x k float32 at region(src) + dgate_off; summed in float32 in an order
- * fixed by H).  Dispatch: recv[slot(kk)] = x, so
+ * fixed by the sizes).  Dispatch: recv[slot(kk)] = x, so
  *   dx_src[t] = bf16(sum_kk drecv[slot(src,t,kk)])
  * (float32 sum in kk order; T x H bf16 at region(src) + dx_off).  y, dy and
  * drecv have the receive layout, W*T*k rows of H bf16; dy may be y itself.

@@ -82,6 +82,16 @@ class Case:
         assert bool(((self.all(self.dx).double() - sums).abs() <= tol).all())
 
 
+# a token's threads: 32, 64 and 128 for many tokens, more for few
+@pytest.mark.parametrize("W,T,H,E,k", [(1, 4999, 64, 8, 2), (2, 2501, 264, 8, 3), (1, 2601, 1032, 16, 2), (1, 1301, 2056, 8, 2), (3, 5, 512, 8, 8),
+                                       (1, 1001, 1024, 40, 32), (8, 700, 8, 16, 9)])
+def test_gradients_by_every_number_of_threads(W, T, H, E, k):
+    c = Case(W, T, H, E, k)
+    c.run()
+    assert c.symm.status()["code"] == 0
+    c.check()
+
+
 @pytest.mark.parametrize("W,T,H,E,k", [(1, 1, 8, 1, 1), (1, 3, 16, 4, 2), (2, 257, 520, 8, 2), (8, 16, 7168, 64, 8), (4, 33, 2048, 16, 3), (3, 50, 2056, 48, 9),
                                        (2, 20, 264, 32, 32), (2, 700, 128, 64, 6)])
 def test_gradients(W, T, H, E, k):

@@ -4,10 +4,13 @@
 //   dispatch: dx[t] = sum_kk drecv[slot(t,kk)]
 //
 // Bound by memory: every row of dout, y and drecv is read once, every row of
-// dy and dx written once.  One CTA a token: its threads hold 8 elements of
+// dy and dx written once.  A token's threads, a warp to a CTA, hold 8 elements of
 // dout each while they walk over the token's rows, so that dy and the partial
-// sums of dgate come from one pass.  No atomics: the sums' order is fixed.
-// 8192 tokens of 7168 with 8 rows each, both gradients: 473 us, 6.5 TB/s.
+// sums of dgate come from one pass.  No atomics: the sums' order is fixed by
+// the call's sizes.
+// 8192 tokens of 7168 with 8 rows each, both gradients: 465 us, 6.6 TB/s.
+#include <type_traits>
+
 #include "tdg_scaled.cuh"
 
 namespace tdg {
@@ -15,6 +18,20 @@ namespace tdg {
 namespace mg {
 constexpr int THREADS = 256;
 constexpr int GROUP = 8; // rows whose loads are in flight together
+
+// The threads of a token.  Many tokens: few threads, so that short rows leave none
+// idle and the ends of all rows are short (both gradients by 32, 64, 128 and 256 in
+// us; 32768 tokens of 256, 2 rows each 38, 63, 107 and 192; 8192 of 1032, 8 rows each
+// 99, 97, 103 and 112; 8192 of 7168 513, 481, 468 and 478).  Few tokens: more, up to
+// what holds a row at once (128 tokens of 7168 84, 45, 25 and 17; 514 of 520, 2 rows
+// each 7.4, 6.4, 5.5 and 6.0).
+inline int threads_of(const MoeRows &m, int sms)
+{
+    int threads = m.H < 1024 ? 32 : m.H < 2048 ? 64 : 128;
+    while (threads < THREADS && threads * 8 < m.H && m.tokens * threads < (int64_t)4 * sms * THREADS)
+        threads *= 2;
+    return threads;
+}
 } // namespace mg
 
 __device__ __forceinline__ void widen8(const uint4 &u, float (&f)[8])
@@ -41,28 +58,34 @@ __device__ __forceinline__ uint4 ld_row(const void *p)
     return v;
 }
 
+// G threads a token
+template <int G>
 __global__ void __launch_bounds__(mg::THREADS) moe_combine_grad_kernel(const __grid_constant__ MoeRows m, uint64_t gate_off, uint64_t dout_off,
                                                                       uint64_t dgate_off, const uint8_t *y, uint8_t *dy)
 {
-    __shared__ int64_t row[32];
-    __shared__ float gate[32], part[mg::THREADS / 32][32];
+    constexpr int TOKENS = mg::THREADS / G;
+    __shared__ int64_t rows[TOKENS][32];
+    __shared__ float gates[TOKENS][32], part[mg::THREADS / 32][32];
     griddep_launch_dependents();
     griddep_wait();
-    const uint32_t src = blockIdx.x / (uint32_t)m.T;
-    const int64_t tok = blockIdx.x, t = blockIdx.x - src * (uint32_t)m.T;
+    const int own = threadIdx.x / G, at = threadIdx.x % G, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int64_t *row = rows[own];
+    float *gate = gates[own];
+    const uint32_t tok32 = blockIdx.x * TOKENS + own, src = tok32 / (uint32_t)m.T;
+    const bool in = tok32 < (uint64_t)m.tokens;
+    const int64_t tok = tok32, t = tok32 - src * (uint32_t)m.T;
     uint8_t *region = m.regions + (uint64_t)src * m.region_bytes;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if ((int)threadIdx.x < m.k) {
-        row[threadIdx.x] = moe_row(m, tok, threadIdx.x, true);
-        gate[threadIdx.x] = reinterpret_cast<const float *>(region + gate_off)[t * m.k + threadIdx.x];
+    if (in && at < m.k) {
+        row[at] = moe_row(m, tok, at, true);
+        gate[at] = reinterpret_cast<const float *>(region + gate_off)[t * m.k + at];
     }
     __syncthreads();
     const uint64_t row_bytes = (uint64_t)m.H * 2;
     const uint8_t *dout = region + dout_off + (uint64_t)t * row_bytes;
-    const int64_t vecs = m.H / 8;
+    const int64_t vecs = in ? m.H / 8 : 0;
     for (int k0 = 0; k0 < m.k; k0 += mg::GROUP) {
         float dot[mg::GROUP] = {};
-        for (int64_t v = threadIdx.x; v < vecs; v += mg::THREADS) {
+        for (int64_t v = at; v < vecs; v += G) {
             uint4 yv[mg::GROUP];
             const uint4 dv = *reinterpret_cast<const uint4 *>(dout + v * 16);
 #pragma unroll
@@ -96,29 +119,36 @@ __global__ void __launch_bounds__(mg::THREADS) moe_combine_grad_kernel(const __g
         }
     }
     __syncthreads();
-    if ((int)threadIdx.x < m.k) {
+    if (in && at < m.k) {
         float sum = 0.f;
 #pragma unroll
-        for (int w = 0; w < mg::THREADS / 32; ++w)
-            sum += part[w][threadIdx.x];
-        reinterpret_cast<float *>(region + dgate_off)[t * m.k + threadIdx.x] = sum;
+        for (int w = 0; w < G / 32; ++w)
+            sum += part[own * (G / 32) + w][at];
+        reinterpret_cast<float *>(region + dgate_off)[t * m.k + at] = sum;
     }
 }
 
+template <int G>
 __global__ void __launch_bounds__(mg::THREADS) moe_dispatch_grad_kernel(const __grid_constant__ MoeRows m, uint64_t dx_off, const uint8_t *drecv)
 {
-    __shared__ int64_t row[32];
+    constexpr int TOKENS = mg::THREADS / G;
+    __shared__ int64_t rows[TOKENS][32];
     griddep_launch_dependents();
     griddep_wait();
-    const uint32_t src = blockIdx.x / (uint32_t)m.T;
-    const int64_t tok = blockIdx.x, t = blockIdx.x - src * (uint32_t)m.T;
-    if ((int)threadIdx.x < m.k)
-        row[threadIdx.x] = moe_row(m, tok, threadIdx.x, true);
+    const int own = threadIdx.x / G, at = threadIdx.x % G;
+    int64_t *row = rows[own];
+    const uint32_t tok32 = blockIdx.x * TOKENS + own, src = tok32 / (uint32_t)m.T;
+    const bool in = tok32 < (uint64_t)m.tokens;
+    const int64_t tok = tok32, t = tok32 - src * (uint32_t)m.T;
+    if (in && at < m.k)
+        row[at] = moe_row(m, tok, at, true);
     __syncthreads();
+    if (!in)
+        return;
     const uint64_t row_bytes = (uint64_t)m.H * 2;
     uint8_t *dx = m.regions + (uint64_t)src * m.region_bytes + dx_off + (uint64_t)t * row_bytes;
     const int64_t vecs = m.H / 8;
-    for (int64_t v = threadIdx.x; v < vecs; v += mg::THREADS) {
+    for (int64_t v = at; v < vecs; v += G) {
         float sum[8] = {};
         for (int k0 = 0; k0 < m.k; k0 += mg::GROUP) {
             uint4 r[mg::GROUP];
@@ -144,6 +174,22 @@ __global__ void __launch_bounds__(mg::THREADS) moe_dispatch_grad_kernel(const __
 
 using namespace tdg;
 using namespace tdg_host;
+
+namespace {
+
+// the kernel with G threads a token
+template <class F> int launch_for(const tdg_symm *h, const MoeRows &m, cudaStream_t s, void **args, const char *what, F kernel)
+{
+    const int threads = mg::threads_of(m, h->sm_count);
+    const int64_t grid = (m.tokens + mg::THREADS / threads - 1) / (mg::THREADS / threads);
+    const void *fn = threads == 32    ? kernel(std::integral_constant<int, 32>{})
+                     : threads == 64  ? kernel(std::integral_constant<int, 64>{})
+                     : threads == 128 ? kernel(std::integral_constant<int, 128>{})
+                                      : kernel(std::integral_constant<int, 256>{});
+    return cuda_err(launch(fn, dim3((unsigned)grid), dim3(mg::THREADS), 0, s, args, false, 1, true), what);
+}
+
+} // namespace
 
 extern "C" int tdg_moe_combine_grad(tdg_symm *h, const tdg_moe_combine_grad_args *a, void *stream)
 {
@@ -172,9 +218,8 @@ extern "C" int tdg_moe_combine_grad(tdg_symm *h, const tdg_moe_combine_grad_args
     const uint8_t *yp = static_cast<const uint8_t *>(a->y);
     uint8_t *dyp = static_cast<uint8_t *>(a->dy);
     void *args[] = {&m, &gate_off, &dout_off, &dgate_off, &yp, &dyp};
-    return cuda_err(launch(reinterpret_cast<const void *>(&moe_combine_grad_kernel), dim3((unsigned)m.tokens), dim3(mg::THREADS), 0,
-                           static_cast<cudaStream_t>(stream), args, false, 1, true),
-                    "moe combine grad launch");
+    return launch_for(h, m, static_cast<cudaStream_t>(stream), args, "moe combine grad launch",
+                      [](auto g) { return reinterpret_cast<const void *>(&moe_combine_grad_kernel<decltype(g)::value>); });
 }
 
 extern "C" int tdg_moe_dispatch_grad(tdg_symm *h, const tdg_moe_dispatch_grad_args *a, void *stream)
@@ -200,7 +245,6 @@ extern "C" int tdg_moe_dispatch_grad(tdg_symm *h, const tdg_moe_dispatch_grad_ar
     uint64_t dx_off = a->dx_off;
     const uint8_t *rp = static_cast<const uint8_t *>(a->drecv);
     void *args[] = {&m, &dx_off, &rp};
-    return cuda_err(launch(reinterpret_cast<const void *>(&moe_dispatch_grad_kernel), dim3((unsigned)m.tokens), dim3(mg::THREADS), 0,
-                           static_cast<cudaStream_t>(stream), args, false, 1, true),
-                    "moe dispatch grad launch");
+    return launch_for(h, m, static_cast<cudaStream_t>(stream), args, "moe dispatch grad launch",
+                      [](auto g) { return reinterpret_cast<const void *>(&moe_dispatch_grad_kernel<decltype(g)::value>); });
 }
