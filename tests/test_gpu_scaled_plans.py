@@ -4,8 +4,9 @@ sends elsewhere fails here instead of leaving a kernel untested."""
 import pytest
 import torch
 
+from expert_util import generator, product
 from launch_util import launches
-from test_gpu_scaled_gemm import MARK, Case
+from test_gpu_scaled_gemm import E4M3, MARK, Case, blocks
 from tile_centric_comm_gb300 import tdg
 
 pytestmark = pytest.mark.gpu
@@ -80,3 +81,100 @@ def test_two_launches_in_a_graph_and_on_streams_at_once(symm):
     torch.cuda.synchronize()
     for c, f in zip(cases, first):
         assert torch.equal(c.out, f)
+
+
+# a pair walks several tiles: of 5, 10, 6 and 3 blocks, so that accumulators, scale chunks (of 4 blocks) and
+# staging buffers carry over from a tile to the next in every phase
+SEVERAL = [(2000, 7160, 528), (5000, 1032, 1168), (2500, 2072, 656), (3000, 5120, 272)]
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("lead", [0, 1])
+@pytest.mark.parametrize("M,N,K", SEVERAL)
+def test_several_wide_tiles_a_pair(symm, M, N, K, lead, f32):
+    c = Case(M, N, K, f32=f32, lead=lead)
+    assert plan(symm, c) == [("wide", 2 * pairs(), 2)] and wide_tiles(M, N) > pairs()
+    c.run(symm)
+    c.check(symm)
+
+
+SHARES = {
+    "ragged": ([700, 0, 513, 257, 1, 900, 29], 2312, 1168), "some empty": ([0, 1000, 0, 0, 611, 384, 0, 300], 2304, 656),
+    "all to one": ([0, 2400, 0, 0], 2312, 1168), "whole tiles": ([256, 512, 768, 256, 512], 2568, 528),
+}
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("first,spare", [(0, 0), (5, 70)])
+@pytest.mark.parametrize("name", SHARES)
+def test_experts_by_wide_tiles(symm, name, first, spare, f32):
+    rows, N, K = SHARES[name]
+    ends = [first]
+    for n in rows:
+        ends.append(ends[-1] + n)
+    c = Case(ends[-1] + spare, N, K, E=len(rows), f32=f32)
+    base = torch.tensor(ends, dtype=torch.int64, device="cuda")
+    assert [(k, n) for k, _, n in plan(symm, c, base)] == [("wide", 2)]
+    c.run(symm, base=base)
+    c.check(symm, ends)
+
+
+def test_wide_offsets_are_read_at_each_replay(symm):
+    c = Case(2400, 2312, 1168, E=6)
+    ends = torch.tensor([0, 400, 400, 900, 1500, 1501, 2400], device="cuda")
+    assert [k for k, _, _ in plan(symm, c, ends)] == ["wide"]
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        c.run(symm, ends)
+    for new in ([0, 400, 400, 900, 1500, 1501, 2400], [3, 3, 2000, 2000, 2001, 2300, 2399], [9, 12, 20, 20, 21, 21, 33]):
+        ends.copy_(torch.tensor(new))
+        c.out.fill_(MARK)
+        graph.replay()
+        torch.cuda.synchronize()
+        c.check(symm, new)
+
+
+def test_integers_are_exact_in_wide_tiles(symm):
+    g = generator(1)
+    c = Case(2500, 2072, 656, f32=True)
+    c.a.copy_(torch.randint(-8, 9, c.a.shape, generator=g, device="cuda").float().to(E4M3))
+    c.b.copy_(torch.randint(-8, 9, c.b.shape, generator=g, device="cuda").float().to(E4M3))
+    c.a_scale.copy_(torch.exp2(torch.randint(-1, 2, c.a_scale.shape, generator=g, device="cuda").float()))
+    c.b_scale.copy_(torch.exp2(torch.randint(-1, 2, c.b_scale.shape, generator=g, device="cuda").float()))
+    assert [k for k, _, _ in plan(symm, c)] == ["wide"]
+    c.run(symm)
+    want, _ = product(c.a, c.a_scale, c.b, c.b_scale)
+    assert torch.equal(c.out.double(), want)
+
+
+def test_a_row_that_is_not_finite_stays_alone_in_wide_tiles(symm):
+    M, N, K = 2500, 2072, 656
+    c = Case(M, N, K)
+    assert [k for k, _, _ in plan(symm, c)] == ["wide"]
+    clean = c.run(symm).clone()
+    c.a.view(torch.uint8)[7, 3] = 0x7F           # NaN
+    c.a_scale[1300, 0] = float("inf")
+    c.a_scale[M - 1, blocks(K) - 1] = float("nan")
+    c.run(symm)
+    good = torch.ones(M, dtype=torch.bool, device="cuda")
+    good[[7, 1300, M - 1]] = False
+    assert torch.equal(c.out[good], clean[good])
+    assert bool(c.out[7].isnan().all()) and not bool(c.out[1300].isfinite().any()) and bool(c.out[M - 1].isnan().all())
+    c = Case(M, N, K)
+    c.b.view(torch.uint8)[1030, 1] = 0xFF        # and a row of weights one column
+    c.run(symm)
+    good = torch.arange(N, device="cuda") != 1030
+    assert torch.equal(c.out[:, good], clean[:, good]) and bool(c.out[:, 1030].isnan().all())
+
+
+def test_rows_behind_an_expert_never_reach_it_in_wide_tiles(symm):
+    """What a tile reads past an expert's last row is another expert's, or NaN; it is neither used nor written."""
+    ends = [0, 600, 600, 1300, 1900, 2250]
+    c = Case(2400, 2312, 1168, E=5)
+    c.a.view(torch.uint8)[2250:] = 0x7F
+    c.a_scale[2250:] = float("nan")
+    base = torch.tensor(ends, device="cuda")
+    assert [k for k, _, _ in plan(symm, c, base)] == ["wide"]
+    c.run(symm, base=base)
+    c.check(symm, ends)
