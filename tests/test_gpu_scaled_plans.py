@@ -4,7 +4,7 @@ sends elsewhere fails here instead of leaving a kernel untested."""
 import pytest
 import torch
 
-from expert_util import generator, product
+from expert_util import check_product, generator, product
 from launch_util import launches
 from test_gpu_scaled_gemm import E4M3, MARK, Case, blocks
 from tile_centric_comm_gb300 import tdg
@@ -178,3 +178,28 @@ def test_rows_behind_an_expert_never_reach_it_in_wide_tiles(symm):
     assert [k for k, _, _ in plan(symm, c, base)] == ["wide"]
     c.run(symm, base=base)
     c.check(symm, ends)
+
+
+@pytest.mark.parametrize("M,N,K,kernel", [(40, 136, 144, "narrow 64"), (2400, 2312, 1168, "wide")])
+@pytest.mark.parametrize("ends,bad", [([-1, .25, .5, 1], {0}), ([0, .25, .125, 1], {1}), ([0, .25, .5, 1.025], {2}), ([0, 2.0 ** 20, .5, .75], {0, 1}),
+                                      ([-2.0 ** 40, 2.0 ** 40, -3, .5], {0, 1, 2})])
+def test_the_expert_whose_offsets_are_bad_is_named_and_left_out(symm, M, N, K, kernel, ends, bad):
+    """ends in parts of M (-1 and -3 as they are): the status names one of the bad experts, and the others' rows are right."""
+    ends = [int(v) if v in (-1, -3) else round(v * M) for v in ends]
+    assert {e for e in range(3) if not 0 <= ends[e] <= ends[e + 1] <= M} == bad
+    c = Case(M, N, K, E=3)
+    base = torch.tensor(ends, dtype=torch.int64, device="cuda")
+    assert [k for k, _, _ in plan(symm, c, base)] == [kernel]
+    c.run(symm, base=base)
+    torch.cuda.synchronize()
+    st = symm.status()
+    assert st["code"] == tdg.TDG_ERR_DEVICE and st["where"] == "cu" and st["index"] in bad
+    covered = torch.zeros(M, dtype=torch.int64, device="cuda")
+    for e in set(range(3)) - bad:
+        covered[ends[e]:ends[e + 1]] += 1
+    for e in set(range(3)) - bad:
+        rows = torch.arange(ends[e], ends[e + 1], device="cuda")
+        rows = rows[covered[rows] == 1]          # (a row of two experts is undefined)
+        want, mag = product(c.a[rows], c.a_scale[rows], c.b[e], c.b_scale[e])
+        check_product(c.out[rows], want, mag, K, f"expert {e}")
+    assert bool((c.out[covered == 0] == MARK).all())
