@@ -50,11 +50,16 @@ __device__ __forceinline__ uint4 narrow8(const float (&f)[8])
     return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
 }
 
-// a row of this call's own: read once, past L1 (dy may be y, so not through the read-only path)
+// A row of this call's own: read once, past L1.  dy may be y: not through the read-only
+// path, and with "memory", since the stores to dy do not depend on the values read from
+// y and nothing else keeps them behind these loads.
 __device__ __forceinline__ uint4 ld_row(const void *p)
 {
     uint4 v;
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p)
+                 : "memory");
     return v;
 }
 
