@@ -189,14 +189,16 @@ __device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uin
 // accesses from the ones at work (481 us instead of 437 at 8192 x 7168 x 8192).
 // One piece of PTX, since the epilogue waits once a block and a phase that is
 // complete must cost it one instruction and one branch.  Sets `failed` when the
-// time is up (the clock is read only between the suspensions).
+// time is up (the clock is read only between the suspensions); a thread that has
+// failed before waits no more than two suspensions.
 __device__ __forceinline__ void mbar_wait_suspended(uint32_t bar, uint32_t parity, uint64_t timeout_ns, uint32_t &failed)
 {
     asm volatile("{\n\t.reg .pred p;\n\t.reg .u64 t, end;\n\t"
                  "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %4;\n\t"
                  "@p bra DONE_%=;\n\t"
                  "mov.u64 end, %%globaltimer;\n\t"
-                 "add.u64 end, end, %3;\n\t"
+                 "setp.eq.u32 p, %0, 0;\n\t"
+                 "@p add.u64 end, end, %3;\n\t"
                  "AGAIN_%=:\n\t"
                  "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %4;\n\t"
                  "@p bra DONE_%=;\n\t"
@@ -601,7 +603,11 @@ __global__ void __launch_bounds__(WideShape::THREADS, 1)
             tc_fence_after();
             load(0);
             float s = scale_at[chunk * S::SK * S::SROW];
-            for (int kb = kb0, in_chunk = 0; kb < kb1 && !failed; ++kb) {
+            // Walked to its end also after a wait that has run out: lanes may differ in that,
+            // and the loads of TMEM take the whole warp.  (Unrolled, registers spill; ended by
+            // a vote of the lanes, 8192 x 7168 x 8192 takes 1 % longer.)
+#pragma unroll 1
+            for (int kb = kb0, in_chunk = 0; kb < kb1; ++kb) {
                 const bool more = kb + 1 < kb1;
                 tmem_ld_wait();
 #pragma unroll
@@ -878,7 +884,8 @@ __global__ void __launch_bounds__(S::THREADS, 1)
             // accumulator is on its way while the one before is added.
             auto add_blocks = [&](auto chunks) {
                 constexpr int N = decltype(chunks)::value;
-                for (int kb = kb0, in_chunk = 0; kb < kb1 && !failed; kb += S::BPS) {
+#pragma unroll 1
+                for (int kb = kb0, in_chunk = 0; kb < kb1; kb += S::BPS) { // (to the end, as in the wide kernel)
                     const bool two = kb + 1 < kb1;
                     if (in_chunk == 0)
                         mbar_wait_suspended(sfull0 + chunk * 8, sphase, tmo, failed);
