@@ -432,23 +432,27 @@ __device__ __forceinline__ void scaled_issue(const ScaledParams &p, ScaledSmem *
         if (!ok) {
             report_fault(p.status, TDG_ERR_TIMEOUT, TDG_WHERE_PIPE, 1, p.epoch);
             ps->abort = 1;
-            // every MMA issued has finished before TMEM is freed (commits tell of
-            // the executing thread's own: the lane elected here is the one above)
-            if (S::PAIR)
-                umma_commit_pair_mask(&ps->drain, pair);
-            else
-                umma_commit(&ps->drain);
-            (void)mbar_wait(&ps->drain, 0, tmo);
         }
     }
     __syncwarp();
 }
 
-// After the roles: where a wait ran out, wait (bounded) until no TMA write of
-// this CTA is still in flight.
-template <class S> __device__ __forceinline__ void scaled_drain(const ScaledParams &p, ScaledSmem *ps, bool leader)
+// After the roles: where any wait of this CTA ran out, wait (bounded) until no
+// MMA that it issued and no TMA write of its own is still in flight.  (Where none
+// did, its epilogue has waited for all of them; a pair's are the leader's.)
+template <class S> __device__ __forceinline__ void scaled_drain(const ScaledParams &p, ScaledSmem *ps)
 {
     __syncthreads();
+    const uint32_t rank = S::PAIR ? cluster_ctarank() : 0; // (read again: kept, it costs the wide epilogue a register)
+    const bool leader = (rank & 1) == 0;
+    // (commits tell of the executing thread's own: the lane elected here is the issuing one)
+    if (ps->abort && leader && threadIdx.x >> 5 == 1 && elected()) {
+        if (S::PAIR)
+            umma_commit_pair_mask(&ps->drain, (uint16_t)(3u << rank));
+        else
+            umma_commit(&ps->drain);
+        (void)mbar_wait(&ps->drain, 0, p.timeout_ns);
+    }
     if (ps->abort && threadIdx.x == 0) {
         if (leader) {
             for (uint32_t f = ps->consumed; f < ps->issued; ++f)
@@ -740,7 +744,7 @@ __global__ void __launch_bounds__(WideShape::THREADS, 1)
     }
     if (p.split > 1 && (warp < 4 || unit >= items))
         cluster_sync(); // the one of the epilogue's exchange
-    scaled_drain<S>(p, ps, half == 0);
+    scaled_drain<S>(p, ps);
     cluster_sync(); // no CTA leaves while the other may still touch it
     if (warp == 1) {
         tc_fence_after();
@@ -1016,7 +1020,7 @@ __global__ void __launch_bounds__(S::THREADS, 1)
             }
         }
     }
-    scaled_drain<S>(p, ps, true);
+    scaled_drain<S>(p, ps);
     if (p.split > 1) {
         cluster_sync(); // the partial sums are there
         if (unit < items && !ps->abort) {
