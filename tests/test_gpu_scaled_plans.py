@@ -203,3 +203,27 @@ def test_the_expert_whose_offsets_are_bad_is_named_and_left_out(symm, M, N, K, k
         want, mag = product(c.a[rows], c.a_scale[rows], c.b[e], c.b_scale[e])
         check_product(c.out[rows], want, mag, K, f"expert {e}")
     assert bool((c.out[covered == 0] == MARK).all())
+
+
+@pytest.mark.parametrize("M,N,K,kernel", [(4000, 512, 256, "narrow 64"), (40000, 512, 1040, "wide")])
+def test_bad_offsets_take_no_longer_than_good_ones(symm, M, N, K, kernel):
+    """Every other expert with all M rows, 128 times as many as there are: what the call computes stays bounded by M and E."""
+    E = 256
+    c = Case(M, N, K, E=E)
+    good = torch.arange(E + 1, device="cuda") * M // E
+    bad = torch.tensor([0, M] * (E // 2) + [0], device="cuda")
+    assert [k for k, _, _ in plan(symm, c, good)] == [kernel]
+
+    def time(base):
+        times = []
+        for _ in range(5):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            c.run(symm, base)
+            b.record()
+            torch.cuda.synchronize()
+            times.append(a.elapsed_time(b))
+        return min(times)
+    usual, ms = time(good), time(bad)
+    assert symm.status()["where"] == "cu"
+    assert ms < 4 * usual + 0.05                 # (128 times the products without the bound)

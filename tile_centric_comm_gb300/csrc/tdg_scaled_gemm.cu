@@ -100,7 +100,7 @@ struct ScaledParams {
     int64_t M, a_scale_stride, out_stride;
     int N, E, k_blocks, n_tiles, n_blocks, out_f32;
     int split;                   // CTAs (wide: pairs) of a cluster that share K (1: none)
-    uint32_t item0, item1;       // wide: the tiles of this launch, [item0, item1)
+    uint32_t item0, item1;       // the tiles of this launch, [item0, item1): at most those that offsets in order give
     const float *a_scale, *b_scale;
     void *out;
     const int64_t *base;
@@ -776,7 +776,7 @@ __global__ void __launch_bounds__(S::THREADS, 1)
     }
     scaled_begin<S>(p, ps, pre);
     const uint32_t tmem = ps->tmem_base;
-    const uint32_t items = p.split > 1 ? min(pre[p.E], units) : pre[p.E]; // with K divided a cluster has one tile
+    const uint32_t items = min(pre[p.E], p.split > 1 ? units : p.item1); // with K divided a cluster has one tile
     // this CTA's blocks of K
     const int kb0 = (int)((int64_t)p.k_blocks * crank / p.split), kb1 = (int)((int64_t)p.k_blocks * (crank + 1) / p.split);
 
@@ -1169,7 +1169,6 @@ extern "C" int tdg_scaled_gemm(tdg_symm *h, const tdg_scaled_gemm_args *a, void 
     p.b_scale = a->b_scale;
     p.out = a->out;
     p.base = a->base;
-    p.item1 = INT32_MAX;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     // The kernel whose tiles take less time (us): rounds of the grid, each of a time for
     // the tile and one for every block of K.  Experts' shares are counted as what tokens
@@ -1188,7 +1187,7 @@ extern "C" int tdg_scaled_gemm(tdg_symm *h, const tdg_scaled_gemm_args *a, void 
     // 6 and 8 start 5 us later: 2048 x 2048, one row, 5.4 by 4 CTAs and 11.8 by 8.)
     struct Plan {
         int split;
-        int64_t units;
+        int64_t units, tiles;
         double time;
     };
     auto narrow = [&](auto shape, double tile, double block, double join) {
@@ -1200,7 +1199,7 @@ extern "C" int tdg_scaled_gemm(tdg_symm *h, const tdg_scaled_gemm_args *a, void 
                 at_once = clusters_at_once<S>(h->device, split);
                 break;
             }
-        return Plan{split, tiles < at_once ? tiles : at_once, time_of(S::BT, S::WTILE, at_once, tile + (split > 1 ? join : 0.), block / split)};
+        return Plan{split, tiles < at_once ? tiles : at_once, tiles, time_of(S::BT, S::WTILE, at_once, tile + (split > 1 ? join : 0.), block / split)};
     };
     // us measured with tiles of 64 rows, of 128, wide, and wide by two pairs a tile:
     //   64 experts of 4096 x 7168, 64 rows each   291  299
@@ -1219,6 +1218,7 @@ extern "C" int tdg_scaled_gemm(tdg_symm *h, const tdg_scaled_gemm_args *a, void 
     // tiles: 26.6 and 27.8).  Halves of K always have a block: two pairs take less time
     // from 10 blocks on.
     const int64_t rest = wide % pairs, whole = wide - rest;
+    p.item1 = (uint32_t)wide;
     if (rest && (!whole || !a->base) && rest <= clusters_at_once<WideShape>(h->device, 4)) {
         const double by_two = 3.6 + 0.415 / 2 * (double)kb + (whole ? (double)(whole / pairs) * (1.6 + 0.415 * (double)kb) + 4.5 : 0.);
         if (by_two < by_wide && by_two < by_narrow) {
@@ -1227,12 +1227,14 @@ extern "C" int tdg_scaled_gemm(tdg_symm *h, const tdg_scaled_gemm_args *a, void 
                 if (const int rc = run<WideShape>(h, a, p, 1, pairs, s))
                     return rc;
                 p.item0 = (uint32_t)whole;
+                p.item1 = (uint32_t)wide;
             }
             return run<WideShape>(h, a, p, 2, rest, s);
         }
     }
     if (by_wide < by_narrow)
         return run<WideShape>(h, a, p, 1, wide < pairs ? wide : pairs, s);
+    p.item1 = (uint32_t)(n64.time <= n128.time ? n64 : n128).tiles;
     if (n64.time <= n128.time)
         return run<NarrowShape<64>>(h, a, p, n64.split, n64.units, s);
     return run<NarrowShape<128>>(h, a, p, n128.split, n128.units, s);
