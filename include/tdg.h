@@ -767,7 +767,8 @@ TDG_API int tdg_moe_dispatch_combine_noalloc(tdg_symm *h, const tdg_moe_args *ar
  * < 2^30, fewer than 2^32 - 128 blocks of 1 x 128 (2^31 of 128 x 128); strides in elements, at least the row's extent, x's a multiple of 8
  * and the codes' of 16; scale_stride >= ceil(K/128) (BLOCKS: equal); x and
  * codes 16-byte aligned, scale 4-byte, count 8-byte; outputs overlapping no
- * input and not each other.  rows == 0 or E == 0 is a no-op.
+ * input and not each other (columns of one buffer, with rows equally many bytes
+ * apart, do not overlap).  rows == 0 or E == 0 is a no-op.
  */
 #define TDG_QUANT_ROWS 0
 #define TDG_QUANT_GATED 1
@@ -812,7 +813,8 @@ TDG_API int tdg_quantise(tdg_symm *h, const tdg_quantise_args *args, void *strea
  * < 2^24; 1 <= E <= 4096, E * N < 2^31, and E = 1 without base; a_stride (a multiple of 16) and
  * out_stride (of 8; of 4 with out_f32) at least the row's extent, all strides below 2^31; a, b and out
  * 16-byte aligned, scales 4-byte, base 8-byte; a_scale_stride >= ceil(K/128);
- * out overlapping no input.  M == 0 is a no-op.
+ * out overlapping no input (columns of one buffer, with rows equally many bytes
+ * apart, do not overlap).  M == 0 is a no-op.
  */
 typedef struct {
     int64_t M, N, K, E;

@@ -305,7 +305,9 @@ extern "C" int tdg_quantise(tdg_symm *h, const tdg_quantise_args *a, void *strea
     const int64_t bands = (a->rows + 127) / 128; // of one matrix
     const Range x{a->x, extent(rows, a->x_stride, width, 2)}, codes{a->codes, extent(rows, a->codes_stride, a->K, 1)};
     const Range scale{a->scale, extent(blocks ? bands * a->E : a->rows, a->scale_stride, kb, 4)}, count{a->count, 8};
-    if (ranges_overlap({codes, scale}, {x, count}) || ranges_overlap({codes}, {scale}))
+    const ByteRows xr{a->x, 2 * a->x_stride, 2 * width}, cr{a->codes, a->codes_stride, a->K}, sr{a->scale, 4 * a->scale_stride, 4 * kb};
+    if (ranges_overlap({codes, scale}, {count}) || rows_share(rows, cr, xr) ||
+        (blocks ? ranges_overlap({scale}, {x, codes}) : rows_share(rows, sr, xr) || rows_share(rows, sr, cr)))
         return TDG_ERR_INVALID;
     QuantParams p;
     memset(&p, 0, sizeof p);

@@ -47,6 +47,18 @@ inline uint64_t extent(int64_t rows, int64_t stride, int64_t width, int esz)
     return rows <= 0 ? 0 : ((uint64_t)(rows - 1) * stride + width) * esz;
 }
 
+// `n` rows of a matrix, stride and width in bytes
+struct ByteRows {
+    const void *at;
+    int64_t stride, width;
+};
+// Whether two matrices of n rows share a byte; columns of one buffer (equal
+// strides) are told apart.  All sizes here are even, for rows_clash's units of 2.
+inline bool rows_share(int64_t n, const ByteRows &a, const ByteRows &b)
+{
+    return rows_clash(n, a.at, a.stride / 2, a.width / 2, n, b.at, b.stride / 2, b.width / 2);
+}
+
 inline bool in_region(const tdg_symm *h, uint64_t off, uint64_t bytes)
 {
     return bytes <= h->region_bytes && off <= h->region_bytes - bytes;

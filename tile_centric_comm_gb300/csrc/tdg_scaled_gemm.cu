@@ -1139,10 +1139,11 @@ extern "C" int tdg_scaled_gemm(tdg_symm *h, const tdg_scaled_gemm_args *a, void 
         !a->b_scale || !aligned4(a->b_scale) || !aligned8(a->base) || !stride_ok(a->a_stride, a->K, 16) ||
         !stride_ok(a->a_scale_stride, kb, 1) || !stride_ok(a->out_stride, a->N, 16 / esz))
         return TDG_ERR_INVALID;
-    const Range out{a->out, extent(a->M, a->out_stride, a->N, esz)}, ra{a->a, extent(a->M, a->a_stride, a->K, 1)};
-    const Range rs{a->a_scale, extent(a->M, a->a_scale_stride, kb, 4)}, rb{a->b, (uint64_t)a->E * a->N * a->K};
+    const Range out{a->out, extent(a->M, a->out_stride, a->N, esz)}, rb{a->b, (uint64_t)a->E * a->N * a->K};
     const Range rbs{a->b_scale, (uint64_t)a->E * nb * kb * 4}, base{a->base, (uint64_t)(a->E + 1) * 8};
-    if (ranges_overlap({out}, {ra, rs, rb, rbs, base}))
+    const ByteRows outr{a->out, esz * a->out_stride, esz * a->N};
+    if (ranges_overlap({out}, {rb, rbs, base}) || rows_share(a->M, outr, {a->a, a->a_stride, a->K}) ||
+        rows_share(a->M, outr, {a->a_scale, 4 * a->a_scale_stride, 4 * kb}))
         return TDG_ERR_INVALID;
     // the tiles, at most, of each kernel's shape: with experts, one more for each than its rows fill
     auto most_tiles = [&](int64_t bt, int64_t wtile) {
