@@ -121,11 +121,11 @@ __device__ __forceinline__ float gated(float g, float u)
     return g * r * u;
 }
 
-// DEPTH blocks a thread, their loads in flight together.  (Gated, one block: 40
-// registers, which keep its four loads together, 58 us for 32768 x 2048; left to
-// itself the compiler takes 32 and 62 us.)
+// DEPTH blocks a thread, their loads in flight together; gated always one, by which
+// 32768 x 2048 take 53 us and by two 67.  (Six CTAs an SM are asked for there, 40
+// registers a thread: without that 59 us.)
 template <bool GATED, int DEPTH>
-__global__ void __launch_bounds__(qn::THREADS, GATED && DEPTH == 1 ? 6 : 1) quantise_rows_kernel(const __grid_constant__ QuantParams p)
+__global__ void __launch_bounds__(qn::THREADS, GATED ? 6 : 1) quantise_rows_kernel(const __grid_constant__ QuantParams p)
 {
     griddep_launch_dependents();
     griddep_wait();
@@ -335,14 +335,13 @@ extern "C" int tdg_quantise(tdg_symm *h, const tdg_quantise_args *a, void *strea
                         "quantise blocks launch");
     }
     const int64_t units = rows * kb;
-    const int depth = !gate && units > (int64_t)h->sm_count * 8 * qn::UNITS ? 2 : 1; // (gated: 80 us by two, 74 by one, whose registers let half as many more warps in)
+    const int depth = !gate && units > (int64_t)h->sm_count * 8 * qn::UNITS ? 2 : 1;
     const int64_t grid = (units + depth * qn::UNITS - 1) / (depth * qn::UNITS);
     if (units > UINT32_MAX - 4 * qn::UNITS)
         return TDG_ERR_INVALID;
-    const void *fn = gate ? (depth == 2 ? reinterpret_cast<const void *>(&quantise_rows_kernel<true, 2>)
-                                        : reinterpret_cast<const void *>(&quantise_rows_kernel<true, 1>))
-                          : (depth == 2 ? reinterpret_cast<const void *>(&quantise_rows_kernel<false, 2>)
-                                        : reinterpret_cast<const void *>(&quantise_rows_kernel<false, 1>));
+    const void *fn = gate         ? reinterpret_cast<const void *>(&quantise_rows_kernel<true, 1>)
+                     : depth == 2 ? reinterpret_cast<const void *>(&quantise_rows_kernel<false, 2>)
+                                  : reinterpret_cast<const void *>(&quantise_rows_kernel<false, 1>);
     void *args[] = {&p};
     return cuda_err(launch(fn, dim3((unsigned)grid), dim3(qn::THREADS), 0, s, args, false, 1, true), "quantise rows launch");
 }
