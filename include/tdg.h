@@ -756,7 +756,10 @@ TDG_API int tdg_moe_dispatch_combine_noalloc(tdg_symm *h, const tdg_moe_args *ar
  *   TDG_QUANT_GATED:  x has `rows` rows of 2K, columns [0, K) the gate g and
  *                     [K, 2K) the up projection u; what is quantised is
  *                     g / (1 + exp(-g)) * u in float32 (not rounded to
- *                     bf16; finite g and u; 0 for g below -87).
+ *                     bf16; finite g and u; 0 for g below -87), by an
+ *                     approximate 2^x and reciprocal: off by at most 2^-20 +
+ *                     2^-23 max(-g, 0) relative (2^-16.5 near -87), and the
+ *                     scale by as much of the block's largest.
  *   TDG_QUANT_BLOCKS: x is E matrices of `rows` x K, one behind the other
  *                     (matrix e from row e * rows on); scale: E matrices of
  *                     ceil(rows/128) x ceil(K/128).

@@ -802,9 +802,9 @@ def quantise_rows(symm: Symm, x, codes, scale, gated=False, count=None, stream=N
     """Rows x (n, K) bfloat16 into e4m3 codes (n, K) with a float32 scale for
     each row and block of 128, scale (n, ceil(K / 128)); rows of all three may
     be strided.  gated: x is (n, 2K), gate columns before up columns, and what
-    is quantised is silu(gate) * up.  count: int64 tensor whose first element is
-    the number of rows in use (base[E:] of the MoE routing); the others are
-    left alone."""
+    is quantised is silu(gate) * up, to 2^-20 + 2^-23 max(-gate, 0) of it.
+    count: int64 tensor whose first element is the number of rows in use
+    (base[E:] of the MoE routing); the others are left alone."""
     if _torch is None:
         _attn()
     dev = symm.device
