@@ -804,7 +804,10 @@ TDG_API int tdg_quantise(tdg_symm *h, const tdg_quantise_args *args, void *strea
  * added in float32 to the blocks before; out is bf16 (rounded once, to
  * nearest even) or, with out_f32 = 1, those sums.  For few tiles K may be cut
  * into parts whose sums are added in a fixed order: results depend on sizes
- * only, not on when a call runs.
+ * only, not on when a call runs.  With base the kernel is chosen by M, as if
+ * all rows were in use and near evenly shared, since the offsets are on the
+ * device: where M is sized for the largest step, a short one takes longer than
+ * with an M of its own (results are right for any offsets).
  * Scales may be any float32 values whose products stay within its range.  A
  * row's codes and scales reach only that row of out (a NaN in one row gives
  * NaN there alone).
