@@ -8,7 +8,9 @@
 // dout each while they walk over the token's rows, so that dy and the partial
 // sums of dgate come from one pass.  No atomics: the sums' order is fixed by
 // the call's sizes.
-// 8192 tokens of 7168 with 8 rows each, both gradients: 465 us, 6.6 TB/s.
+// 8192 tokens of 7168 with 8 rows each, both gradients: 464 us, 6.6 TB/s.  Few
+// long tokens are bound by latency, since a token has one CTA at most: 1 of them
+// 11.5 us, 128 17.3.
 #include <type_traits>
 
 #include "tdg_scaled.cuh"

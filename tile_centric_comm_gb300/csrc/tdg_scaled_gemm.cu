@@ -13,7 +13,8 @@
 //           TMEM's lanes, so a thread of the epilogue needs one scale a block.
 //           Bound by the accumulator's way (products, epilogue, release; TMEM holds two
 //           of 256 columns): 0.42 us a block against 0.27 of tensor work, 1.9 us a
-//           tile for start and store.  8192 rows by 7168 x 8192: 342 us, 2810 TFLOP/s.
+//           tile for start and store.  8192 rows by 7168 x 8192: 369 us
+//           among other calls, 2610 TFLOP/s, and 332 repeated back to back, 2900.
 //           For few tiles two pairs, a cluster of four, halve K and exchange halves
 //           of their sums (192 rows by 7168 x 8192: 32 us by one pair a tile, 21 by two).
 //   narrow  128 weight rows x up to 64 or 128 rows of a.  The weights are the lanes
@@ -22,7 +23,7 @@
 //           is what bounds the call.  With few tiles the blocks of K are divided
 //           over the CTAs of a cluster, whose sums are added in rank order.  64 experts
 //           of 4096 x 7168 with 16 rows each: 280 us, 6.7 TB/s, with 128 rows 329; one
-//           row by 3200 x 5120 7.2 us, which is latency.
+//           row by 3200 x 5120 7.3 us, which is latency.
 //
 // Warps of a CTA (either kernel):
 //   warp 0      TMA loader: the codes of a block into a ring of shared memory
